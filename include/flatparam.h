@@ -15,7 +15,8 @@
  * Around that step: the per-parameter dim-0 layout (FSDP2), accumulation
  * without communication (no_sync), the loss scaler's update and the
  * gradient factor (unscale, global-norm clipping), the reduce of hybrid
- * sharding, and resharding a flat buffer to another rank count.
+ * sharding, resharding a flat buffer to another rank count, and the AdamW
+ * step over many separate tensors with moments in 32 or in 8 bits.
  * On one GPU the N "ranks" are buffers on that GPU.
  *
  * Pages the operations follow (cited by title and section):
@@ -52,7 +53,7 @@
  * The library keeps no global mutable state apart from that message and a
  * per-device cache of occupancy figures (fixed properties of the device and
  * the code object, computed on first use).  Plans (fp_plan, fp_units,
- * fp_shard0_plan, fp_reshard_plan) own the device tables their calls build.
+ * fp_shard0_plan, fp_reshard_plan, fp_params) own the device tables their calls build.
  * A host allocation failure inside a call returns FP_ERR_DEVICE; no C++
  * exception crosses this interface.
  */
@@ -658,6 +659,121 @@ fp_status fp_grad_coef(const double* sq_norm, const float* loss_scale, double ma
  * the pages.  growth_interval >= 1, factors > 0.  One lane, on `stream`. */
 fp_status fp_scaler_update(const int32_t* found_inf, float* scale, int32_t* clean_steps, float growth_factor,
                            float backoff_factor, int32_t growth_interval, void* stream);
+
+/* ------------------------------------------------------------------ params */
+
+/* The optimizer step over many separate tensors: the parameters of a model,
+ * or the local pieces of a parameter group ([DP] FSDP2 sections: a rank
+ * holds its rows of every parameter, fp_shard0_views), each with its own
+ * gradient, fp32 master weights and, where wanted, low-precision copy, in one
+ * launch for all of them.  Beside fp_adamw_shard and fp_units_step, which
+ * take one flat shard or partition, the tensors here stay where they are, and
+ * parameter groups can differ in every hyperparameter.
+ *
+ * fp_params_create: n >= 1 tensors of numel[i] >= 0 elements.
+ * group: host array of n group numbers in [0, FP_MAX_GROUPS), or NULL (all
+ *   0); a step takes one set of hyperparameters per group.
+ * grads: host array of n device pointers to gradients of type grad_dtype
+ *   (FP_DTYPE_*).  master: host array of n device pointers to fp32 weights,
+ *   or NULL for a plan that only takes the norm.  copies: host array of n
+ *   device pointers that receive the weights in copy_dtype (FP_DTYPE_BF16 or
+ *   FP_DTYPE_F16), or NULL.  All tensors contiguous and aligned to their
+ *   element size (views of a buffer at any element); pointers of empty
+ *   tensors may be NULL.  Weights and copies overlap nothing else.
+ * The moments sit in one partition (fp_params_info): tensor i's start at
+ *   element offset_i = sum over j < i of numel[j] rounded up to a multiple of
+ *   32 (fp_params_offsets).  Partition elements between two tensors are
+ *   never written.
+ * The pointers are fixed for the plan's life, except the gradients'
+ * (fp_params_set_grads).  Creation allocates and fills device tables on the
+ * current device with a synchronous copy (a set-up call: not for graph
+ * capture); calls must be made with that device current.
+ * Errors: FP_ERR_RANGE (n, sizes, groups), FP_ERR_INVALID (NULL pointers,
+ * unknown types, overlaps), FP_ERR_ALIGN, FP_ERR_DEVICE. */
+#define FP_DTYPE_F32 0
+#define FP_DTYPE_BF16 1
+#define FP_DTYPE_F16 2
+#define FP_MAX_GROUPS 16
+typedef struct fp_params fp_params;
+fp_status fp_params_create(int32_t n, const int64_t* numel, const int32_t* group, int32_t grad_dtype,
+                           const void* const* grads, float* const* master, int32_t copy_dtype, void* const* copies,
+                           fp_params** out);
+/* Releases the plan; the caller makes sure none of its calls is running. */
+void fp_params_destroy(fp_params* params);
+/* partition: elements of the moments' partition, a multiple of 32;
+ * workspace_bytes: of fp_params_grad_norm.  Either output may be NULL. */
+fp_status fp_params_info(const fp_params* params, int64_t* partition, int64_t* workspace_bytes);
+/* offsets: host array of n elements, receives offset_i. */
+fp_status fp_params_offsets(const fp_params* params, int64_t* offsets);
+
+/* New gradient buffers of the same sizes and type, for callers whose
+ * gradients move from step to step: the table is uploaded on `stream` from
+ * pinned staging (waiting on the host only if the previous upload has not
+ * finished).  Calls that share a plan must be ordered with it on one stream;
+ * graphs captured from the plan's calls then read the new buffers too.  Not
+ * while `stream` is captured (FP_ERR_INVALID). */
+fp_status fp_params_set_grads(fp_params* params, const void* const* grads, void* stream);
+
+/* The gradients' sum of squares (fp64, a fixed order: bitwise reproducible)
+ * into *sq_norm, and FP_FLAG_OVERFLOW or-ed into *found_inf (may be NULL) if
+ * any element is +-inf or NaN: the inputs of fp_grad_coef, the step below and
+ * fp_scaler_update.  workspace: device, fp_params_info's size, 16-byte
+ * aligned, zero-filled once before its first use; every completed call leaves
+ * it reusable, calls that may run concurrently need separate ones.  With no
+ * elements *sq_norm = 0. */
+fp_status fp_params_grad_norm(const fp_params* params, int32_t* found_inf, double* sq_norm, void* workspace,
+                              void* stream);
+
+/* fp_adamw_shard's update of every tensor, from fp32 moments.  hp: host array
+ * of n_groups sets of hyperparameters, tensor i taking hp[group[i]].
+ * exp_avg, exp_avg_sq: device fp32[partition], 16-byte aligned.  found_inf,
+ * grad_coef as in fp_adamw_shard: on a skip the weights and moments are
+ * untouched and the copies receive the unchanged weights.  The copies are the
+ * weights rounded to nearest even. */
+fp_status fp_params_adamw(fp_params* params, int32_t n_groups, const fp_adamw_hparams* hp, float* exp_avg,
+                          float* exp_avg_sq, const int32_t* found_inf, const double* grad_coef, void* stream);
+
+/* The same with moments in 8 bits (6.06 instead of 12 bytes of weights and
+ * moments per element): MXFP8, e4m3 codes and one scale byte b for every 32
+ * consecutive partition elements, standing for code * 2^(b - 127); b = 255
+ * stands for NaN.  exp_avg holds the first moment m, `root` the square root r
+ * of the second (the root keeps v's range in 8 bits).  Per element, in fp64
+ * from the fp32 weights and the decoded moments:
+ *   m' = beta1 m + (1 - beta1) g,  v' = beta2 r^2 + (1 - beta2) g^2,
+ * the weights as in fp_adamw_shard from the unrounded m' and v', and then
+ * m' and r' = sqrt(v') are rounded to fp32 and stochastically to e4m3.  With
+ * x in a block whose largest magnitude is X (elements past a tensor's end do
+ * not count):
+ *   f = (fp32 bits of X + 2^19) >> 23;  b = f >= 255 ? 255 : max(0, f - 7);
+ *   y = |x| 2^(7 - b) as an fp32;  code = ((bits of y) + 16 d) >> 20,
+ * with x's sign; codes of a b = 255 block are 0 (a block with an element that
+ * is not finite reads as NaN until it is reset: pass found_inf).  An r' > 0
+ * whose code would be 0 gets the code 1.  Stochastic, because the moments
+ * change by less than half an e4m3 step: rounded to nearest, a decaying
+ * second moment would never move.  d is the high (for r the low) half of a
+ * 32-bit hash of the element's partition index i and the seed:
+ *   x = (i * 0x9E3779B1) ^ key;  x ^= x >> 16;  x *= 0x6A09E667;
+ *   x ^= x >> 15;  x *= 0xBB67AE85                       (modulo 2^32)
+ *   key: z = seed * 0x9E3779B97F4A7C15;  z ^= z >> 32;
+ *   z *= 0xD6E8FEB86659FD93;  key = low half of z ^ (z >> 32)  (modulo 2^64)
+ * so a step is reproducible from its seed; give every step another one (its
+ * step count will do).  exp_avg, root: device uint8[partition], 16-byte
+ * aligned; exp_avg_scale, root_scale: device uint8[partition / 32].  All-zero
+ * bytes are zero moments. */
+fp_status fp_params_adamw8(fp_params* params, int32_t n_groups, const fp_adamw_hparams* hp, uint8_t* exp_avg,
+                           uint8_t* exp_avg_scale, uint8_t* root, uint8_t* root_scale, uint64_t seed,
+                           const int32_t* found_inf, const double* grad_coef, void* stream);
+
+/* Moments between fp32 and MXFP8 (a checkpoint, resharding: fp_reshard moves
+ * fp32 moments), over n elements.  Quantization rounds to nearest even:
+ *   code = ((bits of y) + 2^19 - 1 + (bit 20 of y)) >> 20,
+ * so values that MXFP8 holds come back as they are.  root != 0: x is a second
+ * moment (>= 0, or NaN results): codes hold its root, sqrt in fp64 rounded to
+ * fp32, and dequantization squares.  x: device fp32[n], codes: device
+ * uint8[n], both 16-byte aligned; scales: device uint8[ceil(n / 32)]. */
+fp_status fp_mx8_quantize(int64_t n, int32_t root, const float* x, uint8_t* codes, uint8_t* scales, void* stream);
+fp_status fp_mx8_dequantize(int64_t n, int32_t root, const uint8_t* codes, const uint8_t* scales, float* x,
+                            void* stream);
 
 /* ------------------------------------------------------------------ helpers */
 

@@ -11,10 +11,14 @@ the C ABI; every step of the path runs in the library's HIP kernels.
     adamw_shard(acc, master, m, v, ...)   # fp32 AdamW + bf16 cast
     unshard(shards, full)                 # gather the bf16 shards
     shard_step(...)                       # the whole step for the last micro-batch
+    params = Params(grads, weights, ...)  # many separate tensors (GPU tables)
+    params.grad_norm(sq_norm, workspace)  # their gradients' norm, overflow flag
+    params.step(moments, step=t, ...)     # AdamW, moments in 32 or in 8 bits
 """
 
 from __future__ import annotations
 
+import contextlib
 import ctypes as C
 import math
 from typing import Optional, Sequence
@@ -25,7 +29,7 @@ from ._lib import (FP_MAX_WORLD, FP_PATH_NO_SKIP, FP_PATH_NO_SKIP_SPLIT, FP_PATH
                    FP_PATH_TWO_PHASE, FP_STEP_EXACT_SKIP, FP_STEP_KEEP_GRAD, FP_STEP_NO_COOP,
                    FP_STEP_NO_SKIP, FP_FLAG_OVERFLOW, FP_FLAG_GAVE_UP, FlatParamError, check, lib)
 
-__all__ = ["Plan", "Units", "Shard0Plan", "ReshardPlan", "reduce_shard_hybrid", "local_accumulate", "local_finish", "grad_coef", "scaler_update", "reduce_shard", "adamw_shard", "unshard", "shard_step", "ShardStep", "state_bytes",
+__all__ = ["Plan", "Units", "Params", "ParamsStep", "mx8_quantize", "mx8_dequantize", "Shard0Plan", "ReshardPlan", "reduce_shard_hybrid", "local_accumulate", "local_finish", "grad_coef", "scaler_update", "reduce_shard", "adamw_shard", "unshard", "shard_step", "ShardStep", "state_bytes",
            "workspace_bytes", "new_workspace", "workspace_timeouts", "FlatParamError", "FP_STEP_EXACT_SKIP",
            "FP_STEP_NO_SKIP", "FP_STEP_KEEP_GRAD", "FP_STEP_NO_COOP", "FP_PATH_ONE_PASS",
            "FP_PATH_TWO_PHASE", "FP_PATH_NO_SKIP", "FP_PATH_NO_SKIP_SPLIT", "FP_PATH_SPECULATIVE",
@@ -55,6 +59,14 @@ def _bf16_dtypes():
 def _stream(t):
     device = t if isinstance(t, _torch().device) else t.device
     return C.c_void_p(_torch().cuda.current_stream(device).cuda_stream)
+
+
+def _device_of(t):
+    """t's device as the current one (nothing to do if it is)."""
+    device = t if isinstance(t, _torch().device) else t.device
+    if device.type == "cuda" and _torch().cuda.current_device() != device.index:
+        return _torch().cuda.device(device)
+    return contextlib.nullcontext()
 
 
 def _dev_ptr(t, dtypes, n, name):
@@ -736,6 +748,252 @@ class Units:
         path = C.c_int32(-1)
         check(lib().fp_units_step_path(self._h, C.byref(a), C.byref(path)))
         return path.value
+
+
+# ------------------------------------------------------------------ params
+def _table(tensors, dtype, name, sizes=None):
+    """Device pointers of contiguous tensors of one dtype (None for empty ones)."""
+    if sizes is not None and len(tensors) != len(sizes):
+        raise ValueError(f"{name}: {len(tensors)} tensors, expected {len(sizes)}")
+    ptrs = []
+    for i, t in enumerate(tensors):
+        if t.dtype != dtype:
+            raise TypeError(f"{name}[{i}] has dtype {t.dtype}, expected {dtype}")
+        if sizes is not None and t.numel() != sizes[i]:
+            raise ValueError(f"{name}[{i}] has {t.numel()} elements, expected {sizes[i]}")
+        ptrs.append(_dev_ptr(t, (dtype,), 0, f"{name}[{i}]") if t.numel() else None)
+    return _ptr_table(ptrs)
+
+
+def _dtype_id(dtype, name):
+    torch = _torch()
+    ids = {torch.float32: _lib.FP_DTYPE_F32, torch.bfloat16: _lib.FP_DTYPE_BF16, torch.float16: _lib.FP_DTYPE_F16}
+    if dtype not in ids:
+        raise TypeError(f"{name} have dtype {dtype}, expected one of {tuple(ids)}")
+    return ids[dtype]
+
+
+def _code_dtypes():
+    torch = _torch()
+    return torch.float8_e4m3fn, torch.uint8
+
+
+def _scale_dtypes():
+    torch = _torch()
+    return torch.float8_e8m0fnu, torch.uint8
+
+
+class Params:
+    """Many separate tensors of one rank stepped together, one launch for all
+    of them (fp_params_*): a model's parameters, or the views of a
+    Shard0Plan's buffers.
+
+    grads: one gradient per tensor, all fp32, bf16 or fp16.  master: their
+    fp32 weights (None: a plan that only takes the norm).  copies: bf16 or
+    fp16 tensors that receive the weights, or None.  groups: a group number
+    per tensor (None: all 0); a step takes hyperparameters per group.
+    Tensors are contiguous, at any element of a buffer.  The moments sit in a
+    partition of `partition` elements, tensor i's from `offsets[i]` (a
+    multiple of 32) on.  The tensors must stay alive and in place for the
+    plan's life (set_grads changes the gradients); the plan is bound to
+    their device.
+    """
+
+    def __init__(self, grads, master=None, copies=None, groups=None):
+        grads = list(grads)
+        if not grads:
+            raise ValueError("need at least one tensor")
+        _one_device(grads, list(master) if master is not None else None, list(copies) if copies is not None else None)
+        torch = _torch()
+        self.sizes = [t.numel() for t in grads]
+        n = len(grads)
+        self._grad_dtype = grads[0].dtype
+        gtab = _table(grads, self._grad_dtype, "grads")
+        mtab = _table(master, torch.float32, "master", self.sizes) if master is not None else None
+        ctab, cid = None, _lib.FP_DTYPE_BF16
+        if copies is not None:
+            if len(copies) != n:
+                raise ValueError(f"copies: {len(copies)} tensors, expected {n}")
+            ctab, cid = _table(copies, copies[0].dtype, "copies", self.sizes), _dtype_id(copies[0].dtype, "copies")
+        self.groups = [0] * n if groups is None else [int(k) for k in groups]
+        if len(self.groups) != n:
+            raise ValueError(f"groups: {len(self.groups)} numbers, expected {n}")
+        self.n_groups = max(self.groups) + 1
+        self._keep = (grads, master, copies)
+        self._device = grads[0].device
+        out = C.c_void_p()
+        with _device_of(self._device):
+            check(lib().fp_params_create(n, (C.c_int64 * n)(*self.sizes), (C.c_int32 * n)(*self.groups),
+                                         _dtype_id(self._grad_dtype, "grads"), gtab, mtab, cid, ctab, C.byref(out)))
+        self._h = out
+        part, ws = C.c_int64(), C.c_int64()
+        check(lib().fp_params_info(self._h, C.byref(part), C.byref(ws)))
+        self.partition, self.workspace_bytes = part.value, ws.value
+        offs = (C.c_int64 * n)()
+        check(lib().fp_params_offsets(self._h, offs))
+        self.offsets = list(offs)
+
+    def close(self):
+        if getattr(self, "_h", None):
+            lib().fp_params_destroy(self._h)
+            self._h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def new_workspace(self):
+        """Zero-filled device workspace of grad_norm."""
+        return _torch().zeros(self.workspace_bytes, dtype=_torch().uint8, device=self._device)
+
+    def new_moments(self, bits: int = 32):
+        """Zero moments: (exp_avg, exp_avg_sq) in fp32, or for bits = 8
+        (exp_avg, exp_avg_scale, root, root_scale) in MXFP8."""
+        torch = _torch()
+        if bits == 32:
+            return tuple(torch.zeros(self.partition, dtype=torch.float32, device=self._device) for _ in range(2))
+        if bits != 8:
+            raise ValueError("moments have 32 or 8 bits")
+        P, B = self.partition, self.partition // _lib.FP_MX_BLOCK
+        return tuple(torch.zeros(n, dtype=torch.uint8, device=self._device).view(d)
+                     for n, d in ((P, _code_dtypes()[0]), (B, _scale_dtypes()[0])) * 2)
+
+    def tensor_slice(self, buf, i: int):
+        """Tensor i's part of a partition-sized tensor, or of its scales."""
+        if buf.numel() == self.partition // _lib.FP_MX_BLOCK and buf.numel() != self.partition:
+            b = _lib.FP_MX_BLOCK
+            return buf.narrow(0, self.offsets[i] // b, -(-self.sizes[i] // b))
+        return buf.narrow(0, self.offsets[i], self.sizes[i])
+
+    def set_grads(self, grads):
+        """New gradient tensors of the same sizes and dtype, for gradients that
+        move from step to step; ordered on the current stream with the plan's
+        other calls."""
+        grads = list(grads)
+        _one_device(grads, self._keep[0])
+        table = _table(grads, self._grad_dtype, "grads", self.sizes)
+        with _device_of(self._device):
+            check(lib().fp_params_set_grads(self._h, table, _stream(self._device)))
+        self._keep = (grads, *self._keep[1:])
+
+    def grad_norm(self, sq_norm, workspace, found_inf=None):
+        """sq_norm (device float64) = the gradients' sum of squares; bit 0 of
+        found_inf (device int32) is set if an element is not finite."""
+        _one_device(sq_norm, workspace, found_inf, self._keep[0][0])
+        torch = _torch()
+        fi = _dev_ptr(found_inf, (torch.int32,), 1, "found_inf") if found_inf is not None else None
+        sq = _dev_ptr(sq_norm, (torch.float64,), 1, "sq_norm")
+        ws = _dev_ptr(workspace, (torch.uint8,), self.workspace_bytes, "workspace")
+        with _device_of(self._device):
+            check(lib().fp_params_grad_norm(self._h, fi, sq, ws, _stream(self._device)))
+        return sq_norm
+
+    def stepper(self, moments, *, lr, beta1, beta2, eps, weight_decay, found_inf=None, grad_coef=None):
+        """A ParamsStep: the step with its arguments marshalled once."""
+        return ParamsStep(self, moments, lr=lr, beta1=beta1, beta2=beta2, eps=eps, weight_decay=weight_decay,
+                          found_inf=found_inf, grad_coef=grad_coef)
+
+    def step(self, moments, *, lr, beta1, beta2, eps, weight_decay, step: int, seed: Optional[int] = None,
+             found_inf=None, grad_coef=None):
+        """AdamW on every tensor.  moments: (exp_avg, exp_avg_sq) in fp32 or
+        (exp_avg, exp_avg_scale, root, root_scale) in MXFP8, which needs a seed
+        of its own for every step.  lr, beta1, beta2, eps, weight_decay: a
+        number, or one per group (groups without a tensor here included)."""
+        self.stepper(moments, lr=lr, beta1=beta1, beta2=beta2, eps=eps, weight_decay=weight_decay,
+                     found_inf=found_inf, grad_coef=grad_coef)(step, seed=seed)
+
+
+class ParamsStep:
+    """Params.step with its arguments marshalled once, for tight step loops:
+    the tensors are checked and their pointers captured at construction; a
+    call sets the step count, the seed (8-bit moments) and, where it changes,
+    the learning rate."""
+
+    def __init__(self, params, moments, *, lr, beta1, beta2, eps, weight_decay, found_inf=None, grad_coef=None):
+        moments = tuple(moments)
+        if len(moments) not in (2, 4):
+            raise ValueError("moments are (exp_avg, exp_avg_sq) or (exp_avg, exp_avg_scale, root, root_scale)")
+        _one_device(list(moments), found_inf, grad_coef, params._keep[0][0])
+        torch = _torch()
+        given = [lr, beta1, beta2, eps, weight_decay]
+        lengths = {len(x) for x in given if hasattr(x, "__len__")}
+        n = lengths.pop() if lengths else params.n_groups
+        if lengths or n < params.n_groups:
+            raise ValueError(f"hyperparameters: a number, or as many values as groups (at least {params.n_groups}) each")
+        self._n = n
+        cols = [self._per_group(x) for x in given]
+        self._hp = (_lib.fp_adamw_hparams * n)(*[_hparams(*row, 1) for row in zip(*cols)])
+        P = params.partition
+        self._eight = len(moments) == 4
+        if self._eight:
+            B = P // _lib.FP_MX_BLOCK
+            self._moments = [_dev_ptr(moments[0], _code_dtypes(), P, "exp_avg"),
+                             _dev_ptr(moments[1], _scale_dtypes(), B, "exp_avg_scale"),
+                             _dev_ptr(moments[2], _code_dtypes(), P, "root"),
+                             _dev_ptr(moments[3], _scale_dtypes(), B, "root_scale")]
+        else:
+            self._moments = [_f32(moments[0], P, "exp_avg"), _f32(moments[1], P, "exp_avg_sq")]
+        self._found = _dev_ptr(found_inf, (torch.int32,), 1, "found_inf") if found_inf is not None else None
+        self._coef = _coef_ptr(grad_coef)
+        self._params = params
+        self._keep = (moments, found_inf, grad_coef)
+        self._fn = lib().fp_params_adamw8 if self._eight else lib().fp_params_adamw
+
+    def _per_group(self, x):
+        v = list(x) if hasattr(x, "__len__") else [x] * self._n
+        if len(v) != self._n:
+            raise ValueError(f"{len(v)} values for {self._n} groups")
+        return [float(k) for k in v]
+
+    def __call__(self, step: int, *, seed: Optional[int] = None, lr=None):
+        p = self._params
+        if self._eight != (seed is not None):
+            raise ValueError("8-bit moments need a seed" if self._eight else "fp32 moments take no seed")
+        for h in self._hp:
+            h.step = int(step)
+        if lr is not None:
+            for h, x in zip(self._hp, self._per_group(lr)):
+                h.lr = x
+        more = (int(seed) & 0xFFFFFFFFFFFFFFFF,) if self._eight else ()
+        with _device_of(p._device):
+            check(self._fn(p._h, self._n, self._hp, *self._moments, *more, self._found, self._coef, _stream(p._device)))
+
+
+def mx8_quantize(src, codes=None, scales=None, *, root: bool = False):
+    """(codes, scales): MXFP8 of fp32 moments, e4m3 codes and one e8m0 scale per
+    32 elements, rounded to nearest even; root: of a second moment, whose root
+    the codes then hold.  Allocated here when None."""
+    torch = _torch()
+    n = src.numel()
+    blocks = -(-n // _lib.FP_MX_BLOCK)
+    x = _f32(src, n, "src")
+    if codes is None:
+        codes = torch.empty(n, dtype=_code_dtypes()[0], device=src.device)
+    if scales is None:
+        scales = torch.empty(blocks, dtype=_scale_dtypes()[0], device=src.device)
+    _one_device(src, codes, scales)
+    cp, sp = _dev_ptr(codes, _code_dtypes(), n, "codes"), _dev_ptr(scales, _scale_dtypes(), blocks, "scales")
+    with _device_of(src):
+        check(lib().fp_mx8_quantize(n, int(bool(root)), x, cp, sp, _stream(src)))
+    return codes, scales
+
+
+def mx8_dequantize(codes, scales, dst=None, *, root: bool = False):
+    """dst (fp32, allocated here when None): what MXFP8 codes and scales stand
+    for, squared with root (a second moment kept as its root)."""
+    torch = _torch()
+    n = codes.numel()
+    cp = _dev_ptr(codes, _code_dtypes(), n, "codes")
+    sp = _dev_ptr(scales, _scale_dtypes(), -(-n // _lib.FP_MX_BLOCK), "scales")
+    if dst is None:
+        dst = torch.empty(n, dtype=torch.float32, device=codes.device)
+    _one_device(codes, scales, dst)
+    x = _f32(dst, n, "dst")
+    with _device_of(codes):
+        check(lib().fp_mx8_dequantize(n, int(bool(root)), cp, sp, x, _stream(codes)))
+    return dst
 
 
 # ------------------------------------------------------------------ helpers

@@ -34,8 +34,14 @@ FP_PATH_SPECULATIVE_ONE_PASS = 6
 FP_WORKSPACE_TIMEOUTS_OFFSET = 8320
 FP_FLAG_OVERFLOW = 1
 FP_FLAG_GAVE_UP = 2
+FP_DTYPE_F32 = 0
+FP_DTYPE_BF16 = 1
+FP_DTYPE_F16 = 2
+FP_MAX_GROUPS = 16
+FP_MX_BLOCK = 32
 
 _i32, _i64, _f32, _f64, _vp = C.c_int32, C.c_int64, C.c_float, C.c_double, C.c_void_p
+_u64 = C.c_uint64
 
 
 class fp_view(C.Structure):
@@ -102,6 +108,16 @@ SIGNATURES = {
     "fp_local_finish": (_i32, [_i64, _vp, _i32, _vp, _vp, _vp]),
     "fp_grad_coef": (_i32, [_vp, _vp, _f64, _vp, _vp]),
     "fp_scaler_update": (_i32, [_vp, _vp, _vp, _f32, _f32, _i32, _vp]),
+    "fp_params_create": (_i32, [_i32, _vp, _vp, _i32, _vp, _vp, _i32, _vp, C.POINTER(_vp)]),
+    "fp_params_destroy": (None, [_vp]),
+    "fp_params_info": (_i32, [_vp, _vp, _vp]),
+    "fp_params_offsets": (_i32, [_vp, _vp]),
+    "fp_params_set_grads": (_i32, [_vp, _vp, _vp]),
+    "fp_params_grad_norm": (_i32, [_vp, _vp, _vp, _vp, _vp]),
+    "fp_params_adamw": (_i32, [_vp, _i32, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "fp_params_adamw8": (_i32, [_vp, _i32, _vp, _vp, _vp, _vp, _vp, _u64, _vp, _vp, _vp]),
+    "fp_mx8_quantize": (_i32, [_i64, _i32, _vp, _vp, _vp, _vp]),
+    "fp_mx8_dequantize": (_i32, [_i64, _i32, _vp, _vp, _vp, _vp]),
     "fp_state_bytes": (_i32, [_f64, _i32, _f64, _i32, C.POINTER(_f64)]),
     "fp_status_string": (C.c_char_p, [_i32]),
     "fp_last_error": (C.c_char_p, []),

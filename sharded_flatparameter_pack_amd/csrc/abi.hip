@@ -737,6 +737,7 @@ extern "C" fp_status fp_step_path(const fp_step_args* args, int32_t* path) {
 
 namespace fpk {
 fp_status report_error(fp_status status, const char* message) { return fail(status, "%s", message); }
+fp_status adam_coef(const fp_adamw_hparams* hp, AdamCoef* c) { return check_hparams(hp, c); }
 
 fp_status shard_step_run(const fp_step_args* args, void* stream, bool give_up_test) {
     if (args == nullptr) return fail(FP_ERR_INVALID, "args is NULL");

@@ -1,0 +1,71 @@
+// fp_params.h -- argument blocks and launcher declarations of the step over
+// many separate tensors (params_kernels.hip) and of the MXFP8 conversions.
+#pragma once
+
+#include "fp_internal.h"
+
+namespace fpk {
+
+// MXFP8: blocks of kMxBlock consecutive elements share one power-of-two scale.
+constexpr int kMxBlock = 32;
+
+// One tensor of a plan.  The moments sit in the rank's partition at element
+// `offset`, a multiple of kMxBlock, so blocks never cross tensors; the
+// gradient pointers have a table of their own, which fp_params_set_grads
+// rewrites.
+struct ParamRec {
+    float* master;    // null in a plan that only takes the norm
+    void* copy;       // bf16 / fp16 weights, or null
+    int64_t numel;
+    int64_t offset;
+    int32_t group;    // parameter group
+    int32_t pad[7];
+};
+static_assert(sizeof(ParamRec) == 64, "one 64-byte record per tensor");
+
+// Tile `index` of tensor `tensor`: what one workgroup works on.
+struct ParamTile {
+    int32_t tensor;
+    int32_t index;
+};
+
+// Elements of one tile (kThreads lanes x one quad).
+constexpr int64_t kParamTile = 4 * (int64_t)kThreads;
+inline int64_t param_tiles(int64_t numel) { return ceil_div64(numel, kParamTile); }
+
+struct ParamsArgs {
+    const ParamRec* recs;
+    const void* const* grads;
+    const ParamTile* tiles;
+    void* exp_avg;            // fp32 or e4m3 [partition]
+    void* exp_avg_sq;         // fp32 second moment, or e4m3 of its root
+    uint8_t* exp_avg_scale;   // e8m0 [partition / kMxBlock]
+    uint8_t* root_scale;
+    const int32_t* found_inf; // may be null: never skip
+    const double* g_coef;     // factor applied to the gradient, may be null (1)
+    uint32_t key;             // of the stochastic rounding
+    int32_t copy_f16;         // the copies are fp16, else bf16
+    AdamCoef c[FP_MAX_GROUPS];
+};
+
+struct ParamsNormArgs {
+    const ParamRec* recs;
+    const void* const* grads;
+    const ParamTile* tiles;
+    int32_t* found_inf;       // may be null
+    double* partials;         // one per tile
+};
+
+struct MxArgs {
+    float* x;                 // read by the quantization, written by the other
+    uint8_t* codes;
+    uint8_t* scales;
+    int64_t n;
+};
+
+// Launchers (return the HIP error of the launch); grad_dtype is FP_DTYPE_*.
+hipError_t launch_params_step(const ParamsArgs& a, int64_t tiles, int grad_dtype, bool mx8, hipStream_t s);
+hipError_t launch_params_norm(const ParamsNormArgs& a, int64_t tiles, int grad_dtype, hipStream_t s);
+hipError_t launch_mx8(const MxArgs& a, bool quantize, bool root, hipStream_t s);
+
+}  // namespace fpk

@@ -1,0 +1,414 @@
+// params_kernels.hip -- gfx950 kernels of the optimizer step over many
+// separate tensors: AdamW with fp32 or MXFP8 moments, the gradients' sum of
+// squares with the overflow check, and the MXFP8 conversions.
+//
+// A workgroup takes one tile of one tensor, found through the tile table
+// (tensor, tile), so that tensors of any size share one launch.  Inside a
+// tile the quad layout of the step kernels holds: lane t has elements
+// [4 t, 4 t + 4), every access of a wave covers one contiguous span.  The
+// tensors may start anywhere on their element size, so their accesses are
+// the unaligned ones (one instruction, as the aligned).
+//
+// MXFP8: 32 consecutive elements, 8 lanes, share the scale 2^(b - 127), one
+// byte b (e8m0; 255 is NaN); an element is an e4m3 code times the scale.
+// With f the exponent field of the block's largest magnitude, rounded to
+// e4m3's four significant bits, b = max(0, f - 7): the largest value lands
+// in [124, 248], so rounding up never leaves e4m3's range (448).  A block
+// with a value that is not finite (f >= 255) gets b = 255: it reads as NaN.
+// The code: |x| 2^(7 - b) as fp32 bits has e4m3's exponent field (bias 7)
+// at bits 23..26 and its three mantissa bits below, fp32's gradual
+// underflow being e4m3's; rounding is an integer add and a shift by 20.
+//
+// Compiled with -ffp-contract=off: every operation is one IEEE
+// round-to-nearest-even operation, in the order written.
+
+#include "fp_params.h"
+#include "step_ops.h"
+
+namespace fpk {
+
+namespace {
+
+// ---------------------------------------------------------------- gradients
+
+template <int kGrad>
+struct GradQuad {
+    uint2 w;
+};
+template <>
+struct GradQuad<FP_DTYPE_F32> {
+    uint4 w;
+};
+
+__device__ __forceinline__ float f16_lo(uint32_t w) {
+    return (float)__builtin_bit_cast(_Float16, (uint16_t)(w & 0xFFFFu));
+}
+__device__ __forceinline__ float f16_hi(uint32_t w) { return f16_lo(w >> 16); }
+
+// Gradient quad starting at element e, all four elements present.
+template <int kGrad>
+__device__ __forceinline__ GradQuad<kGrad> ld_grad(const void* g, int64_t e) {
+    GradQuad<kGrad> q;
+    if constexpr (kGrad == FP_DTYPE_F32) q.w = ld16u(static_cast<const float*>(g) + e);
+    else q.w = ld8u(static_cast<const uint16_t*>(g) + e);
+    return q;
+}
+
+// One gradient element.
+template <int kGrad>
+__device__ __forceinline__ float ld_grad1(const void* g, int64_t e) {
+    if constexpr (kGrad == FP_DTYPE_F32) return static_cast<const FP_GLOBAL float*>((const FP_GLOBAL void*)g)[e];
+    const uint32_t w = static_cast<const FP_GLOBAL uint16_t*>((const FP_GLOBAL void*)g)[e];
+    return kGrad == FP_DTYPE_BF16 ? bf16_lo(w) : f16_lo(w);
+}
+
+template <int kGrad>
+__device__ __forceinline__ void grad_f32(const GradQuad<kGrad>& q, float f[4]) {
+    if constexpr (kGrad == FP_DTYPE_F32) {
+        f[0] = __uint_as_float(q.w.x); f[1] = __uint_as_float(q.w.y);
+        f[2] = __uint_as_float(q.w.z); f[3] = __uint_as_float(q.w.w);
+    } else if constexpr (kGrad == FP_DTYPE_BF16) {
+        bf16x4_to_f32(q.w, f);
+    } else {
+        f[0] = f16_lo(q.w.x); f[1] = f16_hi(q.w.x);
+        f[2] = f16_lo(q.w.y); f[3] = f16_hi(q.w.y);
+    }
+}
+
+__device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
+    return (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)lo) |
+           ((uint32_t)__builtin_bit_cast(uint16_t, (_Float16)hi) << 16);
+}
+
+__device__ __forceinline__ void f32x4_of(const uint4 w, float f[4]) {
+    f[0] = __uint_as_float(w.x); f[1] = __uint_as_float(w.y);
+    f[2] = __uint_as_float(w.z); f[3] = __uint_as_float(w.w);
+}
+
+__device__ __forceinline__ uint4 bits_of(const float f[4]) {
+    return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+}
+
+typedef unsigned int u32x4_a4 __attribute__((ext_vector_type(4), aligned(4)));
+
+// 16 bytes to a 4-byte boundary (fp32 weights that are views of a buffer).
+__device__ __forceinline__ void st16u(void* p, const uint4 v) {
+    const u32x4_a4 w = {v.x, v.y, v.z, v.w};
+    __builtin_nontemporal_store(w, (FP_GLOBAL u32x4_a4*)(p));
+}
+
+// ---------------------------------------------------------------- MXFP8
+
+typedef float f32x2_t __attribute__((ext_vector_type(2)));
+
+// 2^(byte - 127): an exponent field, except for 2^-127 (a denormal) and NaN.
+__device__ __forceinline__ float mx_scale(uint32_t byte) {
+    const uint32_t b = byte << 23;
+    return __uint_as_float(byte == 0u || byte == 255u ? b | 0x00400000u : b);
+}
+
+// The values of four codes; code times scale is exact (4 significant bits).
+__device__ __forceinline__ void mx_decode(uint32_t codes, float scale, float f[4]) {
+    const f32x2_t lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)codes, false);
+    const f32x2_t hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)codes, true);
+    f[0] = lo.x * scale; f[1] = lo.y * scale;
+    f[2] = hi.x * scale; f[3] = hi.y * scale;
+}
+
+// Largest of x over the 8 lanes of a block.
+__device__ __forceinline__ uint32_t block_max(uint32_t x) {
+    uint32_t y = (uint32_t)__builtin_amdgcn_mov_dpp((int)x, 0xB1 /* quad_perm 1,0,3,2 */, 0xF, 0xF, true);
+    x = x > y ? x : y;
+    y = (uint32_t)__builtin_amdgcn_mov_dpp((int)x, 0x4E /* quad_perm 2,3,0,1 */, 0xF, 0xF, true);
+    x = x > y ? x : y;
+    y = (uint32_t)__builtin_amdgcn_mov_dpp((int)x, 0x141 /* row_half_mirror */, 0xF, 0xF, true);
+    return x > y ? x : y;
+}
+
+// Scale byte of the block that the lane's four values belong to.  All lanes
+// of the block take part; elements that do not exist are 0.
+__device__ __forceinline__ uint32_t mx_byte(const float f[4]) {
+    uint32_t top = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const uint32_t a = __float_as_uint(f[e]) & 0x7FFFFFFFu;
+        top = top > a ? top : a;
+    }
+    const uint32_t field = (block_max(top) + 0x00080000u) >> 23;
+    return field >= 255u ? 255u : field < 7u ? 0u : field - 7u;
+}
+
+// Codes of the lane's four values, rounded stochastically with 16 bits of
+// dither each (round[e], in [0, 2^16)) or, without, to nearest even.  kRoot:
+// the values are non-negative and one that is not zero keeps a code above
+// zero, so that a second moment never becomes a division by eps alone.
+template <bool kRoot, bool kDither>
+__device__ __forceinline__ uint32_t mx_encode(const float f[4], uint32_t byte, const uint32_t round[4]) {
+    if (byte == 255u) return 0u;
+    uint32_t w = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const uint32_t x = __float_as_uint(f[e]);
+        const float y = __builtin_amdgcn_ldexpf(__uint_as_float(x & 0x7FFFFFFFu), 7 - (int)byte);
+        const uint32_t b = __float_as_uint(y);
+        uint32_t code = (b + (kDither ? round[e] << 4 : 0x7FFFFu + ((b >> 20) & 1u))) >> 20;
+        if (kRoot) code = code == 0u && (x & 0x7FFFFFFFu) != 0u ? 1u : code;
+        else code |= (x >> 24) & 0x80u;
+        w |= code << (8 * e);
+    }
+    return w;
+}
+
+// 32 bits of dither for partition element e: the element's index and the
+// call's key through two multiplications.  The multipliers are the golden
+// ratio's and the fractions of sqrt(2) and sqrt(3).
+__device__ __forceinline__ uint32_t dither(uint32_t e, uint32_t key) {
+    uint32_t x = (e * 0x9E3779B1u) ^ key;
+    x ^= x >> 16;
+    x *= 0x6A09E667u;
+    x ^= x >> 15;
+    x *= 0xBB67AE85u;
+    return x;
+}
+
+// ---------------------------------------------------------------- AdamW
+
+// adamw_elem with the second moment given and kept as its root: one element
+// in fp64 from the fp32 values, master, first moment and root each rounded
+// once to fp32.
+__device__ __forceinline__ void adamw_root_elem(const AdamCoef& c, float g, float& th, float& m, float& r) {
+    const double gd = (double)g;
+    const double rd0 = (double)r;
+    const double md = c.beta1 * (double)m + c.one_m_beta1 * gd;
+    const double vd = c.beta2 * (rd0 * rd0) + c.one_m_beta2 * gd * gd;
+    const double rd = sqrt(vd);
+    const double denom = rd * c.inv_sqrt_bias2 + c.eps;
+    th = (float)((double)th * c.decay - c.step_size * md / denom);
+    m = (float)md;
+    r = (float)rd;
+}
+
+__device__ __forceinline__ void st_copy(void* copy, int64_t e, const float th[4], bool f16) {
+    uint16_t* p = static_cast<uint16_t*>(copy) + e;
+    st8u(p, f16 ? make_uint2(f16x2(th[0], th[1]), f16x2(th[2], th[3])) : f32x4_to_bf16(th));
+}
+__device__ __forceinline__ void st_copy1(void* copy, int64_t e, float th, bool f16) {
+    static_cast<FP_GLOBAL uint16_t*>((FP_GLOBAL void*)copy)[e] = (uint16_t)(f16 ? f16x2(th, 0.0f) : bf16x2(th, 0.0f));
+}
+
+template <class T>
+__device__ __forceinline__ FP_GLOBAL T* gptr(void* p) {
+    return static_cast<FP_GLOBAL T*>((FP_GLOBAL void*)p);
+}
+template <class T>
+__device__ __forceinline__ const FP_GLOBAL T* gptr(const void* p) {
+    return static_cast<const FP_GLOBAL T*>((const FP_GLOBAL void*)p);
+}
+
+}  // namespace
+
+// One tile of the step.  The loads do not wait for the overflow flag, as in
+// the flat step; on a skip only the copy of the unchanged weights is stored.
+// Partition elements past the tensor (up to the next multiple of 32) are
+// read with their quad and left as they are.
+template <int kGrad, bool kMx8>
+__global__ __launch_bounds__(kThreads) void params_step_kernel(const ParamsArgs a) {
+    const ParamTile tile = a.tiles[blockIdx.x];
+    const ParamRec rec = a.recs[tile.tensor];
+    const void* grad = a.grads[tile.tensor];
+    const AdamCoef c = coef_for(a.c[rec.group], a.g_coef);
+    const int64_t e = (int64_t)tile.index * kParamTile + 4 * (int64_t)threadIdx.x;  // the lane's first element
+    const int64_t left = rec.numel - e;
+    const int have = left >= 4 ? 4 : left > 0 ? (int)left : 0;
+    const int64_t p = rec.offset + e;   // the same in the partition
+
+    float g[4] = {0.0f, 0.0f, 0.0f, 0.0f}, th[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    float m[4] = {0.0f, 0.0f, 0.0f, 0.0f}, v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (have > 0) {
+        if (have == 4) {
+            const GradQuad<kGrad> gq = ld_grad<kGrad>(grad, e);
+            f32x4_of(ld16u(rec.master + e), th);
+            grad_f32<kGrad>(gq, g);
+        } else {
+            for (int k = 0; k < have; ++k) {
+                g[k] = ld_grad1<kGrad>(grad, e + k);
+                th[k] = gptr<float>(rec.master)[e + k];
+            }
+        }
+        if constexpr (kMx8) {
+            const uint32_t cm = gptr<uint32_t>(a.exp_avg)[p >> 2], cv = gptr<uint32_t>(a.exp_avg_sq)[p >> 2];
+            const uint32_t bm = gptr<uint8_t>(a.exp_avg_scale)[p / kMxBlock], bv = gptr<uint8_t>(a.root_scale)[p / kMxBlock];
+            mx_decode(cm, mx_scale(bm), m);
+            mx_decode(cv, mx_scale(bv), v);
+        } else {
+            f32x4_of(ld16(static_cast<const float*>(a.exp_avg) + p), m);
+            f32x4_of(ld16(static_cast<const float*>(a.exp_avg_sq) + p), v);
+        }
+    }
+    const bool skip = a.found_inf != nullptr && *a.found_inf != 0;
+    if (!skip) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            if (kMx8) adamw_root_elem(c, g[k], th[k], m[k], v[k]);
+            else adamw_elem(c, g[k], th[k], m[k], v[k]);
+        }
+        if constexpr (kMx8) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (k >= have) m[k] = v[k] = 0.0f;
+            const uint32_t bm = mx_byte(m), bv = mx_byte(v);
+            uint32_t dm[4], dv[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const uint32_t d = dither((uint32_t)p + (uint32_t)k, a.key);
+                dm[k] = d >> 16;
+                dv[k] = d & 0xFFFFu;
+            }
+            const uint32_t cm = mx_encode<false, true>(m, bm, dm), cv = mx_encode<true, true>(v, bv, dv);
+            if (have == 4) {
+                gptr<uint32_t>(a.exp_avg)[p >> 2] = cm;
+                gptr<uint32_t>(a.exp_avg_sq)[p >> 2] = cv;
+            } else {
+                for (int k = 0; k < have; ++k) {
+                    gptr<uint8_t>(a.exp_avg)[p + k] = (uint8_t)(cm >> (8 * k));
+                    gptr<uint8_t>(a.exp_avg_sq)[p + k] = (uint8_t)(cv >> (8 * k));
+                }
+            }
+            if (have > 0 && (threadIdx.x & 7) == 0) {
+                gptr<uint8_t>(a.exp_avg_scale)[p / kMxBlock] = (uint8_t)bm;
+                gptr<uint8_t>(a.root_scale)[p / kMxBlock] = (uint8_t)bv;
+            }
+        }
+    }
+    if (have == 4) {
+        if (!skip) {
+            st16u(rec.master + e, bits_of(th));
+            if constexpr (!kMx8) {
+                st16(static_cast<float*>(a.exp_avg) + p, bits_of(m));
+                st16(static_cast<float*>(a.exp_avg_sq) + p, bits_of(v));
+            }
+        }
+        if (rec.copy != nullptr) st_copy(rec.copy, e, th, a.copy_f16 != 0);
+    } else {
+        for (int k = 0; k < have; ++k) {
+            if (!skip) {
+                gptr<float>(rec.master)[e + k] = th[k];
+                if constexpr (!kMx8) {
+                    gptr<float>(a.exp_avg)[p + k] = m[k];
+                    gptr<float>(a.exp_avg_sq)[p + k] = v[k];
+                }
+            }
+            if (rec.copy != nullptr) st_copy1(rec.copy, e + k, th[k], a.copy_f16 != 0);
+        }
+    }
+}
+
+// The tile's sum of squares in fp64 and the overflow check.
+template <int kGrad>
+__global__ __launch_bounds__(kThreads) void params_norm_kernel(const ParamsNormArgs a) {
+    const ParamTile tile = a.tiles[blockIdx.x];
+    const int64_t numel = a.recs[tile.tensor].numel;
+    const void* grad = a.grads[tile.tensor];
+    const int64_t e = (int64_t)tile.index * kParamTile + 4 * (int64_t)threadIdx.x;
+    bool bad = false;
+    double sq = 0.0;
+    if (e + 4 <= numel) {
+        float g[4];
+        grad_f32<kGrad>(ld_grad<kGrad>(grad, e), g);
+        check_quad(g, bad, sq, true);
+    } else {
+        for (int64_t k = e; k < numel; ++k) {
+            const float g = ld_grad1<kGrad>(grad, k);
+            bad |= !finite_f32(g);
+            sq += (double)g * (double)g;
+        }
+    }
+    flag_if_any(bad, a.found_inf);
+    const double t = group_sum(sq);
+    if (threadIdx.x == 0) a.partials[blockIdx.x] = t;
+}
+
+template <bool kRoot>
+__global__ __launch_bounds__(kThreads) void mx8_quantize_kernel(const MxArgs a) {
+    const int64_t e = ((int64_t)blockIdx.x * kThreads + threadIdx.x) * 4;
+    const int have = a.n - e >= 4 ? 4 : a.n > e ? (int)(a.n - e) : 0;
+    float f[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (have == 4) f32x4_of(ld16(a.x + e), f);
+    else
+        for (int k = 0; k < have; ++k) f[k] = a.x[e + k];
+    if (kRoot) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) f[k] = (float)sqrt((double)f[k]);
+    }
+    const uint32_t byte = mx_byte(f);
+    const uint32_t none[4] = {0, 0, 0, 0};
+    const uint32_t w = mx_encode<kRoot, false>(f, byte, none);
+    if (have == 4) *reinterpret_cast<uint32_t*>(a.codes + e) = w;
+    else
+        for (int k = 0; k < have; ++k) a.codes[e + k] = (uint8_t)(w >> (8 * k));
+    if (have > 0 && (threadIdx.x & 7) == 0) a.scales[e / kMxBlock] = (uint8_t)byte;
+}
+
+template <bool kRoot>
+__global__ __launch_bounds__(kThreads) void mx8_dequantize_kernel(const MxArgs a) {
+    const int64_t e = ((int64_t)blockIdx.x * kThreads + threadIdx.x) * 4;
+    const int have = a.n - e >= 4 ? 4 : a.n > e ? (int)(a.n - e) : 0;
+    if (have == 0) return;
+    uint32_t w = 0;
+    if (have == 4) w = *reinterpret_cast<const uint32_t*>(a.codes + e);
+    else
+        for (int k = 0; k < have; ++k) w |= (uint32_t)a.codes[e + k] << (8 * k);
+    float f[4];
+    mx_decode(w, mx_scale(a.scales[e / kMxBlock]), f);
+    if (kRoot) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) f[k] = f[k] * f[k];
+    }
+    if (have == 4) st16(a.x + e, bits_of(f));
+    else
+        for (int k = 0; k < have; ++k) a.x[e + k] = f[k];
+}
+
+// ---------------------------------------------------------------- launchers
+
+hipError_t launch_params_step(const ParamsArgs& a, int64_t tiles, int grad_dtype, bool mx8, hipStream_t s) {
+    const unsigned grid = (unsigned)tiles;
+    switch (grad_dtype) {
+        case FP_DTYPE_F32:
+            if (mx8) params_step_kernel<FP_DTYPE_F32, true><<<grid, kThreads, 0, s>>>(a);
+            else params_step_kernel<FP_DTYPE_F32, false><<<grid, kThreads, 0, s>>>(a);
+            break;
+        case FP_DTYPE_BF16:
+            if (mx8) params_step_kernel<FP_DTYPE_BF16, true><<<grid, kThreads, 0, s>>>(a);
+            else params_step_kernel<FP_DTYPE_BF16, false><<<grid, kThreads, 0, s>>>(a);
+            break;
+        default:
+            if (mx8) params_step_kernel<FP_DTYPE_F16, true><<<grid, kThreads, 0, s>>>(a);
+            else params_step_kernel<FP_DTYPE_F16, false><<<grid, kThreads, 0, s>>>(a);
+    }
+    return hipGetLastError();
+}
+
+hipError_t launch_params_norm(const ParamsNormArgs& a, int64_t tiles, int grad_dtype, hipStream_t s) {
+    const unsigned grid = (unsigned)tiles;
+    switch (grad_dtype) {
+        case FP_DTYPE_F32: params_norm_kernel<FP_DTYPE_F32><<<grid, kThreads, 0, s>>>(a); break;
+        case FP_DTYPE_BF16: params_norm_kernel<FP_DTYPE_BF16><<<grid, kThreads, 0, s>>>(a); break;
+        default: params_norm_kernel<FP_DTYPE_F16><<<grid, kThreads, 0, s>>>(a);
+    }
+    return hipGetLastError();
+}
+
+hipError_t launch_mx8(const MxArgs& a, bool quantize, bool root, hipStream_t s) {
+    const unsigned grid = (unsigned)ceil_div64(a.n, 4 * (int64_t)kThreads);
+    if (quantize) {
+        if (root) mx8_quantize_kernel<true><<<grid, kThreads, 0, s>>>(a);
+        else mx8_quantize_kernel<false><<<grid, kThreads, 0, s>>>(a);
+    } else {
+        if (root) mx8_dequantize_kernel<true><<<grid, kThreads, 0, s>>>(a);
+        else mx8_dequantize_kernel<false><<<grid, kThreads, 0, s>>>(a);
+    }
+    return hipGetLastError();
+}
+
+}  // namespace fpk
