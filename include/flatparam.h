@@ -745,7 +745,8 @@ fp_status fp_params_adamw(fp_params* params, int32_t n_groups, const fp_adamw_hp
  * x in a block whose largest magnitude is X (elements past a tensor's end do
  * not count):
  *   f = (fp32 bits of X + 2^19) >> 23;  b = f >= 255 ? 255 : max(0, f - 7);
- *   y = |x| 2^(7 - b) as an fp32;  code = ((bits of y) + 16 d) >> 20,
+ *   y = |x| 2^(127 - b) < 248;  q = e4m3's step at y, 2^(max(floor(log2 y), -6) - 3);
+ *   the code is that of q * floor(y / q + d / 2^16),
  * with x's sign; codes of a b = 255 block are 0 (a block with an element that
  * is not finite reads as NaN until it is reset: pass found_inf).  An r' > 0
  * whose code would be 0 gets the code 1.  Stochastic, because the moments

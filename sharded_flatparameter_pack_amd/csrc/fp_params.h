@@ -23,20 +23,27 @@ struct ParamRec {
 };
 static_assert(sizeof(ParamRec) == 64, "one 64-byte record per tensor");
 
-// Tile `index` of tensor `tensor`: what one workgroup works on.
+// Tile `index` of tensor `tensor`: what one wave works on.
 struct ParamTile {
     int32_t tensor;
     int32_t index;
 };
 
-// Elements of one tile (kThreads lanes x one quad).
-constexpr int64_t kParamTile = 4 * (int64_t)kThreads;
+// A tile: 64 lanes x kParamQuads quads.
+constexpr int kParamQuads = 2;
+constexpr int64_t kParamTile = 256 * kParamQuads;
 inline int64_t param_tiles(int64_t numel) { return ceil_div64(numel, kParamTile); }
+// Workgroups (and partial sums) of the norm.
+inline int64_t params_norm_groups(int64_t tiles) {
+    const int64_t g = ceil_div64(tiles, kWaves);
+    return g < 2048 ? g : 2048;
+}
 
 struct ParamsArgs {
     const ParamRec* recs;
     const void* const* grads;
     const ParamTile* tiles;
+    int64_t n_tiles;
     void* exp_avg;            // fp32 or e4m3 [partition]
     void* exp_avg_sq;         // fp32 second moment, or e4m3 of its root
     uint8_t* exp_avg_scale;   // e8m0 [partition / kMxBlock]
@@ -52,8 +59,9 @@ struct ParamsNormArgs {
     const ParamRec* recs;
     const void* const* grads;
     const ParamTile* tiles;
+    int64_t n_tiles;
     int32_t* found_inf;       // may be null
-    double* partials;         // one per tile
+    double* partials;         // one per workgroup
 };
 
 struct MxArgs {
@@ -64,8 +72,8 @@ struct MxArgs {
 };
 
 // Launchers (return the HIP error of the launch); grad_dtype is FP_DTYPE_*.
-hipError_t launch_params_step(const ParamsArgs& a, int64_t tiles, int grad_dtype, bool mx8, hipStream_t s);
-hipError_t launch_params_norm(const ParamsNormArgs& a, int64_t tiles, int grad_dtype, hipStream_t s);
+hipError_t launch_params_step(const ParamsArgs& a, int grad_dtype, bool mx8, hipStream_t s);
+hipError_t launch_params_norm(const ParamsNormArgs& a, int grad_dtype, hipStream_t s);
 hipError_t launch_mx8(const MxArgs& a, bool quantize, bool root, hipStream_t s);
 
 }  // namespace fpk

@@ -34,7 +34,7 @@ fp_status device_error(hipError_t e, const char* what) {
 bool on(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
 // A dispatch holds at most this many workgroups of kThreads lanes.
-constexpr int64_t kMaxTiles = 0xFFFFFFFFLL / kThreads;
+constexpr int64_t kMaxGroups = 0xFFFFFFFFLL / kThreads;
 
 int64_t dtype_bytes(int32_t dtype) { return dtype == FP_DTYPE_F32 ? 4 : 2; }
 
@@ -168,8 +168,8 @@ fp_status create(int32_t n, const int64_t* numel, const int32_t* group, int32_t 
         }
         partition += ceil_div64(numel[i], kMxBlock) * kMxBlock;
         tiles += param_tiles(numel[i]);
-        if (tiles > kMaxTiles)
-            return bad(FP_ERR_RANGE, "the tensors need more workgroups than one launch holds (%lld)", (long long)kMaxTiles);
+        if (ceil_div64(tiles, kWaves) > kMaxGroups)
+            return bad(FP_ERR_RANGE, "the tensors need more workgroups than one launch holds (%lld)", (long long)kMaxGroups);
     }
     std::sort(written.begin(), written.end());
     for (size_t i = 1; i < written.size(); ++i)
@@ -299,6 +299,7 @@ fp_status step_args(const fp_params* p, int32_t n_groups, const fp_adamw_hparams
     a->recs = p->recs();
     a->grads = p->grads();
     a->tiles = p->tile_table();
+    a->n_tiles = p->tiles;
     a->found_inf = found_inf;
     a->g_coef = grad_coef;
     a->copy_f16 = p->copy_dtype == FP_DTYPE_F16 ? 1 : 0;
@@ -317,7 +318,7 @@ uint32_t key_of(uint64_t seed) {
 fp_status run_step(const fp_params* p, const ParamsArgs& a, bool mx8, void* stream) {
     fp_status st = check_device(p);
     if (st != FP_OK || p->tiles == 0) return st;
-    hipError_t e = launch_params_step(a, p->tiles, p->grad_dtype, mx8, static_cast<hipStream_t>(stream));
+    hipError_t e = launch_params_step(a, p->grad_dtype, mx8, static_cast<hipStream_t>(stream));
     return e == hipSuccess ? FP_OK : device_error(e, "params step launch");
 }
 
@@ -325,7 +326,8 @@ fp_status mx8_call(int64_t n, bool quantize, int32_t root, const float* x, const
                    void* stream) {
     if (n < 0) return bad(FP_ERR_RANGE, "n must be >= 0");
     if (n == 0) return FP_OK;
-    if (ceil_div64(n, 4 * (int64_t)kThreads) > kMaxTiles) return bad(FP_ERR_RANGE, "n %lld needs more workgroups than one launch holds", (long long)n);
+    if (ceil_div64(n, 4 * (int64_t)kThreads) > kMaxGroups)
+        return bad(FP_ERR_RANGE, "n %lld needs more workgroups than one launch holds", (long long)n);
     if (x == nullptr || codes == nullptr || scales == nullptr)
         return bad(FP_ERR_INVALID, "the fp32 buffer, codes or scales is NULL");
     if (!on(x, 16) || !on(codes, 16)) return bad(FP_ERR_ALIGN, "the fp32 buffer and codes must be 16-byte aligned");
@@ -363,7 +365,7 @@ extern "C" void fp_params_destroy(fp_params* params) {
 extern "C" fp_status fp_params_info(const fp_params* params, int64_t* partition, int64_t* workspace_bytes) {
     if (params == nullptr) return bad(FP_ERR_INVALID, "params is NULL");
     if (partition) *partition = params->partition;
-    if (workspace_bytes) *workspace_bytes = 8 * (params->tiles + 1);
+    if (workspace_bytes) *workspace_bytes = 8 * (params_norm_groups(params->tiles) + 1);
     return FP_OK;
 }
 
@@ -386,12 +388,12 @@ extern "C" fp_status fp_params_grad_norm(const fp_params* params, int32_t* found
     if (!on(workspace, 16)) return bad(FP_ERR_ALIGN, "workspace is not 16-byte aligned");
     fp_status st = check_device(params);
     if (st != FP_OK) return st;
-    const ParamsNormArgs a = {params->recs(), params->grads(), params->tile_table(), found_inf,
+    const ParamsNormArgs a = {params->recs(), params->grads(), params->tile_table(), params->tiles, found_inf,
                               static_cast<double*>(workspace)};
     hipStream_t s = static_cast<hipStream_t>(stream);
     hipError_t e = hipSuccess;
-    if (params->tiles > 0) e = launch_params_norm(a, params->tiles, params->grad_dtype, s);
-    if (e == hipSuccess) e = launch_norm_finalize(a.partials, (int)params->tiles, sq_norm, s);
+    if (params->tiles > 0) e = launch_params_norm(a, params->grad_dtype, s);
+    if (e == hipSuccess) e = launch_norm_finalize(a.partials, (int)params_norm_groups(params->tiles), sq_norm, s);
     return e == hipSuccess ? FP_OK : device_error(e, "gradient norm launch");
 }
 

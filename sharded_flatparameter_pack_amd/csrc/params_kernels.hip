@@ -100,19 +100,17 @@ __device__ __forceinline__ void st16u(void* p, const uint4 v) {
 // ---------------------------------------------------------------- MXFP8
 
 typedef float f32x2_t __attribute__((ext_vector_type(2)));
+typedef short s16x2_t __attribute__((ext_vector_type(2)));
 
-// 2^(byte - 127): an exponent field, except for 2^-127 (a denormal) and NaN.
-__device__ __forceinline__ float mx_scale(uint32_t byte) {
-    const uint32_t b = byte << 23;
-    return __uint_as_float(byte == 0u || byte == 255u ? b | 0x00400000u : b);
-}
+// The conversions take the scale as an fp32 of which they use the exponent
+// field, the e8m0 byte itself: 0 is 2^-127, 255 gives NaN.
+__device__ __forceinline__ float mx_scale(uint32_t byte) { return __uint_as_float(byte << 23); }
 
 // The values of four codes; code times scale is exact (4 significant bits).
-__device__ __forceinline__ void mx_decode(uint32_t codes, float scale, float f[4]) {
-    const f32x2_t lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)codes, false);
-    const f32x2_t hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)codes, true);
-    f[0] = lo.x * scale; f[1] = lo.y * scale;
-    f[2] = hi.x * scale; f[3] = hi.y * scale;
+__device__ __forceinline__ void mx_decode(uint32_t codes, uint32_t byte, float f[4]) {
+    const f32x2_t lo = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(codes, mx_scale(byte), false);
+    const f32x2_t hi = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(codes, mx_scale(byte), true);
+    f[0] = lo.x; f[1] = lo.y; f[2] = hi.x; f[3] = hi.y;
 }
 
 // Largest of x over the 8 lanes of a block.
@@ -138,25 +136,39 @@ __device__ __forceinline__ uint32_t mx_byte(const float f[4]) {
     return field >= 255u ? 255u : field < 7u ? 0u : field - 7u;
 }
 
-// Codes of the lane's four values, rounded stochastically with 16 bits of
-// dither each (round[e], in [0, 2^16)) or, without, to nearest even.  kRoot:
-// the values are non-negative and one that is not zero keeps a code above
-// zero, so that a second moment never becomes a division by eps alone.
-template <bool kRoot, bool kDither>
-__device__ __forceinline__ uint32_t mx_encode(const float f[4], uint32_t byte, const uint32_t round[4]) {
-    if (byte == 255u) return 0u;
-    uint32_t w = 0;
+// A root that is not zero does not round to zero, so that a second moment
+// never becomes a division by eps alone: one below the smallest code's value
+// is raised to it.  Rare, so a wave without such values skips it.
+__device__ __forceinline__ void mx_raise(float r[4], uint32_t byte) {
+    const float least = __builtin_amdgcn_ldexpf(1.0f, (int)byte - 136);
+    const float low = fminf(fminf(r[0], r[1]), fminf(r[2], r[3]));
+    if (low < least) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        const uint32_t x = __float_as_uint(f[e]);
-        const float y = __builtin_amdgcn_ldexpf(__uint_as_float(x & 0x7FFFFFFFu), 7 - (int)byte);
-        const uint32_t b = __float_as_uint(y);
-        uint32_t code = (b + (kDither ? round[e] << 4 : 0x7FFFFu + ((b >> 20) & 1u))) >> 20;
-        if (kRoot) code = code == 0u && (x & 0x7FFFFFFFu) != 0u ? 1u : code;
-        else code |= (x >> 24) & 0x80u;
-        w |= code << (8 * e);
+        for (int e = 0; e < 4; ++e) r[e] = r[e] > 0.0f ? fmaxf(r[e], least) : r[e];
     }
-    return w;
+}
+
+// Codes of the lane's four values, rounded stochastically: |x| / scale has
+// 20 bits of random[e] (its high bits) added below e4m3's last bit and is cut
+// there, as the hardware's conversion does in the normal and the subnormal
+// range alike.
+__device__ __forceinline__ uint32_t mx_encode(const float f[4], uint32_t byte, const uint32_t random[4]) {
+    const float s = mx_scale(byte);
+    int w = 0;
+    w = __builtin_amdgcn_cvt_scalef32_sr_fp8_f32(w, f[0], random[0], s, 0);
+    w = __builtin_amdgcn_cvt_scalef32_sr_fp8_f32(w, f[1], random[1], s, 1);
+    w = __builtin_amdgcn_cvt_scalef32_sr_fp8_f32(w, f[2], random[2], s, 2);
+    w = __builtin_amdgcn_cvt_scalef32_sr_fp8_f32(w, f[3], random[3], s, 3);
+    return byte == 255u ? 0u : (uint32_t)w;
+}
+
+// The same rounded to nearest even.
+__device__ __forceinline__ uint32_t mx_encode(const float f[4], uint32_t byte) {
+    const float s = mx_scale(byte);
+    s16x2_t w = {0, 0};
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(w, f[0], f[1], s, false);
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(w, f[2], f[3], s, true);
+    return byte == 255u ? 0u : __builtin_bit_cast(uint32_t, w);
 }
 
 // 32 bits of dither for partition element e: the element's index and the
@@ -175,17 +187,26 @@ __device__ __forceinline__ uint32_t dither(uint32_t e, uint32_t key) {
 
 // adamw_elem with the second moment given and kept as its root: one element
 // in fp64 from the fp32 values, master, first moment and root each rounded
-// once to fp32.
+// once to fp32.  Written for the fewest instructions, since with 8-bit
+// moments they and not the memory are the bound (see params_step_kernel):
+// fused operations, and the root and the quotient from the hardware's
+// estimates (accurate to 2^-24) with one Newton step each, to 2^-47.  kTiny
+// in v keeps a zero second moment out of the estimate's poles; beside any
+// other it is lost.
 __device__ __forceinline__ void adamw_root_elem(const AdamCoef& c, float g, float& th, float& m, float& r) {
-    const double gd = (double)g;
-    const double rd0 = (double)r;
-    const double md = c.beta1 * (double)m + c.one_m_beta1 * gd;
-    const double vd = c.beta2 * (rd0 * rd0) + c.one_m_beta2 * gd * gd;
-    const double rd = sqrt(vd);
-    const double denom = rd * c.inv_sqrt_bias2 + c.eps;
-    th = (float)((double)th * c.decay - c.step_size * md / denom);
+    constexpr double kTiny = 1e-290;
+    const double gd = (double)g, rd = (double)r;
+    const double md = __builtin_fma(c.one_m_beta1, gd, c.beta1 * (double)m);
+    const double vd = __builtin_fma(c.one_m_beta2 * gd, gd, __builtin_fma(c.beta2, rd * rd, kTiny));
+    const double y = __builtin_amdgcn_rsq(vd);
+    const double s0 = vd * y;
+    const double root = __builtin_fma(0.5 * y, __builtin_fma(-s0, s0, vd), s0);
+    const double denom = __builtin_fma(root, c.inv_sqrt_bias2, c.eps);
+    const double q0 = __builtin_amdgcn_rcp(denom);
+    const double q = __builtin_fma(__builtin_fma(-denom, q0, 1.0), q0, q0);
+    th = (float)__builtin_fma(-c.step_size * md, q, (double)th * c.decay);
     m = (float)md;
-    r = (float)rd;
+    r = (float)root;
 }
 
 __device__ __forceinline__ void st_copy(void* copy, int64_t e, const float th[4], bool f16) {
@@ -207,120 +228,160 @@ __device__ __forceinline__ const FP_GLOBAL T* gptr(const void* p) {
 
 }  // namespace
 
-// One tile of the step.  The loads do not wait for the overflow flag, as in
-// the flat step; on a skip only the copy of the unchanged weights is stored.
-// Partition elements past the tensor (up to the next multiple of 32) are
-// read with their quad and left as they are.
-template <int kGrad, bool kMx8>
-__global__ __launch_bounds__(kThreads) void params_step_kernel(const ParamsArgs a) {
-    const ParamTile tile = a.tiles[blockIdx.x];
-    const ParamRec rec = a.recs[tile.tensor];
-    const void* grad = a.grads[tile.tensor];
+// A wave's entry of the step: kParamQuads quads per lane, 64 quads apart.
+// kFull: the tensor has all of its elements.  The loads do not wait for the
+// overflow flag, as in the flat step; on a skip only the copy of the
+// unchanged weights is stored.  Partition elements past the tensor (up to the
+// next multiple of 32) are read with their quad and left as they are.
+template <int kGrad, bool kMx8, bool kFull>
+__device__ __forceinline__ void params_step_entry(const ParamsArgs& a, const ParamRec& rec, const void* grad, int64_t e0) {
+    constexpr int kU = kParamQuads;
     const AdamCoef c = coef_for(a.c[rec.group], a.g_coef);
-    const int64_t e = (int64_t)tile.index * kParamTile + 4 * (int64_t)threadIdx.x;  // the lane's first element
-    const int64_t left = rec.numel - e;
-    const int have = left >= 4 ? 4 : left > 0 ? (int)left : 0;
-    const int64_t p = rec.offset + e;   // the same in the partition
-
-    float g[4] = {0.0f, 0.0f, 0.0f, 0.0f}, th[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    float m[4] = {0.0f, 0.0f, 0.0f, 0.0f}, v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    if (have > 0) {
-        if (have == 4) {
-            const GradQuad<kGrad> gq = ld_grad<kGrad>(grad, e);
-            f32x4_of(ld16u(rec.master + e), th);
-            grad_f32<kGrad>(gq, g);
+    const int lane = threadIdx.x & 63;
+    int have[kU];
+    float g[kU][4], th[kU][4], m[kU][4], v[kU][4];
+    GradQuad<kGrad> gq[kU];
+    uint32_t cm[kU], cv[kU], bm[kU], bv[kU];
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+        const int64_t e = e0 + 256 * u + 4 * lane, p = rec.offset + e;
+        const int64_t left = rec.numel - e;
+        have[u] = kFull || left >= 4 ? 4 : left > 0 ? (int)left : 0;
+        if (kFull || have[u] == 4) {
+            gq[u] = ld_grad<kGrad>(grad, e);
+            f32x4_of(ld16u(rec.master + e), th[u]);
         } else {
-            for (int k = 0; k < have; ++k) {
-                g[k] = ld_grad1<kGrad>(grad, e + k);
-                th[k] = gptr<float>(rec.master)[e + k];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                g[u][k] = k < have[u] ? ld_grad1<kGrad>(grad, e + k) : 0.0f;
+                th[u][k] = k < have[u] ? gptr<float>(rec.master)[e + k] : 0.0f;
             }
         }
-        if constexpr (kMx8) {
-            const uint32_t cm = gptr<uint32_t>(a.exp_avg)[p >> 2], cv = gptr<uint32_t>(a.exp_avg_sq)[p >> 2];
-            const uint32_t bm = gptr<uint8_t>(a.exp_avg_scale)[p / kMxBlock], bv = gptr<uint8_t>(a.root_scale)[p / kMxBlock];
-            mx_decode(cm, mx_scale(bm), m);
-            mx_decode(cv, mx_scale(bv), v);
+        if (kFull || have[u] > 0) {
+            if constexpr (kMx8) {
+                cm[u] = gptr<uint32_t>(a.exp_avg)[p >> 2];
+                cv[u] = gptr<uint32_t>(a.exp_avg_sq)[p >> 2];
+                bm[u] = gptr<uint8_t>(a.exp_avg_scale)[p / kMxBlock];
+                bv[u] = gptr<uint8_t>(a.root_scale)[p / kMxBlock];
+            } else {
+                f32x4_of(ld16(static_cast<const float*>(a.exp_avg) + p), m[u]);
+                f32x4_of(ld16(static_cast<const float*>(a.exp_avg_sq) + p), v[u]);
+            }
+        } else if constexpr (kMx8) {
+            cm[u] = cv[u] = bm[u] = bv[u] = 0u;
         } else {
-            f32x4_of(ld16(static_cast<const float*>(a.exp_avg) + p), m);
-            f32x4_of(ld16(static_cast<const float*>(a.exp_avg_sq) + p), v);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) m[u][k] = v[u][k] = 0.0f;
         }
     }
     const bool skip = a.found_inf != nullptr && *a.found_inf != 0;
-    if (!skip) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            if (kMx8) adamw_root_elem(c, g[k], th[k], m[k], v[k]);
-            else adamw_elem(c, g[k], th[k], m[k], v[k]);
+    for (int u = 0; u < kU; ++u) {
+        const int64_t e = e0 + 256 * u + 4 * lane, p = rec.offset + e;
+        if (!skip) {
+            if (kFull || have[u] == 4) grad_f32<kGrad>(gq[u], g[u]);
+            if constexpr (kMx8) {
+                mx_decode(cm[u], bm[u], m[u]);
+                mx_decode(cv[u], bv[u], v[u]);
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                if (kMx8) adamw_root_elem(c, g[u][k], th[u][k], m[u][k], v[u][k]);
+                else adamw_elem(c, g[u][k], th[u][k], m[u][k], v[u][k]);
+            }
         }
-        if constexpr (kMx8) {
+        if (kMx8 && !skip) {
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-                if (k >= have) m[k] = v[k] = 0.0f;
-            const uint32_t bm = mx_byte(m), bv = mx_byte(v);
+                if (!kFull && k >= have[u]) m[u][k] = v[u][k] = 0.0f;
+            const uint32_t nbm = mx_byte(m[u]), nbv = mx_byte(v[u]);
             uint32_t dm[4], dv[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 const uint32_t d = dither((uint32_t)p + (uint32_t)k, a.key);
-                dm[k] = d >> 16;
-                dv[k] = d & 0xFFFFu;
+                dm[k] = d & 0xFFFF0000u;
+                dv[k] = d << 16;
             }
-            const uint32_t cm = mx_encode<false, true>(m, bm, dm), cv = mx_encode<true, true>(v, bv, dv);
-            if (have == 4) {
-                gptr<uint32_t>(a.exp_avg)[p >> 2] = cm;
-                gptr<uint32_t>(a.exp_avg_sq)[p >> 2] = cv;
+            mx_raise(v[u], nbv);
+            const uint32_t ncm = mx_encode(m[u], nbm, dm), ncv = mx_encode(v[u], nbv, dv);
+            if (kFull || have[u] == 4) {
+                gptr<uint32_t>(a.exp_avg)[p >> 2] = ncm;
+                gptr<uint32_t>(a.exp_avg_sq)[p >> 2] = ncv;
             } else {
-                for (int k = 0; k < have; ++k) {
-                    gptr<uint8_t>(a.exp_avg)[p + k] = (uint8_t)(cm >> (8 * k));
-                    gptr<uint8_t>(a.exp_avg_sq)[p + k] = (uint8_t)(cv >> (8 * k));
+                for (int k = 0; k < have[u]; ++k) {
+                    gptr<uint8_t>(a.exp_avg)[p + k] = (uint8_t)(ncm >> (8 * k));
+                    gptr<uint8_t>(a.exp_avg_sq)[p + k] = (uint8_t)(ncv >> (8 * k));
                 }
             }
-            if (have > 0 && (threadIdx.x & 7) == 0) {
-                gptr<uint8_t>(a.exp_avg_scale)[p / kMxBlock] = (uint8_t)bm;
-                gptr<uint8_t>(a.root_scale)[p / kMxBlock] = (uint8_t)bv;
+            if ((kFull || have[u] > 0) && (lane & 7) == 0) {
+                gptr<uint8_t>(a.exp_avg_scale)[p / kMxBlock] = (uint8_t)nbm;
+                gptr<uint8_t>(a.root_scale)[p / kMxBlock] = (uint8_t)nbv;
             }
         }
-    }
-    if (have == 4) {
-        if (!skip) {
-            st16u(rec.master + e, bits_of(th));
-            if constexpr (!kMx8) {
-                st16(static_cast<float*>(a.exp_avg) + p, bits_of(m));
-                st16(static_cast<float*>(a.exp_avg_sq) + p, bits_of(v));
-            }
-        }
-        if (rec.copy != nullptr) st_copy(rec.copy, e, th, a.copy_f16 != 0);
-    } else {
-        for (int k = 0; k < have; ++k) {
+        if (kFull || have[u] == 4) {
             if (!skip) {
-                gptr<float>(rec.master)[e + k] = th[k];
+                st16u(rec.master + e, bits_of(th[u]));
                 if constexpr (!kMx8) {
-                    gptr<float>(a.exp_avg)[p + k] = m[k];
-                    gptr<float>(a.exp_avg_sq)[p + k] = v[k];
+                    st16(static_cast<float*>(a.exp_avg) + p, bits_of(m[u]));
+                    st16(static_cast<float*>(a.exp_avg_sq) + p, bits_of(v[u]));
                 }
             }
-            if (rec.copy != nullptr) st_copy1(rec.copy, e + k, th[k], a.copy_f16 != 0);
+            if (rec.copy != nullptr) st_copy(rec.copy, e, th[u], a.copy_f16 != 0);
+        } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                if (k >= have[u]) continue;
+                if (!skip) {
+                    gptr<float>(rec.master)[e + k] = th[u][k];
+                    if constexpr (!kMx8) {
+                        gptr<float>(a.exp_avg)[p + k] = m[u][k];
+                        gptr<float>(a.exp_avg_sq)[p + k] = v[u][k];
+                    }
+                }
+                if (rec.copy != nullptr) st_copy1(rec.copy, e + k, th[u][k], a.copy_f16 != 0);
+            }
         }
     }
 }
 
-// The tile's sum of squares in fp64 and the overflow check.
+template <int kGrad, bool kMx8>
+__global__ __launch_bounds__(kThreads) void params_step_kernel(const ParamsArgs a) {
+    const int64_t i = (int64_t)blockIdx.x * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    if (i >= a.n_tiles) return;
+    const ParamTile tile = a.tiles[i];
+    const ParamRec rec = a.recs[tile.tensor];
+    const void* grad = a.grads[tile.tensor];
+    const int64_t e0 = (int64_t)tile.index * kParamTile;
+    if (rec.numel - e0 >= kParamTile) params_step_entry<kGrad, kMx8, true>(a, rec, grad, e0);
+    else params_step_entry<kGrad, kMx8, false>(a, rec, grad, e0);
+}
+
+// The sum of squares in fp64 and the overflow check.
 template <int kGrad>
 __global__ __launch_bounds__(kThreads) void params_norm_kernel(const ParamsNormArgs a) {
-    const ParamTile tile = a.tiles[blockIdx.x];
-    const int64_t numel = a.recs[tile.tensor].numel;
-    const void* grad = a.grads[tile.tensor];
-    const int64_t e = (int64_t)tile.index * kParamTile + 4 * (int64_t)threadIdx.x;
+    const int lane = threadIdx.x & 63;
     bool bad = false;
     double sq = 0.0;
-    if (e + 4 <= numel) {
-        float g[4];
-        grad_f32<kGrad>(ld_grad<kGrad>(grad, e), g);
-        check_quad(g, bad, sq, true);
-    } else {
-        for (int64_t k = e; k < numel; ++k) {
-            const float g = ld_grad1<kGrad>(grad, k);
-            bad |= !finite_f32(g);
-            sq += (double)g * (double)g;
+    for (int64_t i = (int64_t)blockIdx.x * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); i < a.n_tiles;
+         i += (int64_t)gridDim.x * kWaves) {
+        const ParamTile tile = a.tiles[i];
+        const int64_t numel = a.recs[tile.tensor].numel;
+        const void* grad = a.grads[tile.tensor];
+        const int64_t e0 = (int64_t)tile.index * kParamTile;
+#pragma unroll
+        for (int u = 0; u < kParamQuads; ++u) {
+            const int64_t e = e0 + 256 * u + 4 * lane;
+            if (e + 4 <= numel) {
+                float g[4];
+                grad_f32<kGrad>(ld_grad<kGrad>(grad, e), g);
+                check_quad(g, bad, sq, true);
+            } else {
+                for (int64_t k = e; k < numel; ++k) {
+                    const float g = ld_grad1<kGrad>(grad, k);
+                    bad |= !finite_f32(g);
+                    sq += (double)g * (double)g;
+                }
+            }
         }
     }
     flag_if_any(bad, a.found_inf);
@@ -341,8 +402,8 @@ __global__ __launch_bounds__(kThreads) void mx8_quantize_kernel(const MxArgs a) 
         for (int k = 0; k < 4; ++k) f[k] = (float)sqrt((double)f[k]);
     }
     const uint32_t byte = mx_byte(f);
-    const uint32_t none[4] = {0, 0, 0, 0};
-    const uint32_t w = mx_encode<kRoot, false>(f, byte, none);
+    if (kRoot) mx_raise(f, byte);
+    const uint32_t w = mx_encode(f, byte);
     if (have == 4) *reinterpret_cast<uint32_t*>(a.codes + e) = w;
     else
         for (int k = 0; k < have; ++k) a.codes[e + k] = (uint8_t)(w >> (8 * k));
@@ -359,7 +420,7 @@ __global__ __launch_bounds__(kThreads) void mx8_dequantize_kernel(const MxArgs a
     else
         for (int k = 0; k < have; ++k) w |= (uint32_t)a.codes[e + k] << (8 * k);
     float f[4];
-    mx_decode(w, mx_scale(a.scales[e / kMxBlock]), f);
+    mx_decode(w, a.scales[e / kMxBlock], f);
     if (kRoot) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) f[k] = f[k] * f[k];
@@ -371,8 +432,8 @@ __global__ __launch_bounds__(kThreads) void mx8_dequantize_kernel(const MxArgs a
 
 // ---------------------------------------------------------------- launchers
 
-hipError_t launch_params_step(const ParamsArgs& a, int64_t tiles, int grad_dtype, bool mx8, hipStream_t s) {
-    const unsigned grid = (unsigned)tiles;
+hipError_t launch_params_step(const ParamsArgs& a, int grad_dtype, bool mx8, hipStream_t s) {
+    const unsigned grid = (unsigned)ceil_div64(a.n_tiles, kWaves);
     switch (grad_dtype) {
         case FP_DTYPE_F32:
             if (mx8) params_step_kernel<FP_DTYPE_F32, true><<<grid, kThreads, 0, s>>>(a);
@@ -389,8 +450,8 @@ hipError_t launch_params_step(const ParamsArgs& a, int64_t tiles, int grad_dtype
     return hipGetLastError();
 }
 
-hipError_t launch_params_norm(const ParamsNormArgs& a, int64_t tiles, int grad_dtype, hipStream_t s) {
-    const unsigned grid = (unsigned)tiles;
+hipError_t launch_params_norm(const ParamsNormArgs& a, int grad_dtype, hipStream_t s) {
+    const unsigned grid = (unsigned)params_norm_groups(a.n_tiles);
     switch (grad_dtype) {
         case FP_DTYPE_F32: params_norm_kernel<FP_DTYPE_F32><<<grid, kThreads, 0, s>>>(a); break;
         case FP_DTYPE_BF16: params_norm_kernel<FP_DTYPE_BF16><<<grid, kThreads, 0, s>>>(a); break;

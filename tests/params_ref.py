@@ -38,18 +38,20 @@ def scale_bytes(x):
 
 
 def encode(x, scales, dither=None, root=False):
-    """Codes of fp32 values under given scale bytes."""
+    """Codes of fp32 values under given scale bytes: q the width of e4m3's
+    interval at y = |x| / scale, q floor(y / q + dither / 2^16), or y rounded to
+    the nearest multiple of q (ties to even)."""
     x = x.astype(np.float32)
     b = np.repeat(scales, BLOCK)[:x.size].astype(np.int64)
-    with np.errstate(all="ignore"):
-        y = np.ldexp(np.abs(x).astype(np.float64), 7 - np.where(b == 255, 0, b)).astype(np.float32)
-    y = y.view(U32).astype(np.int64)
-    code = (y + (dither.astype(np.int64) << 4 if dither is not None else 0x7FFFF + ((y >> 20) & 1))) >> 20
-    size = x.view(U32) & U32(0x7FFFFFFF)
+    y = np.where(b == 255, 0.0, np.ldexp(np.abs(np.where(b == 255, 0, x)).astype(np.float64), 127 - b))
+    q = np.exp2(np.maximum(np.frexp(y)[1] - 1, -6).astype(float) - 3)
+    v = q * (np.rint(y / q) if dither is None else np.floor(y / q + dither / 65536.0))
+    e = np.where(v > 0, np.frexp(v)[1] - 1, -7)
+    code = np.where(e < -6, v * 512, (e + 7) * 8 + np.ldexp(v, 3 - e) - 8).astype(np.int64)
     if root:
-        code = np.where((code == 0) & (size != 0), 1, code)
+        code = np.where((code == 0) & (y > 0), 1, code)
     else:
-        code = code | ((x.view(U32) >> U32(24)) & U32(0x80)).astype(np.int64)
+        code = code | np.where(np.signbit(x), 0x80, 0)
     return np.where(b == 255, 0, code).astype(np.uint8)
 
 
