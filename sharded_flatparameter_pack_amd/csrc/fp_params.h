@@ -33,11 +33,16 @@ struct ParamTile {
 constexpr int kParamQuads = 2;
 constexpr int64_t kParamTile = 256 * kParamQuads;
 inline int64_t param_tiles(int64_t numel) { return ceil_div64(numel, kParamTile); }
-// Workgroups (and partial sums) of the norm.
+// Workgroups of the norm, a partial sum each: at most as many as are resident
+// together (8 per CU).
+constexpr int64_t kNormGroups = 2048;
 inline int64_t params_norm_groups(int64_t tiles) {
     const int64_t g = ceil_div64(tiles, kWaves);
-    return g < 2048 ? g : 2048;
+    return g < 1 ? 1 : g < kNormGroups ? g : kNormGroups;
 }
+// Workspace of the norm: the counts of finished workgroups, each in a line of
+// its own, then the partial sums.
+constexpr int64_t kNormHeader = 4 * kLineWords * (kSyncGroups + 1);
 
 struct ParamsArgs {
     const ParamRec* recs;
@@ -62,6 +67,8 @@ struct ParamsNormArgs {
     int64_t n_tiles;
     int32_t* found_inf;       // may be null
     double* partials;         // one per workgroup
+    uint32_t* done;           // counts of workgroups that have stored theirs; 0 between calls
+    double* sq_norm;
 };
 
 struct MxArgs {

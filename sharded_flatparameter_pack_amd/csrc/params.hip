@@ -365,7 +365,7 @@ extern "C" void fp_params_destroy(fp_params* params) {
 extern "C" fp_status fp_params_info(const fp_params* params, int64_t* partition, int64_t* workspace_bytes) {
     if (params == nullptr) return bad(FP_ERR_INVALID, "params is NULL");
     if (partition) *partition = params->partition;
-    if (workspace_bytes) *workspace_bytes = 8 * (params_norm_groups(params->tiles) + 1);
+    if (workspace_bytes) *workspace_bytes = kNormHeader + 8 * params_norm_groups(params->tiles);
     return FP_OK;
 }
 
@@ -389,11 +389,9 @@ extern "C" fp_status fp_params_grad_norm(const fp_params* params, int32_t* found
     fp_status st = check_device(params);
     if (st != FP_OK) return st;
     const ParamsNormArgs a = {params->recs(), params->grads(), params->tile_table(), params->tiles, found_inf,
-                              static_cast<double*>(workspace)};
-    hipStream_t s = static_cast<hipStream_t>(stream);
-    hipError_t e = hipSuccess;
-    if (params->tiles > 0) e = launch_params_norm(a, params->grad_dtype, s);
-    if (e == hipSuccess) e = launch_norm_finalize(a.partials, (int)params_norm_groups(params->tiles), sq_norm, s);
+                              reinterpret_cast<double*>(static_cast<char*>(workspace) + kNormHeader),
+                              static_cast<uint32_t*>(workspace), sq_norm};
+    hipError_t e = launch_params_norm(a, params->grad_dtype, static_cast<hipStream_t>(stream));
     return e == hipSuccess ? FP_OK : device_error(e, "gradient norm launch");
 }
 

@@ -356,37 +356,99 @@ __global__ __launch_bounds__(kThreads) void params_step_kernel(const ParamsArgs 
     else params_step_entry<kGrad, kMx8, false>(a, rec, grad, e0);
 }
 
-// The sum of squares in fp64 and the overflow check.
+// Squares of the 8 elements of a 16-byte word (4 of fp32) added to sq[0..3].
+template <int kGrad>
+__device__ __forceinline__ void add_squares(const uint4 w, double sq[4]) {
+    float f[8];
+    constexpr int kN = kGrad == FP_DTYPE_F32 ? 4 : 8;
+    if constexpr (kGrad == FP_DTYPE_F32) {
+        f32x4_of(w, f);
+    } else {
+        GradQuad<kGrad> lo, hi;
+        lo.w = make_uint2(w.x, w.y);
+        hi.w = make_uint2(w.z, w.w);
+        grad_f32<kGrad>(lo, f);
+        grad_f32<kGrad>(hi, f + 4);
+    }
+#pragma unroll
+    for (int k = 0; k < kN; ++k) sq[k & 3] = __builtin_fma((double)f[k], (double)f[k], sq[k & 3]);
+}
+
+// Counts workgroup b of n in; true for the last one, which also leaves the
+// counters at 0 for the next call.  Two levels on lines of their own, as in
+// the step's grid barrier: one counter for all took 35 ns per workgroup.
+__device__ __forceinline__ bool norm_arrive(uint32_t* done, unsigned b, unsigned n) {
+    const unsigned group = b % kSyncGroups;
+    const unsigned members = n / kSyncGroups + (group < n % kSyncGroups ? 1u : 0u);
+    if (sync_add(&done[group * kLineWords], 1u) + 1u != members) return false;
+    sync_store(&done[group * kLineWords], 0u);
+    uint32_t* top = &done[kSyncGroups * kLineWords];
+    if (sync_add(top, 1u) + 1u != sync_groups(n)) return false;
+    sync_store(top, 0u);
+    return true;
+}
+
+// The sum of squares in fp64 and the overflow check, in one launch.  Squares
+// are not negative and their fp64 sum cannot overflow, so a sum that is not
+// finite is the overflow check: three instructions per element, unpack,
+// widen, fused multiply-add, leave the kernel to its loads.  Waves take tiles
+// in turn, so that those in flight cover one window of memory; two, four and
+// eight tiles of a wave in flight at once measured slower (226.5M bf16
+// elements 77, 86 and 103 us against 74, 6.2 TB/s), as did 1536 and 1024
+// workgroups instead of all that are resident together (83 and 110 us).  The
+// last workgroup to finish adds the partial sums in their order, so the
+// result does not depend on who was last.
 template <int kGrad>
 __global__ __launch_bounds__(kThreads) void params_norm_kernel(const ParamsNormArgs a) {
+    constexpr int kPer = kGrad == FP_DTYPE_F32 ? 4 : 8;                      // elements of a word
+    constexpr int kWords = (int)(kParamTile / (64 * kPer));                  // words per lane and tile
     const int lane = threadIdx.x & 63;
-    bool bad = false;
-    double sq = 0.0;
+    double sq[4] = {0.0, 0.0, 0.0, 0.0};
     for (int64_t i = (int64_t)blockIdx.x * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); i < a.n_tiles;
          i += (int64_t)gridDim.x * kWaves) {
         const ParamTile tile = a.tiles[i];
-        const int64_t numel = a.recs[tile.tensor].numel;
-        const void* grad = a.grads[tile.tensor];
         const int64_t e0 = (int64_t)tile.index * kParamTile;
+        const int64_t left = a.recs[tile.tensor].numel - e0;  // elements of the tensor from the tile on
+        const char* from = static_cast<const char*>(a.grads[tile.tensor]) + e0 * (16 / kPer);
+        uint4 w[kWords];
 #pragma unroll
-        for (int u = 0; u < kParamQuads; ++u) {
-            const int64_t e = e0 + 256 * u + 4 * lane;
-            if (e + 4 <= numel) {
-                float g[4];
-                grad_f32<kGrad>(ld_grad<kGrad>(grad, e), g);
-                check_quad(g, bad, sq, true);
-            } else {
-                for (int64_t k = e; k < numel; ++k) {
-                    const float g = ld_grad1<kGrad>(grad, k);
-                    bad |= !finite_f32(g);
-                    sq += (double)g * (double)g;
-                }
-            }
+        for (int u = 0; u < kWords; ++u) {
+            w[u] = make_uint4(0u, 0u, 0u, 0u);
+            if ((64 * u + lane + 1) * kPer <= left) w[u] = ld16u(from + 16 * (64 * u + lane));
+        }
+#pragma unroll
+        for (int u = 0; u < kWords; ++u) add_squares<kGrad>(w[u], sq);
+        if (left < kParamTile && lane < left % kPer) {        // elements past the last whole word
+            const double g = (double)ld_grad1<kGrad>(from, left - left % kPer + lane);
+            sq[0] = __builtin_fma(g, g, sq[0]);
         }
     }
-    flag_if_any(bad, a.found_inf);
-    const double t = group_sum(sq);
-    if (threadIdx.x == 0) a.partials[blockIdx.x] = t;
+    const double mine = (sq[0] + sq[1]) + (sq[2] + sq[3]);
+    flag_if_any(!__builtin_isfinite(mine), a.found_inf);
+    const double t = group_sum(mine);
+    if (gridDim.x == 1) {
+        if (threadIdx.x == 0) *a.sq_norm = t;
+        return;
+    }
+    __shared__ int last;
+    if (threadIdx.x == 0) {
+        // The partial sum travels in an exchange at agent scope, whose result
+        // has to be there before the count goes up; the counts go up by
+        // read-modify-write, and the last workgroup's loads are at agent scope
+        // too.  So every partial is in memory before it is read, without a
+        // write-back of the caches.
+        const double old = __hip_atomic_exchange(&a.partials[blockIdx.x], t, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        asm volatile("" ::"v"(old) : "memory");
+        last = norm_arrive(a.done, blockIdx.x, gridDim.x);
+    }
+    __syncthreads();
+    if (!last) return;
+    double s = 0.0;
+#pragma unroll 8
+    for (unsigned k = threadIdx.x; k < gridDim.x; k += kThreads)
+        s += __hip_atomic_load(&a.partials[k], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    s = group_sum(s);
+    if (threadIdx.x == 0) *a.sq_norm = s;
 }
 
 template <bool kRoot>
