@@ -738,12 +738,13 @@ fp_status fp_params_adamw(fp_params* params, int32_t n_groups, const fp_adamw_hp
  * consecutive partition elements, standing for code * 2^(b - 127); b = 255
  * stands for NaN.  exp_avg holds the first moment m, `root` the square root r
  * of the second (the root keeps v's range in 8 bits).  Per element, in fp64
- * from the fp32 weights and the decoded moments:
- *   m' = beta1 m + (1 - beta1) g,  v' = beta2 r^2 + (1 - beta2) g^2,
- * the weights as in fp_adamw_shard from the unrounded m' and v', and then
- * m' and r' = sqrt(v') are rounded to fp32 and stochastically to e4m3.  With
- * x in a block whose largest magnitude is X (elements past a tensor's end do
- * not count):
+ * from the decoded moments and each rounded once to fp32,
+ *   m' = beta1 m + (1 - beta1) g,  r' = sqrt(beta2 r^2 + (1 - beta2) g^2);
+ * the weights change by what fp_adamw_shard's formula gives for m' and r',
+ * evaluated in fp32 to 2^-20 of the change and added once (an eps below
+ * 2^-126 counts as 2^-126: an element whose m' and r' are 0 only decays); then
+ * m' and r' are rounded stochastically to e4m3.  With x in a block whose
+ * largest magnitude is X (elements past a tensor's end do not count):
  *   f = (fp32 bits of X + 2^19) >> 23;  b = f >= 255 ? 255 : max(0, f - 7);
  *   y = |x| 2^(127 - b) < 248;  q = e4m3's step at y, 2^(max(floor(log2 y), -6) - 3);
  *   the code is that of q * floor(y / q + d / 2^16),
@@ -766,12 +767,12 @@ fp_status fp_params_adamw8(fp_params* params, int32_t n_groups, const fp_adamw_h
                            const int32_t* found_inf, const double* grad_coef, void* stream);
 
 /* Moments between fp32 and MXFP8 (a checkpoint, resharding: fp_reshard moves
- * fp32 moments), over n elements.  Quantization rounds to nearest even:
- *   code = ((bits of y) + 2^19 - 1 + (bit 20 of y)) >> 20,
- * so values that MXFP8 holds come back as they are.  root != 0: x is a second
- * moment (>= 0, or NaN results): codes hold its root, sqrt in fp64 rounded to
- * fp32, and dequantization squares.  x: device fp32[n], codes: device
- * uint8[n], both 16-byte aligned; scales: device uint8[ceil(n / 32)]. */
+ * fp32 moments), over n elements.  Quantization takes the scales above and
+ * rounds y / q to nearest even, so values that it gave come back as they are.
+ * root != 0: x is a second moment (>= 0; a negative one gives NaN); codes hold
+ * its root, taken in fp64 and rounded to fp32, and dequantization squares.
+ * x: device fp32[n], codes: device uint8[n], both 16-byte aligned; scales:
+ * device uint8[ceil(n / 32)]. */
 fp_status fp_mx8_quantize(int64_t n, int32_t root, const float* x, uint8_t* codes, uint8_t* scales, void* stream);
 fp_status fp_mx8_dequantize(int64_t n, int32_t root, const uint8_t* codes, const uint8_t* scales, float* x,
                             void* stream);

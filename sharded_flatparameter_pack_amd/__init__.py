@@ -768,18 +768,19 @@ class Units:
 
 
 # ------------------------------------------------------------------ params
-def _table(tensors, dtype, name, sizes=None):
-    """Device pointers of contiguous tensors of one dtype (None for empty ones)."""
-    if sizes is not None and len(tensors) != len(sizes):
+def _table(tensors, dtype, device, sizes, name):
+    """Device pointers of contiguous tensors of one dtype, device and these sizes."""
+    if len(tensors) != len(sizes):
         raise ValueError(f"{name}: {len(tensors)} tensors, expected {len(sizes)}")
-    ptrs = []
-    for i, t in enumerate(tensors):
-        if t.dtype != dtype:
-            raise TypeError(f"{name}[{i}] has dtype {t.dtype}, expected {dtype}")
-        if sizes is not None and t.numel() != sizes[i]:
-            raise ValueError(f"{name}[{i}] has {t.numel()} elements, expected {sizes[i]}")
-        ptrs.append(_dev_ptr(t, (dtype,), 0, f"{name}[{i}]") if t.numel() else None)
-    return _ptr_table(ptrs)
+    ptrs = (C.c_void_p * len(sizes))()
+    for i, t in enumerate(tensors):  # one line of checks: plans hold up to tens of thousands of tensors
+        if t.dtype != dtype or t.device != device or t.numel() != sizes[i] or not t.is_contiguous():
+            _dev_ptr(t, (dtype,), 0, f"{name}[{i}]")
+            if t.numel() != sizes[i]:
+                raise ValueError(f"{name}[{i}] has {t.numel()} elements, expected {sizes[i]}")
+            raise ValueError(f"tensors of one call sit on several devices: {t.device} and {device}")
+        ptrs[i] = t.data_ptr()
+    return ptrs
 
 
 def _dtype_id(dtype, name):
@@ -820,24 +821,26 @@ class Params:
         grads = list(grads)
         if not grads:
             raise ValueError("need at least one tensor")
-        _one_device(grads, list(master) if master is not None else None, list(copies) if copies is not None else None)
-        torch = _torch()
+        n, device = len(grads), grads[0].device
+        if device.type != "cuda":
+            raise ValueError("grads[0] must be a device tensor")
         self.sizes = [t.numel() for t in grads]
-        n = len(grads)
         self._grad_dtype = grads[0].dtype
-        gtab = _table(grads, self._grad_dtype, "grads")
-        mtab = _table(master, torch.float32, "master", self.sizes) if master is not None else None
-        ctab, cid = None, _lib.FP_DTYPE_BF16
+        gtab = _table(grads, self._grad_dtype, device, self.sizes, "grads")
+        mtab, ctab, cid = None, None, _lib.FP_DTYPE_BF16
+        if master is not None:
+            master = list(master)
+            mtab = _table(master, _torch().float32, device, self.sizes, "master")
         if copies is not None:
-            if len(copies) != n:
-                raise ValueError(f"copies: {len(copies)} tensors, expected {n}")
-            ctab, cid = _table(copies, copies[0].dtype, "copies", self.sizes), _dtype_id(copies[0].dtype, "copies")
+            copies = list(copies)
+            ctab = _table(copies, copies[0].dtype if copies else None, device, self.sizes, "copies")
+            cid = _dtype_id(copies[0].dtype, "copies")
         self.groups = [0] * n if groups is None else [int(k) for k in groups]
         if len(self.groups) != n:
             raise ValueError(f"groups: {len(self.groups)} numbers, expected {n}")
         self.n_groups = max(self.groups) + 1
         self._keep = (grads, master, copies)
-        self._device = grads[0].device
+        self._device = device
         out = C.c_void_p()
         with _device_of(self._device):
             check(lib().fp_params_create(n, (C.c_int64 * n)(*self.sizes), (C.c_int32 * n)(*self.groups),
@@ -889,8 +892,7 @@ class Params:
         move from step to step; ordered on the current stream with the plan's
         other calls."""
         grads = list(grads)
-        _one_device(grads, self._keep[0])
-        table = _table(grads, self._grad_dtype, "grads", self.sizes)
+        table = _table(grads, self._grad_dtype, self._device, self.sizes, "grads")
         with _device_of(self._device):
             check(lib().fp_params_set_grads(self._h, table, _stream(self._device)))
         self._keep = (grads, *self._keep[1:])

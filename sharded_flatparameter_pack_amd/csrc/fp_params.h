@@ -33,6 +33,22 @@ struct ParamTile {
 constexpr int kParamQuads = 2;
 constexpr int64_t kParamTile = 256 * kParamQuads;
 inline int64_t param_tiles(int64_t numel) { return ceil_div64(numel, kParamTile); }
+// LDS that a launch of the step asks for and never touches, so that fewer of
+// its workgroups are resident in a CU: with more, HBM serves their streams
+// slower.  Measured on MI355X with bf16 gradients and copies:
+//   fp32 moments, three per CU against no limit: 4M elements 21.0 and 22.0 us,
+//     17M 78.8 and 79.9, 50M 225.6 and 233.0, 134M 618.5 and 657.9 (two: 666),
+//     but 1.6M, whose last workgroup waits for a place, 11.7 and 8.5;
+//   8-bit moments, five per CU against no limit: 34M 88.0 and 86.0 us, 42M
+//     108.7 and 105.8, 46M 120.0 and 119.8, 50M 133.8 and 138.8, 134M 360.8
+//     and 376.3 -- their arithmetic wants more waves as long as the memory
+//     side keeps up, so the limit starts at kMx8CapTiles.
+constexpr unsigned kParamCapLds = 53504u, kMx8CapLds = 32000u;
+constexpr int64_t kParamCapTiles = 4000000 / kParamTile, kMx8CapTiles = 46000000 / kParamTile;
+inline unsigned params_step_lds(int64_t tiles, bool mx8) {
+    if (!mx8) return tiles >= kParamCapTiles ? kParamCapLds : 0u;
+    return tiles >= kMx8CapTiles ? kMx8CapLds : 0u;
+}
 // Workgroups of the norm, a partial sum each: at most as many as are resident
 // together (8 per CU).
 constexpr int64_t kNormGroups = 2048;
@@ -43,6 +59,14 @@ inline int64_t params_norm_groups(int64_t tiles) {
 // Workspace of the norm: the counts of finished workgroups, each in a line of
 // its own, then the partial sums.
 constexpr int64_t kNormHeader = 4 * kLineWords * (kSyncGroups + 1);
+
+// The coefficients of a weight's change in fp32, from AdamCoef's.
+struct WeightCoef {
+    float step_size;
+    float inv_sqrt_bias2;
+    float eps;     // at least the smallest normal number, so that no denominator is 0
+    float decay;   // lr * weight_decay
+};
 
 struct ParamsArgs {
     const ParamRec* recs;
@@ -58,6 +82,7 @@ struct ParamsArgs {
     uint32_t key;             // of the stochastic rounding
     int32_t copy_f16;         // the copies are fp16, else bf16
     AdamCoef c[FP_MAX_GROUPS];
+    WeightCoef w[FP_MAX_GROUPS];  // of the step with 8-bit moments
 };
 
 struct ParamsNormArgs {

@@ -29,6 +29,16 @@ namespace fpk {
 
 namespace {
 
+// Addresses in global memory (see FP_GLOBAL).
+template <class T>
+__device__ __forceinline__ FP_GLOBAL T* gptr(void* p) {
+    return static_cast<FP_GLOBAL T*>((FP_GLOBAL void*)p);
+}
+template <class T>
+__device__ __forceinline__ const FP_GLOBAL T* gptr(const void* p) {
+    return static_cast<const FP_GLOBAL T*>((const FP_GLOBAL void*)p);
+}
+
 // ---------------------------------------------------------------- gradients
 
 template <int kGrad>
@@ -57,9 +67,25 @@ __device__ __forceinline__ GradQuad<kGrad> ld_grad(const void* g, int64_t e) {
 // One gradient element.
 template <int kGrad>
 __device__ __forceinline__ float ld_grad1(const void* g, int64_t e) {
-    if constexpr (kGrad == FP_DTYPE_F32) return static_cast<const FP_GLOBAL float*>((const FP_GLOBAL void*)g)[e];
-    const uint32_t w = static_cast<const FP_GLOBAL uint16_t*>((const FP_GLOBAL void*)g)[e];
+    if constexpr (kGrad == FP_DTYPE_F32) return gptr<float>(g)[e];
+    const uint32_t w = gptr<uint16_t>(g)[e];
     return kGrad == FP_DTYPE_BF16 ? bf16_lo(w) : f16_lo(w);
+}
+
+// The first `have` < 4 elements of a quad, the others 0.
+template <int kGrad>
+__device__ __forceinline__ GradQuad<kGrad> ld_grad_part(const void* g, int64_t e, int have) {
+    uint32_t w[3] = {0u, 0u, 0u};
+#pragma unroll
+    for (int k = 0; k < 3; ++k)
+        if (k < have) {
+            if constexpr (kGrad == FP_DTYPE_F32) w[k] = gptr<uint32_t>(g)[e + k];
+            else w[k] = gptr<uint16_t>(g)[e + k];
+        }
+    GradQuad<kGrad> q;
+    if constexpr (kGrad == FP_DTYPE_F32) q.w = make_uint4(w[0], w[1], w[2], 0u);
+    else q.w = make_uint2(w[0] | (w[1] << 16), w[2]);
+    return q;
 }
 
 template <int kGrad>
@@ -185,175 +211,220 @@ __device__ __forceinline__ uint32_t dither(uint32_t e, uint32_t key) {
 
 // ---------------------------------------------------------------- AdamW
 
-// adamw_elem with the second moment given and kept as its root: one element
-// in fp64 from the fp32 values, master, first moment and root each rounded
-// once to fp32.  Written for the fewest instructions, since with 8-bit
-// moments they and not the memory are the bound (see params_step_kernel):
-// fused operations, and the root and the quotient from the hardware's
-// estimates (accurate to 2^-24) with one Newton step each, to 2^-47.  kTiny
-// in v keeps a zero second moment out of the estimate's poles; beside any
-// other it is lost.
-__device__ __forceinline__ void adamw_root_elem(const AdamCoef& c, float g, float& th, float& m, float& r) {
+// adamw_elem with the second moment given and kept as its root.  The moments
+// are what the 8-bit codes are rounded from, so they are evaluated in fp64
+// and each rounded once to fp32; the weight's change, at most a few roundings
+// of 2^-24 of itself off, is evaluated in fp32 from them and added once.
+// Written for few instructions, which with 8-bit moments bound the kernel as
+// much as the memory does: fused operations, and the root from the hardware's
+// estimate of 1 / sqrt (accurate to 2^-24) with one Newton step, to 2^-47.
+// kTiny in v keeps a zero second moment out of the estimate's pole; beside
+// any other it is lost.
+__device__ __forceinline__ void adamw_root_elem(const AdamCoef& c, const WeightCoef& w, float g, float& th, float& m,
+                                                float& r) {
     constexpr double kTiny = 1e-290;
     const double gd = (double)g, rd = (double)r;
-    const double md = __builtin_fma(c.one_m_beta1, gd, c.beta1 * (double)m);
+    m = (float)__builtin_fma(c.one_m_beta1, gd, c.beta1 * (double)m);
     const double vd = __builtin_fma(c.one_m_beta2 * gd, gd, __builtin_fma(c.beta2, rd * rd, kTiny));
     const double y = __builtin_amdgcn_rsq(vd);
     const double s0 = vd * y;
-    const double root = __builtin_fma(0.5 * y, __builtin_fma(-s0, s0, vd), s0);
-    const double denom = __builtin_fma(root, c.inv_sqrt_bias2, c.eps);
-    const double q0 = __builtin_amdgcn_rcp(denom);
-    const double q = __builtin_fma(__builtin_fma(-denom, q0, 1.0), q0, q0);
-    th = (float)__builtin_fma(-c.step_size * md, q, (double)th * c.decay);
-    m = (float)md;
-    r = (float)root;
-}
-
-__device__ __forceinline__ void st_copy(void* copy, int64_t e, const float th[4], bool f16) {
-    uint16_t* p = static_cast<uint16_t*>(copy) + e;
-    st8u(p, f16 ? make_uint2(f16x2(th[0], th[1]), f16x2(th[2], th[3])) : f32x4_to_bf16(th));
-}
-__device__ __forceinline__ void st_copy1(void* copy, int64_t e, float th, bool f16) {
-    static_cast<FP_GLOBAL uint16_t*>((FP_GLOBAL void*)copy)[e] = (uint16_t)(f16 ? f16x2(th, 0.0f) : bf16x2(th, 0.0f));
-}
-
-template <class T>
-__device__ __forceinline__ FP_GLOBAL T* gptr(void* p) {
-    return static_cast<FP_GLOBAL T*>((FP_GLOBAL void*)p);
-}
-template <class T>
-__device__ __forceinline__ const FP_GLOBAL T* gptr(const void* p) {
-    return static_cast<const FP_GLOBAL T*>((const FP_GLOBAL void*)p);
+    r = (float)__builtin_fma(0.5 * y, __builtin_fma(-s0, s0, vd), s0);
+    const float denom = __builtin_fmaf(r, w.inv_sqrt_bias2, w.eps);
+    const float change = __builtin_fmaf(m * __builtin_amdgcn_rcpf(denom), w.step_size, w.decay * th);
+    th = th - change;
 }
 
 }  // namespace
 
-// A wave's entry of the step: kParamQuads quads per lane, 64 quads apart.
-// kFull: the tensor has all of its elements.  The loads do not wait for the
-// overflow flag, as in the flat step; on a skip only the copy of the
-// unchanged weights is stored.  Partition elements past the tensor (up to the
-// next multiple of 32) are read with their quad and left as they are.
-template <int kGrad, bool kMx8, bool kFull>
-__device__ __forceinline__ void params_step_entry(const ParamsArgs& a, const ParamRec& rec, const void* grad, int64_t e0) {
-    constexpr int kU = kParamQuads;
-    const AdamCoef c = coef_for(a.c[rec.group], a.g_coef);
-    const int lane = threadIdx.x & 63;
-    int have[kU];
-    float g[kU][4], th[kU][4], m[kU][4], v[kU][4];
-    GradQuad<kGrad> gq[kU];
-    uint32_t cm[kU], cv[kU], bm[kU], bv[kU];
-#pragma unroll
-    for (int u = 0; u < kU; ++u) {
-        const int64_t e = e0 + 256 * u + 4 * lane, p = rec.offset + e;
-        const int64_t left = rec.numel - e;
-        have[u] = kFull || left >= 4 ? 4 : left > 0 ? (int)left : 0;
-        if (kFull || have[u] == 4) {
-            gq[u] = ld_grad<kGrad>(grad, e);
-            f32x4_of(ld16u(rec.master + e), th[u]);
-        } else {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                g[u][k] = k < have[u] ? ld_grad1<kGrad>(grad, e + k) : 0.0f;
-                th[u][k] = k < have[u] ? gptr<float>(rec.master)[e + k] : 0.0f;
-            }
-        }
-        if (kFull || have[u] > 0) {
-            if constexpr (kMx8) {
-                cm[u] = gptr<uint32_t>(a.exp_avg)[p >> 2];
-                cv[u] = gptr<uint32_t>(a.exp_avg_sq)[p >> 2];
-                bm[u] = gptr<uint8_t>(a.exp_avg_scale)[p / kMxBlock];
-                bv[u] = gptr<uint8_t>(a.root_scale)[p / kMxBlock];
-            } else {
-                f32x4_of(ld16(static_cast<const float*>(a.exp_avg) + p), m[u]);
-                f32x4_of(ld16(static_cast<const float*>(a.exp_avg_sq) + p), v[u]);
-            }
-        } else if constexpr (kMx8) {
-            cm[u] = cv[u] = bm[u] = bv[u] = 0u;
-        } else {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) m[u][k] = v[u][k] = 0.0f;
-        }
+// Where a tile is.
+struct TileAt {
+    ParamRec rec;
+    const void* grad;
+    int64_t e0;   // its first element
+};
+
+__device__ __forceinline__ TileAt find_tile(const ParamsArgs& a, int64_t i) {
+    const ParamTile tile = a.tiles[i];
+    return {a.recs[tile.tensor], a.grads[tile.tensor], (int64_t)tile.index * kParamTile};
+}
+
+// The first `have` elements of a quad (kFull: all four).
+template <bool kFull>
+__device__ __forceinline__ void st_f32_part(float* p, const float f[4], int have) {
+    if (kFull || have == 4) {
+        st16u(p, bits_of(f));
+        return;
     }
-    const bool skip = a.found_inf != nullptr && *a.found_inf != 0;
 #pragma unroll
-    for (int u = 0; u < kU; ++u) {
-        const int64_t e = e0 + 256 * u + 4 * lane, p = rec.offset + e;
-        if (!skip) {
-            if (kFull || have[u] == 4) grad_f32<kGrad>(gq[u], g[u]);
-            if constexpr (kMx8) {
-                mx_decode(cm[u], bm[u], m[u]);
-                mx_decode(cv[u], bv[u], v[u]);
-            }
+    for (int k = 0; k < 3; ++k)
+        if (k < have) gptr<float>((void*)p)[k] = f[k];
+}
+template <bool kFull>
+__device__ __forceinline__ void st_codes(uint8_t* p, uint32_t codes, int have) {
+    if (kFull || have == 4) {
+        *gptr<uint32_t>((void*)p) = codes;
+        return;
+    }
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                if (kMx8) adamw_root_elem(c, g[u][k], th[u][k], m[u][k], v[u][k]);
-                else adamw_elem(c, g[u][k], th[u][k], m[u][k], v[u][k]);
-            }
-        }
-        if (kMx8 && !skip) {
+    for (int k = 0; k < 3; ++k)
+        if (k < have) gptr<uint8_t>((void*)p)[k] = (uint8_t)(codes >> (8 * k));
+}
+
+// What a lane reads of a tile: kParamQuads quads, 64 quads apart.
+template <int kGrad, bool kMx8>
+struct TileRaw {
+    GradQuad<kGrad> g[kParamQuads];
+    uint4 th[kParamQuads];
+    uint4 m[kParamQuads], v[kParamQuads];
+};
+template <int kGrad>
+struct TileRaw<kGrad, true> {
+    GradQuad<kGrad> g[kParamQuads];
+    uint4 th[kParamQuads];
+    uint32_t m[kParamQuads], v[kParamQuads];    // four codes
+    uint32_t bm[kParamQuads], bv[kParamQuads];  // the scale byte of their block
+};
+
+// Elements of the lane's quad u that the tensor has.
+__device__ __forceinline__ int quad_have(const TileAt& t, int u) {
+    const int64_t left = t.rec.numel - (t.e0 + 256 * u + 4 * (threadIdx.x & 63));
+    return left >= 4 ? 4 : left > 0 ? (int)left : 0;
+}
+
+// kFull: the tensor has all of the tile's elements.  Else elements past its
+// end read as 0; moments are read with their quad (the partition has room up
+// to the next multiple of 32).
+template <int kGrad, bool kMx8, bool kFull>
+__device__ __forceinline__ void load_tile(const ParamsArgs& a, const TileAt& t, TileRaw<kGrad, kMx8>& r) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-                if (!kFull && k >= have[u]) m[u][k] = v[u][k] = 0.0f;
-            const uint32_t nbm = mx_byte(m[u]), nbv = mx_byte(v[u]);
-            uint32_t dm[4], dv[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const uint32_t d = dither((uint32_t)p + (uint32_t)k, a.key);
-                dm[k] = d & 0xFFFF0000u;
-                dv[k] = d << 16;
-            }
-            mx_raise(v[u], nbv);
-            const uint32_t ncm = mx_encode(m[u], nbm, dm), ncv = mx_encode(v[u], nbv, dv);
-            if (kFull || have[u] == 4) {
-                gptr<uint32_t>(a.exp_avg)[p >> 2] = ncm;
-                gptr<uint32_t>(a.exp_avg_sq)[p >> 2] = ncv;
-            } else {
-                for (int k = 0; k < have[u]; ++k) {
-                    gptr<uint8_t>(a.exp_avg)[p + k] = (uint8_t)(ncm >> (8 * k));
-                    gptr<uint8_t>(a.exp_avg_sq)[p + k] = (uint8_t)(ncv >> (8 * k));
-                }
-            }
-            if ((kFull || have[u] > 0) && (lane & 7) == 0) {
-                gptr<uint8_t>(a.exp_avg_scale)[p / kMxBlock] = (uint8_t)nbm;
-                gptr<uint8_t>(a.root_scale)[p / kMxBlock] = (uint8_t)nbv;
-            }
-        }
-        if (kFull || have[u] == 4) {
-            if (!skip) {
-                st16u(rec.master + e, bits_of(th[u]));
-                if constexpr (!kMx8) {
-                    st16(static_cast<float*>(a.exp_avg) + p, bits_of(m[u]));
-                    st16(static_cast<float*>(a.exp_avg_sq) + p, bits_of(v[u]));
-                }
-            }
-            if (rec.copy != nullptr) st_copy(rec.copy, e, th[u], a.copy_f16 != 0);
+    for (int u = 0; u < kParamQuads; ++u) {
+        const int64_t e = t.e0 + 256 * u + 4 * (threadIdx.x & 63), p = t.rec.offset + e;
+        const int have = kFull ? 4 : quad_have(t, u);
+        if (kFull || have == 4) {
+            r.g[u] = ld_grad<kGrad>(t.grad, e);
+            r.th[u] = ld16u(t.rec.master + e);
         } else {
+            r.g[u] = ld_grad_part<kGrad>(t.grad, e, have);
+            uint32_t w[3] = {0u, 0u, 0u};
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                if (k >= have[u]) continue;
-                if (!skip) {
-                    gptr<float>(rec.master)[e + k] = th[u][k];
-                    if constexpr (!kMx8) {
-                        gptr<float>(a.exp_avg)[p + k] = m[u][k];
-                        gptr<float>(a.exp_avg_sq)[p + k] = v[u][k];
-                    }
-                }
-                if (rec.copy != nullptr) st_copy1(rec.copy, e + k, th[u][k], a.copy_f16 != 0);
+            for (int k = 0; k < 3; ++k)
+                if (k < have) w[k] = gptr<uint32_t>((const void*)t.rec.master)[e + k];
+            r.th[u] = make_uint4(w[0], w[1], w[2], 0u);
+        }
+        if constexpr (kMx8) {
+            r.m[u] = r.v[u] = r.bm[u] = r.bv[u] = 0u;
+            if (kFull || have > 0) {
+                r.m[u] = gptr<uint32_t>(a.exp_avg)[p >> 2];
+                r.v[u] = gptr<uint32_t>(a.exp_avg_sq)[p >> 2];
+                r.bm[u] = gptr<uint8_t>(a.exp_avg_scale)[p / kMxBlock];
+                r.bv[u] = gptr<uint8_t>(a.root_scale)[p / kMxBlock];
+            }
+        } else {
+            r.m[u] = r.v[u] = make_uint4(0u, 0u, 0u, 0u);
+            if (kFull || have > 0) {
+                r.m[u] = ld16(static_cast<const float*>(a.exp_avg) + p);
+                r.v[u] = ld16(static_cast<const float*>(a.exp_avg_sq) + p);
             }
         }
     }
 }
 
+// The tile's update, then its stores, one stream after the other; on a skip
+// only the copy of the unchanged weights is stored.  Partition elements past
+// the tensor are left as they are.
+template <int kGrad, bool kMx8, bool kFull>
+__device__ __forceinline__ void step_tile(const ParamsArgs& a, const TileAt& t, const TileRaw<kGrad, kMx8>& r, bool skip) {
+    constexpr int kU = kParamQuads;
+    const AdamCoef c = coef_for(a.c[t.rec.group], a.g_coef);
+    const int64_t e0 = t.e0 + 4 * (threadIdx.x & 63), p0 = t.rec.offset + e0;
+    int have[kU];
+    float th[kU][4], m[kU][4], v[kU][4];
+    uint32_t cm[kU], cv[kU], bm[kU], bv[kU];
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+        have[u] = kFull ? 4 : quad_have(t, u);
+        f32x4_of(r.th[u], th[u]);
+        if (skip) continue;
+        float g[4];
+        grad_f32<kGrad>(r.g[u], g);
+        if constexpr (kMx8) {
+            mx_decode(r.m[u], r.bm[u], m[u]);
+            mx_decode(r.v[u], r.bv[u], v[u]);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) adamw_root_elem(c, a.w[t.rec.group], g[k], th[u][k], m[u][k], v[u][k]);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (!kFull && k >= have[u]) m[u][k] = v[u][k] = 0.0f;
+            bm[u] = mx_byte(m[u]);
+            bv[u] = mx_byte(v[u]);
+            uint32_t dm[4], dv[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const uint32_t d = dither((uint32_t)(p0 + 256 * u) + (uint32_t)k, a.key);
+                dm[k] = d & 0xFFFF0000u;
+                dv[k] = d << 16;
+            }
+            mx_raise(v[u], bv[u]);
+            cm[u] = mx_encode(m[u], bm[u], dm);
+            cv[u] = mx_encode(v[u], bv[u], dv);
+        } else {
+            f32x4_of(r.m[u], m[u]);
+            f32x4_of(r.v[u], v[u]);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) adamw_elem(c, g[k], th[u][k], m[u][k], v[u][k]);
+        }
+    }
+    if (!skip) {
+#pragma unroll
+        for (int u = 0; u < kU; ++u) st_f32_part<kFull>(t.rec.master + e0 + 256 * u, th[u], have[u]);
+        if constexpr (kMx8) {
+#pragma unroll
+            for (int u = 0; u < kU; ++u) st_codes<kFull>(static_cast<uint8_t*>(a.exp_avg) + p0 + 256 * u, cm[u], have[u]);
+#pragma unroll
+            for (int u = 0; u < kU; ++u) st_codes<kFull>(static_cast<uint8_t*>(a.exp_avg_sq) + p0 + 256 * u, cv[u], have[u]);
+#pragma unroll
+            for (int u = 0; u < kU; ++u)
+                if ((kFull || have[u] > 0) && (threadIdx.x & 7) == 0) {
+                    gptr<uint8_t>(a.exp_avg_scale)[(p0 + 256 * u) / kMxBlock] = (uint8_t)bm[u];
+                    gptr<uint8_t>(a.root_scale)[(p0 + 256 * u) / kMxBlock] = (uint8_t)bv[u];
+                }
+        } else {
+#pragma unroll
+            for (int u = 0; u < kU; ++u) st_f32_part<kFull>(static_cast<float*>(a.exp_avg) + p0 + 256 * u, m[u], have[u]);
+#pragma unroll
+            for (int u = 0; u < kU; ++u) st_f32_part<kFull>(static_cast<float*>(a.exp_avg_sq) + p0 + 256 * u, v[u], have[u]);
+        }
+    }
+    if (t.rec.copy == nullptr) return;
+    uint16_t* copy = static_cast<uint16_t*>(t.rec.copy) + e0;
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+        const uint2 w = a.copy_f16 ? make_uint2(f16x2(th[u][0], th[u][1]), f16x2(th[u][2], th[u][3])) : f32x4_to_bf16(th[u]);
+        if (kFull || have[u] == 4) {
+            st8u(copy + 256 * u, w);
+        } else {
+            const uint32_t h[3] = {w.x, w.x >> 16, w.y};
+#pragma unroll
+            for (int k = 0; k < 3; ++k)
+                if (k < have[u]) gptr<uint16_t>((void*)copy)[256 * u + k] = (uint16_t)h[k];
+        }
+    }
+}
+
+// The step, a tile per wave.  The loads do not wait for the overflow flag, as
+// in the flat step.
 template <int kGrad, bool kMx8>
 __global__ __launch_bounds__(kThreads) void params_step_kernel(const ParamsArgs a) {
     const int64_t i = (int64_t)blockIdx.x * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     if (i >= a.n_tiles) return;
-    const ParamTile tile = a.tiles[i];
-    const ParamRec rec = a.recs[tile.tensor];
-    const void* grad = a.grads[tile.tensor];
-    const int64_t e0 = (int64_t)tile.index * kParamTile;
-    if (rec.numel - e0 >= kParamTile) params_step_entry<kGrad, kMx8, true>(a, rec, grad, e0);
-    else params_step_entry<kGrad, kMx8, false>(a, rec, grad, e0);
+    const TileAt t = find_tile(a, i);
+    const bool full = t.rec.numel - t.e0 >= kParamTile;
+    TileRaw<kGrad, kMx8> r;
+    if (full) load_tile<kGrad, kMx8, true>(a, t, r);
+    else load_tile<kGrad, kMx8, false>(a, t, r);
+    const bool skip = a.found_inf != nullptr && *a.found_inf != 0;
+    if (full) step_tile<kGrad, kMx8, true>(a, t, r, skip);
+    else step_tile<kGrad, kMx8, false>(a, t, r, skip);
 }
 
 // Squares of the 8 elements of a 16-byte word (4 of fp32) added to sq[0..3].
@@ -496,18 +567,19 @@ __global__ __launch_bounds__(kThreads) void mx8_dequantize_kernel(const MxArgs a
 
 hipError_t launch_params_step(const ParamsArgs& a, int grad_dtype, bool mx8, hipStream_t s) {
     const unsigned grid = (unsigned)ceil_div64(a.n_tiles, kWaves);
+    const unsigned lds = params_step_lds(a.n_tiles, mx8);
     switch (grad_dtype) {
         case FP_DTYPE_F32:
-            if (mx8) params_step_kernel<FP_DTYPE_F32, true><<<grid, kThreads, 0, s>>>(a);
-            else params_step_kernel<FP_DTYPE_F32, false><<<grid, kThreads, 0, s>>>(a);
+            if (mx8) params_step_kernel<FP_DTYPE_F32, true><<<grid, kThreads, lds, s>>>(a);
+            else params_step_kernel<FP_DTYPE_F32, false><<<grid, kThreads, lds, s>>>(a);
             break;
         case FP_DTYPE_BF16:
-            if (mx8) params_step_kernel<FP_DTYPE_BF16, true><<<grid, kThreads, 0, s>>>(a);
-            else params_step_kernel<FP_DTYPE_BF16, false><<<grid, kThreads, 0, s>>>(a);
+            if (mx8) params_step_kernel<FP_DTYPE_BF16, true><<<grid, kThreads, lds, s>>>(a);
+            else params_step_kernel<FP_DTYPE_BF16, false><<<grid, kThreads, lds, s>>>(a);
             break;
         default:
-            if (mx8) params_step_kernel<FP_DTYPE_F16, true><<<grid, kThreads, 0, s>>>(a);
-            else params_step_kernel<FP_DTYPE_F16, false><<<grid, kThreads, 0, s>>>(a);
+            if (mx8) params_step_kernel<FP_DTYPE_F16, true><<<grid, kThreads, lds, s>>>(a);
+            else params_step_kernel<FP_DTYPE_F16, false><<<grid, kThreads, lds, s>>>(a);
     }
     return hipGetLastError();
 }

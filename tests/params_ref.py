@@ -7,6 +7,12 @@ plus the fp64 operations' own error, a few 2^-53 of the terms: `near` takes
 reference's only where the value is that close to a border between two codes,
 so a code is right if it is the code of the value moved by a relative 2^-40
 either way or of the value itself.
+
+With 8-bit moments a weight's change is evaluated in fp32 and added once.  Its
+roundings, relative to the change: of r', the root's bias correction, eps, the
+denominator, m', their quotient, the step size, lr * weight_decay, its product
+and the sum, each at most 2^-24, and of the hardware's reciprocal, at most
+2^-23: 12 * 2^-24 in all, below 2^-20.  `near` takes 2^-20 of `change` for it.
 """
 
 import numpy as np
@@ -70,17 +76,18 @@ def dither(index, seed):
 
 
 def adamw(g, th, m, v, hp, t, coef=1.0):
-    """fp64 (weights, first moment, second moment) of one step and the size of
-    the terms that the weights are the sum of."""
+    """fp64 (weights, first moment, second moment) of one step, the size of the
+    terms that the weights are the sum of, and that of their change."""
     g = g.astype(np.float64) * coef
     m = hp["beta1"] * m.astype(np.float64) + (1 - hp["beta1"]) * g
     v = hp["beta2"] * v.astype(np.float64) + (1 - hp["beta2"]) * g * g
     step = hp["lr"] * (m / (1 - hp["beta1"] ** t)) / (np.sqrt(v / (1 - hp["beta2"] ** t)) + hp["eps"])
-    th = th.astype(np.float64) * (1 - hp["lr"] * hp["weight_decay"])
-    return th - step, m, v, np.abs(th) + np.abs(step)
+    th = th.astype(np.float64)
+    decay = hp["lr"] * hp["weight_decay"] * th
+    return th - decay - step, m, v, np.abs(th) + np.abs(step), np.abs(decay) + np.abs(step)
 
 
-def near(got, want, terms=None, what=""):
+def near(got, want, terms=None, what="", change=0.0):
     """`got` (fp32) is the fp64 `want` rounded once (see above)."""
     got, want = np.asarray(got, np.float64), np.asarray(want, np.float64)
     terms = np.abs(want) if terms is None else terms
@@ -88,6 +95,7 @@ def near(got, want, terms=None, what=""):
     assert np.array_equal(np.isnan(got), np.isnan(want)), f"{what}: other NaNs"
     err = np.abs(got[fine] - want[fine])
     tol = 2.0 ** -24 * np.abs(want[fine]) + 2.0 ** -48 * terms[fine] + 2.0 ** -150
+    tol = tol + 2.0 ** -20 * np.broadcast_to(change, want.shape)[fine]
     if (err > tol).any():
         i = int(np.argmax(err - tol))
         raise AssertionError(f"{what}: {int((err > tol).sum())} of {err.size} off; got {got[fine][i]!r} "

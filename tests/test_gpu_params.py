@@ -108,8 +108,8 @@ class Case:
             else:
                 m0 = ref.decode(old[0][p], old[1][b])
                 v0 = ref.decode(old[2][p], old[3][b]) ** 2
-            th, m, v, terms = ref.adamw(before["grad"][d], before["master"][d], m0, v0, hp, t, coef)
-            ref.near(after["master"][d], th, terms, where + " weights")
+            th, m, v, terms, change = ref.adamw(before["grad"][d], before["master"][d], m0, v0, hp, t, coef)
+            ref.near(after["master"][d], th, terms, where + " weights", change if self.bits == 8 else 0.0)
             new = after["moments"]
             if self.bits == 32:
                 g = np.abs(before["grad"][d].astype(np.float64) * coef)
@@ -598,9 +598,9 @@ def test_together_on_the_dim0_layout(fp):
             o, n = params.offsets[i], params.sizes[i]
             p, b = slice(o, o + n), slice(o // 32, o // 32 + -(-n // 32))
             old, hp = before["mom"], hps[params.groups[i]]
-            th, m, v, terms = ref.adamw(x, w0[i].reshape(-1).numpy(), ref.decode(old[0][p], old[1][b]),
+            th, m, v, terms, change = ref.adamw(x, w0[i].reshape(-1).numpy(), ref.decode(old[0][p], old[1][b]),
                                         ref.decode(old[2][p], old[3][b]) ** 2, hp, t, float(coef))
-            ref.near(w1[i].reshape(-1).numpy(), th, terms, f"step {t} tensor {i}")
+            ref.near(w1[i].reshape(-1).numpy(), th, terms, f"step {t} tensor {i}", change)
             dm, dr = ref.dither(np.arange(o, o + n), t)
             ref.check_mx8(after[0][p], after[1][b], m, dm, what=f"step {t} tensor {i}")
             ref.check_mx8(after[2][p], after[3][b], np.sqrt(v), dr, root=True, what=f"step {t} tensor {i}")
@@ -649,8 +649,8 @@ def test_past_32_bit_offsets(fp):
             o = s.start if s else plan.offsets[1]
             k = x.size
             w0 = x if s else np.ones(50, np.float32)
-            th, m, v, terms = ref.adamw(x, w0, np.zeros(k), np.zeros(k), HPS[0], 1)
-            ref.near((w[s] if s else tail_w).cpu().numpy(), th, terms, f"weights at {o}")
+            th, m, v, terms, change = ref.adamw(x, w0, np.zeros(k), np.zeros(k), HPS[0], 1)
+            ref.near((w[s] if s else tail_w).cpu().numpy(), th, terms, f"weights at {o}", change if bits == 8 else 0.0)
             if bits == 32:
                 ref.near(mom[0][o:o + k].cpu().numpy(), m, None, f"first moment at {o}")
                 ref.near(mom[1][o:o + k].cpu().numpy(), v, None, f"second moment at {o}")
