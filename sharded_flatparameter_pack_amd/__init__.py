@@ -65,25 +65,13 @@ def _stream(t):
     return C.c_void_p(torch.cuda.current_stream(device).cuda_stream)
 
 
-class _Here:
-    """Enters nothing: the device is the current one already."""
-
-    def __enter__(self):
-        return self
-
-    def __exit__(self, *exc):
-        return False
-
-
-_HERE = _Here()
-
-
-def _device_of(t):
-    """t's device as the current one (nothing to do if it is)."""
-    device = t if isinstance(t, _torch().device) else t.device
-    if device.type == "cuda" and _torch().cuda.current_device() != device.index:
-        return _torch().cuda.device(device)
-    return _HERE
+def _on_device(device, fn, *args):
+    """check(fn(*args, stream)) with `device` as the current one, on its current stream."""
+    cuda = _torch().cuda
+    if device.type != "cuda" or cuda.current_device() == device.index:
+        return check(fn(*args, _stream(device)))
+    with cuda.device(device):
+        check(fn(*args, _stream(device)))
 
 
 def _dev_ptr(t, dtypes, n, name):
@@ -791,14 +779,16 @@ def _dtype_id(dtype, name):
     return ids[dtype]
 
 
-def _code_dtypes():
-    torch = _torch()
-    return torch.float8_e4m3fn, torch.uint8
+_MX_DTYPES = None
 
 
-def _scale_dtypes():
-    torch = _torch()
-    return torch.float8_e8m0fnu, torch.uint8
+def _mx_dtypes():
+    """(dtypes of codes, dtypes of scales): torch's own, or bytes."""
+    global _MX_DTYPES
+    if _MX_DTYPES is None:
+        torch = _torch()
+        _MX_DTYPES = (torch.float8_e4m3fn, torch.uint8), (torch.float8_e8m0fnu, torch.uint8)
+    return _MX_DTYPES
 
 
 class Params:
@@ -842,7 +832,7 @@ class Params:
         self._keep = (grads, master, copies)
         self._device = device
         out = C.c_void_p()
-        with _device_of(self._device):
+        with _torch().cuda.device(device):
             check(lib().fp_params_create(n, (C.c_int64 * n)(*self.sizes), (C.c_int32 * n)(*self.groups),
                                          _dtype_id(self._grad_dtype, "grads"), gtab, mtab, cid, ctab, C.byref(out)))
         self._h = out
@@ -877,8 +867,9 @@ class Params:
         if bits != 8:
             raise ValueError("moments have 32 or 8 bits")
         P, B = self.partition, self.partition // _lib.FP_MX_BLOCK
+        codes, scales = _mx_dtypes()
         return tuple(torch.zeros(n, dtype=torch.uint8, device=self._device).view(d)
-                     for n, d in ((P, _code_dtypes()[0]), (B, _scale_dtypes()[0])) * 2)
+                     for n, d in ((P, codes[0]), (B, scales[0])) * 2)
 
     def tensor_slice(self, buf, i: int):
         """Tensor i's part of a partition-sized tensor, or of its scales."""
@@ -893,8 +884,7 @@ class Params:
         other calls."""
         grads = list(grads)
         table = _table(grads, self._grad_dtype, self._device, self.sizes, "grads")
-        with _device_of(self._device):
-            check(lib().fp_params_set_grads(self._h, table, _stream(self._device)))
+        _on_device(self._device, lib().fp_params_set_grads, self._h, table)
         self._keep = (grads, *self._keep[1:])
 
     def grad_norm(self, sq_norm, workspace, found_inf=None):
@@ -905,8 +895,7 @@ class Params:
         fi = _dev_ptr(found_inf, (torch.int32,), 1, "found_inf") if found_inf is not None else None
         sq = _dev_ptr(sq_norm, (torch.float64,), 1, "sq_norm")
         ws = _dev_ptr(workspace, (torch.uint8,), self.workspace_bytes, "workspace")
-        with _device_of(self._device):
-            check(lib().fp_params_grad_norm(self._h, fi, sq, ws, _stream(self._device)))
+        _on_device(self._device, lib().fp_params_grad_norm, self._h, fi, sq, ws)
         return sq_norm
 
     def stepper(self, moments, *, lr, beta1, beta2, eps, weight_decay, found_inf=None, grad_coef=None):
@@ -948,10 +937,10 @@ class ParamsStep:
         self._eight = len(moments) == 4
         if self._eight:
             B = P // _lib.FP_MX_BLOCK
-            self._moments = [_dev_ptr(moments[0], _code_dtypes(), P, "exp_avg"),
-                             _dev_ptr(moments[1], _scale_dtypes(), B, "exp_avg_scale"),
-                             _dev_ptr(moments[2], _code_dtypes(), P, "root"),
-                             _dev_ptr(moments[3], _scale_dtypes(), B, "root_scale")]
+            codes, scales = _mx_dtypes()
+            self._moments = [_dev_ptr(moments[0], codes, P, "exp_avg"),
+                             _dev_ptr(moments[1], scales, B, "exp_avg_scale"),
+                             _dev_ptr(moments[2], codes, P, "root"), _dev_ptr(moments[3], scales, B, "root_scale")]
         else:
             self._moments = [_f32(moments[0], P, "exp_avg"), _f32(moments[1], P, "exp_avg_sq")]
         self._found = _dev_ptr(found_inf, (torch.int32,), 1, "found_inf") if found_inf is not None else None
@@ -976,42 +965,39 @@ class ParamsStep:
             for h, x in zip(self._hp, self._per_group(lr)):
                 h.lr = x
         more = (int(seed) & 0xFFFFFFFFFFFFFFFF,) if self._eight else ()
-        with _device_of(p._device):
-            check(self._fn(p._h, self._n, self._hp, *self._moments, *more, self._found, self._coef, _stream(p._device)))
+        _on_device(p._device, self._fn, p._h, self._n, self._hp, *self._moments, *more, self._found, self._coef)
 
 
 def mx8_quantize(src, codes=None, scales=None, *, root: bool = False):
     """(codes, scales): MXFP8 of fp32 moments, e4m3 codes and one e8m0 scale per
     32 elements, rounded to nearest even; root: of a second moment, whose root
     the codes then hold.  Allocated here when None."""
-    torch = _torch()
     n = src.numel()
     blocks = -(-n // _lib.FP_MX_BLOCK)
+    cd, sd = _mx_dtypes()
     x = _f32(src, n, "src")
     if codes is None:
-        codes = torch.empty(n, dtype=_code_dtypes()[0], device=src.device)
+        codes = _torch().empty(n, dtype=cd[0], device=src.device)
     if scales is None:
-        scales = torch.empty(blocks, dtype=_scale_dtypes()[0], device=src.device)
+        scales = _torch().empty(blocks, dtype=sd[0], device=src.device)
     _one_device(src, codes, scales)
-    cp, sp = _dev_ptr(codes, _code_dtypes(), n, "codes"), _dev_ptr(scales, _scale_dtypes(), blocks, "scales")
-    with _device_of(src):
-        check(lib().fp_mx8_quantize(n, int(bool(root)), x, cp, sp, _stream(src)))
+    cp, sp = _dev_ptr(codes, cd, n, "codes"), _dev_ptr(scales, sd, blocks, "scales")
+    _on_device(src.device, lib().fp_mx8_quantize, n, int(bool(root)), x, cp, sp)
     return codes, scales
 
 
 def mx8_dequantize(codes, scales, dst=None, *, root: bool = False):
     """dst (fp32, allocated here when None): what MXFP8 codes and scales stand
     for, squared with root (a second moment kept as its root)."""
-    torch = _torch()
     n = codes.numel()
-    cp = _dev_ptr(codes, _code_dtypes(), n, "codes")
-    sp = _dev_ptr(scales, _scale_dtypes(), -(-n // _lib.FP_MX_BLOCK), "scales")
+    cd, sd = _mx_dtypes()
+    cp = _dev_ptr(codes, cd, n, "codes")
+    sp = _dev_ptr(scales, sd, -(-n // _lib.FP_MX_BLOCK), "scales")
     if dst is None:
-        dst = torch.empty(n, dtype=torch.float32, device=codes.device)
+        dst = _torch().empty(n, dtype=_torch().float32, device=codes.device)
     _one_device(codes, scales, dst)
     x = _f32(dst, n, "dst")
-    with _device_of(codes):
-        check(lib().fp_mx8_dequantize(n, int(bool(root)), cp, sp, x, _stream(codes)))
+    _on_device(codes.device, lib().fp_mx8_dequantize, n, int(bool(root)), cp, sp, x)
     return dst
 
 
