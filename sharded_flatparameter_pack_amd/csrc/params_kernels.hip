@@ -72,20 +72,31 @@ __device__ __forceinline__ float ld_grad1(const void* g, int64_t e) {
     return kGrad == FP_DTYPE_BF16 ? bf16_lo(w) : f16_lo(w);
 }
 
-// The first `have` < 4 elements of a quad, the others 0.
+// The first n < 4 elements of a tensor that has no more, as a quad.
 template <int kGrad>
-__device__ __forceinline__ GradQuad<kGrad> ld_grad_part(const void* g, int64_t e, int have) {
+__device__ __forceinline__ GradQuad<kGrad> ld_grad_few(const void* g, int n) {
     uint32_t w[3] = {0u, 0u, 0u};
 #pragma unroll
     for (int k = 0; k < 3; ++k)
-        if (k < have) {
-            if constexpr (kGrad == FP_DTYPE_F32) w[k] = gptr<uint32_t>(g)[e + k];
-            else w[k] = gptr<uint16_t>(g)[e + k];
+        if (k < n) {
+            if constexpr (kGrad == FP_DTYPE_F32) w[k] = gptr<uint32_t>(g)[k];
+            else w[k] = gptr<uint16_t>(g)[k];
         }
     GradQuad<kGrad> q;
     if constexpr (kGrad == FP_DTYPE_F32) q.w = make_uint4(w[0], w[1], w[2], 0u);
     else q.w = make_uint2(w[0] | (w[1] << 16), w[2]);
     return q;
+}
+
+// A quad without its first s elements (s >= 4: without any), zeros behind.
+__device__ __forceinline__ uint4 drop(const uint4 w, int s) {
+    const uint32_t a = s & 1 ? w.y : w.x, b = s & 1 ? w.z : w.y, c = s & 1 ? w.w : w.z, d = s & 1 ? 0u : w.w;
+    const uint4 r = s & 2 ? make_uint4(c, d, 0u, 0u) : make_uint4(a, b, c, d);
+    return s >= 4 ? make_uint4(0u, 0u, 0u, 0u) : r;
+}
+__device__ __forceinline__ uint2 drop(const uint2 w, int s) {
+    const uint64_t x = (((uint64_t)w.y << 32) | w.x) >> (16 * (s & 3));
+    return s >= 4 ? make_uint2(0u, 0u) : make_uint2((uint32_t)x, (uint32_t)(x >> 32));
 }
 
 template <int kGrad>
@@ -211,24 +222,27 @@ __device__ __forceinline__ uint32_t dither(uint32_t e, uint32_t key) {
 
 // ---------------------------------------------------------------- AdamW
 
+// sqrt(v) rounded to fp32, from the hardware's estimate of 1 / sqrt (accurate
+// to 2^-24) with one Newton step, to 2^-47.  kTiny added to v keeps a zero out
+// of the estimate's pole; beside any other v here it is lost.
+constexpr double kTiny = 1e-290;
+__device__ __forceinline__ float root_f32(double v) {
+    const double y = __builtin_amdgcn_rsq(v);
+    const double s = v * y;
+    return (float)__builtin_fma(0.5 * y, __builtin_fma(-s, s, v), s);
+}
+
 // adamw_elem with the second moment given and kept as its root.  The moments
 // are what the 8-bit codes are rounded from, so they are evaluated in fp64
 // and each rounded once to fp32; the weight's change, at most a few roundings
 // of 2^-24 of itself off, is evaluated in fp32 from them and added once.
 // Written for few instructions, which with 8-bit moments bound the kernel as
-// much as the memory does: fused operations, and the root from the hardware's
-// estimate of 1 / sqrt (accurate to 2^-24) with one Newton step, to 2^-47.
-// kTiny in v keeps a zero second moment out of the estimate's pole; beside
-// any other it is lost.
+// much as the memory does.
 __device__ __forceinline__ void adamw_root_elem(const AdamCoef& c, const WeightCoef& w, float g, float& th, float& m,
                                                 float& r) {
-    constexpr double kTiny = 1e-290;
     const double gd = (double)g, rd = (double)r;
     m = (float)__builtin_fma(c.one_m_beta1, gd, c.beta1 * (double)m);
-    const double vd = __builtin_fma(c.one_m_beta2 * gd, gd, __builtin_fma(c.beta2, rd * rd, kTiny));
-    const double y = __builtin_amdgcn_rsq(vd);
-    const double s0 = vd * y;
-    r = (float)__builtin_fma(0.5 * y, __builtin_fma(-s0, s0, vd), s0);
+    r = root_f32(__builtin_fma(c.one_m_beta2 * gd, gd, __builtin_fma(c.beta2, rd * rd, kTiny)));
     const float denom = __builtin_fmaf(r, w.inv_sqrt_bias2, w.eps);
     const float change = __builtin_fmaf(m * __builtin_amdgcn_rcpf(denom), w.step_size, w.decay * th);
     th = th - change;
@@ -291,42 +305,45 @@ __device__ __forceinline__ int quad_have(const TileAt& t, int u) {
     return left >= 4 ? 4 : left > 0 ? (int)left : 0;
 }
 
-// kFull: the tensor has all of the tile's elements.  Else elements past its
-// end read as 0; moments are read with their quad (the partition has room up
-// to the next multiple of 32).
+// kFull: the tensor has all of the tile's elements.  Else a quad that would
+// pass its end is read so that it ends there (quad_drop says by how many
+// elements early), and moments with the tensor's last quad (the partition has
+// room up to the next multiple of 32): lanes all load, and none waits here.
+// Element by element, tensors of 4001 elements took a quarter longer.
 template <int kGrad, bool kMx8, bool kFull>
 __device__ __forceinline__ void load_tile(const ParamsArgs& a, const TileAt& t, TileRaw<kGrad, kMx8>& r) {
+    const int64_t last = t.rec.numel - 4, last_quad = (t.rec.numel - 1) & ~(int64_t)3;
 #pragma unroll
     for (int u = 0; u < kParamQuads; ++u) {
-        const int64_t e = t.e0 + 256 * u + 4 * (threadIdx.x & 63), p = t.rec.offset + e;
-        const int have = kFull ? 4 : quad_have(t, u);
-        if (kFull || have == 4) {
-            r.g[u] = ld_grad<kGrad>(t.grad, e);
-            r.th[u] = ld16u(t.rec.master + e);
+        const int64_t e = t.e0 + 256 * u + 4 * (threadIdx.x & 63);
+        const int64_t p = t.rec.offset + (kFull || e < last_quad ? e : last_quad);
+        if (kFull || last >= 0) {
+            const int64_t from = kFull || e < last ? e : last;
+            r.g[u] = ld_grad<kGrad>(t.grad, from);
+            r.th[u] = ld16u(t.rec.master + from);
         } else {
-            r.g[u] = ld_grad_part<kGrad>(t.grad, e, have);
-            uint32_t w[3] = {0u, 0u, 0u};
-#pragma unroll
-            for (int k = 0; k < 3; ++k)
-                if (k < have) w[k] = gptr<uint32_t>((const void*)t.rec.master)[e + k];
-            r.th[u] = make_uint4(w[0], w[1], w[2], 0u);
+            const int n = (int)t.rec.numel;
+            const FP_GLOBAL uint32_t* w = gptr<uint32_t>((const void*)t.rec.master);
+            r.g[u] = ld_grad_few<kGrad>(t.grad, n);
+            r.th[u] = make_uint4(w[0], n > 1 ? w[1] : 0u, n > 2 ? w[2] : 0u, 0u);
         }
         if constexpr (kMx8) {
-            r.m[u] = r.v[u] = r.bm[u] = r.bv[u] = 0u;
-            if (kFull || have > 0) {
-                r.m[u] = gptr<uint32_t>(a.exp_avg)[p >> 2];
-                r.v[u] = gptr<uint32_t>(a.exp_avg_sq)[p >> 2];
-                r.bm[u] = gptr<uint8_t>(a.exp_avg_scale)[p / kMxBlock];
-                r.bv[u] = gptr<uint8_t>(a.root_scale)[p / kMxBlock];
-            }
+            r.m[u] = gptr<uint32_t>(a.exp_avg)[p >> 2];
+            r.v[u] = gptr<uint32_t>(a.exp_avg_sq)[p >> 2];
+            r.bm[u] = gptr<uint8_t>(a.exp_avg_scale)[p / kMxBlock];
+            r.bv[u] = gptr<uint8_t>(a.root_scale)[p / kMxBlock];
         } else {
-            r.m[u] = r.v[u] = make_uint4(0u, 0u, 0u, 0u);
-            if (kFull || have > 0) {
-                r.m[u] = ld16(static_cast<const float*>(a.exp_avg) + p);
-                r.v[u] = ld16(static_cast<const float*>(a.exp_avg_sq) + p);
-            }
+            r.m[u] = ld16(static_cast<const float*>(a.exp_avg) + p);
+            r.v[u] = ld16(static_cast<const float*>(a.exp_avg_sq) + p);
         }
     }
+}
+
+// Elements that quad u was read early by (see load_tile).
+__device__ __forceinline__ int quad_drop(const TileAt& t, int u) {
+    const int64_t last = t.rec.numel - 4, e = t.e0 + 256 * u + 4 * (threadIdx.x & 63);
+    if (last < 0) return e == 0 ? 0 : 4;
+    return e <= last ? 0 : e - last < 4 ? (int)(e - last) : 4;
 }
 
 // The tile's update, then its stores, one stream after the other; on a skip
@@ -343,10 +360,16 @@ __device__ __forceinline__ void step_tile(const ParamsArgs& a, const TileAt& t, 
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
         have[u] = kFull ? 4 : quad_have(t, u);
-        f32x4_of(r.th[u], th[u]);
+        GradQuad<kGrad> gq = r.g[u];
+        uint4 tq = r.th[u];
+        if (!kFull) {
+            gq.w = drop(gq.w, quad_drop(t, u));
+            tq = drop(tq, quad_drop(t, u));
+        }
+        f32x4_of(tq, th[u]);
         if (skip) continue;
         float g[4];
-        grad_f32<kGrad>(r.g[u], g);
+        grad_f32<kGrad>(gq, g);
         if constexpr (kMx8) {
             mx_decode(r.m[u], r.bm[u], m[u]);
             mx_decode(r.v[u], r.bv[u], v[u]);
@@ -487,12 +510,11 @@ __global__ __launch_bounds__(kThreads) void params_norm_kernel(const ParamsNormA
             w[u] = make_uint4(0u, 0u, 0u, 0u);
             if ((64 * u + lane + 1) * kPer <= left) w[u] = ld16u(from + 16 * (64 * u + lane));
         }
+        float g = 0.0f;                                       // elements past the last whole word
+        if (left < kParamTile && lane < left % kPer) g = ld_grad1<kGrad>(from, left - left % kPer + lane);
 #pragma unroll
         for (int u = 0; u < kWords; ++u) add_squares<kGrad>(w[u], sq);
-        if (left < kParamTile && lane < left % kPer) {        // elements past the last whole word
-            const double g = (double)ld_grad1<kGrad>(from, left - left % kPer + lane);
-            sq[0] = __builtin_fma(g, g, sq[0]);
-        }
+        sq[0] = __builtin_fma((double)g, (double)g, sq[0]);
     }
     const double mine = (sq[0] + sq[1]) + (sq[2] + sq[3]);
     flag_if_any(!__builtin_isfinite(mine), a.found_inf);
@@ -532,7 +554,7 @@ __global__ __launch_bounds__(kThreads) void mx8_quantize_kernel(const MxArgs a) 
         for (int k = 0; k < have; ++k) f[k] = a.x[e + k];
     if (kRoot) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) f[k] = (float)sqrt((double)f[k]);
+        for (int k = 0; k < 4; ++k) f[k] = root_f32((double)f[k] + kTiny);
     }
     const uint32_t byte = mx_byte(f);
     if (kRoot) mx_raise(f, byte);
