@@ -96,6 +96,10 @@ struct ParamsNormArgs {
     double* sq_norm;
 };
 
+// Elements of a workgroup of the MXFP8 conversions.
+constexpr int kMxQuads = 2;
+constexpr int64_t kMxTile = 4 * (int64_t)kThreads * kMxQuads;
+
 struct MxArgs {
     float* x;                 // read by the quantization, written by the other
     uint8_t* codes;

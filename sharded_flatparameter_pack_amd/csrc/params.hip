@@ -328,7 +328,7 @@ fp_status mx8_call(int64_t n, bool quantize, int32_t root, const float* x, const
                    void* stream) {
     if (n < 0) return bad(FP_ERR_RANGE, "n must be >= 0");
     if (n == 0) return FP_OK;
-    if (ceil_div64(n, 4 * (int64_t)kThreads) > kMaxGroups)
+    if (ceil_div64(n, kMxTile) > kMaxGroups)
         return bad(FP_ERR_RANGE, "n %lld needs more workgroups than one launch holds", (long long)n);
     if (x == nullptr || codes == nullptr || scales == nullptr)
         return bad(FP_ERR_INVALID, "the fp32 buffer, codes or scales is NULL");
