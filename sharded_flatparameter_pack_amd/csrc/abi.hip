@@ -15,6 +15,7 @@
 #include <vector>
 
 #include "fp_extra.h"
+#include "fp_params.h"
 
 using namespace fpk;
 

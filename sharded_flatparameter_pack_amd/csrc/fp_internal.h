@@ -280,11 +280,9 @@ inline int64_t unit_tiles(int64_t S) {
 }
 
 // Host helpers of the entry points (abi.hip): set the calling thread's
-// error message and return `status`; AdamW's coefficients; run fp_shard_step (give_up_test: the
+// error message and return `status`; run fp_shard_step (give_up_test: the
 // one-pass kernel with a barrier that always gives up).
 fp_status report_error(fp_status status, const char* message);
-// Checks hyperparameters and fills the coefficients of one AdamW step.
-fp_status adam_coef(const fp_adamw_hparams* hp, AdamCoef* c);
 fp_status shard_step_run(const fp_step_args* args, void* stream, bool give_up_test);
 
 // Launchers (return the HIP error of the launch).

@@ -36,15 +36,15 @@ inline int64_t param_tiles(int64_t numel) { return ceil_div64(numel, kParamTile)
 // LDS that a launch of the step asks for and never touches, so that fewer of
 // its workgroups are resident in a CU: with more, HBM serves their streams
 // slower.  Measured on MI355X with bf16 gradients and copies:
-//   fp32 moments, three per CU against no limit: 4M elements 21.0 and 22.0 us,
-//     17M 78.8 and 79.9, 50M 225.6 and 233.0, 134M 618.5 and 657.9 (two: 666),
-//     but 1.6M, whose last workgroup waits for a place, 11.7 and 8.5;
+//   fp32 moments, three per CU against no limit: 2.5M elements 14.1 and 13.2
+//     us, 4M 21.0 and 20.5, 8M 38.8 and 38.8, 17M 78.8 and 79.9, 34M 155.3 and
+//     158.6, 50M 225.6 and 233.0, 134M 618.5 and 657.9 (two per CU: 666);
 //   8-bit moments, five per CU against no limit: 34M 88.0 and 86.0 us, 42M
 //     108.7 and 105.8, 46M 120.0 and 119.8, 50M 133.8 and 138.8, 134M 360.8
 //     and 376.3 -- their arithmetic wants more waves as long as the memory
-//     side keeps up, so the limit starts at kMx8CapTiles.
+//     side keeps up, so their limit starts later.
 constexpr unsigned kParamCapLds = 53504u, kMx8CapLds = 32000u;
-constexpr int64_t kParamCapTiles = 4000000 / kParamTile, kMx8CapTiles = 46000000 / kParamTile;
+constexpr int64_t kParamCapTiles = 16000000 / kParamTile, kMx8CapTiles = 46000000 / kParamTile;
 inline unsigned params_step_lds(int64_t tiles, bool mx8) {
     if (!mx8) return tiles >= kParamCapTiles ? kParamCapLds : 0u;
     return tiles >= kMx8CapTiles ? kMx8CapLds : 0u;
@@ -106,6 +106,9 @@ struct MxArgs {
     uint8_t* scales;
     int64_t n;
 };
+
+// abi.hip: checks hyperparameters and fills the coefficients of one AdamW step.
+fp_status adam_coef(const fp_adamw_hparams* hp, AdamCoef* c);
 
 // Launchers (return the HIP error of the launch); grad_dtype is FP_DTYPE_*.
 hipError_t launch_params_step(const ParamsArgs& a, int grad_dtype, bool mx8, hipStream_t s);
