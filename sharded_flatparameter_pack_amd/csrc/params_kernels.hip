@@ -161,15 +161,18 @@ __device__ __forceinline__ uint32_t block_max(uint32_t x) {
 }
 
 // Scale byte of the block that the lane's four values belong to.  All lanes
-// of the block take part; elements that do not exist are 0.
+// of the block take part; elements that do not exist are 0.  kRoot: the
+// values have no sign (a NaN may have one, which leaves it above all others).
+template <bool kRoot>
 __device__ __forceinline__ uint32_t mx_byte(const float f[4]) {
     uint32_t top = 0;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-        const uint32_t a = __float_as_uint(f[e]) & 0x7FFFFFFFu;
+        const uint32_t a = kRoot ? __float_as_uint(f[e]) : __float_as_uint(f[e]) & 0x7FFFFFFFu;
         top = top > a ? top : a;
     }
-    const uint32_t field = (block_max(top) + 0x00080000u) >> 23;
+    top = block_max(top);
+    const uint32_t field = ((kRoot && top > 0x7FFFFFFFu ? 0x7FFFFFFFu : top) + 0x00080000u) >> 23;
     return field >= 255u ? 255u : field < 7u ? 0u : field - 7u;
 }
 
@@ -378,8 +381,8 @@ __device__ __forceinline__ void step_tile(const ParamsArgs& a, const TileAt& t, 
 #pragma unroll
             for (int k = 0; k < 4; ++k)
                 if (!kFull && k >= have[u]) m[u][k] = v[u][k] = 0.0f;
-            bm[u] = mx_byte(m[u]);
-            bv[u] = mx_byte(v[u]);
+            bm[u] = mx_byte<false>(m[u]);
+            bv[u] = mx_byte<true>(v[u]);
             uint32_t dm[4], dv[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
@@ -571,7 +574,7 @@ __global__ __launch_bounds__(kThreads) void mx8_quantize_kernel(const MxArgs a) 
 #pragma unroll
             for (int k = 0; k < 4; ++k) f[u][k] = root_f32((double)f[u][k] + kTiny);
         }
-        const uint32_t byte = mx_byte(f[u]);
+        const uint32_t byte = mx_byte<kRoot>(f[u]);
         if (kRoot) mx_raise(f[u], byte);
         const uint32_t w = mx_encode(f[u], byte);
         if (e + 4 <= a.n) {
