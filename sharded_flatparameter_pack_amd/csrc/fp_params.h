@@ -23,7 +23,7 @@ struct ParamRec {
 };
 static_assert(sizeof(ParamRec) == 64, "one 64-byte record per tensor");
 
-// Tile `index` of tensor `tensor`: what one wave works on.
+// Tile `index` of tensor `tensor`.
 struct ParamTile {
     int32_t tensor;
     int32_t index;
@@ -33,22 +33,23 @@ struct ParamTile {
 constexpr int kParamQuads = 2;
 constexpr int64_t kParamTile = 256 * kParamQuads;
 inline int64_t param_tiles(int64_t numel) { return ceil_div64(numel, kParamTile); }
-// LDS that a launch of the step asks for and never touches, so that fewer of
-// its workgroups are resident in a CU: with more, HBM serves their streams
-// slower.  Measured on MI355X with bf16 gradients and copies:
-//   fp32 moments, three per CU against no limit: 2.5M elements 14.1 and 13.2
-//     us, 4M 21.0 and 20.5, 8M 38.8 and 38.8, 17M 78.8 and 79.9, 34M 155.3 and
-//     158.6, 50M 225.6 and 233.0, 134M 618.5 and 657.9 (two per CU: 666);
-//   8-bit moments, five per CU against no limit: 34M 88.0 and 86.0 us, 42M
-//     108.7 and 105.8, 46M 120.0 and 119.8, 50M 133.8 and 138.8, 134M 360.8
-//     and 376.3 -- their arithmetic wants more waves as long as the memory
-//     side keeps up, so their limit starts later.
-constexpr unsigned kParamCapLds = 53504u, kMx8CapLds = 32000u;
-constexpr int64_t kParamCapTiles = 16000000 / kParamTile, kMx8CapTiles = 46000000 / kParamTile;
-inline unsigned params_step_lds(int64_t tiles, bool mx8) {
-    if (!mx8) return tiles >= kParamCapTiles ? kParamCapLds : 0u;
-    return tiles >= kMx8CapTiles ? kMx8CapLds : 0u;
-}
+// How many of the step's streams are open at a time decides how fast HBM
+// serves them: too many, and it slows.  Measured on MI355X with bf16
+// gradients and copies, medians in us:
+// fp32 moments: a wave takes half a tile (one quad per lane; two measured
+//   652 against 616 at 134M elements), and from kParamCapElems on a launch asks
+//   for LDS that it never touches, so that three workgroups are resident in a
+//   CU.  With that and without: 2M 11.6 and 11.1, 4M 20.6 and 20.8, 17M 77 and
+//   79, 50M 224 and 231, 134M 593 and 622, 226M 1004 (6.3 TB/s) and 1058.
+constexpr unsigned kParamCapLds = 53504u;
+constexpr int64_t kParamCapElems = 4000000;
+// 8-bit moments: arithmetic is nearly half of the kernel's time and wants all
+//   the waves there are.  A wave takes a tile, or from kMx8HalfElems on, where
+//   nothing stays in a cache from step to step, half of one.  Half and whole:
+//   4M 14.0 and 13.4, 17M 46.6 and 44.5, 34M 88.5 and 83.4, 50M 132 and 138,
+//   134M 350 and 371, 226M 594 (6.15 TB/s) and 650.
+constexpr int64_t kMx8HalfElems = 46000000;
+
 // Workgroups of the norm, a partial sum each: at most as many as are resident
 // together (8 per CU).
 constexpr int64_t kNormGroups = 2048;
@@ -111,7 +112,7 @@ struct MxArgs {
 fp_status adam_coef(const fp_adamw_hparams* hp, AdamCoef* c);
 
 // Launchers (return the HIP error of the launch); grad_dtype is FP_DTYPE_*.
-hipError_t launch_params_step(const ParamsArgs& a, int grad_dtype, bool mx8, hipStream_t s);
+hipError_t launch_params_step(const ParamsArgs& a, int64_t partition, int grad_dtype, bool mx8, hipStream_t s);
 hipError_t launch_params_norm(const ParamsNormArgs& a, int grad_dtype, hipStream_t s);
 hipError_t launch_mx8(const MxArgs& a, bool quantize, bool root, hipStream_t s);
 

@@ -168,7 +168,7 @@ fp_status create(int32_t n, const int64_t* numel, const int32_t* group, int32_t 
         }
         partition += ceil_div64(numel[i], kMxBlock) * kMxBlock;
         tiles += param_tiles(numel[i]);
-        if (ceil_div64(tiles, kWaves) > kMaxGroups)
+        if (ceil_div64(tiles * kParamQuads, kWaves) > kMaxGroups)  // one wave per quad of a lane at most
             return bad(FP_ERR_RANGE, "the tensors need more workgroups than one launch holds (%lld)", (long long)kMaxGroups);
     }
     std::sort(written.begin(), written.end());
@@ -320,7 +320,7 @@ uint32_t key_of(uint64_t seed) {
 fp_status run_step(const fp_params* p, const ParamsArgs& a, bool mx8, void* stream) {
     fp_status st = check_device(p);
     if (st != FP_OK || p->tiles == 0) return st;
-    hipError_t e = launch_params_step(a, p->grad_dtype, mx8, static_cast<hipStream_t>(stream));
+    hipError_t e = launch_params_step(a, p->partition, p->grad_dtype, mx8, static_cast<hipStream_t>(stream));
     return e == hipSuccess ? FP_OK : device_error(e, "params step launch");
 }
 

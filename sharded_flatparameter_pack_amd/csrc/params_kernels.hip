@@ -2,12 +2,13 @@
 // separate tensors: AdamW with fp32 or MXFP8 moments, the gradients' sum of
 // squares with the overflow check, and the MXFP8 conversions.
 //
-// A workgroup takes one tile of one tensor, found through the tile table
-// (tensor, tile), so that tensors of any size share one launch.  Inside a
-// tile the quad layout of the step kernels holds: lane t has elements
-// [4 t, 4 t + 4), every access of a wave covers one contiguous span.  The
-// tensors may start anywhere on their element size, so their accesses are
-// the unaligned ones (one instruction, as the aligned).
+// A wave works on a tile of one tensor (the step also on half of one), found
+// through the tile table (tensor, tile), so that tensors of any size share
+// one launch and a small one costs one wave.  Inside a tile the quad layout
+// of the step kernels holds: lane t has elements [4 t, 4 t + 4), every access
+// of a wave covers one contiguous span.  The tensors may start anywhere on
+// their element size, so their accesses are the unaligned ones (one
+// instruction, as the aligned).
 //
 // MXFP8: 32 consecutive elements, 8 lanes, share the scale 2^(b - 127), one
 // byte b (e8m0; 255 is NaN); an element is an e4m3 code times the scale.
@@ -15,9 +16,7 @@
 // e4m3's four significant bits, b = max(0, f - 7): the largest value lands
 // in [124, 248], so rounding up never leaves e4m3's range (448).  A block
 // with a value that is not finite (f >= 255) gets b = 255: it reads as NaN.
-// The code: |x| 2^(7 - b) as fp32 bits has e4m3's exponent field (bias 7)
-// at bits 23..26 and its three mantissa bits below, fp32's gradual
-// underflow being e4m3's; rounding is an integer add and a shift by 20.
+// The hardware's scaled conversions give and take codes under such a scale.
 //
 // Compiled with -ffp-contract=off: every operation is one IEEE
 // round-to-nearest-even operation, in the order written.
@@ -253,17 +252,12 @@ __device__ __forceinline__ void adamw_root_elem(const AdamCoef& c, const WeightC
 
 }  // namespace
 
-// Where a tile is.
+// What a wave works on.
 struct TileAt {
     ParamRec rec;
     const void* grad;
     int64_t e0;   // its first element
 };
-
-__device__ __forceinline__ TileAt find_tile(const ParamsArgs& a, int64_t i) {
-    const ParamTile tile = a.tiles[i];
-    return {a.recs[tile.tensor], a.grads[tile.tensor], (int64_t)tile.index * kParamTile};
-}
 
 // The first `have` elements of a quad (kFull: all four).
 template <bool kFull>
@@ -287,19 +281,19 @@ __device__ __forceinline__ void st_codes(uint8_t* p, uint32_t codes, int have) {
         if (k < have) gptr<uint8_t>((void*)p)[k] = (uint8_t)(codes >> (8 * k));
 }
 
-// What a lane reads of a tile: kParamQuads quads, 64 quads apart.
-template <int kGrad, bool kMx8>
+// What a lane reads: kU quads, 64 quads apart.
+template <int kGrad, bool kMx8, int kU>
 struct TileRaw {
-    GradQuad<kGrad> g[kParamQuads];
-    uint4 th[kParamQuads];
-    uint4 m[kParamQuads], v[kParamQuads];
+    GradQuad<kGrad> g[kU];
+    uint4 th[kU];
+    uint4 m[kU], v[kU];
 };
-template <int kGrad>
-struct TileRaw<kGrad, true> {
-    GradQuad<kGrad> g[kParamQuads];
-    uint4 th[kParamQuads];
-    uint32_t m[kParamQuads], v[kParamQuads];    // four codes
-    uint32_t bm[kParamQuads], bv[kParamQuads];  // the scale byte of their block
+template <int kGrad, int kU>
+struct TileRaw<kGrad, true, kU> {
+    GradQuad<kGrad> g[kU];
+    uint4 th[kU];
+    uint32_t m[kU], v[kU];    // four codes
+    uint32_t bm[kU], bv[kU];  // the scale byte of their block
 };
 
 // Elements of the lane's quad u that the tensor has.
@@ -313,11 +307,11 @@ __device__ __forceinline__ int quad_have(const TileAt& t, int u) {
 // elements early), and moments with the tensor's last quad (the partition has
 // room up to the next multiple of 32): lanes all load, and none waits here.
 // Element by element, tensors of 4001 elements took a quarter longer.
-template <int kGrad, bool kMx8, bool kFull>
-__device__ __forceinline__ void load_tile(const ParamsArgs& a, const TileAt& t, TileRaw<kGrad, kMx8>& r) {
+template <int kGrad, bool kMx8, int kU, bool kFull>
+__device__ __forceinline__ void load_tile(const ParamsArgs& a, const TileAt& t, TileRaw<kGrad, kMx8, kU>& r) {
     const int64_t last = t.rec.numel - 4, last_quad = (t.rec.numel - 1) & ~(int64_t)3;
 #pragma unroll
-    for (int u = 0; u < kParamQuads; ++u) {
+    for (int u = 0; u < kU; ++u) {
         const int64_t e = t.e0 + 256 * u + 4 * (threadIdx.x & 63);
         const int64_t p = t.rec.offset + (kFull || e < last_quad ? e : last_quad);
         if (kFull || last >= 0) {
@@ -352,9 +346,9 @@ __device__ __forceinline__ int quad_drop(const TileAt& t, int u) {
 // The tile's update, then its stores, one stream after the other; on a skip
 // only the copy of the unchanged weights is stored.  Partition elements past
 // the tensor are left as they are.
-template <int kGrad, bool kMx8, bool kFull>
-__device__ __forceinline__ void step_tile(const ParamsArgs& a, const TileAt& t, const TileRaw<kGrad, kMx8>& r, bool skip) {
-    constexpr int kU = kParamQuads;
+template <int kGrad, bool kMx8, int kU, bool kFull>
+__device__ __forceinline__ void step_tile(const ParamsArgs& a, const TileAt& t, const TileRaw<kGrad, kMx8, kU>& r,
+                                          bool skip) {
     const AdamCoef c = coef_for(a.c[t.rec.group], a.g_coef);
     const int64_t e0 = t.e0 + 4 * (threadIdx.x & 63), p0 = t.rec.offset + e0;
     int have[kU];
@@ -437,20 +431,24 @@ __device__ __forceinline__ void step_tile(const ParamsArgs& a, const TileAt& t, 
     }
 }
 
-// The step, a tile per wave.  The loads do not wait for the overflow flag, as
-// in the flat step.
-template <int kGrad, bool kMx8>
+// The step: a wave has a tile, or with kU = 1 half of one.  The loads do not
+// wait for the overflow flag, as in the flat step.
+template <int kGrad, bool kMx8, int kU>
 __global__ __launch_bounds__(kThreads) void params_step_kernel(const ParamsArgs a) {
+    constexpr int kPer = kParamQuads / kU;   // waves per tile
     const int64_t i = (int64_t)blockIdx.x * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    if (i >= a.n_tiles) return;
-    const TileAt t = find_tile(a, i);
-    const bool full = t.rec.numel - t.e0 >= kParamTile;
-    TileRaw<kGrad, kMx8> r;
-    if (full) load_tile<kGrad, kMx8, true>(a, t, r);
-    else load_tile<kGrad, kMx8, false>(a, t, r);
+    if (i >= a.n_tiles * kPer) return;
+    const ParamTile tile = a.tiles[i / kPer];
+    const TileAt t = {a.recs[tile.tensor], a.grads[tile.tensor],
+                      (int64_t)tile.index * kParamTile + (i % kPer) * (256 * kU)};
+    const int64_t left = t.rec.numel - t.e0;
+    if (left <= 0) return;
+    TileRaw<kGrad, kMx8, kU> r;
+    if (left >= 256 * kU) load_tile<kGrad, kMx8, kU, true>(a, t, r);
+    else load_tile<kGrad, kMx8, kU, false>(a, t, r);
     const bool skip = a.found_inf != nullptr && *a.found_inf != 0;
-    if (full) step_tile<kGrad, kMx8, true>(a, t, r, skip);
-    else step_tile<kGrad, kMx8, false>(a, t, r, skip);
+    if (left >= 256 * kU) step_tile<kGrad, kMx8, kU, true>(a, t, r, skip);
+    else step_tile<kGrad, kMx8, kU, false>(a, t, r, skip);
 }
 
 // Squares of the 8 elements of a 16-byte word (4 of fp32) added to sq[0..3].
@@ -626,21 +624,20 @@ __global__ __launch_bounds__(kThreads) void mx8_dequantize_kernel(const MxArgs a
 
 // ---------------------------------------------------------------- launchers
 
-hipError_t launch_params_step(const ParamsArgs& a, int grad_dtype, bool mx8, hipStream_t s) {
-    const unsigned grid = (unsigned)ceil_div64(a.n_tiles, kWaves);
-    const unsigned lds = params_step_lds(a.n_tiles, mx8);
+template <int kGrad>
+void launch_step_of(const ParamsArgs& a, int64_t partition, bool mx8, hipStream_t s) {
+    const unsigned whole = (unsigned)ceil_div64(a.n_tiles, kWaves), half = (unsigned)ceil_div64(2 * a.n_tiles, kWaves);
+    static_assert(kParamQuads == 2, "half a tile is one quad per lane");
+    if (!mx8) params_step_kernel<kGrad, false, 1><<<half, kThreads, partition < kParamCapElems ? 0 : kParamCapLds, s>>>(a);
+    else if (partition < kMx8HalfElems) params_step_kernel<kGrad, true, 2><<<whole, kThreads, 0, s>>>(a);
+    else params_step_kernel<kGrad, true, 1><<<half, kThreads, 0, s>>>(a);
+}
+
+hipError_t launch_params_step(const ParamsArgs& a, int64_t partition, int grad_dtype, bool mx8, hipStream_t s) {
     switch (grad_dtype) {
-        case FP_DTYPE_F32:
-            if (mx8) params_step_kernel<FP_DTYPE_F32, true><<<grid, kThreads, lds, s>>>(a);
-            else params_step_kernel<FP_DTYPE_F32, false><<<grid, kThreads, lds, s>>>(a);
-            break;
-        case FP_DTYPE_BF16:
-            if (mx8) params_step_kernel<FP_DTYPE_BF16, true><<<grid, kThreads, lds, s>>>(a);
-            else params_step_kernel<FP_DTYPE_BF16, false><<<grid, kThreads, lds, s>>>(a);
-            break;
-        default:
-            if (mx8) params_step_kernel<FP_DTYPE_F16, true><<<grid, kThreads, lds, s>>>(a);
-            else params_step_kernel<FP_DTYPE_F16, false><<<grid, kThreads, lds, s>>>(a);
+        case FP_DTYPE_F32: launch_step_of<FP_DTYPE_F32>(a, partition, mx8, s); break;
+        case FP_DTYPE_BF16: launch_step_of<FP_DTYPE_BF16>(a, partition, mx8, s); break;
+        default: launch_step_of<FP_DTYPE_F16>(a, partition, mx8, s);
     }
     return hipGetLastError();
 }
