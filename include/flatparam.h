@@ -733,18 +733,18 @@ fp_status fp_params_grad_norm(const fp_params* params, int32_t* found_inf, doubl
 fp_status fp_params_adamw(fp_params* params, int32_t n_groups, const fp_adamw_hparams* hp, float* exp_avg,
                           float* exp_avg_sq, const int32_t* found_inf, const double* grad_coef, void* stream);
 
-/* The same with moments in 8 bits (6.06 instead of 12 bytes of weights and
- * moments per element): MXFP8, e4m3 codes and one scale byte b for every 32
- * consecutive partition elements, standing for code * 2^(b - 127); b = 255
- * stands for NaN.  exp_avg holds the first moment m, `root` the square root r
- * of the second (the root keeps v's range in 8 bits).  Per element, in fp64
- * from the decoded moments and each rounded once to fp32,
+/* The same with moments in 8 bits: MXFP8, e4m3 codes and one scale byte b for
+ * every 32 consecutive partition elements, standing for code * 2^(b - 127);
+ * b = 255 stands for NaN.  exp_avg holds the first moment m, `root` the square
+ * root r of the second (the root keeps v's range in 8 bits).  Per element, in
+ * fp64 from the decoded moments and each rounded once to fp32,
  *   m' = beta1 m + (1 - beta1) g,  r' = sqrt(beta2 r^2 + (1 - beta2) g^2);
  * the weights change by what fp_adamw_shard's formula gives for m' and r',
- * evaluated in fp32 to 2^-20 of the change and added once (an eps below
- * 2^-126 counts as 2^-126: an element whose m' and r' are 0 only decays); then
- * m' and r' are rounded stochastically to e4m3.  With x in a block whose
- * largest magnitude is X (elements past a tensor's end do not count):
+ * evaluated in fp32 to 2^-20 of the change (r' up to 2^125) and added once
+ * (an eps below 2^-126 counts as 2^-126: an element whose m' and r' are 0 only
+ * decays); then m' and r' are rounded stochastically to e4m3.  With x in a
+ * block whose largest magnitude is X (elements past a tensor's end do not
+ * count):
  *   f = (fp32 bits of X + 2^19) >> 23;  b = f >= 255 ? 255 : max(0, f - 7);
  *   y = |x| 2^(127 - b) < 248;  q = e4m3's step at y, 2^(max(floor(log2 y), -6) - 3);
  *   the code is that of q * floor(y / q + d / 2^16),
@@ -759,9 +759,11 @@ fp_status fp_params_adamw(fp_params* params, int32_t n_groups, const fp_adamw_hp
  *   key: z = seed * 0x9E3779B97F4A7C15;  z ^= z >> 32;
  *   z *= 0xD6E8FEB86659FD93;  key = low half of z ^ (z >> 32)  (modulo 2^64)
  * so a step is reproducible from its seed; give every step another one (its
- * step count will do).  exp_avg, root: device uint8[partition], 16-byte
+ * step count will do; a call captured into a graph repeats its seed, as it
+ * does its hyperparameters).  exp_avg, root: device uint8[partition], 16-byte
  * aligned; exp_avg_scale, root_scale: device uint8[partition / 32].  All-zero
- * bytes are zero moments. */
+ * bytes are zero moments.  (Weights, moments and scales: 6.06 bytes per
+ * element, the k of fp_state_bytes.) */
 fp_status fp_params_adamw8(fp_params* params, int32_t n_groups, const fp_adamw_hparams* hp, uint8_t* exp_avg,
                            uint8_t* exp_avg_scale, uint8_t* root, uint8_t* root_scale, uint64_t seed,
                            const int32_t* found_inf, const double* grad_coef, void* stream);

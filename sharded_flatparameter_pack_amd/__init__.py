@@ -771,9 +771,11 @@ def _table(tensors, dtype, device, sizes, name):
     return ptrs
 
 
-def _dtype_id(dtype, name):
+def _dtype_id(dtype, name, f32=True):
     torch = _torch()
-    ids = {torch.float32: _lib.FP_DTYPE_F32, torch.bfloat16: _lib.FP_DTYPE_BF16, torch.float16: _lib.FP_DTYPE_F16}
+    ids = {torch.float16: _lib.FP_DTYPE_F16, **{d: _lib.FP_DTYPE_BF16 for d in _bf16_dtypes()}}
+    if f32:
+        ids[torch.float32] = _lib.FP_DTYPE_F32
     if dtype not in ids:
         raise TypeError(f"{name} have dtype {dtype}, expected one of {tuple(ids)}")
     return ids[dtype]
@@ -796,10 +798,11 @@ class Params:
     of them (fp_params_*): a model's parameters, or the views of a
     Shard0Plan's buffers.
 
-    grads: one gradient per tensor, all fp32, bf16 or fp16.  master: their
-    fp32 weights (None: a plan that only takes the norm).  copies: bf16 or
-    fp16 tensors that receive the weights, or None.  groups: a group number
-    per tensor (None: all 0); a step takes hyperparameters per group.
+    grads: one gradient per tensor, all fp32, bf16 (or its bits in 16-bit
+    integers) or fp16.  master: their fp32 weights (None: a plan that only
+    takes the norm).  copies: bf16 or fp16 tensors that receive the weights,
+    or None.  groups: a group number per tensor (None: all 0); a step takes
+    hyperparameters per group.
     Tensors are contiguous, at any element of a buffer.  The moments sit in a
     partition of `partition` elements, tensor i's from `offsets[i]` (a
     multiple of 32) on.  The tensors must stay alive and in place for the
@@ -824,7 +827,7 @@ class Params:
         if copies is not None:
             copies = list(copies)
             ctab = _table(copies, copies[0].dtype if copies else None, device, self.sizes, "copies")
-            cid = _dtype_id(copies[0].dtype, "copies")
+            cid = _dtype_id(copies[0].dtype, "copies", f32=False)
         self.groups = [0] * n if groups is None else [int(k) for k in groups]
         if len(self.groups) != n:
             raise ValueError(f"groups: {len(self.groups)} numbers, expected {n}")
@@ -907,7 +910,7 @@ class Params:
              found_inf=None, grad_coef=None):
         """AdamW on every tensor.  moments: (exp_avg, exp_avg_sq) in fp32 or
         (exp_avg, exp_avg_scale, root, root_scale) in MXFP8, which needs a seed
-        of its own for every step.  lr, beta1, beta2, eps, weight_decay: a
+        of its own for every step (a captured call repeats its seed).  lr, beta1, beta2, eps, weight_decay: a
         number, or one per group (groups without a tensor here included)."""
         self.stepper(moments, lr=lr, beta1=beta1, beta2=beta2, eps=eps, weight_decay=weight_decay,
                      found_inf=found_inf, grad_coef=grad_coef)(step, seed=seed)

@@ -350,6 +350,20 @@ def test_shared_gradients(fp):
     assert torch.equal(w[0], w[1]) and torch.equal(w[0][400:], w[2][:200]) and not torch.equal(w[0], w[2])
 
 
+def test_bf16_as_bits(fp):
+    """bf16 gradients and copies in 16-bit integer tensors, as elsewhere here."""
+    say("bits")
+    g = (torch.randn(1000, device=dev()) * 1e-3).bfloat16()
+    w = [torch.ones(1000, device=dev()) for _ in range(2)]
+    c = [torch.zeros(1000, dtype=d, device=dev()) for d in (torch.bfloat16, torch.int16)]
+    for x, k in ((g, 0), (g.view(torch.int16), 1)):
+        plan = fp.Params([x], [w[k]], [c[k]])
+        plan.step(plan.new_moments(8), step=1, seed=1, **HPS[0])
+    assert torch.equal(w[0], w[1]) and torch.equal(c[0].view(torch.int16), c[1]) and not torch.equal(w[0], torch.ones_like(w[0]))
+    with pytest.raises(TypeError):
+        fp.Params([g], [w[0]], [w[1]])
+
+
 def test_new_gradients(fp):
     say("set_grads")
     for bits in (32, 8):
