@@ -683,6 +683,58 @@ def test_together_on_the_dim0_layout(fp):
         assert torch.equal(fp.mx8_dequantize(c, s, root=root), x)
 
 
+@pytest.mark.parametrize("bits", [32, 8])
+def test_together_on_a_flat_shard(fp, bits):
+    """The flat step with parameter groups and 8-bit moments: a rank's fragments
+    of a FlatParameter, reduced, clipped, stepped as tensors, gathered."""
+    say("flat shard", bits)
+    shapes, world, rank = [(33, 5), (33,), (7, 70), (3,), (64, 9), (10,)], 4, 2
+    plan = fp.Plan(shapes, world)
+    S = plan.shard
+    gen = torch.Generator().manual_seed(8)
+    rows = (torch.randn(world, S, generator=gen) * 1e-3).bfloat16().to(dev())
+    master = plan.pack([torch.randn(s, generator=gen).to(dev()) * 0.02 for s in shapes])[rank * S:(rank + 1) * S].clone()
+    others = [None if q == rank else torch.randn(S, generator=gen).bfloat16().to(dev()) for q in range(world)]
+    acc, full = torch.zeros(S, device=dev()), torch.zeros(world * S, dtype=torch.bfloat16, device=dev())
+    own = full[rank * S:(rank + 1) * S]
+    found = torch.zeros(1, dtype=torch.int32, device=dev())
+    sq, coef = (torch.zeros(1, dtype=torch.float64, device=dev()) for _ in range(2))
+    ws = fp.new_workspace(dev(), S)
+    parts = [plan.views(b, rank) for b in (acc, master, own)]
+    assert any(v.numel() == 0 for v in parts[0]) and sum(v.numel() for v in parts[0]) <= S
+    params = fp.Params(*parts, groups=[int(len(s) < 2) for s in shapes])
+    mom = params.new_moments(bits)
+    step = params.stepper(mom, found_inf=found, grad_coef=coef, **columns(HPS))
+    state = [(np.zeros(n), np.zeros(n)) for n in params.sizes]
+    for t in (1, 2, 3):
+        w0 = master.cpu().numpy()
+        fp.reduce_shard(rows * t, acc, scale=1 / world, found_inf=found, sq_norm=sq, workspace=ws)
+        fp.grad_coef(coef, sq_norm=sq, max_norm=0.01)
+        step(t, **({"seed": t} if bits == 8 else {}))
+        fp.unshard(others, full)
+        torch.cuda.synchronize()
+        for i, (d, n) in enumerate(zip(plan.view_descriptors(rank), params.sizes)):
+            if n == 0:
+                continue
+            f, o = slice(d["buf_offset"], d["buf_offset"] + n), params.offsets[i]
+            hp = HPS[params.groups[i]]
+            th, m, v, terms, change = ref.adamw(acc[f].cpu().numpy(), w0[f], *state[i], hp, t, float(coef))
+            ref.near(master[f].cpu().numpy(), th, terms, f"step {t} tensor {i}", change if bits == 8 else 0.0)
+            raw = [x.view(torch.uint8).cpu().numpy() if bits == 8 else x.cpu().numpy() for x in mom]
+            if bits == 8:
+                b = slice(o // 32, o // 32 + -(-n // 32))
+                dm, dr = ref.dither(np.arange(o, o + n), t)
+                ref.check_mx8(raw[0][o:o + n], raw[1][b], m, dm, what=f"step {t} tensor {i}")
+                ref.check_mx8(raw[2][o:o + n], raw[3][b], np.sqrt(v), dr, root=True, what=f"step {t} tensor {i}")
+                state[i] = ref.decode(raw[0][o:o + n], raw[1][b]), ref.decode(raw[2][o:o + n], raw[3][b]) ** 2
+            else:
+                state[i] = raw[0][o:o + n], raw[1][o:o + n]
+                ref.near(state[i][0], m, np.abs(m) + 1e-2, f"step {t} tensor {i}")
+                ref.near(state[i][1], v, None, f"step {t} tensor {i}")
+            assert torch.equal(own[f], master[f].bfloat16())
+        assert all(torch.equal(full[q * S:(q + 1) * S], x) for q, x in enumerate(others) if x is not None)
+
+
 def test_past_32_bit_offsets(fp):
     """A tensor of more than 2^32 elements and a small one behind it."""
     n = (1 << 32) + 5 * 1024 + 7
