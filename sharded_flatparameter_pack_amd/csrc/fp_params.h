@@ -50,11 +50,15 @@ constexpr int64_t kParamCapElems = 4000000;
 //   134M 350 and 371, 226M 594 (6.15 TB/s) and 650.
 constexpr int64_t kMx8HalfElems = 46000000;
 
-// Workgroups of the norm, a partial sum each: at most as many as are resident
-// together (8 per CU).
-constexpr int64_t kNormGroups = 2048;
+// Workgroups of the norm, a partial sum each, at most as many as are resident
+// together.  Of 512 lanes, 4 per CU: counting them in at the end takes time of
+// its own, which 256 lanes and 8 per CU (4M bf16 elements 8.1 against 7.0 us,
+// 42M 20.0 and 17.8, the 10k tensors 21.1 and 19.6) have more of, while 1024
+// and 2 start a small norm later (100k elements 5.8 against 4.9 us).
+constexpr int kNormThreads = 512, kNormWaves = kNormThreads / 64;
+constexpr int64_t kNormGroups = 1024;
 inline int64_t params_norm_groups(int64_t tiles) {
-    const int64_t g = ceil_div64(tiles, kWaves);
+    const int64_t g = ceil_div64(tiles, kNormWaves);
     return g < 1 ? 1 : g < kNormGroups ? g : kNormGroups;
 }
 // Workspace of the norm: the counts of finished workgroups, each in a line of

@@ -63,14 +63,6 @@ __device__ __forceinline__ GradQuad<kGrad> ld_grad(const void* g, int64_t e) {
     return q;
 }
 
-// One gradient element.
-template <int kGrad>
-__device__ __forceinline__ float ld_grad1(const void* g, int64_t e) {
-    if constexpr (kGrad == FP_DTYPE_F32) return gptr<float>(g)[e];
-    const uint32_t w = gptr<uint16_t>(g)[e];
-    return kGrad == FP_DTYPE_BF16 ? bf16_lo(w) : f16_lo(w);
-}
-
 // The first n < 4 elements of a tensor that has no more, as a quad.
 template <int kGrad>
 __device__ __forceinline__ GradQuad<kGrad> ld_grad_few(const void* g, int n) {
@@ -469,6 +461,67 @@ __device__ __forceinline__ void add_squares(const uint4 w, double sq[4]) {
     for (int k = 0; k < kN; ++k) sq[k & 3] = __builtin_fma((double)f[k], (double)f[k], sq[k & 3]);
 }
 
+// A tile of the norm: the elements of its tensor from it on, and where.
+struct NormTile {
+    int64_t left;
+    const char* from;
+};
+template <int kGrad>
+__device__ __forceinline__ NormTile find_norm_tile(const ParamsNormArgs& a, int64_t i) {
+    const ParamTile tile = a.tiles[i];
+    const int64_t e0 = (int64_t)tile.index * kParamTile;
+    return {a.recs[tile.tensor].numel - e0,
+            static_cast<const char*>(a.grads[tile.tensor]) + e0 * (kGrad == FP_DTYPE_F32 ? 4 : 2)};
+}
+
+// What a lane reads of it: whole words, 64 words apart, and in the tensor's
+// last tile one of the elements behind the last whole word.
+template <int kGrad>
+struct NormRaw {
+    static constexpr int kPer = kGrad == FP_DTYPE_F32 ? 4 : 8;      // elements of a word
+    static constexpr int kWords = (int)(kParamTile / (64 * kPer));
+    uint4 w[kWords];
+    uint32_t rest;
+};
+template <int kGrad>
+__device__ __forceinline__ void load_norm_tile(const NormTile& t, NormRaw<kGrad>& r) {
+    constexpr int kPer = NormRaw<kGrad>::kPer;
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int u = 0; u < NormRaw<kGrad>::kWords; ++u) {
+        r.w[u] = make_uint4(0u, 0u, 0u, 0u);
+        if ((64 * u + lane + 1) * kPer <= t.left) r.w[u] = ld16u(t.from + 16 * (64 * u + lane));
+    }
+    r.rest = 0u;
+    if (t.left < kParamTile && lane < t.left % kPer) {
+        const int64_t e = t.left - t.left % kPer + lane;
+        if constexpr (kGrad == FP_DTYPE_F32) r.rest = gptr<uint32_t>((const void*)t.from)[e];
+        else r.rest = gptr<uint16_t>((const void*)t.from)[e];
+    }
+}
+template <int kGrad>
+__device__ __forceinline__ void add_norm_tile(const NormTile& t, const NormRaw<kGrad>& r, double sq[4]) {
+#pragma unroll
+    for (int u = 0; u < NormRaw<kGrad>::kWords; ++u) add_squares<kGrad>(r.w[u], sq);
+    if (t.left < kParamTile) {
+        const float g = kGrad == FP_DTYPE_F32 ? __uint_as_float(r.rest) : kGrad == FP_DTYPE_BF16 ? bf16_lo(r.rest) : f16_lo(r.rest);
+        sq[0] = __builtin_fma((double)g, (double)g, sq[0]);
+    }
+}
+
+// Sum over the norm's workgroup in a fixed order, valid in thread 0.
+__device__ __forceinline__ double norm_group_sum(double x) {
+    __shared__ double waves[kNormWaves];
+    x = wave_sum(x);
+    __syncthreads();   // a call before may still read
+    if ((threadIdx.x & 63) == 0) waves[threadIdx.x >> 6] = x;
+    __syncthreads();
+    double r = 0.0;
+    if (threadIdx.x == 0)
+        for (int w = 0; w < kNormWaves; ++w) r += waves[w];
+    return r;
+}
+
 // Counts workgroup b of n in; true for the last one, which also leaves the
 // counters at 0 for the next call.  Two levels on lines of their own, as in
 // the step's grid barrier: one counter for all took 35 ns per workgroup.
@@ -494,32 +547,18 @@ __device__ __forceinline__ bool norm_arrive(uint32_t* done, unsigned b, unsigned
 // last workgroup to finish adds the partial sums in their order, so the
 // result does not depend on who was last.
 template <int kGrad>
-__global__ __launch_bounds__(kThreads) void params_norm_kernel(const ParamsNormArgs a) {
-    constexpr int kPer = kGrad == FP_DTYPE_F32 ? 4 : 8;                      // elements of a word
-    constexpr int kWords = (int)(kParamTile / (64 * kPer));                  // words per lane and tile
-    const int lane = threadIdx.x & 63;
+__global__ __launch_bounds__(kNormThreads) void params_norm_kernel(const ParamsNormArgs a) {
     double sq[4] = {0.0, 0.0, 0.0, 0.0};
-    for (int64_t i = (int64_t)blockIdx.x * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); i < a.n_tiles;
-         i += (int64_t)gridDim.x * kWaves) {
-        const ParamTile tile = a.tiles[i];
-        const int64_t e0 = (int64_t)tile.index * kParamTile;
-        const int64_t left = a.recs[tile.tensor].numel - e0;  // elements of the tensor from the tile on
-        const char* from = static_cast<const char*>(a.grads[tile.tensor]) + e0 * (16 / kPer);
-        uint4 w[kWords];
-#pragma unroll
-        for (int u = 0; u < kWords; ++u) {
-            w[u] = make_uint4(0u, 0u, 0u, 0u);
-            if ((64 * u + lane + 1) * kPer <= left) w[u] = ld16u(from + 16 * (64 * u + lane));
-        }
-        float g = 0.0f;                                       // elements past the last whole word
-        if (left < kParamTile && lane < left % kPer) g = ld_grad1<kGrad>(from, left - left % kPer + lane);
-#pragma unroll
-        for (int u = 0; u < kWords; ++u) add_squares<kGrad>(w[u], sq);
-        sq[0] = __builtin_fma((double)g, (double)g, sq[0]);
+    for (int64_t i = (int64_t)blockIdx.x * kNormWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); i < a.n_tiles;
+         i += (int64_t)gridDim.x * kNormWaves) {
+        const NormTile t = find_norm_tile<kGrad>(a, i);
+        NormRaw<kGrad> r;
+        load_norm_tile<kGrad>(t, r);
+        add_norm_tile<kGrad>(t, r, sq);
     }
     const double mine = (sq[0] + sq[1]) + (sq[2] + sq[3]);
     flag_if_any(!__builtin_isfinite(mine), a.found_inf);
-    const double t = group_sum(mine);
+    const double t = norm_group_sum(mine);
     if (gridDim.x == 1) {
         if (threadIdx.x == 0) *a.sq_norm = t;
         return;
@@ -538,10 +577,9 @@ __global__ __launch_bounds__(kThreads) void params_norm_kernel(const ParamsNormA
     __syncthreads();
     if (!last) return;
     double s = 0.0;
-#pragma unroll 8
-    for (unsigned k = threadIdx.x; k < gridDim.x; k += kThreads)
+    for (unsigned k = threadIdx.x; k < gridDim.x; k += kNormThreads)
         s += __hip_atomic_load(&a.partials[k], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    s = group_sum(s);
+    s = norm_group_sum(s);
     if (threadIdx.x == 0) *a.sq_norm = s;
 }
 
@@ -645,9 +683,9 @@ hipError_t launch_params_step(const ParamsArgs& a, int64_t partition, int grad_d
 hipError_t launch_params_norm(const ParamsNormArgs& a, int grad_dtype, hipStream_t s) {
     const unsigned grid = (unsigned)params_norm_groups(a.n_tiles);
     switch (grad_dtype) {
-        case FP_DTYPE_F32: params_norm_kernel<FP_DTYPE_F32><<<grid, kThreads, 0, s>>>(a); break;
-        case FP_DTYPE_BF16: params_norm_kernel<FP_DTYPE_BF16><<<grid, kThreads, 0, s>>>(a); break;
-        default: params_norm_kernel<FP_DTYPE_F16><<<grid, kThreads, 0, s>>>(a);
+        case FP_DTYPE_F32: params_norm_kernel<FP_DTYPE_F32><<<grid, kNormThreads, 0, s>>>(a); break;
+        case FP_DTYPE_BF16: params_norm_kernel<FP_DTYPE_BF16><<<grid, kNormThreads, 0, s>>>(a); break;
+        default: params_norm_kernel<FP_DTYPE_F16><<<grid, kNormThreads, 0, s>>>(a);
     }
     return hipGetLastError();
 }

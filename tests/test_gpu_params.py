@@ -323,6 +323,27 @@ def test_norm(fp, sizes, grad):
         assert int(found) == 2 and float(sq) == first
 
 
+def test_norm_of_many_workgroups_again_and_again(fp):
+    """Gradients doubled from call to call, the calls back to back on one
+    workspace: doubling is exact, so every sum is four times the one before,
+    bit for bit; a partial sum of an earlier call would show."""
+    say("norm again and again")
+    sizes = [6_000_000, 3, 1_000_001, 70_000]
+    g = torch.randn(sum(sizes), device=dev()) * 1e-3
+    plan = fp.Params(g.split(sizes))
+    ws = plan.new_workspace()
+    found = torch.zeros(1, dtype=torch.int32, device=dev())
+    sq = torch.zeros(40, dtype=torch.float64, device=dev())
+    for k in range(40):
+        plan.grad_norm(sq[k:k + 1], ws, found)
+        g.mul_(2.0)
+    sq = sq.cpu().numpy()
+    want = float((g.double() * 2.0 ** -40).square().sum())
+    assert abs(sq[0] - want) <= norm_rel_tol(g.numel()) * want
+    np.testing.assert_array_equal(sq, sq[0] * 4.0 ** np.arange(40))
+    assert int(found) == 0
+
+
 def test_norm_only_plan_and_empty_tensors(fp):
     say("empty")
     g = [torch.empty(0, device=dev()), torch.empty(0, device=dev())]
