@@ -1,14 +1,15 @@
 """The optimizer step over many separate tensors on the GPU against the numpy
 reference (params_ref.py, which derives the tolerances)."""
 
-import ctypes as C
 import math
+import os
 
 import numpy as np
 import pytest
 import torch
 
 import params_ref as ref
+from conftest import ROOT
 from gpu_common import dev, norm_rel_tol, say
 
 pytestmark = pytest.mark.gpu
@@ -754,6 +755,28 @@ def test_together_on_a_flat_shard(fp, bits):
                 ref.near(state[i][1], v, None, f"step {t} tensor {i}")
             assert torch.equal(own[f], master[f].bfloat16())
         assert all(torch.equal(full[q * S:(q + 1) * S], x) for q, x in enumerate(others) if x is not None)
+
+
+def test_the_readmes_example(fp):
+    """The README's loop over separate tensors runs and moves the weights."""
+    say("README")
+    text = open(os.path.join(ROOT, "README.md")).read()
+    block = next(b for b in text.split("```python")[1:] if "fp.Params(" in b).split("```")[0]
+    weights = [torch.nn.Parameter(torch.randn(s, device=dev()) * 0.02) for s in ((33, 20), (33,), (5, 7))]
+    for p in weights:
+        p.grad = torch.randn_like(p)
+    before = [p.detach().clone() for p in weights]
+    low = [torch.zeros_like(p, dtype=torch.bfloat16) for p in weights]
+    ns = dict(torch=torch, fp=fp, dev=dev(), weights=weights, bf16_weights=low)
+    exec(block, ns)
+    torch.cuda.synchronize()
+    assert int(ns["flag"]) == 0 and 0 < float(ns["coef"]) < 1
+    for p, b, c in zip(weights, before, low):
+        assert torch.isfinite(p).all() and not torch.equal(p.detach(), b)
+        assert torch.equal(c, p.detach().bfloat16())
+        # a constant gradient: the update is against its sign, lr a step once the moments have settled
+        moved = (b - p.detach()) * p.grad.sign()
+        assert (moved > 0).float().mean() > 0.99
 
 
 def test_past_32_bit_offsets(fp):
