@@ -44,11 +44,13 @@ inline int64_t param_tiles(int64_t numel) { return ceil_div64(numel, kParamTile)
 constexpr unsigned kParamCapLds = 53504u;
 constexpr int64_t kParamCapElems = 4000000;
 // 8-bit moments: arithmetic is nearly half of the kernel's time and wants all
-//   the waves there are.  A wave takes a tile, or from kMx8HalfElems on, where
-//   nothing stays in a cache from step to step, half of one.  Half and whole:
-//   4M 14.0 and 13.4, 17M 46.6 and 44.5, 34M 88.5 and 83.4, 50M 132 and 138,
-//   134M 350 and 371, 226M 594 (6.15 TB/s) and 650.
-constexpr int64_t kMx8HalfElems = 46000000;
+//   the waves there are.  A wave takes a tile from kMx8WholeElems to
+//   kMx8HalfElems; below, where waves are few, and above, where nothing stays in
+//   a cache from step to step, half of one.  Half and whole: 1.6M elements in
+//   12 tensors 6.9 and 7.9, 2.5M 9.2 and 9.4, 4M 14.0 and 13.4, 17M 46.6 and
+//   44.5, 34M 88.5 and 83.4, 50M 132 and 138, 134M 350 and 371, 226M 594 (6.15
+//   TB/s) and 650.
+constexpr int64_t kMx8WholeElems = 3000000, kMx8HalfElems = 46000000;
 
 // Workgroups of the norm, a partial sum each, at most as many as are resident
 // together.  Of 512 lanes, 4 per CU: counting them in at the end takes time of

@@ -188,23 +188,25 @@ def test_far_magnitudes(fp, bits, sigma):
 
 
 @pytest.mark.parametrize("grad", list(GRAD))
-def test_large_plans_step_small_tensors_alike(fp, grad):
-    """A plan of 46 million elements and more splits its work otherwise: the
-    tensors in front of a large one come out bit for bit as in a small plan."""
-    say("large plan", grad)
+@pytest.mark.parametrize("room", [4_000_000, 46_000_000])
+def test_large_plans_step_small_tensors_alike(fp, room, grad):
+    """Plans split their work by their size (below 3, up to 46 million elements,
+    above): the tensors in front of a large one come out bit for bit as in a
+    small plan."""
     sizes = SIZES["edges"] + SIZES["small"] + SIZES["ragged"] + [3, 515, 256, 300]
+    say("large plan", room, grad)
     small = Case(fp, sizes, grad=grad, copy="f16", bits=8, shift=1)
     before = small.host()
     run(small, 5, seed=5)
     small.check(before, 5, 5, what="small plan")
-    n = 46_000_000 - small.plan.partition + 1
+    n = room - small.plan.partition + 1
     twin = Case(fp, sizes, grad=grad, copy="f16", bits=8, shift=1)
     big = [torch.zeros(n, dtype=t.dtype, device=dev()) for t in (twin.grad, twin.master, twin.copy)]
     big[0][-70:] = 0.5
     plan = fp.Params([*twin.grad.split(sizes), big[0]], [*twin.master.split(sizes), big[1]],
                      [*twin.copy.split(sizes), big[2]], groups=twin.groups + [0])
     P = twin.plan.partition
-    assert plan.partition >= 46_000_000 and plan.offsets[:-1] == twin.plan.offsets and plan.offsets[-1] == P
+    assert plan.partition >= room and plan.offsets[:-1] == twin.plan.offsets and plan.offsets[-1] == P
     mom = [x.view(torch.uint8) for x in plan.new_moments(8)]
     for x, y in zip(mom, twin.moments):
         x[:y.numel()] = y
