@@ -88,6 +88,17 @@ def _dev_ptr(t, dtypes, n, name):
 
 def _one_device(*objs):
     """All tensors of one call (nested lists and [N, S] tensors included) on one device."""
+    first = None
+    for o in objs:  # the common call: tensors, all on one device
+        if o is not None:
+            if isinstance(o, (list, tuple)):
+                break
+            if first is None:
+                first = o.device
+            elif o.device != first:
+                break
+    else:
+        return
     devs = set()
     todo = list(objs)
     while todo:
