@@ -577,6 +577,43 @@ def test_on_another_stream(fp):
 
 
 @pytest.mark.parametrize("bits", [32, 8])
+def test_two_at_once(fp, bits):
+    """Norm, factor and step on two streams at once, each with a plan, moments and
+    a workspace of its own: as one after the other."""
+    say("two at once", bits)
+    sizes = [700_001, 33, 4097, 250_000]
+    pair, twin = ([Case(fp, sizes, bits=bits, seed=k) for k in (1, 2)] for _ in range(2))
+    streams = [torch.cuda.Stream() for _ in pair]
+
+    def calls(c):
+        sq, coef = (torch.zeros(1, dtype=torch.float64, device=dev()) for _ in range(2))
+        found = torch.zeros(1, dtype=torch.int32, device=dev())
+        ws = c.plan.new_workspace()
+        step = c.plan.stepper(c.moments, found_inf=found, grad_coef=coef, **columns(c.hps))
+
+        def once(t):
+            c.plan.grad_norm(sq, ws, found)
+            fp.grad_coef(coef, sq_norm=sq, max_norm=0.3)
+            step(t, **({"seed": t} if bits == 8 else {}))
+        return once
+
+    both = [calls(c) for c in pair]
+    torch.cuda.synchronize()
+    for t in range(1, 21):
+        for s, f in zip(streams, both):
+            with torch.cuda.stream(s):
+                f(t)
+    torch.cuda.synchronize()
+    for c, d in zip(pair, twin):
+        f = calls(d)
+        for t in range(1, 21):
+            f(t)
+        torch.cuda.synchronize()
+        assert torch.equal(c.master, d.master) and torch.equal(c.copy, d.copy)
+        assert all(torch.equal(x, y) for x, y in zip(c.moments, d.moments))
+
+
+@pytest.mark.parametrize("bits", [32, 8])
 def test_captured(fp, bits):
     """Norm, factor and step in one graph, replayed with eager work between:
     every replay equals the eager calls from the same state, bit for bit."""
