@@ -59,19 +59,31 @@ def _stream(t):
     """The current stream of t's device, as the library takes it."""
     torch = _torch()
     device = t if isinstance(t, torch.device) else t.device
-    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # 2 us less than by way of a Stream object
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # 2 us less than through a Stream object
     if raw is not None and device.index is not None:
         return C.c_void_p(raw(device.index))
     return C.c_void_p(torch.cuda.current_stream(device).cuda_stream)
 
 
+_CURRENT = None  # (current device's index, its current stream's handle by index), set on first use
+
+
 def _on_device(device, fn, *args):
     """check(fn(*args, stream)) with `device` as the current one, on its current stream."""
-    cuda = _torch().cuda
-    if device.type != "cuda" or cuda.current_device() == device.index:
-        return check(fn(*args, _stream(device)))
-    with cuda.device(device):
-        check(fn(*args, _stream(device)))
+    global _CURRENT
+    if _CURRENT is None:
+        torch = _torch()
+        _CURRENT = (getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device),
+                    getattr(torch._C, "_cuda_getCurrentRawStream", None)
+                    or (lambda index: torch.cuda.current_stream(index).cuda_stream))
+    index = device.index
+    if _CURRENT[0]() == index:
+        status = fn(*args, _CURRENT[1](index))
+        if status:
+            check(status)
+        return
+    with _torch().cuda.device(device):
+        check(fn(*args, _CURRENT[1](index)))
 
 
 def _dev_ptr(t, dtypes, n, name):
@@ -947,6 +959,7 @@ class ParamsStep:
         self._n = n
         cols = [self._per_group(x) for x in given]
         self._hp = (_lib.fp_adamw_hparams * n)(*[_hparams(*row, 1) for row in zip(*cols)])
+        self._rows = list(self._hp)  # the array's own elements
         P = params.partition
         self._eight = len(moments) == 4
         if self._eight:
@@ -973,13 +986,17 @@ class ParamsStep:
         p = self._params
         if self._eight != (seed is not None):
             raise ValueError("8-bit moments need a seed" if self._eight else "fp32 moments take no seed")
-        for h in self._hp:
-            h.step = int(step)
+        step = int(step)
+        for h in self._rows:
+            h.step = step
         if lr is not None:
-            for h, x in zip(self._hp, self._per_group(lr)):
+            for h, x in zip(self._rows, self._per_group(lr)):
                 h.lr = x
-        more = (int(seed) & 0xFFFFFFFFFFFFFFFF,) if self._eight else ()
-        _on_device(p._device, self._fn, p._h, self._n, self._hp, *self._moments, *more, self._found, self._coef)
+        if self._eight:
+            _on_device(p._device, self._fn, p._h, self._n, self._hp, *self._moments, int(seed) & 0xFFFFFFFFFFFFFFFF,
+                       self._found, self._coef)
+        else:
+            _on_device(p._device, self._fn, p._h, self._n, self._hp, *self._moments, self._found, self._coef)
 
 
 def mx8_quantize(src, codes=None, scales=None, *, root: bool = False):
