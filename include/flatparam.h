@@ -737,12 +737,12 @@ fp_status fp_params_adamw(fp_params* params, int32_t n_groups, const fp_adamw_hp
  * every 32 consecutive partition elements, standing for code * 2^(b - 127);
  * b = 255 stands for NaN.  exp_avg holds the first moment m, `root` the square
  * root r of the second (the root keeps v's range in 8 bits).  Per element, in
- * fp64 from the decoded moments and each rounded once to fp32,
+ * fp64 from the decoded moments,
  *   m' = beta1 m + (1 - beta1) g,  r' = sqrt(beta2 r^2 + (1 - beta2) g^2);
- * the weights change by what fp_adamw_shard's formula gives for m' and r',
- * evaluated in fp32 to 2^-20 of the change (r' up to 2^125) and added once
- * (an eps below 2^-126 counts as 2^-126: an element whose m' and r' are 0 only
- * decays); then m' and r' are rounded stochastically to e4m3.  With x in a
+ * the weights change by what fp_adamw_shard's formula gives for m' and r', in
+ * fp64 too (to 2^-44 of its terms), and are rounded once (an eps below 2^-126
+ * counts as 2^-126: an element whose m' and r' are 0 only decays); then m' and
+ * r' are rounded to fp32 and from there stochastically to e4m3.  With x in a
  * block whose largest magnitude is X (elements past a tensor's end do not
  * count):
  *   f = (fp32 bits of X + 2^19) >> 23;  b = f >= 255 ? 255 : max(0, f - 7);

@@ -67,14 +67,6 @@ inline int64_t params_norm_groups(int64_t tiles) {
 // its own, then the partial sums.
 constexpr int64_t kNormHeader = 4 * kLineWords * (kSyncGroups + 1);
 
-// The coefficients of a weight's change in fp32, from AdamCoef's.
-struct WeightCoef {
-    float step_size;
-    float inv_sqrt_bias2;
-    float eps;     // at least the smallest normal number, so that no denominator is 0
-    float decay;   // lr * weight_decay
-};
-
 struct ParamsArgs {
     const ParamRec* recs;
     const void* const* grads;
@@ -89,7 +81,6 @@ struct ParamsArgs {
     uint32_t key;             // of the stochastic rounding
     int32_t copy_f16;         // the copies are fp16, else bf16
     AdamCoef c[FP_MAX_GROUPS];
-    WeightCoef w[FP_MAX_GROUPS];  // of the step with 8-bit moments
 };
 
 struct ParamsNormArgs {

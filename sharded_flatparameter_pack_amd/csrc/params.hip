@@ -293,8 +293,6 @@ fp_status step_args(const fp_params* p, int32_t n_groups, const fp_adamw_hparams
     for (int32_t g = 0; g < n_groups; ++g) {
         fp_status st = adam_coef(&hp[g], &a->c[g]);
         if (st != FP_OK) return st;
-        a->w[g] = {(float)a->c[g].step_size, (float)a->c[g].inv_sqrt_bias2,
-                   std::max((float)a->c[g].eps, 0x1p-126f), (float)(hp[g].lr * hp[g].weight_decay)};
     }
     if (!on(found_inf, 4)) return bad(FP_ERR_ALIGN, "found_inf misaligned");
     if (!on(grad_coef, 8)) return bad(FP_ERR_ALIGN, "grad_coef misaligned");
@@ -435,6 +433,7 @@ extern "C" fp_status fp_params_adamw8(fp_params* params, int32_t n_groups, const
         a.exp_avg_scale = exp_avg_scale;
         a.root_scale = root_scale;
         a.key = key_of(seed);
+        for (int32_t g = 0; g < n_groups; ++g) a.c[g].eps = std::max(a.c[g].eps, 0x1p-126);  // no denominator is 0
         return run_step(params, a, true, stream);
     });
 }

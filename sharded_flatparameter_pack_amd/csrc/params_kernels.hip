@@ -216,30 +216,35 @@ __device__ __forceinline__ uint32_t dither(uint32_t e, uint32_t key) {
 
 // ---------------------------------------------------------------- AdamW
 
-// sqrt(v) rounded to fp32, from the hardware's estimate of 1 / sqrt (accurate
-// to 2^-24) with one Newton step, to 2^-47.  kTiny added to v keeps a zero out
-// of the estimate's pole; beside any other v here it is lost.
+// sqrt(v) from the hardware's estimate of 1 / sqrt (accurate to 2^-23) with one
+// Newton step, to 1.5 * 2^-46.  kTiny added to v keeps a zero out of the
+// estimate's pole; beside any other v here it is lost.
 constexpr double kTiny = 1e-290;
-__device__ __forceinline__ float root_f32(double v) {
+__device__ __forceinline__ double root_f64(double v) {
     const double y = __builtin_amdgcn_rsq(v);
     const double s = v * y;
-    return (float)__builtin_fma(0.5 * y, __builtin_fma(-s, s, v), s);
+    return __builtin_fma(0.5 * y, __builtin_fma(-s, s, v), s);
 }
 
-// adamw_elem with the second moment given and kept as its root.  The moments
-// are what the 8-bit codes are rounded from, so they are evaluated in fp64
-// and each rounded once to fp32; the weight's change, at most a few roundings
-// of 2^-24 of itself off, is evaluated in fp32 from them and added once.
-// Written for few instructions, which with 8-bit moments bound the kernel as
-// much as the memory does.
-__device__ __forceinline__ void adamw_root_elem(const AdamCoef& c, const WeightCoef& w, float g, float& th, float& m,
-                                                float& r) {
+// adamw_elem with the second moment given and kept as its root: all in fp64,
+// the weight and the two moments, which the 8-bit codes are rounded from, each
+// rounded once to fp32.  The quotient is the hardware's reciprocal (accurate to
+// 2^-23) with one Newton step, to 2^-46; with the root's error the weight's
+// change is within 2^-44 of its terms before the weight is rounded.  The
+// denominator is at least 2^-126 (eps) and below 2^160, far inside fp64.  The
+// change in fp32 is faster (226.5M elements 594 against 629 us), but off by up
+// to 2^-20 of itself, which shows in weights near zero, and its reciprocal is
+// lost above 2^126, which a root of 2^121 reaches at the first step.
+__device__ __forceinline__ void adamw_root_elem(const AdamCoef& c, float g, float& th, float& m, float& r) {
     const double gd = (double)g, rd = (double)r;
-    m = (float)__builtin_fma(c.one_m_beta1, gd, c.beta1 * (double)m);
-    r = root_f32(__builtin_fma(c.one_m_beta2 * gd, gd, __builtin_fma(c.beta2, rd * rd, kTiny)));
-    const float denom = __builtin_fmaf(r, w.inv_sqrt_bias2, w.eps);
-    const float change = __builtin_fmaf(m * __builtin_amdgcn_rcpf(denom), w.step_size, w.decay * th);
-    th = th - change;
+    const double md = __builtin_fma(c.one_m_beta1, gd, c.beta1 * (double)m);
+    const double root = root_f64(__builtin_fma(c.one_m_beta2 * gd, gd, __builtin_fma(c.beta2, rd * rd, kTiny)));
+    const double denom = __builtin_fma(root, c.inv_sqrt_bias2, c.eps);
+    double y = __builtin_amdgcn_rcp(denom);
+    y = __builtin_fma(__builtin_fma(-denom, y, 1.0), y, y);
+    th = (float)__builtin_fma(-c.step_size * md, y, c.decay * (double)th);
+    m = (float)md;
+    r = (float)root;
 }
 
 }  // namespace
@@ -363,7 +368,7 @@ __device__ __forceinline__ void step_tile(const ParamsArgs& a, const TileAt& t, 
             mx_decode(r.m[u], r.bm[u], m[u]);
             mx_decode(r.v[u], r.bv[u], v[u]);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) adamw_root_elem(c, a.w[t.rec.group], g[k], th[u][k], m[u][k], v[u][k]);
+            for (int k = 0; k < 4; ++k) adamw_root_elem(c, g[k], th[u][k], m[u][k], v[u][k]);
 #pragma unroll
             for (int k = 0; k < 4; ++k)
                 if (!kFull && k >= have[u]) m[u][k] = v[u][k] = 0.0f;
@@ -614,7 +619,7 @@ __global__ __launch_bounds__(kThreads) void mx8_quantize_kernel(const MxArgs a) 
         const int64_t e = e0 + 4 * kThreads * u;
         if (kRoot) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) f[u][k] = root_f32((double)f[u][k] + kTiny);
+            for (int k = 0; k < 4; ++k) f[u][k] = (float)root_f64((double)f[u][k] + kTiny);
         }
         const uint32_t byte = mx_byte<kRoot>(f[u]);
         if (kRoot) mx_raise(f[u], byte);
