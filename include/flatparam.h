@@ -771,8 +771,16 @@ fp_status fp_params_adamw8(fp_params* params, int32_t n_groups, const fp_adamw_h
 /* Moments between fp32 and MXFP8 (a checkpoint, resharding: fp_reshard moves
  * fp32 moments), over n elements.  Quantization takes the scales above and
  * rounds y / q to nearest even, so values that it gave come back as they are.
+ * So do those that a step gave, except in a block whose largest value the step
+ * rounded up to 256 of its scale: its scale doubles, and values below 2^-13 of
+ * that largest one may move by their last bit.
  * root != 0: x is a second moment (>= 0; a negative one gives NaN); codes hold
- * its root, taken in fp64 and rounded to fp32, and dequantization squares.
+ * its root, taken in fp64 and rounded to fp32, and dequantization squares, in
+ * fp32.  A root r comes back from its square for 2^-71 <= r < 2^64, and 0;
+ * below, the square loses bits or is 0 (a step divides by eps alone then),
+ * above, it is inf (and quantized again, its block reads as NaN).  root = 0
+ * both ways keeps r itself at any magnitude: the form for the fp32 checkpoint
+ * of an 8-bit run; root != 0 is for moments shared with fp32 runs.
  * x: device fp32[n], codes: device uint8[n], both 16-byte aligned; scales:
  * device uint8[ceil(n / 32)]. */
 fp_status fp_mx8_quantize(int64_t n, int32_t root, const float* x, uint8_t* codes, uint8_t* scales, void* stream);

@@ -1002,7 +1002,8 @@ class ParamsStep:
 def mx8_quantize(src, codes=None, scales=None, *, root: bool = False):
     """(codes, scales): MXFP8 of fp32 moments, e4m3 codes and one e8m0 scale per
     32 elements, rounded to nearest even; root: of a second moment, whose root
-    the codes then hold.  Allocated here when None."""
+    the codes then hold (without root, src is what the codes stand for: a first
+    moment, or a root already).  Allocated here when None."""
     n = src.numel()
     blocks = -(-n // _lib.FP_MX_BLOCK)
     cd, sd = _mx_dtypes()
@@ -1019,7 +1020,10 @@ def mx8_quantize(src, codes=None, scales=None, *, root: bool = False):
 
 def mx8_dequantize(codes, scales, dst=None, *, root: bool = False):
     """dst (fp32, allocated here when None): what MXFP8 codes and scales stand
-    for, squared with root (a second moment kept as its root)."""
+    for, squared with root (a second moment kept as its root).  The square is an
+    fp32 that gives the root back for 2^-71 <= r < 2^64 and 0; without root the
+    roots themselves come out at any magnitude, for mx8_quantize to take back
+    without root: the fp32 checkpoint of an 8-bit run."""
     n = codes.numel()
     cd, sd = _mx_dtypes()
     cp = _dev_ptr(codes, cd, n, "codes")

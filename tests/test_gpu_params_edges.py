@@ -71,3 +71,58 @@ def test_changes_at_all_magnitudes(fp, e, eps):
         check_weights(case, before, t, f"2^{e} step {t}", [dict(HPS[0], eps=max(eps, 2.0 ** -126))])
         case.hps = [dict(HPS[0], eps=max(eps, 2.0 ** -126))]
         case.check(before, t, t, what=f"2^{e} step {t}")
+
+
+def roots(seed, lo, hi):
+    """fp32 roots whose non-zero MXFP8 values lie in [2^lo, 2^hi]."""
+    r = np.random.default_rng(seed)
+    x = np.exp2(r.uniform(lo, hi, (64, 1)) - r.uniform(0, 20, (64, 32)))
+    x = np.where(r.random(x.shape) < 0.1, 0.0, np.maximum(x, 2.0 ** lo))
+    return x.reshape(-1).astype(np.float32)
+
+
+@pytest.mark.parametrize("lo,hi", [(-71, -50), (-30, 0), (20, 63.9)])
+def test_second_moments_come_back_as_fp32(fp, lo, hi):
+    say("second moments", lo, hi)
+    c, s = fp.mx8_quantize(torch.from_numpy(roots(1, lo, hi)).to(dev()))
+    r = ref.decode(*(x.view(torch.uint8).cpu().numpy() for x in (c, s)))
+    assert r[r > 0].min() >= 2.0 ** -71 and r.max() < 2.0 ** 64
+    v = fp.mx8_dequantize(c, s, root=True)
+    np.testing.assert_array_equal(v.cpu().numpy(), r * r)
+    c2, s2 = fp.mx8_quantize(v, root=True)
+    assert torch.equal(c2.view(torch.uint8), c.view(torch.uint8)) and torch.equal(s2.view(torch.uint8), s.view(torch.uint8))
+
+
+@pytest.mark.parametrize("lo,hi", [(-149, -120), (-100, -72), (64, 90), (100, 127.9), (-149, 127.9)])
+def test_roots_come_back_at_every_magnitude(fp, lo, hi):
+    """Where a second moment would leave fp32's range, its root does not."""
+    say("roots", lo, hi)
+    c, s = fp.mx8_quantize(torch.from_numpy(roots(2, lo, hi)).to(dev()))
+    r = fp.mx8_dequantize(c, s)
+    c2, s2 = fp.mx8_quantize(r)
+    assert torch.equal(c2.view(torch.uint8), c.view(torch.uint8)) and torch.equal(s2.view(torch.uint8), s.view(torch.uint8))
+    with np.errstate(over="ignore", under="ignore"):
+        want = np.square(r.cpu().numpy())
+    np.testing.assert_array_equal(fp.mx8_dequantize(c, s, root=True).cpu().numpy(), want)
+
+
+@pytest.mark.parametrize("sigma", [1e-30, 1e-3, 1e25])
+def test_a_checkpoint_in_fp32(fp, sigma):
+    """Moments of an 8-bit run as fp32, cut for three ranks, joined and taken back
+    into 8 bits, where the second moments themselves have left fp32's range too."""
+    say("checkpoint", sigma)
+    case = Case(fp, [4096, 96], grad="f32", copy=None, bits=8, warm=False, grad_sigma=sigma)
+    for t in range(1, 5):
+        run(case, t, seed=t)
+    P = case.plan.partition
+    for codes, scales in (case.moments[:2], case.moments[2:]):
+        x = fp.mx8_dequantize(codes, scales)
+        cut = fp.ReshardPlan(P, 1, 3).reshard([x])
+        back = fp.ReshardPlan(P, 3, 1).reshard(list(cut.split(cut.numel() // 3)))[:P]
+        c, s = fp.mx8_quantize(back)
+        y = fp.mx8_dequantize(c, s)
+        top = ref.decode(codes.cpu().numpy() & 0x7F, np.full(P // 32, 127, np.uint8)).reshape(-1, 32).max(1)
+        same = torch.from_numpy(np.repeat(top < 256, 32)).to(dev())
+        assert torch.equal(y[same], x[same]) and bool(same.float().mean() > 0.8) and bool((x != 0).any())
+        lost = (x != y) & (x.abs() >= 2.0 ** -13 * x.abs().view(-1, 32).amax(1).repeat_interleave(32))
+        assert not bool(lost.any())

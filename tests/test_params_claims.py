@@ -1,0 +1,55 @@
+"""What the header says of MXFP8 moments, checked with the numpy reference."""
+
+import os
+import re
+
+import numpy as np
+
+import params_ref as ref
+from conftest import ROOT
+
+HEADER = open(os.path.join(ROOT, "include", "flatparam.h")).read()
+HEADER = re.sub(r"\s+", " ", re.sub(r"\n \* ?", " ", HEADER))
+CODES = np.arange(0, 127, dtype=np.uint8)
+
+
+def test_the_range_whose_squares_are_fp32():
+    """Every root in the range that the header states comes back from its square
+    in fp32; just outside, some do not."""
+    lo, hi = map(int, re.search(r"2\^(-\d+) <= r < 2\^(\d+)", HEADER).groups())
+    seen = []
+    with np.errstate(over="ignore", under="ignore"):
+        for b in range(255):
+            r = ref.decode(CODES, np.full(4, b, np.uint8))
+            v = r.astype(np.float32) * r.astype(np.float32)
+            back = np.sqrt(v.astype(np.float64)).astype(np.float32)
+            seen += list(zip(r, back == r))
+    assert all(ok for r, ok in seen if r == 0 or 2.0 ** lo <= r < 2.0 ** hi)
+    assert any(not ok for r, ok in seen if 2.0 ** (lo - 1) < r < 2.0 ** lo)
+    assert not any(ok for r, ok in seen if 2.0 ** hi <= r < 2.0 ** (hi + 1))
+
+
+def test_values_that_come_back():
+    """Quantization gives back what it gave, and what a step's rounding gave
+    unless a block's largest value went up to 256 units: its scale doubles and
+    values below 2^-13 of that value may move by their last bit."""
+    assert "2^-13 of" in HEADER
+    r = np.random.default_rng(0)
+    n = 32 * 4096
+    x = (r.uniform(200, 247.99, (4096, 32)) * np.exp2(-r.integers(0, 18, (4096, 32)))).astype(np.float32)
+    x[:, 0] = r.uniform(125, 247.99, 4096)
+    x = x.reshape(-1) * np.where(r.random(n) < 0.5, np.float32(-1), np.float32(1))
+    s = ref.scale_bytes(x)
+    for d in (None, r.integers(0, 65536, n).astype(np.uint32)):
+        y = ref.decode(ref.encode(x, s, d), s)
+        s2 = ref.scale_bytes(y)
+        z = ref.decode(ref.encode(y.astype(np.float32), s2), s2)
+        top = np.repeat(np.abs(y).reshape(-1, 32).max(1), 32)
+        went = top == 256
+        assert np.array_equal(z[~went], y[~went])
+        if d is None:
+            assert not went.any()
+            continue
+        assert went.any() and (z != y)[went].any()
+        moved = went & (z != y)
+        assert (np.abs(y[moved]) < 2.0 ** -13 * 256).all() and (np.abs(z - y)[moved] == 2.0 ** -9).all()
