@@ -749,9 +749,10 @@ fp_status fp_params_adamw(fp_params* params, int32_t n_groups, const fp_adamw_hp
  *   y = |x| 2^(127 - b) < 248;  q = e4m3's step at y, 2^(max(floor(log2 y), -6) - 3);
  *   the code is that of q * floor(y / q + d / 2^16),
  * with x's sign; codes of a b = 255 block are 0 (a block with an element that
- * is not finite reads as NaN until it is reset: pass found_inf).  An r' > 0
- * whose code would be 0 gets the code 1.  Stochastic, because the moments
- * change by less than half an e4m3 step: rounded to nearest, a decaying
+ * is not finite, or of 1.9375 * 2^127 and more, which e4m3's bits round past
+ * fp32's range, reads as NaN until it is reset: pass found_inf for the first).
+ * An r' > 0 whose code would be 0 gets the code 1.  Stochastic, because the
+ * moments change by less than half an e4m3 step: rounded to nearest, a decaying
  * second moment would never move.  d is the high (for r the low) half of a
  * 32-bit hash of the element's partition index i and the seed:
  *   x = (i * 0x9E3779B1) ^ key;  x ^= x >> 16;  x *= 0x6A09E667;

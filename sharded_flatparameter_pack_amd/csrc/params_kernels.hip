@@ -15,7 +15,8 @@
 // With f the exponent field of the block's largest magnitude, rounded to
 // e4m3's four significant bits, b = max(0, f - 7): the largest value lands
 // in [124, 248], so rounding up never leaves e4m3's range (448).  A block
-// with a value that is not finite (f >= 255) gets b = 255: it reads as NaN.
+// with f >= 255 gets b = 255 and reads as NaN: its largest value is not finite
+// or is at least 1.9375 * 2^127, which rounds to 2^128, past fp32's range.
 // The hardware's scaled conversions give and take codes under such a scale.
 //
 // Compiled with -ffp-contract=off: every operation is one IEEE

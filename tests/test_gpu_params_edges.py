@@ -73,6 +73,26 @@ def test_changes_at_all_magnitudes(fp, e, eps):
         case.check(before, t, t, what=f"2^{e} step {t}")
 
 
+@pytest.mark.parametrize("top,finite", [(1.9374, True), (1.9375, False), (1.9999, False)])
+def test_blocks_at_fp32s_end(fp, top, finite):
+    """A block whose largest value rounds past fp32's range reads as NaN, by the
+    conversion and by the step; one just below keeps its values."""
+    say("fp32's end", top)
+    x = np.full(64, 2.0 ** 125, np.float32)
+    x[3] = -top * 2.0 ** 127
+    t = torch.from_numpy(x).to(dev())
+    c, s = fp.mx8_quantize(t)
+    y = fp.mx8_dequantize(c, s)
+    assert bool(torch.isnan(y[:32]).all()) != finite and bool(torch.isfinite(y[:32]).all()) == finite
+    assert torch.equal(y[32:], t[32:])
+    w = torch.zeros(64, device=dev())
+    plan = fp.Params([t], [w])
+    mom = plan.new_moments(8)
+    plan.step(mom, step=1, seed=1, **dict(HPS[0], beta1=0.0))
+    assert int(mom[1].view(torch.uint8)[0]) == (247 if finite else 255) and int(mom[1].view(torch.uint8)[1]) < 255
+    assert bool(torch.isfinite(w).all())
+
+
 def roots(seed, lo, hi):
     """fp32 roots whose non-zero MXFP8 values lie in [2^lo, 2^hi]."""
     r = np.random.default_rng(seed)

@@ -4,6 +4,7 @@ import os
 import re
 
 import numpy as np
+import pytest
 
 import params_ref as ref
 from conftest import ROOT
@@ -53,3 +54,14 @@ def test_values_that_come_back():
         assert went.any() and (z != y)[went].any()
         moved = went & (z != y)
         assert (np.abs(y[moved]) < 2.0 ** -13 * 256).all() and (np.abs(z - y)[moved] == 2.0 ** -9).all()
+
+
+@pytest.mark.parametrize("top", [1.9375, 1.96, 2 - 2.0 ** -23])
+def test_blocks_that_round_past_fp32(top):
+    """They have no scale under which the rounded value is an fp32."""
+    assert "1.9375 * 2^127" in HEADER
+    x = np.zeros(32, np.float32)
+    x[5] = top * 2.0 ** 127
+    assert np.isfinite(x).all() and ref.scale_bytes(x)[0] == 255
+    y = ref.decode(ref.encode(x, np.array([248], np.uint8)), np.array([248], np.uint8))
+    assert y[5] == 2.0 ** 128  # not an fp32
