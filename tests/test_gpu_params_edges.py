@@ -73,6 +73,40 @@ def test_changes_at_all_magnitudes(fp, e, eps):
         case.check(before, t, t, what=f"2^{e} step {t}")
 
 
+@pytest.mark.parametrize("e", [-149, -146, -140, -136, -130, -127, -126, -123, -120, -119, -118])
+def test_mx8_under_the_smallest_scales(fp, e):
+    """Blocks whose largest value is 2^e to 2^(e + 1), subnormal ones and those
+    under the scale byte 0 among them, both signs and zeros."""
+    say("mx8 small", e)
+    r = np.random.default_rng(e + 1000)
+    n = 32 * 40 + 7
+    x = np.ldexp(r.uniform(1, 2, n), e) * np.exp2(-r.integers(0, 12, n)) * r.choice([-1.0, 0.0, 1.0], n)
+    x[::32] = np.ldexp(r.uniform(1, 2, x[::32].size), e)
+    x = x.astype(np.float32)
+    c, s = fp.mx8_quantize(torch.from_numpy(x).to(dev()))
+    c, s = (t.view(torch.uint8).cpu().numpy() for t in (c, s))
+    ref.check_mx8(c, s, x.astype(np.float64), what=f"2^{e}")
+    assert s.max() <= max(0, e + 1 + 127 - 7) and (e >= -120 or not s.any())
+    out = fp.mx8_dequantize(torch.from_numpy(c).to(dev()), torch.from_numpy(s).to(dev()))
+    np.testing.assert_array_equal(out.cpu().numpy(), ref.decode(c, s).astype(np.float32))
+
+
+@pytest.mark.parametrize("e", range(-137, -119))
+def test_steps_under_the_smallest_scales(fp, e):
+    """Moments that the step rounds stochastically under scale bytes 0 to 9, and
+    roots that it raises there."""
+    say("step small", e)
+    case = Case(fp, [32 * 50 + 3, 40], grad="f32", copy=None, bits=8, warm=False)
+    r = np.random.default_rng(e + 1000)
+    g = np.ldexp(r.uniform(1, 2, case.n), e) * np.exp2(-r.integers(0, 14, case.n)) * r.choice([-1.0, 0.0, 1.0], case.n)
+    case.grad.copy_(torch.from_numpy(g.astype(np.float32)).to(dev()))
+    for t in (1, 2, 3):
+        before = case.host()
+        run(case, t, seed=t)
+        case.check(before, t, t, what=f"2^{e} step {t}")
+    assert int(case.moments[1].max()) <= 9 and int(case.moments[3].max()) <= 9
+
+
 @pytest.mark.parametrize("top,finite", [(1.9374, True), (1.9375, False), (1.9999, False)])
 def test_blocks_at_fp32s_end(fp, top, finite):
     """A block whose largest value rounds past fp32's range reads as NaN, by the
