@@ -180,3 +180,17 @@ def test_a_checkpoint_in_fp32(fp, sigma):
         assert torch.equal(y[same], x[same]) and bool(same.float().mean() > 0.8) and bool((x != 0).any())
         lost = (x != y) & (x.abs() >= 2.0 ** -13 * x.abs().view(-1, 32).amax(1).repeat_interleave(32))
         assert not bool(lost.any())
+
+
+@pytest.mark.parametrize("copy", ["bf16", "f16", None])
+@pytest.mark.parametrize("bits,first", [(8, 3_000_000), (32, 4_000_000)])
+def test_larger_plans(fp, bits, first, copy):
+    """Plans of the sizes at which waves take whole tiles (8-bit moments) and at
+    which fewer workgroups are resident (fp32 moments), with every kind of copy."""
+    say("larger", bits, copy)
+    for shift in (0, 1):
+        case = Case(fp, [first, 5, 70_001, 512, 0, 515, 3], "bf16" if copy != "f16" else "f16", copy, bits, shift, seed=3)
+        for t in (1, 7):
+            before = case.host()
+            run(case, t, seed=t)
+            case.check(before, t, t, what=f"{copy} {bits} bits shift {shift} step {t}")
