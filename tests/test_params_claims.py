@@ -56,6 +56,22 @@ def test_values_that_come_back():
         assert (np.abs(y[moved]) < 2.0 ** -13 * 256).all() and (np.abs(z - y)[moved] == 2.0 ** -9).all()
 
 
+def test_the_dithers_mean():
+    """Over all dithers a value comes out low by less than 2^-16 of a code's
+    width, 2^-17 on average."""
+    assert "2^-17 of" in HEADER
+    r = np.random.default_rng(1)
+    d = np.arange(65536, dtype=np.uint32)
+    s = np.full(2048, 127, np.uint8)
+    low = []
+    for y in np.concatenate([r.uniform(16, 32, 100), r.uniform(2.0 ** -7, 2.0 ** -6, 100)]).astype(np.float32):
+        q = 2.0 if y >= 16 else 2.0 ** -9
+        got = ref.decode(ref.encode(np.full(65536, y, np.float32), s, d), s).mean()
+        low.append((float(y) - got) / q)
+    assert 0 <= min(low) and max(low) < 2.0 ** -16
+    assert abs(np.mean(low) - 2.0 ** -17) < 0.2 * 2.0 ** -17  # sigma of the mean: 2^-16 / sqrt(12 * 200)
+
+
 @pytest.mark.parametrize("top", [1.9375, 1.96, 2 - 2.0 ** -23])
 def test_blocks_that_round_past_fp32(top):
     """They have no scale under which the rounded value is an fp32."""
