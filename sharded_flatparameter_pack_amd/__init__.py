@@ -816,6 +816,29 @@ def _mx_dtypes():
     return _MX_DTYPES
 
 
+_BUMP = None
+
+
+def _bump_versions(tensors):
+    """Tells autograd that the tensors have changed, as torch's in-place operations do."""
+    global _BUMP
+    if _BUMP is None:
+        torch = _torch()
+        _BUMP = getattr(torch._C, "_increment_version", None) or torch.autograd.graph.increment_version
+    _BUMP(tensors)
+
+
+def _version_holders(tensors):
+    """One tensor for every version counter of these (views share their base's)."""
+    held = {}
+    for t in tensors:
+        b = t._base
+        if b is None:
+            b = t
+        held[id(b)] = b
+    return [b for b in held.values() if not b.is_inference()]  # those have none
+
+
 class Params:
     """Many separate tensors of one rank stepped together, one launch for all
     of them (fp_params_*): a model's parameters, or the views of a
@@ -831,6 +854,10 @@ class Params:
     multiple of 32) on.  The tensors must stay alive and in place for the
     plan's life (set_grads changes the gradients); the plan is bound to
     their device.
+    A step counts as an in-place change of the weights and copies, one that the
+    overflow flag skips too: a backward pass that kept one of them from before
+    the step raises, as after a torch optimizer.  (A graph's replay runs none of
+    this: it changes them unseen.)
     """
 
     def __init__(self, grads, master=None, copies=None, groups=None):
@@ -856,6 +883,7 @@ class Params:
             raise ValueError(f"groups: {len(self.groups)} numbers, expected {n}")
         self.n_groups = max(self.groups) + 1
         self._keep = (grads, master, copies)
+        self._written = _version_holders([*(master or ()), *(copies or ())])
         self._device = device
         out = C.c_void_p()
         with _torch().cuda.device(device):
@@ -998,6 +1026,7 @@ class ParamsStep:
                        self._found, self._coef)
         else:
             _on_device(p._device, self._fn, p._h, self._n, self._hp, *self._moments, self._found, self._coef)
+        _bump_versions(p._written)
 
 
 def mx8_quantize(src, codes=None, scales=None, *, root: bool = False):

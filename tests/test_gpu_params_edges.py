@@ -182,6 +182,31 @@ def test_a_checkpoint_in_fp32(fp, sigma):
         assert not bool(lost.any())
 
 
+def test_backward_through_stepped_weights_raises(fp):
+    """As after a torch optimizer: autograd sees that a weight or a copy that it
+    kept for a backward pass has changed."""
+    say("versions")
+    for bits in (32, 8):
+        flat = torch.randn(96, device=dev())
+        weights = [torch.nn.Parameter(torch.randn(64, device=dev())), torch.nn.Parameter(flat[:32].view(4, 8)), flat[32:]]
+        copies = [w.detach().bfloat16() for w in weights]
+        x = [torch.randn_like(w, requires_grad=True) for w in weights]
+        plan = fp.Params([torch.ones_like(w) for w in weights], weights, copies)
+        mom = plan.new_moments(bits)
+        sq, ws = torch.zeros(1, dtype=torch.float64, device=dev()), plan.new_workspace()
+        for kept in weights + copies:
+            y = [x[i].to(kept.dtype) * kept for i in range(3) if x[i].shape == kept.shape][0].sum()
+            plan.grad_norm(sq, ws)
+            y.backward(retain_graph=True)
+            plan.step(mom, step=1, seed=1 if bits == 8 else None, **HPS[0])
+            with pytest.raises(RuntimeError, match="inplace"):
+                y.backward()
+        with torch.inference_mode():
+            w = torch.zeros(8, device=dev())
+            fp.Params([torch.ones_like(w)], [w]).step([torch.zeros(32, device=dev()) for _ in range(2)], step=1, **HPS[0])
+        assert bool((w < 0).all())
+
+
 @pytest.mark.parametrize("copy", ["bf16", "f16", None])
 @pytest.mark.parametrize("bits,first", [(8, 3_000_000), (32, 4_000_000)])
 def test_larger_plans(fp, bits, first, copy):
