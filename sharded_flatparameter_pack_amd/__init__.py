@@ -972,7 +972,9 @@ class ParamsStep:
     """Params.step with its arguments marshalled once, for tight step loops:
     the tensors are checked and their pointers captured at construction; a
     call sets the step count, the seed (8-bit moments) and, where it changes,
-    the learning rate."""
+    the learning rate, which later calls keep (a refused call leaves the one
+    before).  For one thread at a time: a call fills arguments that the library
+    then reads without the interpreter's lock."""
 
     def __init__(self, params, moments, *, lr, beta1, beta2, eps, weight_decay, found_inf=None, grad_coef=None):
         moments = tuple(moments)
@@ -1019,13 +1021,20 @@ class ParamsStep:
         for h in self._rows:
             h.step = step
         if lr is not None:
+            before = [h.lr for h in self._rows]
             for h, x in zip(self._rows, self._per_group(lr)):
                 h.lr = x
-        if self._eight:
-            _on_device(p._device, self._fn, p._h, self._n, self._hp, *self._moments, int(seed) & 0xFFFFFFFFFFFFFFFF,
-                       self._found, self._coef)
-        else:
-            _on_device(p._device, self._fn, p._h, self._n, self._hp, *self._moments, self._found, self._coef)
+        try:
+            if self._eight:
+                _on_device(p._device, self._fn, p._h, self._n, self._hp, *self._moments, int(seed) & 0xFFFFFFFFFFFFFFFF,
+                           self._found, self._coef)
+            else:
+                _on_device(p._device, self._fn, p._h, self._n, self._hp, *self._moments, self._found, self._coef)
+        except Exception:
+            if lr is not None:
+                for h, x in zip(self._rows, before):
+                    h.lr = x
+            raise
         _bump_versions(p._written)
 
 

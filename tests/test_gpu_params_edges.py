@@ -207,6 +207,27 @@ def test_backward_through_stepped_weights_raises(fp):
         assert bool((w < 0).all())
 
 
+def test_a_refused_rate_does_not_stay(fp):
+    say("refused rate")
+    w = [torch.ones(64, device=dev()) for _ in range(2)]
+    g = torch.randn(64, device=dev())
+    steps = []
+    for x in w:
+        plan = fp.Params([g], [x])
+        steps.append(plan.stepper(plan.new_moments(), **HPS[0]))
+    for bad in (math.nan, math.inf):
+        with pytest.raises(fp.FlatParamError, match="finite"):
+            steps[0](1, lr=bad)
+    steps[0](1)
+    steps[1](1)
+    assert torch.equal(w[0], w[1]) and not torch.equal(w[0], torch.ones_like(w[0]))
+    steps[0](2, lr=0.5)   # one that is taken stays
+    steps[0](3)
+    steps[1](2, lr=0.5)
+    steps[1](3, lr=0.5)
+    assert torch.equal(w[0], w[1])
+
+
 @pytest.mark.parametrize("copy", ["bf16", "f16", None])
 @pytest.mark.parametrize("bits,first", [(8, 3_000_000), (32, 4_000_000)])
 def test_larger_plans(fp, bits, first, copy):
