@@ -779,18 +779,29 @@ class Units:
 
 
 # ------------------------------------------------------------------ params
+def _no_none(tensors, name):
+    for i, t in enumerate(tensors):
+        if t is None:
+            raise TypeError(f"{name}[{i}] is None: a plan holds only tensors that are there (leave a weight without "
+                            "a gradient out of it)")
+
+
 def _table(tensors, dtype, device, sizes, name):
     """Device pointers of contiguous tensors of one dtype, device and these sizes."""
     if len(tensors) != len(sizes):
         raise ValueError(f"{name}: {len(tensors)} tensors, expected {len(sizes)}")
     ptrs = (C.c_void_p * len(sizes))()
-    for i, t in enumerate(tensors):  # one line of checks: plans hold up to tens of thousands of tensors
-        if t.dtype != dtype or t.device != device or t.numel() != sizes[i] or not t.is_contiguous():
-            _dev_ptr(t, (dtype,), 0, f"{name}[{i}]")
-            if t.numel() != sizes[i]:
-                raise ValueError(f"{name}[{i}] has {t.numel()} elements, expected {sizes[i]}")
-            raise ValueError(f"tensors of one call sit on several devices: {t.device} and {device}")
-        ptrs[i] = t.data_ptr()
+    try:
+        for i, t in enumerate(tensors):  # one line of checks: plans hold up to tens of thousands of tensors
+            if t.dtype != dtype or t.device != device or t.numel() != sizes[i] or not t.is_contiguous():
+                _dev_ptr(t, (dtype,), 0, f"{name}[{i}]")
+                if t.numel() != sizes[i]:
+                    raise ValueError(f"{name}[{i}] has {t.numel()} elements, expected {sizes[i]}")
+                raise ValueError(f"tensors of one call sit on several devices: {t.device} and {device}")
+            ptrs[i] = t.data_ptr()
+    except AttributeError:
+        _no_none(tensors, name)
+        raise
     return ptrs
 
 
@@ -847,7 +858,8 @@ class Params:
     grads: one gradient per tensor, all fp32, bf16 (or its bits in 16-bit
     integers) or fp16.  master: their fp32 weights (None: a plan that only
     takes the norm).  copies: bf16 or fp16 tensors that receive the weights,
-    or None.  groups: a group number per tensor (None: all 0); a step takes
+    or None.  None among them is refused: a weight without a gradient stays out
+    of the plan.  groups: a group number per tensor (None: all 0); a step takes
     hyperparameters per group.
     Tensors are contiguous, at any element of a buffer.  The moments sit in a
     partition of `partition` elements, tensor i's from `offsets[i]` (a
@@ -864,6 +876,7 @@ class Params:
         grads = list(grads)
         if not grads:
             raise ValueError("need at least one tensor")
+        _no_none(grads, "grads")
         n, device = len(grads), grads[0].device
         if device.type != "cuda":
             raise ValueError("grads[0] must be a device tensor")
@@ -876,6 +889,7 @@ class Params:
             mtab = _table(master, _torch().float32, device, self.sizes, "master")
         if copies is not None:
             copies = list(copies)
+            _no_none(copies[:1], "copies")
             ctab = _table(copies, copies[0].dtype if copies else None, device, self.sizes, "copies")
             cid = _dtype_id(copies[0].dtype, "copies", f32=False)
         self.groups = [0] * n if groups is None else [int(k) for k in groups]

@@ -228,6 +228,19 @@ def test_a_refused_rate_does_not_stay(fp):
     assert torch.equal(w[0], w[1])
 
 
+def test_a_gradient_that_is_not_there(fp):
+    say("no gradient")
+    t = [torch.zeros(8, device=dev()) for _ in range(4)]
+    for grads, master, copies, match in (([t[0], None], t[2:], None, r"grads\[1\] is None"),
+                                         (t[:2], [t[2], None], None, r"master\[1\] is None"),
+                                         (t[:2], t[2:], [None, None], r"copies\[0\] is None")):
+        with pytest.raises(TypeError, match=match):
+            fp.Params(grads, master, copies)
+    plan = fp.Params(t[:2], t[2:])
+    with pytest.raises(TypeError, match=r"grads\[1\] is None"):
+        plan.set_grads([t[0], None])
+
+
 @pytest.mark.parametrize("copy", ["bf16", "f16", None])
 @pytest.mark.parametrize("bits,first", [(8, 3_000_000), (32, 4_000_000)])
 def test_larger_plans(fp, bits, first, copy):

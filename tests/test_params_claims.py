@@ -1,4 +1,5 @@
-"""What the header says of MXFP8 moments, checked with the numpy reference."""
+"""What the header says of MXFP8 moments, checked with the numpy reference, and
+plans that the binding refuses before it asks a GPU."""
 
 import os
 import re
@@ -81,3 +82,9 @@ def test_blocks_that_round_past_fp32(top):
     assert np.isfinite(x).all() and ref.scale_bytes(x)[0] == 255
     y = ref.decode(ref.encode(x, np.array([248], np.uint8)), np.array([248], np.uint8))
     assert y[5] == 2.0 ** 128  # not an fp32
+
+
+@pytest.mark.parametrize("grads", [[None], [None, None]])
+def test_a_gradient_that_is_not_there(fp, grads):
+    with pytest.raises(TypeError, match=r"grads\[0\] is None"):
+        fp.Params(grads)
