@@ -878,6 +878,12 @@ class Params:
             raise ValueError("need at least one tensor")
         _no_none(grads, "grads")
         n, device = len(grads), grads[0].device
+        self.groups = [0] * n if groups is None else [int(k) for k in groups]
+        if len(self.groups) != n:
+            raise ValueError(f"groups: {len(self.groups)} numbers, expected {n}")
+        for k in (min(self.groups), max(self.groups)):  # here, as C takes their low 32 bits
+            if not 0 <= k < _lib.FP_MAX_GROUPS:
+                raise ValueError(f"group number {k} outside [0, {_lib.FP_MAX_GROUPS})")
         if device.type != "cuda":
             raise ValueError("grads[0] must be a device tensor")
         self.sizes = [t.numel() for t in grads]
@@ -892,9 +898,6 @@ class Params:
             _no_none(copies[:1], "copies")
             ctab = _table(copies, copies[0].dtype if copies else None, device, self.sizes, "copies")
             cid = _dtype_id(copies[0].dtype, "copies", f32=False)
-        self.groups = [0] * n if groups is None else [int(k) for k in groups]
-        if len(self.groups) != n:
-            raise ValueError(f"groups: {len(self.groups)} numbers, expected {n}")
         self.n_groups = max(self.groups) + 1
         self._keep = (grads, master, copies)
         self._written = _version_holders([*(master or ()), *(copies or ())])

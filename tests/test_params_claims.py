@@ -88,3 +88,11 @@ def test_blocks_that_round_past_fp32(top):
 def test_a_gradient_that_is_not_there(fp, grads):
     with pytest.raises(TypeError, match=r"grads\[0\] is None"):
         fp.Params(grads)
+
+
+@pytest.mark.parametrize("groups", [[16], [-1], [1 << 32], [(1 << 32) + 1]])
+def test_group_numbers_out_of_range(fp, groups):
+    """Also those whose low 32 bits are a group's."""
+    import torch
+    with pytest.raises(ValueError, match="group"):
+        fp.Params([torch.zeros(4)], groups=groups)
