@@ -43,14 +43,16 @@ inline int64_t param_tiles(int64_t numel) { return ceil_div64(numel, kParamTile)
 //   79, 50M 224 and 231, 134M 593 and 622, 226M 1004 (6.3 TB/s) and 1058.
 constexpr unsigned kParamCapLds = 53504u;
 constexpr int64_t kParamCapElems = 4000000;
-// 8-bit moments: arithmetic is nearly half of the kernel's time and wants all
-//   the waves there are.  A wave takes a tile from kMx8WholeElems to
-//   kMx8HalfElems; below, where waves are few, and above, where nothing stays in
-//   a cache from step to step, half of one.  Half and whole: 1.6M elements in
-//   12 tensors 6.9 and 7.9, 2.5M 9.2 and 9.4, 4M 14.0 and 13.4, 17M 46.6 and
-//   44.5, 34M 88.5 and 83.4, 50M 132 and 138, 134M 350 and 371, 226M 594 (6.15
-//   TB/s) and 650.
-constexpr int64_t kMx8WholeElems = 3000000, kMx8HalfElems = 46000000;
+// 8-bit moments: the vector units are busy most of the kernel's time beside the
+//   memory.  A wave takes a tile, whose two quads per lane hide each other's
+//   latencies, and below kMx8WholeElems, where waves are few, half of one.  Half
+//   and whole, in 12 tensors: 1.6M elements 7.9 and 8.1, 3M 12.8 and 12.2, 4M
+//   15.3 and 15.0, 17M 51.6 and 49.2, 42M 118 and 111, 134M 385 and 366, 200M
+//   595 and 611, 226M 660 and 660, 450M 1289 and 1342; the 226M of eight
+//   matrices and their biases 665 and 622.  In 10 000 tensors, whose last tiles
+//   are mostly empty: 1.6M 15.5 and 19.5, 3M 19.4 and 22.7, 10M 37.7 and 38.8,
+//   17M 56.5 and 56.0, 42M 125 and 119, 200M 591 and 567.
+constexpr int64_t kMx8WholeElems = 3000000;
 
 // Workgroups of the norm, a partial sum each, at most as many as are resident
 // together.  Of 512 lanes, 4 per CU: counting them in at the end takes time of

@@ -679,7 +679,7 @@ void launch_step_of(const ParamsArgs& a, int64_t partition, bool mx8, hipStream_
     const unsigned whole = (unsigned)ceil_div64(a.n_tiles, kWaves), half = (unsigned)ceil_div64(2 * a.n_tiles, kWaves);
     static_assert(kParamQuads == 2, "half a tile is one quad per lane");
     if (!mx8) params_step_kernel<kGrad, false, 1><<<half, kThreads, partition < kParamCapElems ? 0 : kParamCapLds, s>>>(a);
-    else if (partition < kMx8WholeElems || partition >= kMx8HalfElems) params_step_kernel<kGrad, true, 1><<<half, kThreads, 0, s>>>(a);
+    else if (partition < kMx8WholeElems) params_step_kernel<kGrad, true, 1><<<half, kThreads, 0, s>>>(a);
     else params_step_kernel<kGrad, true, 2><<<whole, kThreads, 0, s>>>(a);
 }
 
