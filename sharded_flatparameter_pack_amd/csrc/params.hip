@@ -307,7 +307,9 @@ fp_status step_args(const fp_params* p, int32_t n_groups, const fp_adamw_hparams
 }
 
 // The stochastic rounding's key: the seed through two rounds of
-// multiplication, so that seeds that count steps give unrelated keys.
+// multiplication, so that seeds that count steps give unrelated keys.  The
+// first multiplier is 2^64 over the golden ratio; the second, with the shifts by
+// 32 around it, is the published 64-bit integer mixer known as degski's.
 uint32_t key_of(uint64_t seed) {
     uint64_t z = seed * 0x9E3779B97F4A7C15ull;
     z ^= z >> 32;

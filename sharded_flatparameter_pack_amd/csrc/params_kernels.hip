@@ -170,7 +170,8 @@ __device__ __forceinline__ uint32_t mx_byte(const float f[4]) {
 
 // A root that is not zero does not round to zero, so that a second moment
 // never becomes a division by eps alone: one below the smallest code's value
-// is raised to it.  Rare, so a wave without such values skips it.
+// is raised to it.  A wave without a value below it skips that; zeros are below
+// it too, so one with rows that no token has reached does not.
 __device__ __forceinline__ void mx_raise(float r[4], uint32_t byte) {
     const float least = __builtin_amdgcn_ldexpf(1.0f, (int)byte - 136);
     const float low = fminf(fminf(r[0], r[1]), fminf(r[2], r[3]));
@@ -431,11 +432,13 @@ __device__ __forceinline__ void step_tile(const ParamsArgs& a, const TileAt& t, 
 
 // The step: a wave has a tile, or with kU = 1 half of one; fp_params.h says
 // which form runs when and what they measured.  One pass: 16.1 bytes per
-// element with 8-bit moments, bf16 gradients and copies (226.5M elements 599
-// us, 6.1 TB/s), 28 with fp32 moments (226.5M 1004 us, 6.3 TB/s).  The loads
-// do not wait for the overflow flag, as in the flat step.  A wave ends after
-// its stores: with several tiles per wave and the next one's loads in flight
-// it had to wait for them (one counter for both), and took 711 us.
+// element with 8-bit moments, bf16 gradients and copies (226.5M elements 622
+// us, 5.9 TB/s; the loads and stores without the arithmetic 646, so the memory
+// sets it, while 42.6M in 10 000 short tensors take 131 with and 122 without),
+// 28 with fp32 moments (226.5M 1004 us, 6.3 TB/s).  The loads do not wait for
+// the overflow flag, as in the flat step.  A wave ends after its stores: with
+// several tiles per wave and the next one's loads in flight it had to wait for
+// them (one counter for both), and took 711 us where it otherwise took 640.
 template <int kGrad, bool kMx8, int kU>
 __global__ __launch_bounds__(kThreads) void params_step_kernel(const ParamsArgs a) {
     constexpr int kPer = kParamQuads / kU;   // waves per tile
@@ -553,9 +556,9 @@ __device__ __forceinline__ bool norm_arrive(uint32_t* done, unsigned b, unsigned
 // widen, fused multiply-add, leave the kernel to its loads.  Waves take tiles
 // in turn, so that those in flight cover one window of memory; two, four and
 // eight tiles of a wave in flight at once measured slower (226.5M bf16
-// elements 77, 86 and 103 us against 74, 6.2 TB/s), as did the next tile's
-// loads before a tile's sums (77) and three quarters or half of the waves
-// that are resident together (83 and 110 us).  The last workgroup to finish
+// elements 74, 83 and 90 us against 72, 6.3 TB/s), as did the next tile's
+// loads before a tile's sums (74) and three quarters or half of the waves
+// that are resident together (81 and 107 us).  The last workgroup to finish
 // adds the partial sums in their order, so the result does not depend on who
 // was last.
 template <int kGrad>
