@@ -765,8 +765,10 @@ fp_status fp_params_adamw(fp_params* params, int32_t n_groups, const fp_adamw_hp
  *   key: z = seed * 0x9E3779B97F4A7C15;  z ^= z >> 32;
  *   z *= 0xD6E8FEB86659FD93;  key = low half of z ^ (z >> 32)  (modulo 2^64)
  * so a step is reproducible from its seed; give every step another one (its
- * step count will do; a call captured into a graph repeats its seed, as it
- * does its hyperparameters).  exp_avg, root: device uint8[partition], 16-byte
+ * step count will do).  A call captured into a graph repeats its seed, as it
+ * does its hyperparameters; with one seed nearly every moment that changes by
+ * less than a code's width a step stays where it is, so a captured step's
+ * replays are no training run.  exp_avg, root: device uint8[partition], 16-byte
  * aligned; exp_avg_scale, root_scale: device uint8[partition / 32].  All-zero
  * bytes are zero moments.  (Weights, moments and scales: 6.06 bytes per
  * element, the k of fp_state_bytes.) */

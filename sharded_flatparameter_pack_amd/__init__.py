@@ -978,7 +978,8 @@ class Params:
              found_inf=None, grad_coef=None):
         """AdamW on every tensor.  moments: (exp_avg, exp_avg_sq) in fp32 or
         (exp_avg, exp_avg_scale, root, root_scale) in MXFP8, which needs a seed
-        of its own for every step (a captured call repeats its seed) and whose roots come out low by 0.7 % at
+        of its own for every step (a captured call repeats its seed, with which moments stick: its replays are no
+        training run) and whose roots come out low by 0.7 % at
         beta2 = 0.9999 (fp32 moments above it).  lr, beta1, beta2, eps, weight_decay: a
         number, or one per group (groups without a tensor here included)."""
         self.stepper(moments, lr=lr, beta1=beta1, beta2=beta2, eps=eps, weight_decay=weight_decay,

@@ -73,6 +73,25 @@ def test_the_dithers_mean():
     assert abs(np.mean(low) - 2.0 ** -17) < 0.2 * 2.0 ** -17  # sigma of the mean: 2^-16 / sqrt(12 * 200)
 
 
+def test_one_seed_for_every_step_sticks():
+    """Why every step needs a seed of its own: decaying without gradients, nearly
+    every root stays where it is under a repeated dither, and none under new ones."""
+    assert "with one seed nearly every moment that changes by less than a code's width a step stays where it is" in HEADER
+    n = 4096
+    i = np.arange(n)
+    first = np.full(n, 200.0, np.float32)
+    for seed_of, stuck in ((lambda t: 1, True), (lambda t: t, False)):
+        s = ref.scale_bytes(first)
+        x = ref.decode(ref.encode(first, s, ref.dither(i, 1)[1], root=True), s)
+        start = x.copy()
+        for t in range(2, 402):
+            y = (x * np.sqrt(0.999)).astype(np.float32)
+            s = ref.scale_bytes(y)
+            x = ref.decode(ref.encode(y, s, ref.dither(i, seed_of(t))[1], root=True), s)
+        assert ((x == start).mean() > 0.95) == stuck
+        assert (abs(x.mean() / start.mean() - 0.999 ** 200) < 0.01) != stuck
+
+
 @pytest.mark.parametrize("top", [1.9375, 1.96, 2 - 2.0 ** -23])
 def test_blocks_that_round_past_fp32(top):
     """They have no scale under which the rounded value is an fp32."""
