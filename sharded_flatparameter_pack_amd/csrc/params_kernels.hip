@@ -23,108 +23,12 @@
 // round-to-nearest-even operation, in the order written.
 
 #include "fp_params.h"
+#include "param_ops.h"
 #include "step_ops.h"
 
 namespace fpk {
 
 namespace {
-
-// Addresses in global memory (see FP_GLOBAL).
-template <class T>
-__device__ __forceinline__ FP_GLOBAL T* gptr(void* p) {
-    return static_cast<FP_GLOBAL T*>((FP_GLOBAL void*)p);
-}
-template <class T>
-__device__ __forceinline__ const FP_GLOBAL T* gptr(const void* p) {
-    return static_cast<const FP_GLOBAL T*>((const FP_GLOBAL void*)p);
-}
-
-// ---------------------------------------------------------------- gradients
-
-template <int kGrad>
-struct GradQuad {
-    uint2 w;
-};
-template <>
-struct GradQuad<FP_DTYPE_F32> {
-    uint4 w;
-};
-
-__device__ __forceinline__ float f16_lo(uint32_t w) {
-    return (float)__builtin_bit_cast(_Float16, (uint16_t)(w & 0xFFFFu));
-}
-__device__ __forceinline__ float f16_hi(uint32_t w) { return f16_lo(w >> 16); }
-
-// Gradient quad starting at element e, all four elements present.
-template <int kGrad>
-__device__ __forceinline__ GradQuad<kGrad> ld_grad(const void* g, int64_t e) {
-    GradQuad<kGrad> q;
-    if constexpr (kGrad == FP_DTYPE_F32) q.w = ld16u(static_cast<const float*>(g) + e);
-    else q.w = ld8u(static_cast<const uint16_t*>(g) + e);
-    return q;
-}
-
-// The first n < 4 elements of a tensor that has no more, as a quad.
-template <int kGrad>
-__device__ __forceinline__ GradQuad<kGrad> ld_grad_few(const void* g, int n) {
-    uint32_t w[3] = {0u, 0u, 0u};
-#pragma unroll
-    for (int k = 0; k < 3; ++k)
-        if (k < n) {
-            if constexpr (kGrad == FP_DTYPE_F32) w[k] = gptr<uint32_t>(g)[k];
-            else w[k] = gptr<uint16_t>(g)[k];
-        }
-    GradQuad<kGrad> q;
-    if constexpr (kGrad == FP_DTYPE_F32) q.w = make_uint4(w[0], w[1], w[2], 0u);
-    else q.w = make_uint2(w[0] | (w[1] << 16), w[2]);
-    return q;
-}
-
-// A quad without its first s elements (s >= 4: without any), zeros behind.
-__device__ __forceinline__ uint4 drop(const uint4 w, int s) {
-    const uint32_t a = s & 1 ? w.y : w.x, b = s & 1 ? w.z : w.y, c = s & 1 ? w.w : w.z, d = s & 1 ? 0u : w.w;
-    const uint4 r = s & 2 ? make_uint4(c, d, 0u, 0u) : make_uint4(a, b, c, d);
-    return s >= 4 ? make_uint4(0u, 0u, 0u, 0u) : r;
-}
-__device__ __forceinline__ uint2 drop(const uint2 w, int s) {
-    const uint64_t x = (((uint64_t)w.y << 32) | w.x) >> (16 * (s & 3));
-    return s >= 4 ? make_uint2(0u, 0u) : make_uint2((uint32_t)x, (uint32_t)(x >> 32));
-}
-
-template <int kGrad>
-__device__ __forceinline__ void grad_f32(const GradQuad<kGrad>& q, float f[4]) {
-    if constexpr (kGrad == FP_DTYPE_F32) {
-        f[0] = __uint_as_float(q.w.x); f[1] = __uint_as_float(q.w.y);
-        f[2] = __uint_as_float(q.w.z); f[3] = __uint_as_float(q.w.w);
-    } else if constexpr (kGrad == FP_DTYPE_BF16) {
-        bf16x4_to_f32(q.w, f);
-    } else {
-        f[0] = f16_lo(q.w.x); f[1] = f16_hi(q.w.x);
-        f[2] = f16_lo(q.w.y); f[3] = f16_hi(q.w.y);
-    }
-}
-
-__device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
-    return (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)lo) |
-           ((uint32_t)__builtin_bit_cast(uint16_t, (_Float16)hi) << 16);
-}
-
-__device__ __forceinline__ void f32x4_of(const uint4 w, float f[4]) {
-    f[0] = __uint_as_float(w.x); f[1] = __uint_as_float(w.y);
-    f[2] = __uint_as_float(w.z); f[3] = __uint_as_float(w.w);
-}
-
-__device__ __forceinline__ uint4 bits_of(const float f[4]) {
-    return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
-}
-
-typedef unsigned int u32x4_a4 __attribute__((ext_vector_type(4), aligned(4)));
-
-// 16 bytes to a 4-byte boundary (fp32 weights that are views of a buffer).
-__device__ __forceinline__ void st16u(void* p, const uint4 v) {
-    const u32x4_a4 w = {v.x, v.y, v.z, v.w};
-    __builtin_nontemporal_store(w, (FP_GLOBAL u32x4_a4*)(p));
-}
 
 // ---------------------------------------------------------------- MXFP8
 
@@ -202,18 +106,6 @@ __device__ __forceinline__ uint32_t mx_encode(const float f[4], uint32_t byte) {
     w = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(w, f[0], f[1], s, false);
     w = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(w, f[2], f[3], s, true);
     return byte == 255u ? 0u : __builtin_bit_cast(uint32_t, w);
-}
-
-// 32 bits of dither for partition element e: the element's index and the
-// call's key through two multiplications.  The multipliers are the golden
-// ratio's and the fractions of sqrt(2) and sqrt(3).
-__device__ __forceinline__ uint32_t dither(uint32_t e, uint32_t key) {
-    uint32_t x = (e * 0x9E3779B1u) ^ key;
-    x ^= x >> 16;
-    x *= 0x6A09E667u;
-    x ^= x >> 15;
-    x *= 0xBB67AE85u;
-    return x;
 }
 
 // ---------------------------------------------------------------- AdamW
