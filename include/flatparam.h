@@ -795,6 +795,122 @@ fp_status fp_mx8_quantize(int64_t n, int32_t root, const float* x, uint8_t* code
 fp_status fp_mx8_dequantize(int64_t n, int32_t root, const uint8_t* codes, const uint8_t* scales, float* x,
                             void* stream);
 
+/* ------------------------------------------------------------------ muon */
+
+/* The optimizer step over separate matrices whose update is orthogonalised
+ * (the Muon optimizer), beside fp_params_* for the tensors that AdamW takes,
+ * and the orthogonalisation by itself.  With g a matrix's gradient, k =
+ * *grad_coef (1 when NULL), r x c its shape, per matrix:
+ *   M' = beta M + (1 - beta) k g;  U = nesterov ? (1 - beta) k g + beta M' : M'
+ *   X = U / (|U|_F + eps);  steps times  X <- a X + (b A + c A^2) X, A = X X^T
+ *   (X <- X (a + b A + c A^2), A = X^T X, for r > c: the same matrix)
+ *   W' = (1 - lr weight_decay) W - lr adjust X
+ * adjust: FP_MUON_ADJUST_RMS 0.2 sqrt(max(r, c)) (updates of AdamW's size),
+ * FP_MUON_ADJUST_SHAPE sqrt(max(1, r / c)), FP_MUON_ADJUST_NONE 1.
+ * Momentum and weights are fp32, each rounded once from fp64.  The products
+ * take fp16 operands, with X and the diagonals of A and of b A + c A^2 held in
+ * fp32 and fp32 sums: five steps end within 3e-3 (2-norm, relative; mostly
+ * within 1e-3) of the formula.  A matrix of zeros gives zeros; one with an
+ * element that is not finite gives NaN (pass found_inf).
+ *
+ * fp_muon_create: n >= 1 matrices of rows[i] x cols[i], each side in
+ *   [0, 2^20], row-major and contiguous; group, grad_dtype, grads, master,
+ *   copy_dtype, copies as in fp_params_create.  updates: host array of n device
+ *   pointers to matrices of update_dtype (FP_DTYPE_*) that
+ *   fp_muon_orthogonalize writes, or NULL.  At least one of master and
+ *   updates.  Weights, copies and updates overlap nothing else.
+ * fp_muon_info: partition as in fp_params_info, of the momentum;
+ *   workspace_bytes: of every call, about 10 bytes per element of the matrices
+ *   that are worked on together (up to 2 GiB, or the largest matrix's), with
+ *   both sides counted in multiples of 64.
+ * Creation, destruction, fp_muon_set_grads and devices as for fp_params.
+ * Errors: FP_ERR_RANGE, FP_ERR_INVALID, FP_ERR_ALIGN, FP_ERR_DEVICE. */
+#define FP_MUON_ADJUST_NONE 0
+#define FP_MUON_ADJUST_RMS 1
+#define FP_MUON_ADJUST_SHAPE 2
+#define FP_MUON_MAX_STEPS 32
+typedef struct {
+    double lr;
+    double beta;          /* of the momentum, in [0, 1) */
+    double weight_decay;
+    int32_t nesterov;     /* 0 or 1 */
+    int32_t adjust;       /* FP_MUON_ADJUST_* */
+} fp_muon_hparams;
+typedef struct fp_muon fp_muon;
+fp_status fp_muon_create(int32_t n, const int64_t* rows, const int64_t* cols, const int32_t* group, int32_t grad_dtype,
+                         const void* const* grads, float* const* master, int32_t copy_dtype, void* const* copies,
+                         int32_t update_dtype, void* const* updates, fp_muon** out);
+void fp_muon_destroy(fp_muon* muon);
+fp_status fp_muon_info(const fp_muon* muon, int64_t* partition, int64_t* workspace_bytes);
+fp_status fp_muon_offsets(const fp_muon* muon, int64_t* offsets);
+fp_status fp_muon_set_grads(fp_muon* muon, const void* const* grads, void* stream);
+
+/* updates[i] = the orthogonalised grads[i] (U = g above).  steps in
+ * [1, FP_MUON_MAX_STEPS]; coefs: host array of steps x (a, b, c), which may
+ * differ from step to step; FP_ERR_RANGE for coefficients that let a singular
+ * value of X, which starts at 1 at most, pass 256.  eps > 0.  workspace:
+ * device, fp_muon_info's size, 256-byte aligned, in any state; calls that may
+ * run concurrently, graphs' replays among them, need separate ones. */
+fp_status fp_muon_orthogonalize(fp_muon* muon, int32_t steps, const double* coefs, double eps, void* workspace,
+                                void* stream);
+
+/* The step.  hp: host array of n_groups sets of hyperparameters, matrix i
+ * taking hp[group[i]].  momentum: device fp32[partition], 16-byte aligned,
+ * zero-filled before the first step.  found_inf and grad_coef as in
+ * fp_params_adamw: on a skip weights and momentum are untouched and the copies
+ * receive the unchanged weights. */
+fp_status fp_muon_step(fp_muon* muon, int32_t n_groups, const fp_muon_hparams* hp, int32_t steps, const double* coefs,
+                       double eps, float* momentum, const int32_t* found_inf, const double* grad_coef, void* workspace,
+                       void* stream);
+
+/* ------------------------------------------------------------------ MXFP4 */
+
+/* Matrices in MXFP4, the form that a layer's products read, of the weights
+ * that a step wrote, of activations and of gradients.  A row's 32 consecutive
+ * elements share one scale byte s, an element being its e2m1 code (0, 0.5, 1,
+ * 1.5, 2, 3, 4, 6 and their negatives, 4 bits, the first element's in a byte's
+ * low half) times 2^(s - 127); s = 255 stands for NaN.  A row of n elements
+ * takes P = fp_mx4_padded(n) (n rounded up to a multiple of 256), the rest zero
+ * codes under zero scales: codes are uint8[rows][P / 2], scales
+ * uint8[rows][P / 32], back to back.
+ *
+ * fp_mx4_quantize: codes and scales receive the matrix x (rows x cols, row r
+ * from element r * pitch on, of `dtype`) along its rows: the operand of a
+ * product that contracts the columns; codes_t and scales_t along its columns,
+ * as a matrix of `cols` rows of `rows` elements: the operand of one that
+ * contracts the rows.  Either pair may be NULL.  In a block whose largest
+ * magnitude has the fp32 bits X (elements past the matrix's end do not count),
+ *   f = (X + h) >> 23;  s = f >= 255 ? 255 : max(0, f - 2);
+ *   y = |x| 2^(127 - s);  q = 0.5 for y < 2, 1 for y < 4, else 2;
+ * stochastic = 0: h = 2^21, the code is that of q * (y / q rounded to the
+ *   nearest whole number, ties to even);
+ * stochastic = 1: h = 2^22 - 1, the code is that of q * floor(y / q + d / 2^16),
+ *   d the high (columns' form: the low) half of the hash of fp_params_adamw8
+ *   with i = r * cols + c modulo 2^32 and the call's seed: unbiased but for
+ *   2^-17 of q, for gradients.  Give every call another seed.
+ * The code takes x's sign; codes of an s = 255 block are 0 (a block with an
+ * element that is not finite, or whose scale would pass fp32's range).
+ * fp_mx4_dequantize: out (rows x cols, pitch as above, of `dtype`) receives what
+ * codes and scales stand for; exact in fp32 and bf16 (a scale of 2^-133 and more),
+ * rounded to nearest even in fp16.
+ * fp_mx4_matmul: out[i][j] = sum over t < k of a[i][t] b[j][t], with a of m and
+ * b of n rows of k elements, summed in fp32 and rounded once to `dtype`;
+ * accumulate = 1 adds out's old value to the fp32 sum first.  A layer y = x w^T
+ * is (x by rows, w by rows), its input's gradient (dy by rows, w by columns), its
+ * weights' gradient (dy by columns, x by columns).  k in [1, 2^22].
+ * Rows and columns in [0, 2^31]; calls without elements do nothing.  codes are
+ * 16-byte aligned, scales 8-byte, x and out to their element size.  No buffer
+ * overlaps another that a call writes. */
+int64_t fp_mx4_padded(int64_t n);
+fp_status fp_mx4_quantize(int64_t rows, int64_t cols, int64_t pitch, int32_t dtype, const void* x, uint8_t* codes,
+                          uint8_t* scales, uint8_t* codes_t, uint8_t* scales_t, int32_t stochastic, uint64_t seed,
+                          void* stream);
+fp_status fp_mx4_dequantize(int64_t rows, int64_t cols, const uint8_t* codes, const uint8_t* scales, int32_t dtype,
+                            void* out, int64_t pitch, void* stream);
+fp_status fp_mx4_matmul(int64_t m, int64_t n, int64_t k, const uint8_t* a_codes, const uint8_t* a_scales,
+                        const uint8_t* b_codes, const uint8_t* b_scales, int32_t dtype, void* out, int64_t pitch,
+                        int32_t accumulate, void* stream);
+
 /* ------------------------------------------------------------------ helpers */
 
 /* Model-state bytes per GPU.  [DP] ZeRO figure (one formula per row) and

@@ -28,7 +28,7 @@ from ._lib import (FP_MAX_WORLD, FP_PATH_NO_SKIP, FP_PATH_NO_SKIP_SPLIT, FP_PATH
                    FP_PATH_TWO_PHASE, FP_STEP_EXACT_SKIP, FP_STEP_KEEP_GRAD, FP_STEP_NO_COOP,
                    FP_STEP_NO_SKIP, FP_FLAG_OVERFLOW, FP_FLAG_GAVE_UP, FlatParamError, check, lib)
 
-__all__ = ["Plan", "Units", "Params", "ParamsStep", "mx8_quantize", "mx8_dequantize", "Shard0Plan", "ReshardPlan", "reduce_shard_hybrid", "local_accumulate", "local_finish", "grad_coef", "scaler_update", "reduce_shard", "adamw_shard", "unshard", "shard_step", "ShardStep", "state_bytes",
+__all__ = ["Plan", "Units", "Params", "ParamsStep", "mx8_quantize", "mx8_dequantize", "Muon", "MuonStep", "MUON_COEFS", "mx4_padded", "mx4_empty", "mx4_quantize", "mx4_dequantize", "mx4_matmul", "Shard0Plan", "ReshardPlan", "reduce_shard_hybrid", "local_accumulate", "local_finish", "grad_coef", "scaler_update", "reduce_shard", "adamw_shard", "unshard", "shard_step", "ShardStep", "state_bytes",
            "workspace_bytes", "new_workspace", "workspace_timeouts", "FlatParamError", "FP_STEP_EXACT_SKIP",
            "FP_STEP_NO_SKIP", "FP_STEP_KEEP_GRAD", "FP_STEP_NO_COOP", "FP_PATH_ONE_PASS",
            "FP_PATH_TWO_PHASE", "FP_PATH_NO_SKIP", "FP_PATH_NO_SKIP_SPLIT", "FP_PATH_SPECULATIVE",
@@ -1091,6 +1091,345 @@ def mx8_dequantize(codes, scales, dst=None, *, root: bool = False):
     x = _f32(dst, n, "dst")
     _on_device(codes.device, lib().fp_mx8_dequantize, n, int(bool(root)), cp, sp, x)
     return dst
+
+
+# ------------------------------------------------------------------ muon
+MUON_COEFS = (3.4445, -4.7750, 2.0315)
+_ADJUST = {None: _lib.FP_MUON_ADJUST_NONE, "rms": _lib.FP_MUON_ADJUST_RMS, "shape": _lib.FP_MUON_ADJUST_SHAPE}
+
+
+def _muon_coefs(steps, coefs):
+    """(steps, array): coefs is (a, b, c) for every step, or one such triple per step."""
+    rows = [tuple(map(float, c)) for c in coefs] if hasattr(coefs[0], "__len__") else [tuple(map(float, coefs))] * int(steps)
+    if len(rows) != int(steps):
+        raise ValueError(f"{len(rows)} sets of coefficients for {steps} steps")
+    if any(len(r) != 3 for r in rows):
+        raise ValueError("coefficients are (a, b, c)")
+    return len(rows), (C.c_double * (3 * len(rows)))(*[x for r in rows for x in r])
+
+
+class Muon:
+    """Separate matrices of one rank whose optimizer step is orthogonalised
+    (fp_muon_*), beside Params for the tensors that AdamW takes.
+
+    grads: one 2-D gradient per matrix, all fp32, bf16 (or its bits in 16-bit
+    integers) or fp16.  master: their fp32 weights (None: a plan that only
+    orthogonalises).  copies: bf16 or fp16 matrices that receive the weights, or
+    None.  updates: fp32, bf16 or fp16 matrices that orthogonalize() writes, or
+    None.  groups: a group number per matrix (None: all 0).
+    Matrices are contiguous, at any element of a buffer.  The momentum sits in
+    an fp32 partition of `partition` elements, matrix i's from `offsets[i]` (a
+    multiple of 32) on.  The tensors must stay alive and in place for the plan's
+    life (set_grads changes the gradients); the plan is bound to their device.
+    A workspace belongs to calls that run one after the other.
+    Written tensors count as changed in place, as with Params.
+    """
+
+    def __init__(self, grads, master=None, copies=None, updates=None, groups=None):
+        grads = list(grads)
+        if not grads:
+            raise ValueError("need at least one matrix")
+        _no_none(grads, "grads")
+        n, device = len(grads), grads[0].device
+        for i, t in enumerate(grads):
+            if t.dim() != 2:
+                raise ValueError(f"grads[{i}] has {t.dim()} dimensions, a matrix has 2")
+        self.groups = [0] * n if groups is None else [int(k) for k in groups]
+        if len(self.groups) != n:
+            raise ValueError(f"groups: {len(self.groups)} numbers, expected {n}")
+        for k in (min(self.groups), max(self.groups)):  # here, as C takes their low 32 bits
+            if not 0 <= k < _lib.FP_MAX_GROUPS:
+                raise ValueError(f"group number {k} outside [0, {_lib.FP_MAX_GROUPS})")
+        if device.type != "cuda":
+            raise ValueError("grads[0] must be a device tensor")
+        if master is None and updates is None:
+            raise ValueError("neither master weights nor updates")
+        self.shapes = [tuple(t.shape) for t in grads]
+        self.sizes = [t.numel() for t in grads]
+        self._grad_dtype = grads[0].dtype
+
+        def table(tensors, dtype, name):
+            tensors = list(tensors)
+            _no_none(tensors[:1], name)
+            ptrs = _table(tensors, dtype or tensors[0].dtype, device, self.sizes, name)
+            for i, t in enumerate(tensors):
+                if tuple(t.shape) != self.shapes[i]:
+                    raise ValueError(f"{name}[{i}] has shape {tuple(t.shape)}, expected {self.shapes[i]}")
+            return tensors, ptrs
+
+        grads, gtab = table(grads, self._grad_dtype, "grads")
+        mtab = ctab = utab = None
+        cid = uid = _lib.FP_DTYPE_BF16
+        if master is not None:
+            master, mtab = table(master, _torch().float32, "master")
+        if copies is not None:
+            copies, ctab = table(copies, None, "copies")
+            cid = _dtype_id(copies[0].dtype, "copies", f32=False)
+        if updates is not None:
+            updates, utab = table(updates, None, "updates")
+            uid = _dtype_id(updates[0].dtype, "updates")
+        self.n_groups = max(self.groups) + 1
+        self._keep = (grads, master, copies, updates)
+        self._stepped = _version_holders([*(master or ()), *(copies or ())])
+        self._updated = _version_holders(updates or ())
+        self._device = device
+        out = C.c_void_p()
+        sides = [(C.c_int64 * n)(*[s[k] for s in self.shapes]) for k in (0, 1)]
+        with _torch().cuda.device(device):
+            check(lib().fp_muon_create(n, *sides, (C.c_int32 * n)(*self.groups), _dtype_id(self._grad_dtype, "grads"), gtab,
+                                       mtab, cid, ctab, uid, utab, C.byref(out)))
+        self._h = out
+        part, ws = C.c_int64(), C.c_int64()
+        check(lib().fp_muon_info(self._h, C.byref(part), C.byref(ws)))
+        self.partition, self.workspace_bytes = part.value, ws.value
+        offs = (C.c_int64 * n)()
+        check(lib().fp_muon_offsets(self._h, offs))
+        self.offsets = list(offs)
+
+    def close(self):
+        if getattr(self, "_h", None):
+            lib().fp_muon_destroy(self._h)
+            self._h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def new_workspace(self):
+        """Device workspace of a step or an orthogonalisation."""
+        return _torch().empty(self.workspace_bytes, dtype=_torch().uint8, device=self._device)
+
+    def new_momentum(self):
+        return _torch().zeros(self.partition, dtype=_torch().float32, device=self._device)
+
+    def tensor_slice(self, buf, i: int):
+        """Matrix i's part of a partition-sized tensor."""
+        return buf.narrow(0, self.offsets[i], self.sizes[i])
+
+    def set_grads(self, grads):
+        """New gradient tensors of the same shapes and dtype; ordered on the
+        current stream with the plan's other calls."""
+        grads = list(grads)
+        table = _table(grads, self._grad_dtype, self._device, self.sizes, "grads")
+        for i, t in enumerate(grads):
+            if tuple(t.shape) != self.shapes[i]:
+                raise ValueError(f"grads[{i}] has shape {tuple(t.shape)}, expected {self.shapes[i]}")
+        _on_device(self._device, lib().fp_muon_set_grads, self._h, table)
+        self._keep = (grads, *self._keep[1:])
+
+    def _workspace(self, workspace):
+        return _dev_ptr(workspace, (_torch().uint8,), self.workspace_bytes, "workspace")
+
+    def orthogonalize(self, workspace, *, steps: int = 5, coefs=MUON_COEFS, eps: float = 1e-7):
+        """updates[i] = grads[i] orthogonalised: its singular vectors with singular
+        values near 1 (for the default coefficients within about 0.3), by
+        `steps` Newton-Schulz steps.  coefs: (a, b, c), or one triple per step."""
+        if self._keep[3] is None:
+            raise ValueError("the plan has no updates")
+        _one_device(workspace, self._keep[0][0])
+        n, c = _muon_coefs(steps, coefs)
+        _on_device(self._device, lib().fp_muon_orthogonalize, self._h, n, c, float(eps), self._workspace(workspace))
+        _bump_versions(self._updated)
+        return self._keep[3]
+
+    def stepper(self, momentum, workspace, *, lr, beta=0.95, nesterov: bool = True, weight_decay=0.0, adjust="rms",
+                steps: int = 5, coefs=MUON_COEFS, eps: float = 1e-7, found_inf=None, grad_coef=None):
+        """A MuonStep: the step with its arguments marshalled once."""
+        return MuonStep(self, momentum, workspace, lr=lr, beta=beta, nesterov=nesterov, weight_decay=weight_decay,
+                        adjust=adjust, steps=steps, coefs=coefs, eps=eps, found_inf=found_inf, grad_coef=grad_coef)
+
+    def step(self, momentum, workspace, **kw):
+        """One step of every matrix: momentum, its orthogonalisation, weights and
+        copies.  Arguments of stepper(); lr, beta and weight_decay a number, or
+        one per group.  adjust: what the update is multiplied by beside lr,
+        "rms" (0.2 sqrt of the larger side), "shape" (sqrt of rows / columns, at
+        least 1) or None (1)."""
+        self.stepper(momentum, workspace, **kw)()
+
+
+class MuonStep:
+    """Muon.step with its arguments marshalled once: a call takes the learning
+    rate where it changes, which later calls keep (a refused call leaves the one
+    before).  For one thread at a time, as ParamsStep."""
+
+    def __init__(self, plan, momentum, workspace, *, lr, beta, nesterov, weight_decay, adjust, steps, coefs, eps, found_inf,
+                 grad_coef):
+        if plan._keep[1] is None:
+            raise ValueError("the plan has no master weights")
+        _one_device(momentum, workspace, found_inf, grad_coef, plan._keep[0][0])
+        if adjust not in _ADJUST:
+            raise ValueError(f"adjust is one of {tuple(_ADJUST)}, not {adjust!r}")
+        given = [lr, beta, weight_decay]
+        lengths = {len(x) for x in given if hasattr(x, "__len__")}
+        n = lengths.pop() if lengths else plan.n_groups
+        if lengths or n < plan.n_groups:
+            raise ValueError(f"hyperparameters: a number, or as many values as groups (at least {plan.n_groups}) each")
+        self._n = n
+        rows = zip(*[self._per_group(x) for x in given])
+        self._hp = (_lib.fp_muon_hparams * n)(*[_lib.fp_muon_hparams(*r, int(bool(nesterov)), _ADJUST[adjust]) for r in rows])
+        self._steps, self._coefs = _muon_coefs(steps, coefs)
+        self._eps = float(eps)
+        self._momentum = _f32(momentum, plan.partition, "momentum")
+        self._workspace = plan._workspace(workspace)
+        self._found = _dev_ptr(found_inf, (_torch().int32,), 1, "found_inf") if found_inf is not None else None
+        self._coef = _coef_ptr(grad_coef)
+        self._plan = plan
+        self._keep = (momentum, workspace, found_inf, grad_coef)
+
+    def _per_group(self, x):
+        v = list(x) if hasattr(x, "__len__") else [x] * self._n
+        if len(v) != self._n:
+            raise ValueError(f"{len(v)} values for {self._n} groups")
+        return [float(k) for k in v]
+
+    def __call__(self, *, lr=None):
+        p = self._plan
+        before = [h.lr for h in self._hp]
+        if lr is not None:
+            for h, x in zip(self._hp, self._per_group(lr)):
+                h.lr = x
+        try:
+            _on_device(p._device, lib().fp_muon_step, p._h, self._n, self._hp, self._steps, self._coefs, self._eps,
+                       self._momentum, self._found, self._coef, self._workspace)
+        except Exception:
+            for h, x in zip(self._hp, before):
+                h.lr = x
+            raise
+        _bump_versions(p._stepped)
+
+
+# ------------------------------------------------------------------ MXFP4
+_MX4_DTYPES = None
+
+
+def _mx4_dtypes():
+    """(dtypes of codes, dtypes of scales): bytes, or torch's own."""
+    global _MX4_DTYPES
+    if _MX4_DTYPES is None:
+        torch = _torch()
+        pair = getattr(torch, "float4_e2m1fn_x2", None)
+        _MX4_DTYPES = (torch.uint8, *([pair] if pair is not None else [])), (torch.float8_e8m0fnu, torch.uint8)
+    return _MX4_DTYPES
+
+
+def mx4_padded(n: int) -> int:
+    """Elements that a row of n takes in MXFP4: n rounded up to a multiple of 256."""
+    p = lib().fp_mx4_padded(int(n))
+    if p < 0:
+        raise ValueError(f"rows of {n} elements")
+    return p
+
+
+def _matrix(t, dtypes, name):
+    """(pointer, rows, columns, pitch) of a device matrix whose rows are contiguous."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    if dtypes is not None and t.dtype not in dtypes:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected one of {dtypes}")
+    if t.dim() != 2:
+        raise ValueError(f"{name} has {t.dim()} dimensions, a matrix has 2")
+    r, c = t.shape
+    pitch = t.stride(0) if r > 1 else c
+    if (c > 1 and t.stride(1) != 1) or (r > 1 and pitch < c):
+        raise ValueError(f"{name}: a row's elements must be contiguous, and rows must not overlap (strides {t.stride()})")
+    return t.data_ptr(), r, c, pitch
+
+
+def _mx4_form(codes, scales, rows, width, name):
+    """Pointers of one MXFP4 form, checked against its shape."""
+    cd, sd = _mx4_dtypes()
+    p = mx4_padded(width)
+    if tuple(codes.shape) != (rows, p // 2) or tuple(scales.shape) != (rows, p // _lib.FP_MX_BLOCK):
+        raise ValueError(f"{name}: codes {tuple(codes.shape)} and scales {tuple(scales.shape)}, expected "
+                         f"{(rows, p // 2)} and {(rows, p // _lib.FP_MX_BLOCK)} for {rows} rows of {width}")
+    return _dev_ptr(codes, cd, 0, f"{name} codes"), _dev_ptr(scales, sd, 0, f"{name} scales")
+
+
+def mx4_empty(rows: int, width: int, device):
+    """(codes, scales) for `rows` rows of `width` elements, not filled."""
+    torch, p = _torch(), mx4_padded(width)
+    return (torch.empty(rows, p // 2, dtype=torch.uint8, device=device),
+            torch.empty(rows, p // _lib.FP_MX_BLOCK, dtype=torch.uint8, device=device).view(_mx4_dtypes()[1][0]))
+
+
+def mx4_quantize(src, codes=None, scales=None, codes_t=None, scales_t=None, *, rows: bool = True, transposed: bool = False,
+                 seed: Optional[int] = None):
+    """MXFP4 of a matrix (fp32, bf16 or fp16; its rows may be apart): (codes,
+    scales) along its rows, what a product that contracts the columns reads;
+    with transposed also (codes_t, scales_t) along its columns, as a matrix of
+    src.shape[1] rows, what a product that contracts the rows reads; with
+    rows=False that alone.  Rounded to nearest even, or with a seed
+    stochastically (gradients; another seed for every call).  Buffers that are
+    not given are allocated, those of a form that is not wanted may not be."""
+    _one_device(src, codes, scales, codes_t, scales_t)
+    x, r, c, pitch = _matrix(src, None, "src")
+    dtype = _dtype_id(src.dtype, "src")
+    if not rows and not transposed:
+        raise ValueError("neither the rows' nor the columns' form is wanted")
+    got, ptrs = [], []
+    for want, held, shape, name in ((rows, (codes, scales), (r, c), "rows' form"),
+                                    (transposed, (codes_t, scales_t), (c, r), "columns' form")):
+        if not want:
+            if held != (None, None):
+                raise ValueError(f"buffers of the {name}, which is not wanted")
+            ptrs += [None, None]
+            continue
+        if (held[0] is None) != (held[1] is None):
+            raise ValueError("codes and scales go together")
+        if held[0] is None:
+            held = mx4_empty(*shape, src.device)
+        got += held
+        ptrs += _mx4_form(*held, *shape, name)
+    _on_device(src.device, lib().fp_mx4_quantize, r, c, pitch, dtype, x, *ptrs, int(seed is not None),
+               0 if seed is None else int(seed) & 0xFFFFFFFFFFFFFFFF)
+    return tuple(got)
+
+
+def mx4_dequantize(codes, scales, cols: int, dst=None, *, dtype=None):
+    """dst (rows x cols; allocated here in `dtype`, bf16 by default, when None):
+    what MXFP4 codes and scales stand for."""
+    torch = _torch()
+    r = codes.shape[0]
+    ptrs = _mx4_form(codes, scales, r, int(cols), "operand")
+    if dst is None:
+        dst = torch.empty(r, int(cols), dtype=dtype or torch.bfloat16, device=codes.device)
+    elif dtype is not None and dst.dtype != dtype:
+        raise TypeError(f"dst has dtype {dst.dtype}, not {dtype}")
+    _one_device(codes, scales, dst)
+    x, rows, width, pitch = _matrix(dst, None, "dst")
+    if (rows, width) != (r, int(cols)):
+        raise ValueError(f"dst has shape {(rows, width)}, expected {(r, int(cols))}")
+    _on_device(codes.device, lib().fp_mx4_dequantize, r, width, *ptrs, _dtype_id(dst.dtype, "dst"), x, pitch)
+    return dst
+
+
+def mx4_matmul(a, b, out=None, *, accumulate: bool = False, dtype=None):
+    """out (rows of a x rows of b; allocated here in `dtype`, bf16 by default,
+    when None) = a b^T of two MXFP4 operands (codes, scales) with rows of one
+    padded length; accumulate adds to out.  A layer y = x w^T with x and w by
+    rows; its input's gradient: dy by rows, w by columns; its weights' gradient:
+    dy by columns, x by columns."""
+    torch = _torch()
+    (ac, asc), (bc, bsc) = a, b
+    k = 2 * ac.shape[1]
+    if bc.shape[1] != ac.shape[1]:
+        raise ValueError(f"rows of {k} and {2 * bc.shape[1]} elements (padded)")
+    m, n = ac.shape[0], bc.shape[0]
+    ptrs = (*_mx4_form(ac, asc, m, k, "a"), *_mx4_form(bc, bsc, n, k, "b"))
+    if out is None:
+        if accumulate:
+            raise ValueError("accumulate needs out")
+        out = torch.empty(m, n, dtype=dtype or torch.bfloat16, device=ac.device)
+    elif dtype is not None and out.dtype != dtype:
+        raise TypeError(f"out has dtype {out.dtype}, not {dtype}")
+    _one_device(ac, asc, bc, bsc, out)
+    x, rows, cols, pitch = _matrix(out, None, "out")
+    if (rows, cols) != (m, n):
+        raise ValueError(f"out has shape {(rows, cols)}, expected {(m, n)}")
+    _on_device(ac.device, lib().fp_mx4_matmul, m, n, k, *ptrs, _dtype_id(out.dtype, "out"), x, pitch, int(bool(accumulate)))
+    return out
 
 
 # ------------------------------------------------------------------ helpers

@@ -39,6 +39,10 @@ FP_DTYPE_BF16 = 1
 FP_DTYPE_F16 = 2
 FP_MAX_GROUPS = 16
 FP_MX_BLOCK = 32
+FP_MUON_ADJUST_NONE = 0
+FP_MUON_ADJUST_RMS = 1
+FP_MUON_ADJUST_SHAPE = 2
+FP_MUON_MAX_STEPS = 32
 
 _i32, _i64, _f32, _f64, _vp = C.c_int32, C.c_int64, C.c_float, C.c_double, C.c_void_p
 _u64 = C.c_uint64
@@ -52,6 +56,10 @@ class fp_view(C.Structure):
 class fp_adamw_hparams(C.Structure):
     _fields_ = [("lr", _f64), ("beta1", _f64), ("beta2", _f64), ("eps", _f64),
                 ("weight_decay", _f64), ("step", _i64)]
+
+
+class fp_muon_hparams(C.Structure):
+    _fields_ = [("lr", _f64), ("beta", _f64), ("weight_decay", _f64), ("nesterov", _i32), ("adjust", _i32)]
 
 
 class fp_step_args(C.Structure):
@@ -118,6 +126,17 @@ SIGNATURES = {
     "fp_params_adamw8": (_i32, [_vp, _i32, _vp, _vp, _vp, _vp, _vp, _u64, _vp, _vp, _vp]),
     "fp_mx8_quantize": (_i32, [_i64, _i32, _vp, _vp, _vp, _vp]),
     "fp_mx8_dequantize": (_i32, [_i64, _i32, _vp, _vp, _vp, _vp]),
+    "fp_muon_create": (_i32, [_i32, _vp, _vp, _vp, _i32, _vp, _vp, _i32, _vp, _i32, _vp, C.POINTER(_vp)]),
+    "fp_muon_destroy": (None, [_vp]),
+    "fp_muon_info": (_i32, [_vp, _vp, _vp]),
+    "fp_muon_offsets": (_i32, [_vp, _vp]),
+    "fp_muon_set_grads": (_i32, [_vp, _vp, _vp]),
+    "fp_muon_orthogonalize": (_i32, [_vp, _i32, _vp, _f64, _vp, _vp]),
+    "fp_muon_step": (_i32, [_vp, _i32, _vp, _i32, _vp, _f64, _vp, _vp, _vp, _vp, _vp]),
+    "fp_mx4_padded": (_i64, [_i64]),
+    "fp_mx4_quantize": (_i32, [_i64, _i64, _i64, _i32, _vp, _vp, _vp, _vp, _vp, _i32, _u64, _vp]),
+    "fp_mx4_dequantize": (_i32, [_i64, _i64, _vp, _vp, _i32, _vp, _i64, _vp]),
+    "fp_mx4_matmul": (_i32, [_i64, _i64, _i64, _vp, _vp, _vp, _vp, _i32, _vp, _i64, _i32, _vp]),
     "fp_state_bytes": (_i32, [_f64, _i32, _f64, _i32, C.POINTER(_f64)]),
     "fp_status_string": (C.c_char_p, [_i32]),
     "fp_last_error": (C.c_char_p, []),

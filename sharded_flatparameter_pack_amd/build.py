@@ -19,7 +19,7 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libflatparam.so")
 SOURCES = ["abi.hip", "step_kernels.hip", "unit_kernels.hip", "segment_kernels.hip",
            "local_kernels.hip", "hybrid_kernels.hip", "noalloc.hip", "params.hip",
-           "params_kernels.hip"]
+           "params_kernels.hip", "muon.hip", "muon_kernels.hip", "mx4.hip", "mx4_kernels.hip"]
 ARCH = "gfx950"
 
 FLAGS = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}", "-ffp-contract=off",

@@ -1,0 +1,117 @@
+// fp_matrix.h -- argument blocks and launcher declarations of the operators on
+// matrix parameters: Newton-Schulz orthogonalisation and the step that takes
+// it (muon_kernels.hip), MXFP4 quantisation and product (mx4_kernels.hip).
+#pragma once
+
+#include "fp_internal.h"
+
+namespace fpk {
+
+// ---------------------------------------------------------------- muon
+
+// One matrix of a plan.  Inside the workspace it is padded with zeros to
+// multiples of kPad rows and columns.  With m the smaller side and n the
+// other: P is the matrix as m rows of n, Q as n rows of m (one of the two has
+// the matrix's own orientation), both fp16; x the matrix in fp32, in its own
+// orientation.  Offsets are bytes from the workspace's start.
+struct MuonRec {
+    float* master;            // null in a plan that only orthogonalises
+    void* copy;               // bf16 / fp16 weights, or null
+    void* update;             // receives the orthogonalised matrix, or null
+    int64_t offset;           // of the momentum, in the partition
+    int32_t rows, cols;
+    int32_t rp, cp;           // padded
+    int32_t group;
+    int32_t chunks;           // of the norm's partial sums
+    int64_t chunk;            // elements of one
+    int64_t x, p, q[2];       // Q has two places: a step of the iteration reads one and writes the other
+    int64_t a, b;             // fp16 [m][m], their diagonals zero
+    int64_t da, db;           // fp32 [m]: the diagonals
+    int64_t part;             // fp64 [chunks]
+};
+
+constexpr int kPad = 64;
+inline int64_t pad64(int64_t n) { return (n + kPad - 1) / kPad * kPad; }
+
+// Tile (ti, tj) of matrix `mat`; what a tile is depends on the kernel.
+struct MatTile {
+    int32_t mat, ti, tj, pad;
+};
+
+struct MuonGroup {
+    double lr, beta, decay;   // decay = 1 - lr * weight_decay
+    int32_t nesterov, adjust;
+};
+
+// The scales of one step of the iteration: powers of two by which the fp16
+// forms are multiplied so that no element passes fp16's range.
+struct MuonScale {
+    float x, a, b, x_next;
+};
+
+struct MuonArgs {
+    const MuonRec* recs;
+    const void* const* grads;
+    char* ws;
+    float* momentum;          // null: the gradients themselves are orthogonalised
+    const int32_t* found_inf;
+    const double* g_coef;
+    double eps;
+    int32_t grad_dtype, copy_dtype, update_dtype;
+    float ca, cb, cc;         // the iteration's coefficients
+    MuonScale s;
+    int32_t step;             // of the iteration: which Q is read
+    const MatTile* tiles;
+    int32_t n_tiles;
+    MuonGroup g[FP_MAX_GROUPS];
+};
+
+enum { kTile256 = 0, kTile128 = 1, kTile64 = 2 };
+constexpr int kTileSide[3] = {256, 128, 64};
+
+hipError_t launch_muon_moment(const MuonArgs& a, hipStream_t s);
+hipError_t launch_muon_cast(const MuonArgs& a, hipStream_t s);
+hipError_t launch_muon_gram(const MuonArgs& a, int shape, hipStream_t s);
+hipError_t launch_muon_poly(const MuonArgs& a, int shape, hipStream_t s);
+// last: the matrix leaves, as update (to_weights 0) or into the weights.
+hipError_t launch_muon_next(const MuonArgs& a, int shape, bool last, bool to_weights, hipStream_t s);
+
+// ---------------------------------------------------------------- MXFP4
+
+constexpr int kMx4Block = 32;
+constexpr int kMx4Pad = 256;  // rows are padded to multiples of so many elements
+inline int64_t mx4_pad(int64_t n) { return (n + kMx4Pad - 1) / kMx4Pad * kMx4Pad; }
+
+struct Mx4QuantArgs {
+    const void* x;
+    int64_t rows, cols, pitch;      // elements
+    uint8_t *codes, *scales;        // rows' form, or null
+    uint8_t *codes_t, *scales_t;    // columns' form, or null
+    int64_t cp, rp;                 // padded columns and rows
+    uint32_t key;
+    int32_t dtype, stochastic;
+};
+
+struct Mx4DequantArgs {
+    const uint8_t *codes, *scales;
+    void* out;
+    int64_t rows, cols, pitch, cp;
+    int32_t dtype;
+};
+
+struct Mx4MatmulArgs {
+    const uint8_t *a, *as, *b, *bs;
+    void* out;
+    int64_t m, n, kp, pitch;
+    int32_t dtype, accumulate;
+    int32_t tiles_m, tiles_n;
+};
+
+// Lanes of a launch.
+int64_t mx4_quantize_lanes(const Mx4QuantArgs& a);
+int64_t mx4_matmul_lanes(const Mx4MatmulArgs& a);
+hipError_t launch_mx4_quantize(const Mx4QuantArgs& a, hipStream_t s);
+hipError_t launch_mx4_dequantize(const Mx4DequantArgs& a, hipStream_t s);
+hipError_t launch_mx4_matmul(const Mx4MatmulArgs& a, hipStream_t s);
+
+}  // namespace fpk

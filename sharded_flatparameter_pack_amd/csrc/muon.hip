@@ -1,0 +1,522 @@
+// muon.hip -- the entry points of the orthogonalisation and of the step that
+// takes it (fp_muon_*): argument checks, plans, their device tables, the
+// iteration's scales.  Every check runs before anything is enqueued.
+
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstring>
+#include <mutex>
+#include <vector>
+
+#include "fp_matrix.h"
+#include "plan_util.h"
+
+using namespace fpk;
+
+namespace {
+
+constexpr int64_t kMaxSide = 1 << 20;
+
+int64_t dtype_bytes(int32_t dtype) { return dtype == FP_DTYPE_F32 ? 4 : 2; }
+
+// The matrices of a batch share every launch and the workspace.  A batch is
+// closed once it holds this much of it.
+constexpr int64_t kBatchBytes = (int64_t)1 << 31;
+
+// Tiles [first, first + n) of the plan's table.
+struct Run {
+    int64_t first = 0, n = 0;
+};
+
+struct Batch {
+    int32_t from = 0, to = 0;  // matrices
+    Run moment, cast, half, full;
+    int half_shape = kTile64, full_shape = kTile64;
+};
+
+int64_t tiles_half(const MuonRec& r, int side) {
+    const int64_t m = ceil_div64(std::min(r.rp, r.cp), side);
+    return m * (m + 1) / 2;
+}
+int64_t tiles_full(const MuonRec& r, int side) { return ceil_div64(r.rp, side) * ceil_div64(r.cp, side); }
+
+}  // namespace
+
+struct fp_muon {
+    int32_t n = 0;
+    int device = -1;
+    int32_t grad_dtype = FP_DTYPE_F32, copy_dtype = FP_DTYPE_BF16, update_dtype = FP_DTYPE_BF16;
+    bool has_master = false, has_update = false;
+    int32_t max_group = 0;
+    int64_t partition = 0, workspace = 0, tiles = 0;
+    std::vector<int64_t> numel, offset;
+    std::vector<Batch> batches;
+    std::vector<Span> written;         // weights, copies and updates
+    void* dev = nullptr;               // records, gradient table, tile table
+    void* staging = nullptr;           // pinned, of the gradient table's uploads
+    hipEvent_t uploaded = nullptr;
+    std::mutex mu;                     // guards the fields below
+    std::vector<Span> read;            // gradients
+    const void* checked[2] = {};       // momentum and workspace that last passed the overlap checks
+    bool have_checked = false;
+
+    const MuonRec* recs() const { return static_cast<const MuonRec*>(dev); }
+    const void** grads() const { return reinterpret_cast<const void**>(static_cast<char*>(dev) + sizeof(MuonRec) * (size_t)n); }
+    const MatTile* tile_table() const { return reinterpret_cast<const MatTile*>(grads() + (n + 1) / 2 * 2); }
+};
+
+namespace {
+
+void free_plan(fp_muon* p) {
+    int cur = -1;
+    (void)hipGetDevice(&cur);
+    if (p->device >= 0) (void)hipSetDevice(p->device);
+    if (p->uploaded) (void)hipEventSynchronize(p->uploaded), (void)hipEventDestroy(p->uploaded);
+    if (p->staging) (void)hipHostFree(p->staging);
+    if (p->dev) (void)hipFree(p->dev);
+    if (cur >= 0) (void)hipSetDevice(cur);
+    delete p;
+}
+
+fp_status check_device(const fp_muon* p) {
+    int device = -1;
+    hipError_t e = hipGetDevice(&device);
+    if (e != hipSuccess) return device_error(e, "hipGetDevice");
+    if (device != p->device)
+        return bad(FP_ERR_INVALID, "muon plan was created on device %d, current is %d", p->device, device);
+    return FP_OK;
+}
+
+fp_status check_grads(const std::vector<int64_t>& numel, int32_t dtype, const std::vector<Span>& written,
+                      const void* const* grads, std::vector<Span>* spans) {
+    const int64_t es = dtype_bytes(dtype);
+    std::vector<Span> v;
+    for (size_t i = 0; i < numel.size(); ++i) {
+        if (numel[i] == 0) continue;
+        if (grads[i] == nullptr) return bad(FP_ERR_INVALID, "grads[%zu] is NULL", i);
+        if (!on(grads[i], (uintptr_t)es)) return bad(FP_ERR_ALIGN, "grads[%zu] misaligned", i);
+        v.push_back(span_of(grads[i], numel[i] * es));
+        if (meets_any(v.back(), written)) return bad(FP_ERR_INVALID, "grads[%zu] overlaps a weight, a copy or an update", i);
+    }
+    *spans = joined(std::move(v));
+    return FP_OK;
+}
+
+// Lays the matrix out in the workspace from byte `at` on; returns its end.
+int64_t lay_out(MuonRec* r, int64_t at) {
+    auto take = [&](int64_t bytes) {
+        const int64_t from = at;
+        at += ceil_div64(bytes, 256) * 256;
+        return from;
+    };
+    const int64_t all = (int64_t)r->rp * r->cp, m = std::min(r->rp, r->cp);
+    r->x = take(4 * all);
+    r->p = take(2 * all);
+    r->q[0] = take(2 * all);
+    r->q[1] = take(2 * all);
+    r->a = take(2 * m * m);
+    r->b = take(2 * m * m);
+    r->da = take(4 * m);
+    r->db = take(4 * m);
+    r->part = take(8 * r->chunks);
+    return at;
+}
+
+// The tile that a batch's products take: with n tiles on 256 CUs, the busiest
+// has ceil(n / 256), which take kWork each, or kAlone where one by itself
+// leaves its CU waiting (in units of a 256-wide tile's time).
+int choose_shape(const std::vector<MuonRec>& recs, int32_t from, int32_t to, int64_t (*tiles)(const MuonRec&, int)) {
+    constexpr double kWork[3] = {1.0, 0.31, 0.12}, kAlone[3] = {1.0, 0.45, 0.25};
+    int best = kTile64;
+    double least = 0.0;
+    for (int shape : {kTile256, kTile128, kTile64}) {
+        int64_t n = 0;
+        for (int32_t i = from; i < to; ++i) n += tiles(recs[(size_t)i], kTileSide[shape]);
+        const double time = std::max(kAlone[shape], kWork[shape] * (double)ceil_div64(n, 256));
+        if (shape == kTile256 || time < least) best = shape, least = time;
+    }
+    return best;
+}
+
+// Closes a batch: its tiles, appended to the table.
+void close_batch(const std::vector<MuonRec>& recs, Batch* b, std::vector<MatTile>* table) {
+    b->half_shape = choose_shape(recs, b->from, b->to, tiles_half);
+    b->full_shape = choose_shape(recs, b->from, b->to, tiles_full);
+    auto run = [&](Run* r, auto&& each) {
+        r->first = (int64_t)table->size();
+        for (int32_t i = b->from; i < b->to; ++i)
+            if (recs[i].rows > 0 && recs[i].cols > 0) each(i, recs[i]);
+        r->n = (int64_t)table->size() - r->first;
+    };
+    auto grid = [&](int32_t i, int64_t rows, int64_t cols) {
+        for (int64_t ti = 0; ti < rows; ++ti)
+            for (int64_t tj = 0; tj < cols; ++tj) table->push_back({i, (int32_t)ti, (int32_t)tj, 0});
+    };
+    run(&b->moment, [&](int32_t i, const MuonRec& r) { grid(i, r.chunks, 1); });
+    run(&b->cast, [&](int32_t i, const MuonRec& r) { grid(i, r.rp / 64, r.cp / 64); });
+    run(&b->half, [&](int32_t i, const MuonRec& r) {
+        const int64_t m = ceil_div64(std::min(r.rp, r.cp), kTileSide[b->half_shape]);
+        for (int64_t ti = 0; ti < m; ++ti)
+            for (int64_t tj = 0; tj <= ti; ++tj) table->push_back({i, (int32_t)ti, (int32_t)tj, 0});
+    });
+    run(&b->full, [&](int32_t i, const MuonRec& r) {
+        const int side = kTileSide[b->full_shape];
+        grid(i, ceil_div64(r.rp, side), ceil_div64(r.cp, side));
+    });
+}
+
+fp_status create(int32_t n, const int64_t* rows, const int64_t* cols, const int32_t* group, int32_t grad_dtype,
+                 const void* const* grads, float* const* master, int32_t copy_dtype, void* const* copies,
+                 int32_t update_dtype, void* const* updates, fp_muon** out) {
+    if (out == nullptr) return bad(FP_ERR_INVALID, "out is NULL");
+    *out = nullptr;
+    if (n < 1) return bad(FP_ERR_RANGE, "n must be >= 1");
+    if (rows == nullptr || cols == nullptr || grads == nullptr) return bad(FP_ERR_INVALID, "rows, cols or grads is NULL");
+    if (grad_dtype < FP_DTYPE_F32 || grad_dtype > FP_DTYPE_F16) return bad(FP_ERR_INVALID, "unknown grad_dtype %d", grad_dtype);
+    if (copies != nullptr && copy_dtype != FP_DTYPE_BF16 && copy_dtype != FP_DTYPE_F16)
+        return bad(FP_ERR_INVALID, "copy_dtype must be bf16 or fp16 (got %d)", copy_dtype);
+    if (updates != nullptr && (update_dtype < FP_DTYPE_F32 || update_dtype > FP_DTYPE_F16))
+        return bad(FP_ERR_INVALID, "unknown update_dtype %d", update_dtype);
+    if (copies != nullptr && master == nullptr) return bad(FP_ERR_INVALID, "copies need master weights");
+    if (master == nullptr && updates == nullptr) return bad(FP_ERR_INVALID, "neither master weights nor updates");
+    std::vector<MuonRec> recs((size_t)n);
+    std::vector<MatTile> table;
+    std::vector<Batch> batches;
+    std::vector<Span> written;
+    std::vector<int64_t> sizes, offsets;
+    int64_t partition = 0, workspace = 0, at = 0;
+    int32_t max_group = 0;
+    Batch open;
+    for (int32_t i = 0; i < n; ++i) {
+        if (rows[i] < 0 || rows[i] > kMaxSide || cols[i] < 0 || cols[i] > kMaxSide)
+            return bad(FP_ERR_RANGE, "matrix %d: %lld x %lld, sides go up to %lld", i, (long long)rows[i], (long long)cols[i],
+                       (long long)kMaxSide);
+        MuonRec& r = recs[(size_t)i];
+        std::memset(&r, 0, sizeof r);
+        if (group != nullptr) {
+            if (group[i] < 0 || group[i] >= FP_MAX_GROUPS)
+                return bad(FP_ERR_RANGE, "matrix %d: group %d outside [0, %d)", i, group[i], FP_MAX_GROUPS);
+            r.group = group[i];
+            max_group = std::max(max_group, group[i]);
+        }
+        const int64_t numel = rows[i] * cols[i];
+        sizes.push_back(numel);
+        offsets.push_back(partition);
+        r.offset = partition;
+        r.rows = (int32_t)rows[i];
+        r.cols = (int32_t)cols[i];
+        if (numel > 0) {
+            auto place = [&](void* p, int64_t size, const char* what) -> fp_status {
+                if (p == nullptr) return bad(FP_ERR_INVALID, "%s[%d] is NULL", what, i);
+                if (!on(p, (uintptr_t)size)) return bad(FP_ERR_ALIGN, "%s[%d] misaligned", what, i);
+                written.push_back(span_of(p, numel * size));
+                return FP_OK;
+            };
+            fp_status st = FP_OK;
+            if (master != nullptr) {
+                if ((st = place(master[i], 4, "master")) != FP_OK) return st;
+                r.master = master[i];
+            }
+            if (copies != nullptr) {
+                if ((st = place(copies[i], 2, "copies")) != FP_OK) return st;
+                r.copy = copies[i];
+            }
+            if (updates != nullptr) {
+                if ((st = place(updates[i], dtype_bytes(update_dtype), "updates")) != FP_OK) return st;
+                r.update = updates[i];
+            }
+            r.rp = (int32_t)pad64(rows[i]);
+            r.cp = (int32_t)pad64(cols[i]);
+            r.chunk = std::max<int64_t>(8192, ceil_div64(ceil_div64(numel, 256), 1024) * 1024);
+            r.chunks = (int32_t)ceil_div64(numel, r.chunk);
+            partition += ceil_div64(numel, 32) * 32;
+            if ((int64_t)(r.rp / 64) * (r.cp / 64) > 0xFFFFFFFFLL / 256)
+                return bad(FP_ERR_RANGE, "matrix %d needs more workgroups than one launch holds", i);
+            at = lay_out(&r, at);
+            workspace = std::max(workspace, at);
+        }
+        open.to = i + 1;
+        if (at >= kBatchBytes || i + 1 == n) {
+            close_batch(recs, &open, &table);
+            batches.push_back(open);
+            open = Batch();
+            open.from = open.to = i + 1;
+            at = 0;
+        }
+    }
+    std::sort(written.begin(), written.end());
+    for (size_t i = 1; i < written.size(); ++i)
+        if (meet(written[i - 1], written[i])) return bad(FP_ERR_INVALID, "two of the weights, copies and updates overlap");
+    written = joined(std::move(written));
+    std::vector<Span> read;
+    fp_status st = check_grads(sizes, grad_dtype, written, grads, &read);
+    if (st != FP_OK) return st;
+
+    fp_muon* p = new fp_muon();
+    p->n = n;
+    p->grad_dtype = grad_dtype;
+    p->copy_dtype = copy_dtype;
+    p->update_dtype = update_dtype;
+    p->has_master = master != nullptr;
+    p->has_update = updates != nullptr;
+    p->max_group = max_group;
+    p->partition = partition;
+    p->workspace = workspace;
+    p->tiles = (int64_t)table.size();
+    p->numel = std::move(sizes);
+    p->offset = std::move(offsets);
+    p->batches = std::move(batches);
+    p->written = std::move(written);
+    p->read = std::move(read);
+    const size_t rec_b = sizeof(MuonRec) * (size_t)n, ptr_b = sizeof(void*) * (size_t)((n + 1) / 2 * 2);
+    const size_t tile_b = sizeof(MatTile) * table.size();
+    hipError_t e = hipGetDevice(&p->device);
+    if (e == hipSuccess) e = hipMalloc(&p->dev, rec_b + ptr_b + tile_b);
+    char* dev = static_cast<char*>(p->dev);
+    if (e == hipSuccess) e = hipMemcpy(dev, recs.data(), rec_b, hipMemcpyHostToDevice);
+    if (e == hipSuccess) e = hipMemcpy(dev + rec_b, grads, sizeof(void*) * (size_t)n, hipMemcpyHostToDevice);
+    if (e == hipSuccess && tile_b > 0) e = hipMemcpy(dev + rec_b + ptr_b, table.data(), tile_b, hipMemcpyHostToDevice);
+    if (e != hipSuccess) {
+        free_plan(p);
+        return device_error(e, "building the muon tables");
+    }
+    *out = p;
+    return FP_OK;
+}
+
+fp_status set_grads(fp_muon* p, const void* const* grads, void* stream) {
+    if (p == nullptr || grads == nullptr) return bad(FP_ERR_INVALID, "muon or grads is NULL");
+    fp_status st = check_device(p);
+    if (st != FP_OK) return st;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    hipStreamCaptureStatus capture = hipStreamCaptureStatusNone;
+    hipError_t e = hipStreamIsCapturing(s, &capture);
+    if (e != hipSuccess) return device_error(e, "hipStreamIsCapturing");
+    if (capture != hipStreamCaptureStatusNone)
+        return bad(FP_ERR_INVALID, "the gradients cannot be changed while the stream is captured");
+    std::vector<Span> read;
+    if ((st = check_grads(p->numel, p->grad_dtype, p->written, grads, &read)) != FP_OK) return st;
+    std::lock_guard<std::mutex> lock(p->mu);
+    const size_t bytes = sizeof(void*) * (size_t)p->n;
+    if (p->staging == nullptr) {
+        if ((e = hipHostMalloc(&p->staging, bytes, hipHostMallocDefault)) != hipSuccess) {
+            p->staging = nullptr;
+            return device_error(e, "allocating the gradient table's staging");
+        }
+    }
+    if (p->uploaded == nullptr) {
+        if ((e = hipEventCreateWithFlags(&p->uploaded, hipEventDisableTiming)) != hipSuccess) {
+            p->uploaded = nullptr;
+            return device_error(e, "creating the upload event");
+        }
+    } else if ((e = hipEventSynchronize(p->uploaded)) != hipSuccess) {  // the staging may still feed the last upload
+        return device_error(e, "hipEventSynchronize");
+    }
+    std::memcpy(p->staging, grads, bytes);
+    if ((e = hipMemcpyAsync(p->grads(), p->staging, bytes, hipMemcpyHostToDevice, s)) != hipSuccess)
+        return device_error(e, "uploading the gradient table");
+    if ((e = hipEventRecord(p->uploaded, s)) != hipSuccess) return device_error(e, "hipEventRecord");
+    p->read = std::move(read);
+    p->have_checked = false;
+    return FP_OK;
+}
+
+// Momentum (may be null) and workspace: alignment, and no overlap with each
+// other or with the plan's tensors.
+fp_status check_buffers(fp_muon* p, const float* momentum, bool step, const void* workspace) {
+    if (step && momentum == nullptr && p->partition > 0) return bad(FP_ERR_INVALID, "momentum is NULL");
+    if (!on(momentum, 16)) return bad(FP_ERR_ALIGN, "momentum is not 16-byte aligned");
+    if (workspace == nullptr && p->workspace > 0) return bad(FP_ERR_INVALID, "workspace is NULL");
+    if (!on(workspace, 256)) return bad(FP_ERR_ALIGN, "workspace is not 256-byte aligned");
+    std::lock_guard<std::mutex> lock(p->mu);
+    if (p->have_checked && p->checked[0] == momentum && p->checked[1] == workspace) return FP_OK;
+    const Span ws = span_of(workspace, p->workspace), mo = span_of(momentum, step ? 4 * p->partition : 0);
+    if (meets_any(ws, p->written) || meets_any(ws, p->read)) return bad(FP_ERR_INVALID, "workspace overlaps one of the plan's tensors");
+    if (meet(ws, mo)) return bad(FP_ERR_INVALID, "workspace overlaps momentum");
+    if (meets_any(mo, p->written) || meets_any(mo, p->read)) return bad(FP_ERR_INVALID, "momentum overlaps one of the plan's tensors");
+    p->checked[0] = momentum;
+    p->checked[1] = workspace;
+    p->have_checked = true;
+    return FP_OK;
+}
+
+// One step of the iteration: its coefficients and scales.
+struct Step {
+    float a, b, c;
+    MuonScale s;
+};
+
+// The largest power of two that keeps values up to `most` below 60000.
+float scale_for(double most) { return (float)std::ldexp(1.0, (int)std::floor(std::log2(60000.0 / most))); }
+
+// Bounds of what fp16 has to hold.  With s the largest singular value of X, no
+// element of X passes s, none of A s^2, none of B the largest |b t + c t^2| for
+// t in [0, s^2]; the next s is the largest |a x + b x^3 + c x^5| for x in [0, s].
+// Both are taken at the ends and where the derivative is 0.  s starts at 1, the
+// Frobenius norm, and 1/64 is added for the roundings.
+fp_status plan_steps(int32_t steps, const double* coefs, std::vector<Step>* out) {
+    if (steps < 1 || steps > FP_MUON_MAX_STEPS) return bad(FP_ERR_RANGE, "steps %d outside [1, %d]", steps, FP_MUON_MAX_STEPS);
+    if (coefs == nullptr) return bad(FP_ERR_INVALID, "coefs is NULL");
+    double s = 1.0;
+    for (int32_t i = 0; i < steps; ++i) {
+        const double a = coefs[3 * i], b = coefs[3 * i + 1], c = coefs[3 * i + 2];
+        if (!std::isfinite(a) || !std::isfinite(b) || !std::isfinite(c)) return bad(FP_ERR_RANGE, "coefs of step %d are not finite", i);
+        s *= 1.0 + 1.0 / 64;
+        Step t;
+        t.a = (float)a; t.b = (float)b; t.c = (float)c;
+        const double s2 = s * s;
+        double top = std::fabs(s2 * (b + c * s2));
+        if (c != 0.0) {
+            const double x = -b / (2 * c);
+            if (x > 0.0 && x < s2) top = std::max(top, std::fabs(x * (b + c * x)));
+        }
+        double next = std::fabs(s * (a + s2 * (b + c * s2)));
+        auto at = [&](double t2) {  // x^2 where the polynomial may be largest
+            if (t2 > 0.0 && t2 < s2) next = std::max(next, std::fabs(std::sqrt(t2) * (a + t2 * (b + c * t2))));
+        };
+        if (c != 0.0) {
+            const double disc = 9 * b * b - 20 * a * c;
+            if (disc >= 0.0) at((-3 * b + std::sqrt(disc)) / (10 * c)), at((-3 * b - std::sqrt(disc)) / (10 * c));
+        } else if (b != 0.0) {
+            at(-a / (3 * b));
+        }
+        // beyond these the fp32 sums and the fp16 scales leave their ranges
+        if (!(s <= 256.0) || !(top <= 60000.0) || !(next <= 256.0))
+            return bad(FP_ERR_RANGE, "coefs of step %d let singular values grow to %g", i, next);
+        t.s.x = scale_for(s);
+        t.s.a = scale_for(s2);
+        t.s.b = scale_for(std::max(top, 1e-3));
+        s = std::max(next, 1e-3);
+        t.s.x_next = scale_for(s * (1.0 + 1.0 / 64));
+        out->push_back(t);
+    }
+    return FP_OK;
+}
+
+fp_status run(fp_muon* p, MuonArgs a, const std::vector<Step>& steps, bool to_weights, void* stream) {
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    a.recs = p->recs();
+    a.grads = p->grads();
+    a.grad_dtype = p->grad_dtype;
+    a.copy_dtype = p->copy_dtype;
+    a.update_dtype = p->update_dtype;
+    for (const Batch& b : p->batches) {
+        if (b.full.n == 0) continue;
+        auto over = [&](const Run& r) {
+            a.tiles = p->tile_table() + r.first;
+            a.n_tiles = (int32_t)r.n;
+        };
+        hipError_t e;
+        over(b.moment);
+        if ((e = launch_muon_moment(a, s)) != hipSuccess) return device_error(e, "momentum launch");
+        over(b.cast);
+        a.s = steps[0].s;
+        if ((e = launch_muon_cast(a, s)) != hipSuccess) return device_error(e, "cast launch");
+        for (size_t i = 0; i < steps.size(); ++i) {
+            a.s = steps[i].s;
+            a.ca = steps[i].a;
+            a.cb = steps[i].b;
+            a.cc = steps[i].c;
+            a.step = (int32_t)i;
+            over(b.half);
+            if ((e = launch_muon_gram(a, b.half_shape, s)) != hipSuccess) return device_error(e, "product launch");
+            if ((e = launch_muon_poly(a, b.half_shape, s)) != hipSuccess) return device_error(e, "product launch");
+            over(b.full);
+            if ((e = launch_muon_next(a, b.full_shape, i + 1 == steps.size(), to_weights, s)) != hipSuccess)
+                return device_error(e, "product launch");
+        }
+    }
+    return FP_OK;
+}
+
+fp_status check_eps(double eps) {
+    return std::isfinite(eps) && eps > 0.0 ? FP_OK : bad(FP_ERR_RANGE, "eps must be positive and finite");
+}
+
+}  // namespace
+
+extern "C" fp_status fp_muon_create(int32_t n, const int64_t* rows, const int64_t* cols, const int32_t* group,
+                                    int32_t grad_dtype, const void* const* grads, float* const* master,
+                                    int32_t copy_dtype, void* const* copies, int32_t update_dtype, void* const* updates,
+                                    fp_muon** out) {
+    return guarded([&] {
+        return create(n, rows, cols, group, grad_dtype, grads, master, copy_dtype, copies, update_dtype, updates, out);
+    });
+}
+
+extern "C" void fp_muon_destroy(fp_muon* muon) {
+    if (muon != nullptr) free_plan(muon);
+}
+
+extern "C" fp_status fp_muon_info(const fp_muon* muon, int64_t* partition, int64_t* workspace_bytes) {
+    if (muon == nullptr) return bad(FP_ERR_INVALID, "muon is NULL");
+    if (partition) *partition = muon->partition;
+    if (workspace_bytes) *workspace_bytes = muon->workspace;
+    return FP_OK;
+}
+
+extern "C" fp_status fp_muon_offsets(const fp_muon* muon, int64_t* offsets) {
+    if (muon == nullptr || offsets == nullptr) return bad(FP_ERR_INVALID, "muon or offsets is NULL");
+    std::copy(muon->offset.begin(), muon->offset.end(), offsets);
+    return FP_OK;
+}
+
+extern "C" fp_status fp_muon_set_grads(fp_muon* muon, const void* const* grads, void* stream) {
+    return guarded([&] { return set_grads(muon, grads, stream); });
+}
+
+extern "C" fp_status fp_muon_orthogonalize(fp_muon* muon, int32_t steps, const double* coefs, double eps, void* workspace,
+                                           void* stream) {
+    return guarded([&]() -> fp_status {
+        if (muon == nullptr) return bad(FP_ERR_INVALID, "muon is NULL");
+        if (!muon->has_update) return bad(FP_ERR_INVALID, "muon plan has no updates");
+        std::vector<Step> it;
+        fp_status st = plan_steps(steps, coefs, &it);
+        if (st != FP_OK || (st = check_eps(eps)) != FP_OK) return st;
+        if ((st = check_buffers(muon, nullptr, false, workspace)) != FP_OK) return st;
+        if ((st = check_device(muon)) != FP_OK) return st;
+        MuonArgs a;
+        std::memset(&a, 0, sizeof a);
+        a.ws = static_cast<char*>(workspace);
+        a.eps = eps;
+        return run(muon, a, it, false, stream);
+    });
+}
+
+extern "C" fp_status fp_muon_step(fp_muon* muon, int32_t n_groups, const fp_muon_hparams* hp, int32_t steps,
+                                  const double* coefs, double eps, float* momentum, const int32_t* found_inf,
+                                  const double* grad_coef, void* workspace, void* stream) {
+    return guarded([&]() -> fp_status {
+        if (muon == nullptr) return bad(FP_ERR_INVALID, "muon is NULL");
+        if (!muon->has_master) return bad(FP_ERR_INVALID, "muon plan has no master weights");
+        if (n_groups <= muon->max_group || n_groups > FP_MAX_GROUPS)
+            return bad(FP_ERR_RANGE, "n_groups %d: the matrices use groups up to %d, at most %d", n_groups, muon->max_group,
+                       FP_MAX_GROUPS);
+        if (hp == nullptr) return bad(FP_ERR_INVALID, "hparams is NULL");
+        MuonArgs a;
+        std::memset(&a, 0, sizeof a);
+        for (int32_t g = 0; g < n_groups; ++g) {
+            const fp_muon_hparams& h = hp[g];
+            if (!std::isfinite(h.lr) || !std::isfinite(h.weight_decay) || !(h.beta >= 0.0 && h.beta < 1.0))
+                return bad(FP_ERR_RANGE, "group %d: lr and weight_decay must be finite, beta in [0, 1)", g);
+            if (h.adjust < FP_MUON_ADJUST_NONE || h.adjust > FP_MUON_ADJUST_SHAPE)
+                return bad(FP_ERR_INVALID, "group %d: unknown adjust %d", g, h.adjust);
+            a.g[g] = {h.lr, h.beta, 1.0 - h.lr * h.weight_decay, h.nesterov != 0, h.adjust};
+        }
+        std::vector<Step> it;
+        fp_status st = plan_steps(steps, coefs, &it);
+        if (st != FP_OK || (st = check_eps(eps)) != FP_OK) return st;
+        if (!on(found_inf, 4)) return bad(FP_ERR_ALIGN, "found_inf misaligned");
+        if (!on(grad_coef, 8)) return bad(FP_ERR_ALIGN, "grad_coef misaligned");
+        if ((st = check_buffers(muon, momentum, true, workspace)) != FP_OK) return st;
+        if ((st = check_device(muon)) != FP_OK) return st;
+        a.ws = static_cast<char*>(workspace);
+        a.eps = eps;
+        a.momentum = momentum;
+        a.found_inf = found_inf;
+        a.g_coef = grad_coef;
+        return run(muon, a, it, true, stream);
+    });
+}

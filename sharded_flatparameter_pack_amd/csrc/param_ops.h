@@ -105,6 +105,18 @@ __device__ __forceinline__ void st16u(void* p, const uint4 v) {
     __builtin_nontemporal_store(w, (FP_GLOBAL u32x4_a4*)(p));
 }
 
+// 16 and 8 aligned bytes of data that is used again (no non-temporal hint).
+__device__ __forceinline__ uint4 get16(const void* p) {
+    const u32x4_t v = *gptr<u32x4_t>(p);
+    return make_uint4(v.x, v.y, v.z, v.w);
+}
+__device__ __forceinline__ uint2 get8(const void* p) {
+    const u32x2_t v = *gptr<u32x2_t>(p);
+    return make_uint2(v.x, v.y);
+}
+__device__ __forceinline__ void put16(void* p, const uint4 v) { *gptr<u32x4_t>(p) = u32x4_t{v.x, v.y, v.z, v.w}; }
+__device__ __forceinline__ void put8(void* p, const uint2 v) { *gptr<u32x2_t>(p) = u32x2_t{v.x, v.y}; }
+
 // 32 bits of dither for partition element e: the element's index and the
 // call's key through two multiplications.  The multipliers are the golden
 // ratio's and the fractions of sqrt(2) and sqrt(3).
