@@ -10,10 +10,9 @@ namespace fpk {
 // ---------------------------------------------------------------- muon
 
 // One matrix of a plan.  Inside the workspace it is padded with zeros to
-// multiples of kPad rows and columns.  With m the smaller side and n the
-// other: P is the matrix as m rows of n, Q as n rows of m (one of the two has
-// the matrix's own orientation), both fp16; x the matrix in fp32, in its own
-// orientation.  Offsets are bytes from the workspace's start.
+// multiples of kPad rows and columns, and held in two parts, X times a power of
+// two being h (fp16) + l (bf16).  m: the smaller padded side.  Offsets are bytes
+// from the workspace's start.
 struct MuonRec {
     float* master;            // null in a plan that only orthogonalises
     void* copy;               // bf16 / fp16 weights, or null
@@ -24,7 +23,7 @@ struct MuonRec {
     int32_t group;
     int32_t chunks;           // of the norm's partial sums
     int64_t chunk;            // elements of one
-    int64_t x, p, q[2];       // Q has two places: a step of the iteration reads one and writes the other
+    int64_t h[2], l;          // h has two places: a step of the iteration reads one and writes the other
     int64_t a, b;             // fp16 [m][m], their diagonals zero
     int64_t da, db;           // fp32 [m]: the diagonals
     int64_t part;             // fp64 [chunks]
@@ -60,11 +59,14 @@ struct MuonArgs {
     int32_t grad_dtype, copy_dtype, update_dtype;
     float ca, cb, cc;         // the iteration's coefficients
     MuonScale s;
-    int32_t step;             // of the iteration: which Q is read
+    int32_t step;             // of the iteration: which h is read
     const MatTile* tiles;
     int32_t n_tiles;
     MuonGroup g[FP_MAX_GROUPS];
 };
+
+// Of the kernel that writes X: the padded matrix in pieces of so many rows and columns.
+constexpr int kCastRows = 16, kCastCols = 128;
 
 enum { kTile256 = 0, kTile128 = 1, kTile64 = 2 };
 constexpr int kTileSide[3] = {256, 128, 64};

@@ -112,10 +112,9 @@ int64_t lay_out(MuonRec* r, int64_t at) {
         return from;
     };
     const int64_t all = (int64_t)r->rp * r->cp, m = std::min(r->rp, r->cp);
-    r->x = take(4 * all);
-    r->p = take(2 * all);
-    r->q[0] = take(2 * all);
-    r->q[1] = take(2 * all);
+    r->h[0] = take(2 * all);
+    r->h[1] = take(2 * all);
+    r->l = take(2 * all);
     r->a = take(2 * m * m);
     r->b = take(2 * m * m);
     r->da = take(4 * m);
@@ -155,7 +154,7 @@ void close_batch(const std::vector<MuonRec>& recs, Batch* b, std::vector<MatTile
             for (int64_t tj = 0; tj < cols; ++tj) table->push_back({i, (int32_t)ti, (int32_t)tj, 0});
     };
     run(&b->moment, [&](int32_t i, const MuonRec& r) { grid(i, r.chunks, 1); });
-    run(&b->cast, [&](int32_t i, const MuonRec& r) { grid(i, r.rp / 64, r.cp / 64); });
+    run(&b->cast, [&](int32_t i, const MuonRec& r) { grid(i, r.rp / kCastRows, ceil_div64(r.cp, kCastCols)); });
     run(&b->half, [&](int32_t i, const MuonRec& r) {
         const int64_t m = ceil_div64(std::min(r.rp, r.cp), kTileSide[b->half_shape]);
         for (int64_t ti = 0; ti < m; ++ti)
@@ -232,7 +231,7 @@ fp_status create(int32_t n, const int64_t* rows, const int64_t* cols, const int3
             r.chunk = std::max<int64_t>(8192, ceil_div64(ceil_div64(numel, 256), 1024) * 1024);
             r.chunks = (int32_t)ceil_div64(numel, r.chunk);
             partition += ceil_div64(numel, 32) * 32;
-            if ((int64_t)(r.rp / 64) * (r.cp / 64) > 0xFFFFFFFFLL / 256)
+            if (r.rp / kCastRows * ceil_div64(r.cp, kCastCols) > 0xFFFFFFFFLL / 256)
                 return bad(FP_ERR_RANGE, "matrix %d needs more workgroups than one launch holds", i);
             at = lay_out(&r, at);
             workspace = std::max(workspace, at);

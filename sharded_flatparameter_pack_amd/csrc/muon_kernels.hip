@@ -5,16 +5,19 @@
 // has m rows, its smaller side, and n columns:
 //   X = U / (|U|_F + eps);  steps times  A = X X^T,  B = b A + c A^2,
 //   X <- a X + B X.
-// Launches: the momentum and |U|_F^2's partial sums (moment); X in fp32 and
-// fp16, both ways round (cast); for every step of the iteration A (gram), B
-// (poly) and the next X (next), the last of which writes the weights.  All
-// matrices of a batch share each launch.
+// Launches: the momentum and |U|_F^2's partial sums (moment); X (cast); for
+// every step of the iteration A (gram), B (poly) and the next X (next), the last
+// of which writes the weights.  All matrices of a batch share each launch.  A
+// matrix stays as it lies: where a product contracts its rows, its fragments
+// come out of LDS through the transposing read.
 //
 // Precision.  The products run on fp16 operands with fp32 sums.  What fp16
-// loses is kept small by holding apart, in fp32, what carries most: X itself,
-// and the diagonals of A and B, which stand far above the other elements.  With
-// D the diagonal of B and R the rest, X <- (a + D) X + R X_h, X_h in fp16:
-// only R's product sees the rounded X.  Relative 2-norm errors of five steps
+// loses is kept small by holding apart what carries most: X, of which only the
+// first of two parts goes into products (h in fp16 + l in bf16: 20 bits, and
+// fp32's range for a matrix far below eps), and in fp32 the diagonals of A and
+// B, which stand far above the other elements.  With D the
+// diagonal of B and R the rest, X <- (a + D) X + R X_h: only R's product sees the
+// rounded X.  Relative 2-norm errors of five steps
 // against 64 bits (512 x 512: normal / singular values i^-1 / 8 of them 8 times
 // the rest's norm): 7e-4 / 3e-4 / 1e-4; fp16 for everything 1.7e-3 / 3e-3 /
 // 6e-3, bf16 for everything 1e-2 / 2e-2 / 5e-2 (2^-8 is 4e-3).
@@ -130,13 +133,44 @@ __global__ __launch_bounds__(256) void moment_kernel(const MuonArgs a) {
     if (threadIdx.x == 0) gptr<double>((void*)(a.ws + r.part))[t.ti] = sum;
 }
 
+// ---------------------------------------------------------------- the forms of X
+
+// Eight values, scaled, into both parts.
+__device__ __forceinline__ void st_x(char* ws, int64_t h, int64_t l, int64_t at, const float x[8]) {
+    uint32_t hw[4], lw[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        hw[k] = f16x2(x[2 * k], x[2 * k + 1]);
+        lw[k] = bf16x2(x[2 * k] - f16_lo(hw[k]), x[2 * k + 1] - f16_hi(hw[k]));
+    }
+    put16(ws + h + 2 * at, make_uint4(hw[0], hw[1], hw[2], hw[3]));
+    put16(ws + l + 2 * at, make_uint4(lw[0], lw[1], lw[2], lw[3]));
+}
+__device__ __forceinline__ void ld_x(const char* ws, int64_t h, int64_t l, int64_t at, float x[8]) {
+    const uint4 a = get16(ws + h + 2 * at), b = get16(ws + l + 2 * at);
+    const uint32_t hw[4] = {a.x, a.y, a.z, a.w}, lw[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        x[2 * k] = f16_lo(hw[k]) + bf16_lo(lw[k]);
+        x[2 * k + 1] = f16_hi(hw[k]) + bf16_hi(lw[k]);
+    }
+}
+__device__ __forceinline__ void ld_f16(const void* p, float x[8]) {
+    const uint4 a = get16(p);
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) x[2 * k] = f16_lo(w[k]), x[2 * k + 1] = f16_hi(w[k]);
+}
+__device__ __forceinline__ void st_f16(void* p, const float x[8]) {
+    put16(p, make_uint4(f16x2(x[0], x[1]), f16x2(x[2], x[3]), f16x2(x[4], x[5]), f16x2(x[6], x[7])));
+}
+
 // ---------------------------------------------------------------- cast
 
-// A 64 x 64 tile of the padded matrix: X in fp32 and in fp16 both ways round.
+// kCastRows x kCastCols of the padded matrix: X = U / (|U| + eps).
 template <int kGrad, bool kStep>
 __global__ __launch_bounds__(256) void cast_kernel(const MuonArgs a) {
     __shared__ double lds[4];
-    __shared__ uint16_t turn[64][64 + 4];
     if (kStep && skipped(a)) return;
     const MatTile t = a.tiles[blockIdx.x];
     const MuonRec& r = a.recs[t.mat];
@@ -147,17 +181,15 @@ __global__ __launch_bounds__(256) void cast_kernel(const MuonArgs a) {
     const MuonGroup& hp = a.g[kStep ? r.group : 0];
     const double k = kStep && a.g_coef != nullptr ? *a.g_coef : 1.0;
     const double mine = kStep ? (1.0 - hp.beta) * k : 1.0;
-    const bool turned = r.rows > r.cols;
-    char* own = a.ws + (turned ? r.q[0] : r.p);
-    char* other = a.ws + (turned ? r.p : r.q[0]);
-    const int c4 = (threadIdx.x & 15) * 4, col = t.tj * 64 + c4;
+    const int row = t.ti * kCastRows + (threadIdx.x >> 4), col = t.tj * kCastCols + (threadIdx.x & 15) * 8;
+    if (row >= r.rp || col >= r.cp) return;
+    float x[8];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int lr = (threadIdx.x >> 4) + 16 * i, row = t.ti * 64 + lr;
-        const int left = r.cols - col, have = row >= r.rows || left <= 0 ? 0 : left < 4 ? left : 4;
-        float x[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int q = 0; q < 8; q += 4) {
+        const int left = r.cols - col - q, have = row >= r.rows || left <= 0 ? 0 : left < 4 ? left : 4;
+        x[q] = x[q + 1] = x[q + 2] = x[q + 3] = 0.0f;
         if (have > 0) {
-            const int64_t e = (int64_t)row * r.cols + col;
+            const int64_t e = (int64_t)row * r.cols + col + q;
             float g[4], m[4];
             if (!kStep || hp.nesterov) grad4<kGrad>(grad, e, have, g);
             if constexpr (kStep) ld_f32(a.momentum + r.offset + e, have, m);
@@ -166,59 +198,34 @@ __global__ __launch_bounds__(256) void cast_kernel(const MuonArgs a) {
                 if (j < have) {
                     const double u = !kStep ? (double)g[j]
                                      : hp.nesterov ? hp.beta * (double)m[j] + mine * (double)g[j] : (double)m[j];
-                    x[j] = (float)(u * scale);
+                    x[q + j] = (float)(u * scale) * a.s.x;
                 }
         }
-        const int64_t to = (int64_t)row * r.cp + col;
-        put16(a.ws + r.x + 4 * to, bits_of(x));
-#pragma unroll
-        for (int j = 0; j < 4; ++j) x[j] *= a.s.x;
-        const uint2 h = f16x4(x);
-        put8(own + 2 * to, h);
-        turn[c4][lr] = (uint16_t)h.x;
-        turn[c4 + 1][lr] = (uint16_t)(h.x >> 16);
-        turn[c4 + 2][lr] = (uint16_t)h.y;
-        turn[c4 + 3][lr] = (uint16_t)(h.y >> 16);
     }
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int lc = (threadIdx.x >> 4) + 16 * i;
-        const uint16_t* from = &turn[lc][c4];
-        const uint2 h = make_uint2(from[0] | (uint32_t)from[1] << 16, from[2] | (uint32_t)from[3] << 16);
-        put8(other + 2 * ((int64_t)(t.tj * 64 + lc) * r.rp + t.ti * 64 + c4), h);
-    }
+    st_x(a.ws, r.h[0], r.l, (int64_t)row * r.cp + col, x);
 }
 
 // ---------------------------------------------------------------- products
 
 struct Sides {
     int m, n;     // padded
-    bool turned;
+    bool turned;  // tall: m counts the columns
 };
 __device__ __forceinline__ Sides sides(const MuonRec& r) {
     const bool turned = r.rows > r.cols;
     return turned ? Sides{r.cp, r.rp, true} : Sides{r.rp, r.cp, false};
 }
 
-__device__ __forceinline__ Operand f16_rows(const char* base, int64_t row, int64_t rows, int64_t width) {
-    return {base + 2 * row * width, 2 * width, (int)(rows - row), nullptr};
+// The tile's rows (columns) from `first` on, of fp16 rows of `width`.
+__device__ __forceinline__ Operand rows_of(const char* base, int64_t first, int64_t rows, int64_t width) {
+    return {base + 2 * first * width, 2 * width, (int)(rows - first), nullptr};
+}
+__device__ __forceinline__ Operand columns_of(const char* base, int64_t first, int64_t width) {
+    return {base + 2 * first, 2 * width, (int)(width - first), nullptr};
 }
 
-// Four elements (row, col .. col + 3) of a symmetric matrix's lower half, and
+// A = X X^T (X^T X of a tall matrix): the tiles on and below the diagonal, and
 // their mirror images.
-__device__ __forceinline__ void st_symmetric(char* to, int64_t side, int row, int col, uint2 h, bool mirror) {
-    put8(to + 2 * (row * side + col), h);
-    if (mirror) {
-        FP_GLOBAL uint16_t* p = gptr<uint16_t>((void*)(to + 2 * (col * side + row)));
-        p[0] = (uint16_t)h.x;
-        p[side] = (uint16_t)(h.x >> 16);
-        p[2 * side] = (uint16_t)h.y;
-        p[3 * side] = (uint16_t)(h.y >> 16);
-    }
-}
-
-// A = X X^T: the tiles on and below the diagonal, and their mirror images.
 template <class S>
 __global__ __launch_bounds__(S::kThreadsWg) void gram_kernel(const MuonArgs a) {
     extern __shared__ __align__(16) char lds[];
@@ -226,32 +233,40 @@ __global__ __launch_bounds__(S::kThreadsWg) void gram_kernel(const MuonArgs a) {
     const MatTile t = a.tiles[die_tile(blockIdx.x, a.n_tiles)];
     const MuonRec& r = a.recs[t.mat];
     const Sides z = sides(r);
-    const char* p = a.ws + r.p;
-    const int i0 = t.ti * S::kBM, j0 = t.tj * S::kBN;
-    TileProduct<S, false> tile;
-    tile.run(f16_rows(p, i0, z.m, z.n), f16_rows(p, j0, z.m, z.n), z.n / 64, lds);
+    const char* h = a.ws + r.h[a.step & 1];
+    const int i0 = t.ti * S::kBM, j0 = t.tj * S::kBN, steps = z.n / kStepF16;
+    TileProduct<S> tile;
+    if (z.turned) run_tile<kColumnsF16, kColumnsF16>(tile, columns_of(h, i0, z.m), columns_of(h, j0, z.m), steps, lds);
+    else run_tile<kRowsF16, kRowsF16>(tile, rows_of(h, i0, z.m, z.n), rows_of(h, j0, z.m, z.n), steps, lds);
     const float unscale = 1.0f / (a.s.x * a.s.x);
     const float out = a.s.a * unscale;
+    char* to = a.ws + r.a;
+    auto body = [&](int tr, int tc, const float* v) {
+        const int row = i0 + tr, col = j0 + tc;
+        if (row >= z.m || col >= z.m) return;
+        float f[8];
 #pragma unroll
-    for (int fm = 0; fm < S::kFM; ++fm) {
-        const int row = i0 + tile.row0() + 16 * fm;
-        if (row >= z.m) continue;
-#pragma unroll
-        for (int fn = 0; fn < S::kFN; ++fn) {
-            const int col = j0 + tile.col0() + 16 * fn;
-            if (col >= z.m) continue;
-            float f[4];
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                f[q] = tile.acc[fm][fn][q] * out;
-                if (row == col + q) {
-                    gptr<float>((void*)(a.ws + r.da))[row] = tile.acc[fm][fn][q] * unscale;
-                    f[q] = 0.0f;
-                }
+        for (int k = 0; k < 8; ++k) {
+            f[k] = v[k] * out;
+            if (row == col + k) {
+                gptr<float>((void*)(a.ws + r.da))[row] = v[k] * unscale;
+                f[k] = 0.0f;
             }
-            st_symmetric(a.ws + r.a, z.m, row, col, f16x4(f), t.ti != t.tj);
         }
+        st_f16(to + 2 * ((int64_t)row * z.m + col), f);
+    };
+    if (t.ti == t.tj) {
+        tile.each(lds, body);
+        return;
     }
+    tile.template each<true>(lds, body, [&](int tr, int tc, const float* v) {
+        const int row = i0 + tr, col = j0 + tc;
+        if (row >= z.m || col >= z.m) return;
+        float f[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) f[k] = v[k] * out;
+        st_f16(to + 2 * ((int64_t)col * z.m + row), f);
+    });
 }
 
 // B = b A + c A^2 in the same way; db holds a + B's diagonal.  With d the
@@ -263,36 +278,42 @@ __global__ __launch_bounds__(S::kThreadsWg) void poly_kernel(const MuonArgs a) {
     const MatTile t = a.tiles[die_tile(blockIdx.x, a.n_tiles)];
     const MuonRec& r = a.recs[t.mat];
     const Sides z = sides(r);
-    const char* p = a.ws + r.a;
+    const char* n = a.ws + r.a;
     const int i0 = t.ti * S::kBM, j0 = t.tj * S::kBN;
-    TileProduct<S, false> tile;
-    tile.run(f16_rows(p, i0, z.m, z.m), f16_rows(p, j0, z.m, z.m), z.m / 64, lds);
+    TileProduct<S> tile;
+    run_tile<kRowsF16, kRowsF16>(tile, rows_of(n, i0, z.m, z.m), rows_of(n, j0, z.m, z.m), z.m / kStepF16, lds);
     const float un_a = 1.0f / a.s.a, un_s = un_a * un_a;
     const FP_GLOBAL float* d = gptr<float>((const void*)(a.ws + r.da));
-#pragma unroll
-    for (int fm = 0; fm < S::kFM; ++fm) {
-        const int row = i0 + tile.row0() + 16 * fm;
-        if (row >= z.m) continue;
+    char* to = a.ws + r.b;
+    // eight elements (row, col ..); the mirror images are those of the other row, N being symmetric
+    auto poly = [&](int row, int col, const float* v, float f[8]) {
+        float x[8];
+        ld_f16(n + 2 * ((int64_t)row * z.m + col), x);
         const float di = d[row];
 #pragma unroll
-        for (int fn = 0; fn < S::kFN; ++fn) {
-            const int col = j0 + tile.col0() + 16 * fn;
-            if (col >= z.m) continue;
-            const uint2 w = get8(p + 2 * ((int64_t)row * z.m + col));
-            const float n[4] = {f16_lo(w.x), f16_hi(w.x), f16_lo(w.y), f16_hi(w.y)};
-            float f[4];
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const float square = tile.acc[fm][fn][q] * un_s, x = n[q] * un_a;
-                f[q] = (a.cb * x + a.cc * (square + (di + d[col + q]) * x)) * a.s.b;
-                if (row == col + q) {
-                    gptr<float>((void*)(a.ws + r.db))[row] = a.ca + (a.cb * di + a.cc * (square + di * di));
-                    f[q] = 0.0f;
-                }
+        for (int k = 0; k < 8; ++k) {
+            const float square = v[k] * un_s;
+            x[k] *= un_a;
+            f[k] = (a.cb * x[k] + a.cc * (square + (di + d[col + k]) * x[k])) * a.s.b;
+            if (row == col + k) {
+                gptr<float>((void*)(a.ws + r.db))[row] = a.ca + (a.cb * di + a.cc * (square + di * di));
+                f[k] = 0.0f;
             }
-            st_symmetric(a.ws + r.b, z.m, row, col, f16x4(f), t.ti != t.tj);
         }
+        st_f16(to + 2 * ((int64_t)row * z.m + col), f);
+    };
+    auto body = [&](int tr, int tc, const float* v) {
+        float f[8];
+        if (i0 + tr < z.m && j0 + tc < z.m) poly(i0 + tr, j0 + tc, v, f);
+    };
+    if (t.ti == t.tj) {
+        tile.each(lds, body);
+        return;
     }
+    tile.template each<true>(lds, body, [&](int tr, int tc, const float* v) {
+        float f[8];
+        if (i0 + tr < z.m && j0 + tc < z.m) poly(j0 + tc, i0 + tr, v, f);
+    });
 }
 
 // How the orthogonalised matrix leaves.
@@ -308,21 +329,17 @@ __global__ __launch_bounds__(S::kThreadsWg) void next_kernel(const MuonArgs a) {
     const Sides z = sides(r);
     const int i0 = t.ti * S::kBM, j0 = t.tj * S::kBN;
     const bool skip = skipped(a);
-    if (kOut == kToWeights ? skip && r.copy == nullptr : skip) return;
-    const char* q = a.ws + r.q[a.step & 1];
+    if (skip && (kOut != kToWeights || r.copy == nullptr)) return;
+    const char* h = a.ws + r.h[a.step & 1];
     const char* b = a.ws + r.b;
-    TileProduct<S, false> tile;
-    if (!(kOut == kToWeights && skip)) {
-        if (z.turned) tile.run(f16_rows(q, i0, r.rp, z.m), f16_rows(b, j0, z.m, z.m), z.m / 64, lds);
-        else tile.run(f16_rows(b, i0, z.m, z.m), f16_rows(q, j0, r.cp, z.m), z.m / 64, lds);
-    } else {
-        tile.lane = threadIdx.x & 63;
-        tile.wave = threadIdx.x >> 6;
+    TileProduct<S> tile;
+    if (!skip) {
+        const int steps = z.m / kStepF16;
+        if (z.turned) run_tile<kRowsF16, kRowsF16>(tile, rows_of(h, i0, z.n, z.m), rows_of(b, j0, z.m, z.m), steps, lds);
+        else run_tile<kRowsF16, kColumnsF16>(tile, rows_of(b, i0, z.m, z.m), columns_of(h, j0, z.n), steps, lds);
     }
-    const float unscale = 1.0f / (a.s.b * a.s.x);
+    const float unscale = 1.0f / (a.s.b * a.s.x), un_x = 1.0f / a.s.x;
     const FP_GLOBAL float* d = gptr<float>((const void*)(a.ws + r.db));
-    char* own = a.ws + (z.turned ? r.q[(a.step + 1) & 1] : r.p);
-    char* other = a.ws + (z.turned ? r.p : r.q[(a.step + 1) & 1]);
     double rate = 0.0, decay = 1.0;
     if constexpr (kOut == kToWeights) {
         const MuonGroup& hp = a.g[r.group];
@@ -332,45 +349,36 @@ __global__ __launch_bounds__(S::kThreadsWg) void next_kernel(const MuonArgs a) {
                                                             : 1.0);
         decay = hp.decay;
     }
+    tile.each(lds, [&](int tr, int tc, const float* v) {
+        const int row = i0 + tr, col = j0 + tc;
+        if (row >= (kOut == kGoesOn ? r.rp : r.rows) || col >= (kOut == kGoesOn ? r.cp : r.cols)) return;
+        const int64_t at = (int64_t)row * r.cp + col;
+        float x[8];
+        if (!skip) {
+            ld_x(a.ws, r.h[a.step & 1], r.l, at, x);
 #pragma unroll
-    for (int fm = 0; fm < S::kFM; ++fm) {
-        const int row = i0 + tile.row0() + 16 * fm;
-        if (row >= (kOut == kGoesOn ? r.rp : r.rows)) continue;
+            for (int k = 0; k < 8; ++k) x[k] = d[z.turned ? col + k : row] * (x[k] * un_x) + v[k] * unscale;
+        }
+        if constexpr (kOut == kGoesOn) {
 #pragma unroll
-        for (int fn = 0; fn < S::kFN; ++fn) {
-            const int col = j0 + tile.col0() + 16 * fn;
-            if (col >= (kOut == kGoesOn ? r.cp : r.cols)) continue;
-            const int64_t at = (int64_t)row * r.cp + col;
-            float x[4] = {0.f, 0.f, 0.f, 0.f};
-            if (!(kOut == kToWeights && skip)) {
-                f32x4_of(get16(a.ws + r.x + 4 * at), x);
+            for (int k = 0; k < 8; ++k) x[k] *= a.s.x_next;
+            st_x(a.ws, r.h[(a.step + 1) & 1], r.l, at, x);
+        } else {
 #pragma unroll
-                for (int k = 0; k < 4; ++k) x[k] = d[z.turned ? col + k : row] * x[k] + tile.acc[fm][fn][k] * unscale;
-            }
-            if constexpr (kOut == kGoesOn) {
-                put16(a.ws + r.x + 4 * at, bits_of(x));
-#pragma unroll
-                for (int k = 0; k < 4; ++k) x[k] *= a.s.x_next;
-                const uint2 h = f16x4(x);
-                put8(own + 2 * at, h);
-                FP_GLOBAL uint16_t* o = gptr<uint16_t>((void*)(other + 2 * ((int64_t)col * r.rp + row)));
-                o[0] = (uint16_t)h.x;
-                o[r.rp] = (uint16_t)(h.x >> 16);
-                o[2 * (int64_t)r.rp] = (uint16_t)h.y;
-                o[3 * (int64_t)r.rp] = (uint16_t)(h.y >> 16);
-            } else {
-                const int have = r.cols - col < 4 ? r.cols - col : 4;
-                const int64_t e = (int64_t)row * r.cols + col;
+            for (int q = 0; q < 8; q += 4) {
+                const int left = r.cols - col - q, have = left < 4 ? left : 4;
+                if (have <= 0) break;
+                const int64_t e = (int64_t)row * r.cols + col + q;
                 if constexpr (kOut == kToUpdate) {
-                    if (a.update_dtype == FP_DTYPE_F32) st_f32(static_cast<float*>(r.update) + e, have, x);
+                    if (a.update_dtype == FP_DTYPE_F32) st_f32(static_cast<float*>(r.update) + e, have, x + q);
                     else st_16bit(static_cast<uint16_t*>(r.update) + e, have,
-                                  a.update_dtype == FP_DTYPE_F16 ? f16x4(x) : f32x4_to_bf16(x));
+                                  a.update_dtype == FP_DTYPE_F16 ? f16x4(x + q) : f32x4_to_bf16(x + q));
                 } else {
                     float w[4];
                     ld_f32(r.master + e, have, w);
                     if (!skip) {
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) w[k] = (float)(decay * (double)w[k] - rate * (double)x[k]);
+                        for (int k = 0; k < 4; ++k) w[k] = (float)(decay * (double)w[k] - rate * (double)x[q + k]);
                         st_f32(r.master + e, have, w);
                     }
                     if (r.copy != nullptr)
@@ -379,7 +387,7 @@ __global__ __launch_bounds__(S::kThreadsWg) void next_kernel(const MuonArgs a) {
                 }
             }
         }
-    }
+    });
 }
 
 // Launches kernel(a) over the argument block's tiles.

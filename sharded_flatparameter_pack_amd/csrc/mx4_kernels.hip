@@ -230,8 +230,7 @@ __global__ __launch_bounds__(256) void dequantize_kernel(const Mx4DequantArgs a,
         for (int k = 0; k < 4; ++k)
             w[k] = kDtype == FP_DTYPE_F16 ? f16x2(f[2 * k], f[2 * k + 1]) : bf16x2(f[2 * k], f[2 * k + 1]);
         if (left >= 8) {
-            st8u(p, make_uint2(w[0], w[1]));
-            st8u(p + 4, make_uint2(w[2], w[3]));
+            st16u16(p, make_uint4(w[0], w[1], w[2], w[3]));
         } else {
             for (int k = 0; k < (int)left; ++k) gptr<uint16_t>((void*)p)[k] = (uint16_t)(w[k >> 1] >> (16 * (k & 1)));
         }
@@ -240,68 +239,75 @@ __global__ __launch_bounds__(256) void dequantize_kernel(const Mx4DequantArgs a,
 
 // ---------------------------------------------------------------- product
 
-// Elements (row, col .. col + have - 1) of the output, have in [1, 4].
-__device__ __forceinline__ void st_out(const Mx4MatmulArgs& a, int64_t row, int64_t col, const f32x4_t v) {
+// Eight neighbouring elements (row, col ..) of the output, those it has.
+__device__ __forceinline__ void st_out(const Mx4MatmulArgs& a, int64_t row, int64_t col, const float v[8]) {
     const int64_t left = a.n - col, at = row * a.pitch + col;
-    const int have = left < 4 ? (int)left : 4;
-    float f[4] = {v.x, v.y, v.z, v.w};
+    if (left <= 0) return;
+    const int have = left < 8 ? (int)left : 8;
+    float f[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) f[k] = v[k];
     if (a.dtype == FP_DTYPE_F32) {
         float* p = static_cast<float*>(a.out) + at;
-        if (have == 4) {
+        if (have == 8) {
             if (a.accumulate) {
-                float o[4];
+                float o[8];
                 f32x4_of(ld16u(p), o);
+                f32x4_of(ld16u(p + 4), o + 4);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) f[k] += o[k];
+                for (int k = 0; k < 8; ++k) f[k] += o[k];
             }
             st16u(p, bits_of(f));
+            st16u(p + 4, bits_of(f + 4));
             return;
         }
-        for (int k = 0; k < have; ++k) {
-            FP_GLOBAL float* o = gptr<float>((void*)(p + k));
-            *o = a.accumulate ? *o + f[k] : f[k];
-        }
+        for (int k = 0; k < 7; ++k)
+            if (k < have) {
+                FP_GLOBAL float* o = gptr<float>((void*)(p + k));
+                *o = a.accumulate ? *o + v[k] : v[k];
+            }
         return;
     }
     const bool half = a.dtype == FP_DTYPE_F16;
     uint16_t* p = static_cast<uint16_t*>(a.out) + at;
     if (a.accumulate) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
+        for (int k = 0; k < 8; ++k)
             if (k < have) {
                 const uint32_t o = gptr<uint16_t>((const void*)p)[k];
                 f[k] += half ? f16_lo(o) : bf16_lo(o);
             }
     }
-    const uint2 w = half ? make_uint2(f16x2(f[0], f[1]), f16x2(f[2], f[3])) : f32x4_to_bf16(f);
-    if (have == 4) {
-        st8u(p, w);
+    uint32_t w[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) w[k] = half ? f16x2(f[2 * k], f[2 * k + 1]) : bf16x2(f[2 * k], f[2 * k + 1]);
+    if (have == 8) {
+        st16u16(p, make_uint4(w[0], w[1], w[2], w[3]));
         return;
     }
-    const uint64_t x = ((uint64_t)w.y << 32) | w.x;
-    for (int k = 0; k < have; ++k) gptr<uint16_t>((void*)p)[k] = (uint16_t)(x >> (16 * k));
+#pragma unroll
+    for (int k = 0; k < 7; ++k)
+        if (k < have) gptr<uint16_t>((void*)p)[k] = (uint16_t)(w[k >> 1] >> (16 * (k & 1)));
 }
 
 template <class S>
 __global__ __launch_bounds__(S::kThreadsWg) void matmul_kernel(const Mx4MatmulArgs a) {
     extern __shared__ __align__(16) char lds[];
     const int t = die_tile(blockIdx.x, a.tiles_m * a.tiles_n);
-    const int64_t i0 = (int64_t)(t / a.tiles_n) * S::kBM, j0 = (int64_t)(t % a.tiles_n) * S::kBN;
+    // bands of kBand rows of tiles, column by column: tiles that run together read few operands
+    constexpr int kBand = 4;
+    const int band = t / (kBand * a.tiles_n), in = t - band * kBand * a.tiles_n;
+    const int rows = a.tiles_m - band * kBand < kBand ? a.tiles_m - band * kBand : kBand;
+    const int64_t i0 = (int64_t)(band * kBand + in % rows) * S::kBM, j0 = (int64_t)(in / rows) * S::kBN;
     const int64_t pitch = a.kp >> 1, spitch = a.kp >> 5;
     const int64_t lm = a.m - i0, ln = a.n - j0;
-    TileProduct<S, true> tile;
-    tile.run({a.a + i0 * pitch, pitch, lm < S::kBM ? (int)lm : S::kBM, a.as + i0 * spitch},
-             {a.b + j0 * pitch, pitch, ln < S::kBN ? (int)ln : S::kBN, a.bs + j0 * spitch}, (int)(a.kp >> 8), lds);
-#pragma unroll
-    for (int fm = 0; fm < S::kFM; ++fm) {
-        const int64_t row = i0 + tile.row0() + 16 * fm;
-        if (row >= a.m) continue;
-#pragma unroll
-        for (int fn = 0; fn < S::kFN; ++fn) {
-            const int64_t col = j0 + tile.col0() + 16 * fn;
-            if (col < a.n) st_out(a, row, col, tile.acc[fm][fn]);
-        }
-    }
+    TileProduct<S> tile;
+    run_tile<kRowsFp4, kRowsFp4>(tile, {a.a + i0 * pitch, pitch, lm < S::kBM ? (int)lm : S::kBM, a.as + i0 * spitch},
+                                 {a.b + j0 * pitch, pitch, ln < S::kBN ? (int)ln : S::kBN, a.bs + j0 * spitch},
+                                 (int)(a.kp >> 8), lds);
+    tile.each(lds, [&](int r, int c, const float* v) {
+        if (i0 + r < a.m) st_out(a, i0 + r, j0 + c, v);
+    });
 }
 
 using Shape256 = TileShape<256, 256, 128, 64>;
@@ -312,11 +318,11 @@ template <class S>
 hipError_t run_matmul(Mx4MatmulArgs a, hipStream_t s) {
     a.tiles_m = (int32_t)ceil_div64(a.m, S::kBM);
     a.tiles_n = (int32_t)ceil_div64(a.n, S::kBN);
-    if (S::kLds > 65536) {
-        const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(matmul_kernel<S>), hipFuncAttributeMaxDynamicSharedMemorySize, S::kLds);
+    if (S::kLdsFp4 > 65536) {
+        const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(matmul_kernel<S>), hipFuncAttributeMaxDynamicSharedMemorySize, S::kLdsFp4);
         if (e != hipSuccess) return e;
     }
-    matmul_kernel<S><<<(unsigned)(a.tiles_m * a.tiles_n), S::kThreadsWg, S::kLds, s>>>(a);
+    matmul_kernel<S><<<(unsigned)(a.tiles_m * a.tiles_n), S::kThreadsWg, S::kLdsFp4, s>>>(a);
     return hipGetLastError();
 }
 

@@ -117,6 +117,12 @@ __device__ __forceinline__ uint2 get8(const void* p) {
 __device__ __forceinline__ void put16(void* p, const uint4 v) { *gptr<u32x4_t>(p) = u32x4_t{v.x, v.y, v.z, v.w}; }
 __device__ __forceinline__ void put8(void* p, const uint2 v) { *gptr<u32x2_t>(p) = u32x2_t{v.x, v.y}; }
 
+// 16 bytes to a 2-byte boundary.
+__device__ __forceinline__ void st16u16(void* p, const uint4 v) {
+    const u32x4_a2 w = {v.x, v.y, v.z, v.w};
+    __builtin_nontemporal_store(w, (FP_GLOBAL u32x4_a2*)(p));
+}
+
 // 32 bits of dither for partition element e: the element's index and the
 // call's key through two multiplications.  The multipliers are the golden
 // ratio's and the fractions of sqrt(2) and sqrt(3).
