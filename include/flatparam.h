@@ -820,7 +820,7 @@ fp_status fp_mx8_dequantize(int64_t n, int32_t root, const uint8_t* codes, const
  *   fp_muon_orthogonalize writes, or NULL.  At least one of master and
  *   updates.  Weights, copies and updates overlap nothing else.
  * fp_muon_info: partition as in fp_params_info, of the momentum;
- *   workspace_bytes: of every call, about 10 bytes per element of the matrices
+ *   workspace_bytes: of every call, 6 bytes per element and 4 per element of A of the matrices
  *   that are worked on together (up to 2 GiB, or the largest matrix's), with
  *   both sides counted in multiples of 64.
  * Creation, destruction, fp_muon_set_grads and devices as for fp_params.

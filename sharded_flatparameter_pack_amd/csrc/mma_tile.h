@@ -18,11 +18,11 @@
 // tile on 4 waves of 64 x 64 145, a 64-wide one 275.  MXFP4 at 4096^2 x 16384
 // (scales from LDS): 125 us (4.4 PFLOP/s).
 //
-// The loop: two stages in LDS, filled by loads that go to LDS directly, and two
-// sets of fragments in registers.  While the first half's products run, the
-// second half's fragments are read; then, behind the step's one barrier, the
-// stage just read is refilled for the step after next and the next step's first
-// fragments are read under the second half's products.  Read as they are needed
+// The loop: stages in LDS, filled by loads that go to LDS directly, and two sets
+// of fragments in registers.  While the first half's products run, the second
+// half's fragments are read; then, behind the step's one barrier, the stage just
+// read is refilled for a later step and the next step's first fragments are read
+// under the second half's products.  Read as they are needed
 // instead, the same tiles take 121 and 250 us.
 #pragma once
 
@@ -50,11 +50,17 @@ struct TileShape {
     static constexpr int kBM = kBM_, kBN = kBN_, kWM = kWM_, kWN = kWN_;
     static constexpr int kRows = kBM / kWM, kCols = kBN / kWN;  // of waves
     static constexpr int kWavesWg = kRows * kCols, kThreadsWg = 64 * kWavesWg;
+    // Waves per SIMD that registers are kept free for: so many as are resident
+    // with the tile's LDS.  Said to the compiler, it holds everything in plain
+    // registers; unsaid, it moved 88 in and out of the accumulation ones per step
+    // of a 128-wide tile.
+    static constexpr int kWavesSimd = kBM >= 128 ? 2 : 4;
     static constexpr int kFM = kWM / 16, kFN = kWN / 16;        // 16x16 fragments of a wave
     static constexpr int kStage = (kBM + kBN) * kStepBytes;
     static constexpr int kScaleStage = (kBM + kBN) * 8;
-    static constexpr int kLds = 2 * kStage;
-    static constexpr int kLdsFp4 = kLds + 2 * kScaleStage;
+    static constexpr int kStages = kBM >= 128 ? 2 : 4;  // a power of two
+    static constexpr int kLds = kStages * kStage;
+    static constexpr int kLdsFp4 = kLds + kStages * kScaleStage;
 };
 
 // How an operand lies in memory.
@@ -236,7 +242,7 @@ struct TileProduct {
 
         auto load = [&](int k) {  // past the end the last step again: nothing reads it
             const int step = k < steps ? k : steps - 1;
-            char* to = lds + (k & 1) * S::kStage;
+            char* to = lds + k % S::kStages * S::kStage;
             l.load(to, wave, step);
             r.load(to + S::kBM * kStepBytes, wave, step);
             if constexpr (kFp4) {
@@ -246,18 +252,18 @@ struct TileProduct {
                     const uint8_t* from = dword / 2 >= S::kBM ? right.scales : left.scales;
                     __builtin_amdgcn_raw_ptr_buffer_load_lds(
                         __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(from), 0, -1, 0x00020000),
-                        (FP_LDS void*)(scales + (k & 1) * S::kScaleStage + dword * 4), 4, soffset[i], step * 8, 0, 0);
+                        (FP_LDS void*)(scales + k % S::kStages * S::kScaleStage + dword * 4), 4, soffset[i], step * 8, 0, 0);
                 }
             }
         };
         auto read = [&](int k, auto half, Frags& f) {
-            const char* from = lds + (k & 1) * S::kStage;
+            const char* from = lds + k % S::kStages * S::kStage;
             r.template read<decltype(half)::value>(from + S::kBM * kStepBytes, f.b);
             l.template read<decltype(half)::value>(from, f.a);
         };
         auto read_scales = [&](int k, Scales& s) {
             if constexpr (kFp4) {
-                const char* from = scales + (k & 1) * S::kScaleStage;
+                const char* from = scales + k % S::kStages * S::kScaleStage;
                 auto two = [&](int at) { return *(const uint16_t*)(from + at) | (uint32_t) * (const uint16_t*)(from + at + 128) << 16; };
 #pragma unroll
                 for (int n = 0; n < S::kFN; n += 2) s.b[n / 2] = two(sb + n * 128);
@@ -268,19 +274,24 @@ struct TileProduct {
         const std::integral_constant<int, 0> first{};
         const std::integral_constant<int, 1> second{};
 
+        // Loads of a wave per stage: a stage is there once no more than those of
+        // the stages behind it are on their way (they end in order).
+        constexpr int kPerStage = S::kStage / 1024 / S::kWavesWg + (kFp4 ? kSLoads : 0);
         Frags f0, f1;
         Scales s0, s1;
-        load(0);
-        __syncthreads();
-        load(1);
+#pragma unroll
+        for (int k = 0; k < S::kStages; ++k) load(k);
+        wait_loads<(S::kStages - 1) * kPerStage>();
+        barrier_lds();
         read(0, first, f0);
         read_scales(0, s0);
         for (int k = 0; k < steps; ++k) {
             read(k, second, f1);
             multiply<kFp4, 0>(f0, s0);
             interleave<kLeft, kRight>();
-            __syncthreads();  // the next step's stage is there, and this one is read to its end
-            load(k + 2);
+            wait_loads<(S::kStages - 2) * kPerStage>();
+            barrier_lds();  // the next step's stage is there, and this one is read to its end
+            load(k + S::kStages);
             read(k + 1, first, f0);
             read_scales(k + 1, s1);
             multiply<kFp4, 1>(f1, s0);
@@ -290,51 +301,90 @@ struct TileProduct {
         __syncthreads();
     }
 
-    // Walks the tile along its rows: body(row, col, v) with 8 neighbouring
-    // columns from `col` on, a row's neighbours in neighbouring lanes, through
-    // LDS (the lanes' own fragments are 16 rows of 8 or 16 bytes).  kTurned
-    // also calls turned(row, col, v) with 8 neighbouring rows from `row` on.
-    // The values are read from registers a few fragments at a time, 64 rows of
-    // the tile for a 256-wide one.
-    template <bool kTurned, class F, class G>
-    __device__ __forceinline__ void each(char* lds, F body, G turned) {
-        constexpr int kPer = S::kFM < 2 ? S::kFM : 2;   // fragments along the rows, per pass
+    // The column that a lane has in each(): the first of its eight.
+    static __device__ __forceinline__ int each_col() { return (int)threadIdx.x % (S::kBN / 8) * 8; }
+
+    // Walks the tile along its rows, through LDS (the lanes' own fragments are
+    // 16 rows of 16 bytes): body(row, col, v, f) with 8 neighbouring columns from
+    // each_col() on, a row's neighbours in neighbouring lanes.  f is what
+    // fetch(row, col) gave: it is called one pass of kPer fragments ahead, so that
+    // what the lane reads from memory is there when it is needed (without, the
+    // tile of a 1024-wide product waited 25 us for its 16 reads, one by one).
+    // kTurned: also turned(row, col, v, f) with 8 neighbouring rows from `row` on
+    // and f = fetch_turned(row, col).
+    template <int kPer, bool kTurned, class L, class F, class M, class G>
+    __device__ __forceinline__ void each(char* lds, L fetch, F body, M fetch_turned, G turned) {
         constexpr int kPitch = S::kBN + 4;              // floats
         constexpr int kPassRows = S::kRows * kPer * 16;
+        constexpr int kAcross = S::kBN / 8, kDown = kPassRows / 8;
+        constexpr int kTimes = kPassRows * kAcross / S::kThreadsWg;
+        static_assert(S::kFM % kPer == 0 && kTimes >= 1 && kTimes * S::kThreadsWg == kPassRows * kAcross, "whole passes");
+        static_assert(S::kThreadsWg % kAcross == 0 && S::kThreadsWg % kDown == 0, "whole rows");
         static_assert(kPassRows * kPitch * 4 <= S::kLds, "a pass fits into the stages");
         float* to = reinterpret_cast<float*>(lds);
+        const int c = each_col(), r = (int)threadIdx.x / kAcross;
+        const int tr = (int)threadIdx.x % kDown * 8, tc = (int)threadIdx.x / kDown;
+        auto tile_row = [&](int p, int i) { return i / (kPer * 16) * S::kWM + p * 16 + i % (kPer * 16); };
+        decltype(fetch(0, 0)) f[kTimes], ahead[kTimes];
+        decltype(fetch_turned(0, 0)) ft[kTimes], ahead_t[kTimes];
+        auto fetch_pass = [&](int p) {
+#pragma unroll
+            for (int t = 0; t < kTimes; ++t) {
+                ahead[t] = fetch(tile_row(p, r + t * (S::kThreadsWg / kAcross)), c);
+                if constexpr (kTurned) ahead_t[t] = fetch_turned(tile_row(p, tr), tc + t * (S::kThreadsWg / kDown));
+            }
+        };
+        fetch_pass(0);
 #pragma unroll
         for (int p = 0; p < S::kFM; p += kPer) {
-            if (p > 0) __syncthreads();
+            if (p > 0) barrier_lds();
 #pragma unroll
             for (int m = 0; m < kPer; ++m)
 #pragma unroll
                 for (int n = 0; n < S::kFN; ++n)
                     *(f32x4_t*)(to + (wave / S::kCols * kPer * 16 + m * 16 + (lane & 15)) * kPitch + col0() + 16 * n) = acc[p + m][n];
-            __syncthreads();
-            auto tile_row = [&](int r) { return r / (kPer * 16) * S::kWM + p * 16 + r % (kPer * 16); };
-#pragma unroll 1
-            for (int i = threadIdx.x; i < kPassRows * S::kBN / 8; i += S::kThreadsWg) {
-                const int r = i / (S::kBN / 8), c = i % (S::kBN / 8) * 8;
-                const f32x4_t a = *(const f32x4_t*)(to + r * kPitch + c), b = *(const f32x4_t*)(to + r * kPitch + c + 4);
+#pragma unroll
+            for (int t = 0; t < kTimes; ++t) f[t] = ahead[t], ft[t] = ahead_t[t];
+            if (p + kPer < S::kFM) fetch_pass(p + kPer);
+            barrier_lds();
+#pragma unroll
+            for (int t = 0; t < kTimes; ++t) {
+                const int i = r + t * (S::kThreadsWg / kAcross);
+                const f32x4_t a = *(const f32x4_t*)(to + i * kPitch + c), b = *(const f32x4_t*)(to + i * kPitch + c + 4);
                 const float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-                body(tile_row(r), c, v);
+                body(tile_row(p, i), c, v, f[t]);
             }
             if constexpr (kTurned) {
-#pragma unroll 1
-                for (int i = threadIdx.x; i < kPassRows * S::kBN / 8; i += S::kThreadsWg) {
-                    const int r = i % (kPassRows / 8) * 8, c = i / (kPassRows / 8);
+#pragma unroll
+                for (int t = 0; t < kTimes; ++t) {
+                    const int i = tc + t * (S::kThreadsWg / kDown);
                     float v[8];
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) v[k] = to[(r + k) * kPitch + c];
-                    turned(tile_row(r), c, v);
+                    for (int k = 0; k < 8; ++k) v[k] = to[(tr + k) * kPitch + i];
+                    turned(tile_row(p, tr), i, v, ft[t]);
                 }
             }
         }
     }
-    template <class F>
-    __device__ __forceinline__ void each(char* lds, F body) {
-        each<false>(lds, body, 0);
+    struct Nothing {};
+    static __device__ __forceinline__ Nothing nothing(int, int) { return {}; }
+    template <int kPer, class L, class F>
+    __device__ __forceinline__ void each(char* lds, L fetch, F body) {
+        each<kPer, false>(lds, fetch, body, nothing, 0);
+    }
+
+    // Waits until at most kN of the wave's memory accesses are on their way.
+    template <int kN>
+    static __device__ __forceinline__ void wait_loads() {
+        static_assert(kN >= 0 && kN < 64, "six bits");
+        __builtin_amdgcn_s_waitcnt((kN & 15) | (kN >> 4) << 14 | 7 << 4 | 15 << 8);  // the other counters: no wait
+    }
+
+    // A barrier for what was written to LDS: loads from memory stay in flight.
+    static __device__ __forceinline__ void barrier_lds() {
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+        __builtin_amdgcn_s_barrier();
+        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
     }
 };
 

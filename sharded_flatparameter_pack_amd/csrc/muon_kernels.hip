@@ -68,7 +68,7 @@ __device__ __forceinline__ void ld_f32(const float* p, int have, float f[4]) {
 
 __device__ __forceinline__ void st_f32(float* p, int have, const float f[4]) {
     if (have == 4) {
-        st16u(p, bits_of(f));
+        put16u(p, bits_of(f));
         return;
     }
 #pragma unroll
@@ -78,7 +78,7 @@ __device__ __forceinline__ void st_f32(float* p, int have, const float f[4]) {
 
 __device__ __forceinline__ void st_16bit(void* p, int have, uint2 w) {
     if (have == 4) {
-        st8u(p, w);
+        put8h(p, w);
         return;
     }
     const uint64_t x = ((uint64_t)w.y << 32) | w.x;
@@ -87,7 +87,7 @@ __device__ __forceinline__ void st_16bit(void* p, int have, uint2 w) {
         if (k < have) gptr<uint16_t>(p)[k] = (uint16_t)(x >> (16 * k));
 }
 
-__device__ __forceinline__ uint2 f16x4(const float f[4]) { return make_uint2(f16x2(f[0], f[1]), f16x2(f[2], f[3])); }
+__device__ __forceinline__ uint2 f16x4(const float f[4]) { return make_uint2(f16_pair(f[0], f[1]), f16_pair(f[2], f[3])); }
 
 // ---------------------------------------------------------------- moment
 
@@ -140,14 +140,13 @@ __device__ __forceinline__ void st_x(char* ws, int64_t h, int64_t l, int64_t at,
     uint32_t hw[4], lw[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-        hw[k] = f16x2(x[2 * k], x[2 * k + 1]);
+        hw[k] = f16_pair(x[2 * k], x[2 * k + 1]);
         lw[k] = bf16x2(x[2 * k] - f16_lo(hw[k]), x[2 * k + 1] - f16_hi(hw[k]));
     }
     put16(ws + h + 2 * at, make_uint4(hw[0], hw[1], hw[2], hw[3]));
     put16(ws + l + 2 * at, make_uint4(lw[0], lw[1], lw[2], lw[3]));
 }
-__device__ __forceinline__ void ld_x(const char* ws, int64_t h, int64_t l, int64_t at, float x[8]) {
-    const uint4 a = get16(ws + h + 2 * at), b = get16(ws + l + 2 * at);
+__device__ __forceinline__ void x_of(const uint4 a, const uint4 b, float x[8]) {
     const uint32_t hw[4] = {a.x, a.y, a.z, a.w}, lw[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -155,14 +154,13 @@ __device__ __forceinline__ void ld_x(const char* ws, int64_t h, int64_t l, int64
         x[2 * k + 1] = f16_hi(hw[k]) + bf16_hi(lw[k]);
     }
 }
-__device__ __forceinline__ void ld_f16(const void* p, float x[8]) {
-    const uint4 a = get16(p);
+__device__ __forceinline__ void f16x8_to_f32(const uint4 a, float x[8]) {
     const uint32_t w[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
     for (int k = 0; k < 4; ++k) x[2 * k] = f16_lo(w[k]), x[2 * k + 1] = f16_hi(w[k]);
 }
 __device__ __forceinline__ void st_f16(void* p, const float x[8]) {
-    put16(p, make_uint4(f16x2(x[0], x[1]), f16x2(x[2], x[3]), f16x2(x[4], x[5]), f16x2(x[6], x[7])));
+    put16(p, make_uint4(f16_pair(x[0], x[1]), f16_pair(x[2], x[3]), f16_pair(x[4], x[5]), f16_pair(x[6], x[7])));
 }
 
 // ---------------------------------------------------------------- cast
@@ -227,7 +225,7 @@ __device__ __forceinline__ Operand columns_of(const char* base, int64_t first, i
 // A = X X^T (X^T X of a tall matrix): the tiles on and below the diagonal, and
 // their mirror images.
 template <class S>
-__global__ __launch_bounds__(S::kThreadsWg) void gram_kernel(const MuonArgs a) {
+__global__ __launch_bounds__(S::kThreadsWg, S::kWavesSimd) void gram_kernel(const MuonArgs a) {
     extern __shared__ __align__(16) char lds[];
     if (skipped(a)) return;
     const MatTile t = a.tiles[die_tile(blockIdx.x, a.n_tiles)];
@@ -241,7 +239,8 @@ __global__ __launch_bounds__(S::kThreadsWg) void gram_kernel(const MuonArgs a) {
     const float unscale = 1.0f / (a.s.x * a.s.x);
     const float out = a.s.a * unscale;
     char* to = a.ws + r.a;
-    auto body = [&](int tr, int tc, const float* v) {
+    typedef typename TileProduct<S>::Nothing Nothing;
+    auto body = [&](int tr, int tc, const float* v, Nothing) {
         const int row = i0 + tr, col = j0 + tc;
         if (row >= z.m || col >= z.m) return;
         float f[8];
@@ -256,10 +255,10 @@ __global__ __launch_bounds__(S::kThreadsWg) void gram_kernel(const MuonArgs a) {
         st_f16(to + 2 * ((int64_t)row * z.m + col), f);
     };
     if (t.ti == t.tj) {
-        tile.each(lds, body);
+        tile.template each<2>(lds, tile.nothing, body);
         return;
     }
-    tile.template each<true>(lds, body, [&](int tr, int tc, const float* v) {
+    tile.template each<2, true>(lds, tile.nothing, body, tile.nothing, [&](int tr, int tc, const float* v, Nothing) {
         const int row = i0 + tr, col = j0 + tc;
         if (row >= z.m || col >= z.m) return;
         float f[8];
@@ -272,7 +271,7 @@ __global__ __launch_bounds__(S::kThreadsWg) void gram_kernel(const MuonArgs a) {
 // B = b A + c A^2 in the same way; db holds a + B's diagonal.  With d the
 // diagonal of A and N the rest, A^2 = N^2 + (d_i + d_j) N off the diagonal.
 template <class S>
-__global__ __launch_bounds__(S::kThreadsWg) void poly_kernel(const MuonArgs a) {
+__global__ __launch_bounds__(S::kThreadsWg, S::kWavesSimd) void poly_kernel(const MuonArgs a) {
     extern __shared__ __align__(16) char lds[];
     if (skipped(a)) return;
     const MatTile t = a.tiles[die_tile(blockIdx.x, a.n_tiles)];
@@ -285,35 +284,54 @@ __global__ __launch_bounds__(S::kThreadsWg) void poly_kernel(const MuonArgs a) {
     const float un_a = 1.0f / a.s.a, un_s = un_a * un_a;
     const FP_GLOBAL float* d = gptr<float>((const void*)(a.ws + r.da));
     char* to = a.ws + r.b;
-    // eight elements (row, col ..); the mirror images are those of the other row, N being symmetric
-    auto poly = [&](int row, int col, const float* v, float f[8]) {
-        float x[8];
-        ld_f16(n + 2 * ((int64_t)row * z.m + col), x);
-        const float di = d[row];
+    // eight elements (row, col ..) of N, with their part of the diagonals; the
+    // mirror images of a tile are those of the other row, N being symmetric
+    struct Fetched {
+        uint4 n;
+        float row;
+    };
+    auto fetch = [&](int row, int col) {
+        Fetched f = {make_uint4(0u, 0u, 0u, 0u), 0.0f};
+        if (row < z.m && col < z.m) f = {get16(n + 2 * ((int64_t)row * z.m + col)), d[row]};
+        return f;
+    };
+    auto poly = [&](int row, int col, const float* v, const Fetched& e, const float dc[8]) {
+        if (row >= z.m || col >= z.m) return;
+        float x[8], f[8];
+        f16x8_to_f32(e.n, x);
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
             const float square = v[k] * un_s;
             x[k] *= un_a;
-            f[k] = (a.cb * x[k] + a.cc * (square + (di + d[col + k]) * x[k])) * a.s.b;
+            f[k] = __builtin_fmaf(a.cb, x[k], a.cc * __builtin_fmaf(e.row + dc[k], x[k], square)) * a.s.b;
             if (row == col + k) {
-                gptr<float>((void*)(a.ws + r.db))[row] = a.ca + (a.cb * di + a.cc * (square + di * di));
+                gptr<float>((void*)(a.ws + r.db))[row] = a.ca + (a.cb * e.row + a.cc * (square + e.row * e.row));
                 f[k] = 0.0f;
             }
         }
         st_f16(to + 2 * ((int64_t)row * z.m + col), f);
     };
-    auto body = [&](int tr, int tc, const float* v) {
-        float f[8];
-        if (i0 + tr < z.m && j0 + tc < z.m) poly(i0 + tr, j0 + tc, v, f);
-    };
+    float dc[8], dr[8];  // of the lane's columns; of the eight rows of a mirror image, per pass
+#pragma unroll
+    for (int k = 0; k < 8; ++k) dc[k] = j0 + tile.each_col() < z.m ? d[j0 + tile.each_col() + k] : 0.0f;
+    auto body = [&](int tr, int tc, const float* v, const Fetched& e) { poly(i0 + tr, j0 + tc, v, e, dc); };
+    auto straight = [&](int tr, int tc) { return fetch(i0 + tr, j0 + tc); };
+    constexpr int kPer = S::kFM > 4 ? 1 : 2;  // as many registers as there are
     if (t.ti == t.tj) {
-        tile.each(lds, body);
+        tile.template each<kPer>(lds, straight, body);
         return;
     }
-    tile.template each<true>(lds, body, [&](int tr, int tc, const float* v) {
-        float f[8];
-        if (i0 + tr < z.m && j0 + tc < z.m) poly(j0 + tc, i0 + tr, v, f);
-    });
+    int had = -1;
+    tile.template each<kPer, true>(
+        lds, straight, body, [&](int tr, int tc) { return fetch(j0 + tc, i0 + tr); },
+        [&](int tr, int tc, const float* v, const Fetched& e) {
+            if (tr != had) {
+                had = tr;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) dr[k] = i0 + tr < z.m ? d[i0 + tr + k] : 0.0f;
+            }
+            poly(j0 + tc, i0 + tr, v, e, dr);
+        });
 }
 
 // How the orthogonalised matrix leaves.
@@ -322,7 +340,7 @@ enum { kGoesOn = 0, kToUpdate = 1, kToWeights = 2 };
 // X <- (a + D) X + R X_h, in the matrix's own orientation: B X of a wide
 // matrix, X B of a tall one.
 template <class S, int kOut>
-__global__ __launch_bounds__(S::kThreadsWg) void next_kernel(const MuonArgs a) {
+__global__ __launch_bounds__(S::kThreadsWg, S::kWavesSimd) void next_kernel(const MuonArgs a) {
     extern __shared__ __align__(16) char lds[];
     const MatTile t = a.tiles[die_tile(blockIdx.x, a.n_tiles)];
     const MuonRec& r = a.recs[t.mat];
@@ -349,45 +367,75 @@ __global__ __launch_bounds__(S::kThreadsWg) void next_kernel(const MuonArgs a) {
                                                             : 1.0);
         decay = hp.decay;
     }
-    tile.each(lds, [&](int tr, int tc, const float* v) {
-        const int row = i0 + tr, col = j0 + tc;
-        if (row >= (kOut == kGoesOn ? r.rp : r.rows) || col >= (kOut == kGoesOn ? r.cp : r.cols)) return;
-        const int64_t at = (int64_t)row * r.cp + col;
-        float x[8];
-        if (!skip) {
-            ld_x(a.ws, r.h[a.step & 1], r.l, at, x);
+    const int rows = kOut == kGoesOn ? r.rp : r.rows, cols = kOut == kGoesOn ? r.cp : r.cols;
+    float dc[8];  // of a tall matrix: of the lane's columns
+    const int c0 = j0 + tile.each_col();
 #pragma unroll
-            for (int k = 0; k < 8; ++k) x[k] = d[z.turned ? col + k : row] * (x[k] * un_x) + v[k] * unscale;
-        }
-        if constexpr (kOut == kGoesOn) {
+    for (int k = 0; k < 8; ++k) dc[k] = !skip && z.turned && c0 < z.m ? d[c0 + k] : 0.0f;
+    struct Fetched {
+        uint4 h, l;
+        float d;
+        float w[kOut == kToWeights ? 8 : 1];
+    };
+    auto have_of = [&](int col, int q) { const int left = cols - col - q; return left < 4 ? left : 4; };
+    // a pass ahead: two fragments' rows, or one's with the weights, which take as many registers again
+    tile.template each<kOut == kToWeights ? 1 : 2>(
+        lds,
+        [&](int tr, int tc) {
+            const int row = i0 + tr, col = j0 + tc;
+            const uint4 none = make_uint4(0u, 0u, 0u, 0u);
+            Fetched f;
+            f.h = f.l = none;
+            f.d = 0.0f;
+            if (row >= rows || col >= cols) return f;
+            const int64_t at = 2 * ((int64_t)row * r.cp + col);
+            if (!skip) {
+                f.h = get16(h + at);
+                f.l = get16(a.ws + r.l + at);
+                f.d = z.turned ? 0.0f : d[row];
+            }
+            if constexpr (kOut == kToWeights) {
 #pragma unroll
-            for (int k = 0; k < 8; ++k) x[k] *= a.s.x_next;
-            st_x(a.ws, r.h[(a.step + 1) & 1], r.l, at, x);
-        } else {
+                for (int q = 0; q < 8; q += 4)
+                    if (have_of(col, q) > 0) ld_f32(r.master + (int64_t)row * r.cols + col + q, have_of(col, q), f.w + q);
+            }
+            return f;
+        },
+        [&](int tr, int tc, const float* v, Fetched& f) {
+            const int row = i0 + tr, col = j0 + tc;
+            if (row >= rows || col >= cols) return;
+            float x[8];
+            x_of(f.h, f.l, x);
 #pragma unroll
-            for (int q = 0; q < 8; q += 4) {
-                const int left = r.cols - col - q, have = left < 4 ? left : 4;
-                if (have <= 0) break;
-                const int64_t e = (int64_t)row * r.cols + col + q;
-                if constexpr (kOut == kToUpdate) {
-                    if (a.update_dtype == FP_DTYPE_F32) st_f32(static_cast<float*>(r.update) + e, have, x + q);
-                    else st_16bit(static_cast<uint16_t*>(r.update) + e, have,
-                                  a.update_dtype == FP_DTYPE_F16 ? f16x4(x + q) : f32x4_to_bf16(x + q));
-                } else {
-                    float w[4];
-                    ld_f32(r.master + e, have, w);
-                    if (!skip) {
+            for (int k = 0; k < 8; ++k) x[k] = __builtin_fmaf((z.turned ? dc[k] : f.d) * un_x, x[k], v[k] * unscale);
+            if constexpr (kOut == kGoesOn) {
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) w[k] = (float)(decay * (double)w[k] - rate * (double)x[q + k]);
-                        st_f32(r.master + e, have, w);
+                for (int k = 0; k < 8; ++k) x[k] *= a.s.x_next;
+                st_x(a.ws, r.h[(a.step + 1) & 1], r.l, (int64_t)row * r.cp + col, x);
+            } else {
+#pragma unroll
+                for (int q = 0; q < 8; q += 4) {
+                    const int have = have_of(col, q);
+                    if (have <= 0) break;
+                    const int64_t e = (int64_t)row * r.cols + col + q;
+                    if constexpr (kOut == kToUpdate) {
+                        if (a.update_dtype == FP_DTYPE_F32) st_f32(static_cast<float*>(r.update) + e, have, x + q);
+                        else st_16bit(static_cast<uint16_t*>(r.update) + e, have,
+                                      a.update_dtype == FP_DTYPE_F16 ? f16x4(x + q) : f32x4_to_bf16(x + q));
+                    } else {
+                        float* w = f.w + q;
+                        if (!skip) {
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) w[k] = (float)(decay * (double)w[k] - rate * (double)x[q + k]);
+                            st_f32(r.master + e, have, w);
+                        }
+                        if (r.copy != nullptr)
+                            st_16bit(static_cast<uint16_t*>(r.copy) + e, have,
+                                     a.copy_dtype == FP_DTYPE_F16 ? f16x4(w) : f32x4_to_bf16(w));
                     }
-                    if (r.copy != nullptr)
-                        st_16bit(static_cast<uint16_t*>(r.copy) + e, have,
-                                 a.copy_dtype == FP_DTYPE_F16 ? f16x4(w) : f32x4_to_bf16(w));
                 }
             }
-        }
-    });
+        });
 }
 
 // Launches kernel(a) over the argument block's tiles.

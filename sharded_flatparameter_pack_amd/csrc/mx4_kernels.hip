@@ -218,8 +218,8 @@ __global__ __launch_bounds__(256) void dequantize_kernel(const Mx4DequantArgs a,
     if constexpr (kDtype == FP_DTYPE_F32) {
         float* p = static_cast<float*>(a.out) + to;
         if (left >= 8) {
-            st16u(p, bits_of(f));
-            st16u(p + 4, bits_of(f + 4));
+            put16u(p, bits_of(f));
+            put16u(p + 4, bits_of(f + 4));
         } else {
             for (int k = 0; k < (int)left; ++k) gptr<float>((void*)p)[k] = f[k];
         }
@@ -228,9 +228,9 @@ __global__ __launch_bounds__(256) void dequantize_kernel(const Mx4DequantArgs a,
         uint32_t w[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-            w[k] = kDtype == FP_DTYPE_F16 ? f16x2(f[2 * k], f[2 * k + 1]) : bf16x2(f[2 * k], f[2 * k + 1]);
+            w[k] = kDtype == FP_DTYPE_F16 ? f16_pair(f[2 * k], f[2 * k + 1]) : bf16x2(f[2 * k], f[2 * k + 1]);
         if (left >= 8) {
-            st16u16(p, make_uint4(w[0], w[1], w[2], w[3]));
+            put16h(p, make_uint4(w[0], w[1], w[2], w[3]));
         } else {
             for (int k = 0; k < (int)left; ++k) gptr<uint16_t>((void*)p)[k] = (uint16_t)(w[k >> 1] >> (16 * (k & 1)));
         }
@@ -239,50 +239,55 @@ __global__ __launch_bounds__(256) void dequantize_kernel(const Mx4DequantArgs a,
 
 // ---------------------------------------------------------------- product
 
-// Eight neighbouring elements (row, col ..) of the output, those it has.
-__device__ __forceinline__ void st_out(const Mx4MatmulArgs& a, int64_t row, int64_t col, const float v[8]) {
+// Up to eight neighbouring elements of the output, as bits.
+struct Old {
+    uint32_t w[8];
+};
+
+// The output's old values, where they are added to.
+__device__ __forceinline__ Old ld_old(const Mx4MatmulArgs& a, int64_t row, int64_t col) {
+    Old o;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) o.w[k] = 0u;
+    if (a.accumulate && row < a.m && col < a.n) {
+        const int64_t left = a.n - col, at = row * a.pitch + col;
+        const int have = left < 8 ? (int)left : 8;
+        if (a.dtype == FP_DTYPE_F32) ld_bits<FP_DTYPE_F32>(a.out, at, have, o.w);
+        else ld_bits<FP_DTYPE_BF16>(a.out, at, have, o.w);
+    }
+    return o;
+}
+
+// Stores eight neighbouring elements (row, col ..), those that the output has.
+__device__ __forceinline__ void st_out(const Mx4MatmulArgs& a, int64_t row, int64_t col, const float v[8], const Old& o) {
+    if (row >= a.m || col >= a.n) return;
     const int64_t left = a.n - col, at = row * a.pitch + col;
-    if (left <= 0) return;
     const int have = left < 8 ? (int)left : 8;
+    const bool half = a.dtype == FP_DTYPE_F16;
     float f[8];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) f[k] = v[k];
+    for (int k = 0; k < 8; ++k) {
+        f[k] = v[k];
+        if (a.accumulate) f[k] += a.dtype == FP_DTYPE_F32 ? __uint_as_float(o.w[k]) : half ? f16_lo(o.w[k]) : bf16_lo(o.w[k]);
+    }
     if (a.dtype == FP_DTYPE_F32) {
         float* p = static_cast<float*>(a.out) + at;
         if (have == 8) {
-            if (a.accumulate) {
-                float o[8];
-                f32x4_of(ld16u(p), o);
-                f32x4_of(ld16u(p + 4), o + 4);
-#pragma unroll
-                for (int k = 0; k < 8; ++k) f[k] += o[k];
-            }
-            st16u(p, bits_of(f));
-            st16u(p + 4, bits_of(f + 4));
+            put16u(p, bits_of(f));
+            put16u(p + 4, bits_of(f + 4));
             return;
         }
+#pragma unroll
         for (int k = 0; k < 7; ++k)
-            if (k < have) {
-                FP_GLOBAL float* o = gptr<float>((void*)(p + k));
-                *o = a.accumulate ? *o + v[k] : v[k];
-            }
+            if (k < have) gptr<float>((void*)p)[k] = f[k];
         return;
     }
-    const bool half = a.dtype == FP_DTYPE_F16;
     uint16_t* p = static_cast<uint16_t*>(a.out) + at;
-    if (a.accumulate) {
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-            if (k < have) {
-                const uint32_t o = gptr<uint16_t>((const void*)p)[k];
-                f[k] += half ? f16_lo(o) : bf16_lo(o);
-            }
-    }
     uint32_t w[4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) w[k] = half ? f16x2(f[2 * k], f[2 * k + 1]) : bf16x2(f[2 * k], f[2 * k + 1]);
+    for (int k = 0; k < 4; ++k) w[k] = half ? f16_pair(f[2 * k], f[2 * k + 1]) : bf16x2(f[2 * k], f[2 * k + 1]);
     if (have == 8) {
-        st16u16(p, make_uint4(w[0], w[1], w[2], w[3]));
+        put16h(p, make_uint4(w[0], w[1], w[2], w[3]));
         return;
     }
 #pragma unroll
@@ -291,7 +296,7 @@ __device__ __forceinline__ void st_out(const Mx4MatmulArgs& a, int64_t row, int6
 }
 
 template <class S>
-__global__ __launch_bounds__(S::kThreadsWg) void matmul_kernel(const Mx4MatmulArgs a) {
+__global__ __launch_bounds__(S::kThreadsWg, S::kWavesSimd) void matmul_kernel(const Mx4MatmulArgs a) {
     extern __shared__ __align__(16) char lds[];
     const int t = die_tile(blockIdx.x, a.tiles_m * a.tiles_n);
     // bands of kBand rows of tiles, column by column: tiles that run together read few operands
@@ -305,9 +310,9 @@ __global__ __launch_bounds__(S::kThreadsWg) void matmul_kernel(const Mx4MatmulAr
     run_tile<kRowsFp4, kRowsFp4>(tile, {a.a + i0 * pitch, pitch, lm < S::kBM ? (int)lm : S::kBM, a.as + i0 * spitch},
                                  {a.b + j0 * pitch, pitch, ln < S::kBN ? (int)ln : S::kBN, a.bs + j0 * spitch},
                                  (int)(a.kp >> 8), lds);
-    tile.each(lds, [&](int r, int c, const float* v) {
-        if (i0 + r < a.m) st_out(a, i0 + r, j0 + c, v);
-    });
+    tile.template each<S::kFM < 2 ? 1 : 2>(
+        lds, [&](int r, int c) { return ld_old(a, i0 + r, j0 + c); },
+        [&](int r, int c, const float* v, const Old& o) { st_out(a, i0 + r, j0 + c, v, o); });
 }
 
 using Shape256 = TileShape<256, 256, 128, 64>;

@@ -88,6 +88,13 @@ __device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
            ((uint32_t)__builtin_bit_cast(uint16_t, (_Float16)hi) << 16);
 }
 
+// The same in one instruction.
+__device__ __forceinline__ uint32_t f16_pair(float lo, float hi) {
+    typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
+    typedef float f32x2_t __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2_t{lo, hi}), f16x2_t));
+}
+
 __device__ __forceinline__ void f32x4_of(const uint4 w, float f[4]) {
     f[0] = __uint_as_float(w.x); f[1] = __uint_as_float(w.y);
     f[2] = __uint_as_float(w.z); f[3] = __uint_as_float(w.w);
@@ -105,7 +112,9 @@ __device__ __forceinline__ void st16u(void* p, const uint4 v) {
     __builtin_nontemporal_store(w, (FP_GLOBAL u32x4_a4*)(p));
 }
 
-// 16 and 8 aligned bytes of data that is used again (no non-temporal hint).
+// 16 and 8 bytes without the non-temporal hint: data that is used again, and
+// stores whose lines several instructions write (non-temporal ones do not meet in
+// the L2: a step's weights and copies went to memory twice).
 __device__ __forceinline__ uint4 get16(const void* p) {
     const u32x4_t v = *gptr<u32x4_t>(p);
     return make_uint4(v.x, v.y, v.z, v.w);
@@ -114,14 +123,16 @@ __device__ __forceinline__ uint2 get8(const void* p) {
     const u32x2_t v = *gptr<u32x2_t>(p);
     return make_uint2(v.x, v.y);
 }
+__device__ __forceinline__ void put16u(void* p, const uint4 v) {  // from a 4-byte boundary
+    typedef unsigned int u32x4_a4u __attribute__((ext_vector_type(4), aligned(4)));
+    *gptr<u32x4_a4u>(p) = u32x4_a4u{v.x, v.y, v.z, v.w};
+}
+__device__ __forceinline__ void put16h(void* p, const uint4 v) {  // from a 2-byte boundary
+    *gptr<u32x4_a2>(p) = u32x4_a2{v.x, v.y, v.z, v.w};
+}
+__device__ __forceinline__ void put8h(void* p, const uint2 v) { *gptr<u32x2_a2>(p) = u32x2_a2{v.x, v.y}; }
 __device__ __forceinline__ void put16(void* p, const uint4 v) { *gptr<u32x4_t>(p) = u32x4_t{v.x, v.y, v.z, v.w}; }
 __device__ __forceinline__ void put8(void* p, const uint2 v) { *gptr<u32x2_t>(p) = u32x2_t{v.x, v.y}; }
-
-// 16 bytes to a 2-byte boundary.
-__device__ __forceinline__ void st16u16(void* p, const uint4 v) {
-    const u32x4_a2 w = {v.x, v.y, v.z, v.w};
-    __builtin_nontemporal_store(w, (FP_GLOBAL u32x4_a2*)(p));
-}
 
 // 32 bits of dither for partition element e: the element's index and the
 // call's key through two multiplications.  The multipliers are the golden
