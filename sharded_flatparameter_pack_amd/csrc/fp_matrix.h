@@ -32,7 +32,8 @@ struct MuonRec {
 constexpr int kPad = 64;
 inline int64_t pad64(int64_t n) { return (n + kPad - 1) / kPad * kPad; }
 
-// Tile (ti, tj) of matrix `mat`; what a tile is depends on the kernel.
+// Tile (ti, tj) of matrix `mat`; what a tile is depends on the kernel.  mat < 0:
+// none, in the tables of the products, which deal each die its own.
 struct MatTile {
     int32_t mat, ti, tj, pad;
 };

@@ -58,7 +58,9 @@ struct TileShape {
     static constexpr int kFM = kWM / 16, kFN = kWN / 16;        // 16x16 fragments of a wave
     static constexpr int kStage = (kBM + kBN) * kStepBytes;
     static constexpr int kScaleStage = (kBM + kBN) * 8;
-    static constexpr int kStages = kBM >= 128 ? 2 : 4;  // a power of two
+    // Four stages for the 64-wide tile save a 1024-wide product 2 of 12 us, and
+    // cost a 2048-wide one 19 of 32: two workgroups fit a CU then, not five.
+    static constexpr int kStages = 2;  // a power of two
     static constexpr int kLds = kStages * kStage;
     static constexpr int kLdsFp4 = kLds + kStages * kScaleStage;
 };

@@ -36,12 +36,6 @@ struct Batch {
     int half_shape = kTile64, full_shape = kTile64;
 };
 
-int64_t tiles_half(const MuonRec& r, int side) {
-    const int64_t m = ceil_div64(std::min(r.rp, r.cp), side);
-    return m * (m + 1) / 2;
-}
-int64_t tiles_full(const MuonRec& r, int side) { return ceil_div64(r.rp, side) * ceil_div64(r.cp, side); }
-
 }  // namespace
 
 struct fp_muon {
@@ -123,47 +117,124 @@ int64_t lay_out(MuonRec* r, int64_t at) {
     return at;
 }
 
-// The tile that a batch's products take: with n tiles on 256 CUs, the busiest
-// has ceil(n / 256), which take kWork each, or kAlone where one by itself
-// leaves its CU waiting (in units of a 256-wide tile's time).
-int choose_shape(const std::vector<MuonRec>& recs, int32_t from, int32_t to, int64_t (*tiles)(const MuonRec&, int)) {
-    constexpr double kWork[3] = {1.0, 0.31, 0.12}, kAlone[3] = {1.0, 0.45, 0.25};
-    int best = kTile64;
-    double least = 0.0;
-    for (int shape : {kTile256, kTile128, kTile64}) {
-        int64_t n = 0;
-        for (int32_t i = from; i < to; ++i) n += tiles(recs[(size_t)i], kTileSide[shape]);
-        const double time = std::max(kAlone[shape], kWork[shape] * (double)ceil_div64(n, 256));
-        if (shape == kTile256 || time < least) best = shape, least = time;
+// Neighbouring tiles of one matrix's product, and the steps along K of each.
+struct Chunk {
+    int32_t mat;
+    int64_t steps;
+    std::vector<MatTile> tiles;
+};
+
+// The tiles of one matrix in an order in which neighbours read the same rows
+// and columns: bands of four rows, column by column.  half: those on and below
+// the diagonal of the smaller side's square.
+std::vector<MatTile> ordered(const MuonRec& r, int32_t mat, int side, bool half) {
+    const int64_t m = std::min(r.rp, r.cp);
+    const int32_t rows = (int32_t)ceil_div64(half ? m : r.rp, side), cols = (int32_t)ceil_div64(half ? m : r.cp, side);
+    std::vector<MatTile> v;
+    for (int32_t band = 0; band < rows; band += 4)
+        for (int32_t j = 0; j < cols; ++j)
+            for (int32_t i = band; i < std::min(rows, band + 4); ++i)
+                if (!half || j <= i) v.push_back({mat, i, j, 0});
+    return v;
+}
+
+// A batch's product on tiles of one shape: when would its last workgroup end?
+// In us, from what one step of a tile takes when its CU is full and when it is
+// alone there, and from what a tile takes beside its steps (MI355X, the tiles'
+// kernels at 1024 to 4096).
+double finish(const std::vector<MuonRec>& recs, const Batch& b, int shape, bool half) {
+    constexpr double kStep[3] = {1.6, 0.56, 0.26}, kAlone[3] = {1.3, 0.65, 0.36}, kBeside[3] = {14.0, 6.0, 2.0};
+    std::vector<double> cost;   // by descending length, a run for each matrix
+    std::vector<std::pair<int64_t, int64_t>> runs;  // steps, tiles
+    for (int32_t i = b.from; i < b.to; ++i) {
+        const MuonRec& r = recs[(size_t)i];
+        if (r.rows == 0 || r.cols == 0) continue;
+        const int64_t m = std::min(r.rp, r.cp), n = std::max(r.rp, r.cp), t = ceil_div64(m, kTileSide[shape]);
+        runs.push_back({(half ? n : m) / 64, half ? t * (t + 1) / 2 : t * ceil_div64(n, kTileSide[shape])});
     }
+    std::sort(runs.rbegin(), runs.rend());
+    constexpr int kCus = 256;
+    double load[kCus] = {};
+    int64_t held[kCus] = {};
+    double alone = 0.0;
+    for (const auto& run : runs) {
+        const double c = kStep[shape] * (double)run.first + kBeside[shape];
+        alone = std::max(alone, kAlone[shape] * (double)run.first + kBeside[shape]);
+        int64_t left = run.second;
+        const int64_t each = left / kCus > 4 ? left / kCus - 2 : 0;  // most of a long run goes everywhere alike
+        for (int k = 0; k < kCus; ++k) load[k] += c * (double)each, held[k] += each;
+        for (left -= each * kCus; left > 0; --left) {
+            const int k = (int)(std::min_element(load, load + kCus) - load);
+            load[k] += c;
+            ++held[k];
+        }
+    }
+    double end = alone;
+    for (int k = 0; k < kCus; ++k)
+        if (held[k] > 1) end = std::max(end, load[k]);
+    return end;
+}
+
+int choose_shape(const std::vector<MuonRec>& recs, const Batch& b, bool half) {
+    int best = kTile256;
+    for (int shape : {kTile128, kTile64})
+        if (finish(recs, b, shape, half) < finish(recs, b, best, half)) best = shape;
     return best;
+}
+
+// The table of a product.  The hardware deals workgroups out to the 8 dies in
+// turn, each with an L2 of its own: entry 8 i + d is die d's i-th tile.  Runs of
+// neighbours go to the die with the least work so far, the longest tiles first.
+void deal(const std::vector<MuonRec>& recs, const Batch& b, int side, bool half, std::vector<MatTile>* table) {
+    constexpr int kDies = 8;
+    std::vector<Chunk> chunks;
+    int64_t total = 0;
+    for (int32_t i = b.from; i < b.to; ++i) {
+        const MuonRec& r = recs[(size_t)i];
+        if (r.rows == 0 || r.cols == 0) continue;
+        Chunk c = {i, (half ? std::max(r.rp, r.cp) : std::min(r.rp, r.cp)) / 64, ordered(r, i, side, half)};
+        total += (int64_t)c.tiles.size();
+        chunks.push_back(std::move(c));
+    }
+    std::stable_sort(chunks.begin(), chunks.end(), [](const Chunk& x, const Chunk& y) { return x.steps > y.steps; });
+    // at most a quarter of a die's share, so that the shares come out alike
+    const size_t most = (size_t)std::max<int64_t>(1, std::min<int64_t>(32, total / (4 * kDies)));
+    std::vector<MatTile> die[kDies];
+    int64_t load[kDies] = {};
+    for (const Chunk& c : chunks)
+        for (size_t at = 0; at < c.tiles.size(); at += most) {
+            const size_t n = std::min(most, c.tiles.size() - at);
+            const int d = (int)(std::min_element(load, load + kDies) - load);
+            load[d] += c.steps * (int64_t)n;
+            die[d].insert(die[d].end(), c.tiles.begin() + (int64_t)at, c.tiles.begin() + (int64_t)(at + n));
+        }
+    size_t rows = 0;
+    for (const auto& d : die) rows = std::max(rows, d.size());
+    for (size_t i = 0; i < rows; ++i)
+        for (const auto& d : die) table->push_back(i < d.size() ? d[i] : MatTile{-1, 0, 0, 0});
 }
 
 // Closes a batch: its tiles, appended to the table.
 void close_batch(const std::vector<MuonRec>& recs, Batch* b, std::vector<MatTile>* table) {
-    b->half_shape = choose_shape(recs, b->from, b->to, tiles_half);
-    b->full_shape = choose_shape(recs, b->from, b->to, tiles_full);
-    auto run = [&](Run* r, auto&& each) {
+    auto run = [&](Run* r, auto&& fill) {
         r->first = (int64_t)table->size();
-        for (int32_t i = b->from; i < b->to; ++i)
-            if (recs[i].rows > 0 && recs[i].cols > 0) each(i, recs[i]);
+        fill();
         r->n = (int64_t)table->size() - r->first;
     };
-    auto grid = [&](int32_t i, int64_t rows, int64_t cols) {
-        for (int64_t ti = 0; ti < rows; ++ti)
-            for (int64_t tj = 0; tj < cols; ++tj) table->push_back({i, (int32_t)ti, (int32_t)tj, 0});
+    auto grid = [&](auto&& rows, auto&& cols) {
+        for (int32_t i = b->from; i < b->to; ++i)
+            if (recs[(size_t)i].rows > 0 && recs[(size_t)i].cols > 0)
+                for (int64_t ti = 0; ti < rows(recs[(size_t)i]); ++ti)
+                    for (int64_t tj = 0; tj < cols(recs[(size_t)i]); ++tj) table->push_back({i, (int32_t)ti, (int32_t)tj, 0});
     };
-    run(&b->moment, [&](int32_t i, const MuonRec& r) { grid(i, r.chunks, 1); });
-    run(&b->cast, [&](int32_t i, const MuonRec& r) { grid(i, r.rp / kCastRows, ceil_div64(r.cp, kCastCols)); });
-    run(&b->half, [&](int32_t i, const MuonRec& r) {
-        const int64_t m = ceil_div64(std::min(r.rp, r.cp), kTileSide[b->half_shape]);
-        for (int64_t ti = 0; ti < m; ++ti)
-            for (int64_t tj = 0; tj <= ti; ++tj) table->push_back({i, (int32_t)ti, (int32_t)tj, 0});
+    run(&b->moment, [&] { grid([](const MuonRec& r) { return (int64_t)r.chunks; }, [](const MuonRec&) { return (int64_t)1; }); });
+    run(&b->cast, [&] {
+        grid([](const MuonRec& r) { return (int64_t)r.rp / kCastRows; }, [](const MuonRec& r) { return ceil_div64(r.cp, kCastCols); });
     });
-    run(&b->full, [&](int32_t i, const MuonRec& r) {
-        const int side = kTileSide[b->full_shape];
-        grid(i, ceil_div64(r.rp, side), ceil_div64(r.cp, side));
-    });
+    b->half_shape = choose_shape(recs, *b, true);
+    b->full_shape = choose_shape(recs, *b, false);
+    run(&b->half, [&] { deal(recs, *b, kTileSide[b->half_shape], true, table); });
+    run(&b->full, [&] { deal(recs, *b, kTileSide[b->full_shape], false, table); });
 }
 
 fp_status create(int32_t n, const int64_t* rows, const int64_t* cols, const int32_t* group, int32_t grad_dtype,

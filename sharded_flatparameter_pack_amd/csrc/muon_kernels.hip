@@ -228,7 +228,8 @@ template <class S>
 __global__ __launch_bounds__(S::kThreadsWg, S::kWavesSimd) void gram_kernel(const MuonArgs a) {
     extern __shared__ __align__(16) char lds[];
     if (skipped(a)) return;
-    const MatTile t = a.tiles[die_tile(blockIdx.x, a.n_tiles)];
+    const MatTile t = a.tiles[blockIdx.x];
+    if (t.mat < 0) return;
     const MuonRec& r = a.recs[t.mat];
     const Sides z = sides(r);
     const char* h = a.ws + r.h[a.step & 1];
@@ -274,7 +275,8 @@ template <class S>
 __global__ __launch_bounds__(S::kThreadsWg, S::kWavesSimd) void poly_kernel(const MuonArgs a) {
     extern __shared__ __align__(16) char lds[];
     if (skipped(a)) return;
-    const MatTile t = a.tiles[die_tile(blockIdx.x, a.n_tiles)];
+    const MatTile t = a.tiles[blockIdx.x];
+    if (t.mat < 0) return;
     const MuonRec& r = a.recs[t.mat];
     const Sides z = sides(r);
     const char* n = a.ws + r.a;
@@ -342,7 +344,8 @@ enum { kGoesOn = 0, kToUpdate = 1, kToWeights = 2 };
 template <class S, int kOut>
 __global__ __launch_bounds__(S::kThreadsWg, S::kWavesSimd) void next_kernel(const MuonArgs a) {
     extern __shared__ __align__(16) char lds[];
-    const MatTile t = a.tiles[die_tile(blockIdx.x, a.n_tiles)];
+    const MatTile t = a.tiles[blockIdx.x];
+    if (t.mat < 0) return;
     const MuonRec& r = a.recs[t.mat];
     const Sides z = sides(r);
     const int i0 = t.ti * S::kBM, j0 = t.tj * S::kBN;
