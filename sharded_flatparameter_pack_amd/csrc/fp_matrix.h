@@ -46,7 +46,16 @@ struct MuonGroup {
 // The scales of one step of the iteration: powers of two by which the fp16
 // forms are multiplied so that no element passes fp16's range.
 struct MuonScale {
-    float x, a, b, x_next;
+    float x, b, x_next;       // X's, B's and the next X's
+    float gram;               // what the products of X's fp16 forms become A's by: a / x^2
+    float un_x, un_xx, un_a, un_bx;  // 1 / x, 1 / x^2, 1 / a, 1 / (b x)
+};
+
+// A whole iteration, for the kernel that runs all of it.
+struct MuonSteps {
+    int32_t n;
+    MuonScale s[FP_MUON_MAX_STEPS];
+    float c[FP_MUON_MAX_STEPS][3];
 };
 
 struct MuonArgs {
@@ -69,9 +78,30 @@ struct MuonArgs {
 // Of the kernel that writes X: the padded matrix in pieces of so many rows and columns.
 constexpr int kCastRows = 16, kCastCols = 128;
 
-enum { kTile256 = 0, kTile128 = 1, kTile64 = 2 };
-constexpr int kTileSide[3] = {256, 128, 64};
+// Tiles of the products.  kTile64Deep: with eight stages in LDS, for a
+// workgroup that has its CU to itself.
+enum { kTile256 = 0, kTile128 = 1, kTile64 = 2, kTile64Deep = 3, kTileShapes = 4 };
+constexpr int kTileSide[kTileShapes] = {256, 128, 64, 64};
 
+constexpr unsigned kMaxLds = (160u << 10) - 512;  // a workgroup's, without what a kernel declares itself
+
+// Small matrices: what one workgroup needs for one of rows x cols, in bytes of
+// LDS and in 16 x 16 tiles per wave: up to 4 as they come, else four by four.
+constexpr int kSmallThreads = 512;
+constexpr int kSmallTiles = 16;
+inline int64_t small_lds(int64_t rows, int64_t cols) {
+    const int64_t m = ceil_div64(rows < cols ? rows : cols, 32) * 32, n = ceil_div64(rows < cols ? cols : rows, 32) * 32;
+    return m * (2 * n + 16) + 2 * m * (2 * m + 16) + 8 * m;
+}
+inline int64_t small_tiles(int64_t rows, int64_t cols) {
+    const int64_t blocks = ceil_div64(rows, 32) * ceil_div64(cols, 32), waves = kSmallThreads / 64;
+    return 4 * blocks <= 4 * waves ? ceil_div64(4 * blocks, waves) : 4 * ceil_div64(blocks, waves);
+}
+inline bool is_small(int64_t rows, int64_t cols) {
+    return small_tiles(rows, cols) <= kSmallTiles && small_lds(rows, cols) <= (int64_t)kMaxLds;
+}
+
+hipError_t launch_muon_small(const MuonArgs& a, const MuonSteps& steps, int tiles, unsigned lds, hipStream_t s);
 hipError_t launch_muon_moment(const MuonArgs& a, hipStream_t s);
 hipError_t launch_muon_cast(const MuonArgs& a, hipStream_t s);
 hipError_t launch_muon_gram(const MuonArgs& a, int shape, hipStream_t s);

@@ -44,8 +44,32 @@ typedef int i32x8_t __attribute__((ext_vector_type(8)));
 constexpr int kStepBytes = 128;  // of a row, per step along K
 constexpr int kStepF16 = 64;
 
-// kBM x kBN of the output per workgroup, kWM x kWN of it per wave.
-template <int kBM_, int kBN_, int kWM_, int kWN_>
+// A buffer's descriptor: raw bytes, offsets from `base` on.
+__device__ __forceinline__ i32x4_t buffer_of(const void* base) {
+    const uint64_t p = (uint64_t)base;
+    return i32x4_t{(int)(uint32_t)p, (int)(uint32_t)(p >> 32) & 0xFFFF, -1, 0x00020000};
+}
+
+// Loads 16 (4) bytes per lane into LDS, the wave's one behind the other from
+// `to` on; buffer, `to` and soffset are the same in all lanes.  Written out, as
+// the compiler waits for all such loads before every transposing read of LDS
+// that follows the builtin's (a 1400 x 64 matrix's A: 16 us, without 10).  It
+// counts neither these loads nor waits for them: the loop does (wait_loads).
+// M0 is LDS's base and needs a wait state behind its write.
+__device__ __forceinline__ void load_lds16(i32x4_t buffer, const char* to, int voffset, int soffset) {
+    const uint32_t at = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(FP_LDS const char*)to);
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+                 :: "s"(at), "v"(voffset), "s"(buffer), "s"(soffset) : "memory", "m0");
+}
+__device__ __forceinline__ void load_lds4(i32x4_t buffer, const char* to, int voffset, int soffset) {
+    const uint32_t at = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(FP_LDS const char*)to);
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, %3 offen lds"
+                 :: "s"(at), "v"(voffset), "s"(buffer), "s"(soffset) : "memory", "m0");
+}
+
+// kBM x kBN of the output per workgroup, kWM x kWN of it per wave; a power of
+// two of stages.
+template <int kBM_, int kBN_, int kWM_, int kWN_, int kStages_ = 2>
 struct TileShape {
     static constexpr int kBM = kBM_, kBN = kBN_, kWM = kWM_, kWN = kWN_;
     static constexpr int kRows = kBM / kWM, kCols = kBN / kWN;  // of waves
@@ -58,9 +82,7 @@ struct TileShape {
     static constexpr int kFM = kWM / 16, kFN = kWN / 16;        // 16x16 fragments of a wave
     static constexpr int kStage = (kBM + kBN) * kStepBytes;
     static constexpr int kScaleStage = (kBM + kBN) * 8;
-    // Four stages for the 64-wide tile save a 1024-wide product 2 of 12 us, and
-    // cost a 2048-wide one 19 of 32: two workgroups fit a CU then, not five.
-    static constexpr int kStages = 2;  // a power of two
+    static constexpr int kStages = kStages_;
     static constexpr int kLds = kStages * kStage;
     static constexpr int kLdsFp4 = kLds + kStages * kScaleStage;
 };
@@ -129,11 +151,10 @@ struct Side {
 
     __device__ __forceinline__ void load(char* stage, int wave, int step) const {
         const char* from = kColumns ? base + (int64_t)step * kStepF16 * pitch : base;
-        const __amdgpu_buffer_rsrc_t rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(from), 0, -1, 0x00020000);
+        const i32x4_t buffer = buffer_of(from);
 #pragma unroll
         for (int i = 0; i < kLoads; ++i)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (FP_LDS void*)(stage + (i * S::kWavesWg + wave) * 1024), 16,
-                                                     voffset[i], kColumns ? 0 : step * kStepBytes, 0, 0);
+            load_lds16(buffer, stage + (i * S::kWavesWg + wave) * 1024, voffset[i], kColumns ? 0 : step * kStepBytes);
     }
     template <int kH>
     __device__ __forceinline__ void read(const char* stage, i32x4_t (&f)[kF]) const {
@@ -252,9 +273,7 @@ struct TileProduct {
                 for (int i = 0; i < kSLoads; ++i) {
                     const int dword = i * S::kThreadsWg + wave * 64;
                     const uint8_t* from = dword / 2 >= S::kBM ? right.scales : left.scales;
-                    __builtin_amdgcn_raw_ptr_buffer_load_lds(
-                        __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(from), 0, -1, 0x00020000),
-                        (FP_LDS void*)(scales + k % S::kStages * S::kScaleStage + dword * 4), 4, soffset[i], step * 8, 0, 0);
+                    load_lds4(buffer_of(from), scales + k % S::kStages * S::kScaleStage + dword * 4, soffset[i], step * 8);
                 }
             }
         };
@@ -300,7 +319,8 @@ struct TileProduct {
             interleave<kLeft, kRight>();
             if constexpr (kFp4) s0 = s1;
         }
-        __syncthreads();
+        wait_loads<0>();
+        barrier_lds();
     }
 
     // The column that a lane has in each(): the first of its eight.

@@ -30,8 +30,15 @@ struct Run {
     int64_t first = 0, n = 0;
 };
 
+// Small matrices that need about as much: one launch.
+struct Small {
+    Run run;
+    int tiles = 0;
+    unsigned lds = 0;
+};
+
 struct Batch {
-    int32_t from = 0, to = 0;  // matrices
+    std::vector<int32_t> mats;
     Run moment, cast, half, full;
     int half_shape = kTile64, full_shape = kTile64;
 };
@@ -47,6 +54,7 @@ struct fp_muon {
     int64_t partition = 0, workspace = 0, tiles = 0;
     std::vector<int64_t> numel, offset;
     std::vector<Batch> batches;
+    std::vector<Small> smalls;
     std::vector<Span> written;         // weights, copies and updates
     void* dev = nullptr;               // records, gradient table, tile table
     void* staging = nullptr;           // pinned, of the gradient table's uploads
@@ -143,12 +151,10 @@ std::vector<MatTile> ordered(const MuonRec& r, int32_t mat, int side, bool half)
 // alone there, and from what a tile takes beside its steps (MI355X, the tiles'
 // kernels at 1024 to 4096).
 double finish(const std::vector<MuonRec>& recs, const Batch& b, int shape, bool half) {
-    constexpr double kStep[3] = {1.6, 0.56, 0.26}, kAlone[3] = {1.3, 0.65, 0.36}, kBeside[3] = {14.0, 6.0, 2.0};
-    std::vector<double> cost;   // by descending length, a run for each matrix
+    constexpr double kStep[] = {1.6, 0.56, 0.26, 0.4}, kAlone[] = {1.3, 0.65, 0.36, 0.2}, kBeside[] = {14.0, 6.0, 2.0, 3.0};
     std::vector<std::pair<int64_t, int64_t>> runs;  // steps, tiles
-    for (int32_t i = b.from; i < b.to; ++i) {
+    for (int32_t i : b.mats) {
         const MuonRec& r = recs[(size_t)i];
-        if (r.rows == 0 || r.cols == 0) continue;
         const int64_t m = std::min(r.rp, r.cp), n = std::max(r.rp, r.cp), t = ceil_div64(m, kTileSide[shape]);
         runs.push_back({(half ? n : m) / 64, half ? t * (t + 1) / 2 : t * ceil_div64(n, kTileSide[shape])});
     }
@@ -177,7 +183,7 @@ double finish(const std::vector<MuonRec>& recs, const Batch& b, int shape, bool 
 
 int choose_shape(const std::vector<MuonRec>& recs, const Batch& b, bool half) {
     int best = kTile256;
-    for (int shape : {kTile128, kTile64})
+    for (int shape = kTile128; shape < kTileShapes; ++shape)
         if (finish(recs, b, shape, half) < finish(recs, b, best, half)) best = shape;
     return best;
 }
@@ -189,9 +195,8 @@ void deal(const std::vector<MuonRec>& recs, const Batch& b, int side, bool half,
     constexpr int kDies = 8;
     std::vector<Chunk> chunks;
     int64_t total = 0;
-    for (int32_t i = b.from; i < b.to; ++i) {
+    for (int32_t i : b.mats) {
         const MuonRec& r = recs[(size_t)i];
-        if (r.rows == 0 || r.cols == 0) continue;
         Chunk c = {i, (half ? std::max(r.rp, r.cp) : std::min(r.rp, r.cp)) / 64, ordered(r, i, side, half)};
         total += (int64_t)c.tiles.size();
         chunks.push_back(std::move(c));
@@ -222,10 +227,9 @@ void close_batch(const std::vector<MuonRec>& recs, Batch* b, std::vector<MatTile
         r->n = (int64_t)table->size() - r->first;
     };
     auto grid = [&](auto&& rows, auto&& cols) {
-        for (int32_t i = b->from; i < b->to; ++i)
-            if (recs[(size_t)i].rows > 0 && recs[(size_t)i].cols > 0)
-                for (int64_t ti = 0; ti < rows(recs[(size_t)i]); ++ti)
-                    for (int64_t tj = 0; tj < cols(recs[(size_t)i]); ++tj) table->push_back({i, (int32_t)ti, (int32_t)tj, 0});
+        for (int32_t i : b->mats)
+            for (int64_t ti = 0; ti < rows(recs[(size_t)i]); ++ti)
+                for (int64_t tj = 0; tj < cols(recs[(size_t)i]); ++tj) table->push_back({i, (int32_t)ti, (int32_t)tj, 0});
     };
     run(&b->moment, [&] { grid([](const MuonRec& r) { return (int64_t)r.chunks; }, [](const MuonRec&) { return (int64_t)1; }); });
     run(&b->cast, [&] {
@@ -235,6 +239,31 @@ void close_batch(const std::vector<MuonRec>& recs, Batch* b, std::vector<MatTile
     b->full_shape = choose_shape(recs, *b, false);
     run(&b->half, [&] { deal(recs, *b, kTileSide[b->half_shape], true, table); });
     run(&b->full, [&] { deal(recs, *b, kTileSide[b->full_shape], false, table); });
+}
+
+// The small matrices by what they need, largest first, in launches: a new one
+// where a matrix needs half as much as the launch's first or less (its LDS
+// decides how many workgroups a CU holds, its tiles how many registers), but not
+// for the few that a launch of their own would cost more than it saves.
+std::vector<Small> group_small(const std::vector<MuonRec>& recs, std::vector<int32_t> mats, std::vector<MatTile>* table) {
+    auto lds = [&](int32_t i) { return small_lds(recs[(size_t)i].rows, recs[(size_t)i].cols); };
+    auto tiles = [&](int32_t i) { return small_tiles(recs[(size_t)i].rows, recs[(size_t)i].cols); };
+    std::stable_sort(mats.begin(), mats.end(), [&](int32_t x, int32_t y) { return lds(x) > lds(y); });
+    std::vector<Small> v;
+    for (size_t at = 0; at < mats.size(); ++at) {
+        const int32_t i = mats[at];
+        if (v.empty() || (2 * lds(i) <= (int64_t)v.back().lds && mats.size() - at > 512)) {
+            Small s;
+            s.run.first = (int64_t)table->size();
+            s.lds = (unsigned)lds(i);
+            v.push_back(s);
+        }
+        Small& s = v.back();
+        s.tiles = std::max(s.tiles, (int)tiles(i));
+        ++s.run.n;
+        table->push_back({i, 0, 0, 0});
+    }
+    return v;
 }
 
 fp_status create(int32_t n, const int64_t* rows, const int64_t* cols, const int32_t* group, int32_t grad_dtype,
@@ -259,6 +288,7 @@ fp_status create(int32_t n, const int64_t* rows, const int64_t* cols, const int3
     int64_t partition = 0, workspace = 0, at = 0;
     int32_t max_group = 0;
     Batch open;
+    std::vector<int32_t> small;
     for (int32_t i = 0; i < n; ++i) {
         if (rows[i] < 0 || rows[i] > kMaxSide || cols[i] < 0 || cols[i] > kMaxSide)
             return bad(FP_ERR_RANGE, "matrix %d: %lld x %lld, sides go up to %lld", i, (long long)rows[i], (long long)cols[i],
@@ -304,18 +334,22 @@ fp_status create(int32_t n, const int64_t* rows, const int64_t* cols, const int3
             partition += ceil_div64(numel, 32) * 32;
             if (r.rp / kCastRows * ceil_div64(r.cp, kCastCols) > 0xFFFFFFFFLL / 256)
                 return bad(FP_ERR_RANGE, "matrix %d needs more workgroups than one launch holds", i);
-            at = lay_out(&r, at);
-            workspace = std::max(workspace, at);
+            if (is_small(rows[i], cols[i])) {
+                small.push_back(i);
+            } else {
+                open.mats.push_back(i);
+                at = lay_out(&r, at);
+                workspace = std::max(workspace, at);
+            }
         }
-        open.to = i + 1;
-        if (at >= kBatchBytes || i + 1 == n) {
+        if (at >= kBatchBytes || (i + 1 == n && at > 0)) {
             close_batch(recs, &open, &table);
-            batches.push_back(open);
+            batches.push_back(std::move(open));
             open = Batch();
-            open.from = open.to = i + 1;
             at = 0;
         }
     }
+    std::vector<Small> smalls = group_small(recs, std::move(small), &table);
     std::sort(written.begin(), written.end());
     for (size_t i = 1; i < written.size(); ++i)
         if (meet(written[i - 1], written[i])) return bad(FP_ERR_INVALID, "two of the weights, copies and updates overlap");
@@ -338,6 +372,7 @@ fp_status create(int32_t n, const int64_t* rows, const int64_t* cols, const int3
     p->numel = std::move(sizes);
     p->offset = std::move(offsets);
     p->batches = std::move(batches);
+    p->smalls = std::move(smalls);
     p->written = std::move(written);
     p->read = std::move(read);
     const size_t rec_b = sizeof(MuonRec) * (size_t)n, ptr_b = sizeof(void*) * (size_t)((n + 1) / 2 * 2);
@@ -455,9 +490,14 @@ fp_status plan_steps(int32_t steps, const double* coefs, std::vector<Step>* out)
         // beyond these the fp32 sums and the fp16 scales leave their ranges
         if (!(s <= 256.0) || !(top <= 60000.0) || !(next <= 256.0))
             return bad(FP_ERR_RANGE, "coefs of step %d let singular values grow to %g", i, next);
+        const float of_a = scale_for(s2);
         t.s.x = scale_for(s);
-        t.s.a = scale_for(s2);
         t.s.b = scale_for(std::max(top, 1e-3));
+        t.s.un_x = 1.0f / t.s.x;
+        t.s.un_xx = t.s.un_x * t.s.un_x;
+        t.s.un_a = 1.0f / of_a;
+        t.s.un_bx = t.s.un_x / t.s.b;
+        t.s.gram = of_a * t.s.un_xx;
         s = std::max(next, 1e-3);
         t.s.x_next = scale_for(s * (1.0 + 1.0 / 64));
         out->push_back(t);
@@ -472,13 +512,27 @@ fp_status run(fp_muon* p, MuonArgs a, const std::vector<Step>& steps, bool to_we
     a.grad_dtype = p->grad_dtype;
     a.copy_dtype = p->copy_dtype;
     a.update_dtype = p->update_dtype;
+    auto over = [&](const Run& r) {
+        a.tiles = p->tile_table() + r.first;
+        a.n_tiles = (int32_t)r.n;
+    };
+    hipError_t e;
+    if (!p->smalls.empty()) {
+        MuonSteps it;
+        std::memset(&it, 0, sizeof it);
+        it.n = (int32_t)steps.size();
+        for (size_t i = 0; i < steps.size(); ++i) {
+            it.s[i] = steps[i].s;
+            it.c[i][0] = steps[i].a;
+            it.c[i][1] = steps[i].b;
+            it.c[i][2] = steps[i].c;
+        }
+        for (const Small& m : p->smalls) {
+            over(m.run);
+            if ((e = launch_muon_small(a, it, m.tiles, m.lds, s)) != hipSuccess) return device_error(e, "small matrices' launch");
+        }
+    }
     for (const Batch& b : p->batches) {
-        if (b.full.n == 0) continue;
-        auto over = [&](const Run& r) {
-            a.tiles = p->tile_table() + r.first;
-            a.n_tiles = (int32_t)r.n;
-        };
-        hipError_t e;
         over(b.moment);
         if ((e = launch_muon_moment(a, s)) != hipSuccess) return device_error(e, "momentum launch");
         over(b.cast);

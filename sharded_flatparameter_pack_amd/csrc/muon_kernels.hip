@@ -25,6 +25,9 @@
 //
 // Compiled with -ffp-contract=off.
 
+#include <atomic>
+#include <type_traits>
+
 #include "fp_matrix.h"
 #include "mma_tile.h"
 #include "param_ops.h"
@@ -36,6 +39,7 @@ namespace {
 using Shape256 = TileShape<256, 256, 128, 64>;
 using Shape128 = TileShape<128, 128, 64, 64>;
 using Shape64 = TileShape<64, 64, 32, 32>;
+using Shape64Deep = TileShape<64, 64, 32, 32, 8>;
 
 __device__ __forceinline__ bool skipped(const MuonArgs& a) { return a.found_inf != nullptr && *a.found_inf != 0; }
 
@@ -237,8 +241,7 @@ __global__ __launch_bounds__(S::kThreadsWg, S::kWavesSimd) void gram_kernel(cons
     TileProduct<S> tile;
     if (z.turned) run_tile<kColumnsF16, kColumnsF16>(tile, columns_of(h, i0, z.m), columns_of(h, j0, z.m), steps, lds);
     else run_tile<kRowsF16, kRowsF16>(tile, rows_of(h, i0, z.m, z.n), rows_of(h, j0, z.m, z.n), steps, lds);
-    const float unscale = 1.0f / (a.s.x * a.s.x);
-    const float out = a.s.a * unscale;
+    const float unscale = a.s.un_xx, out = a.s.gram;
     char* to = a.ws + r.a;
     typedef typename TileProduct<S>::Nothing Nothing;
     auto body = [&](int tr, int tc, const float* v, Nothing) {
@@ -283,7 +286,7 @@ __global__ __launch_bounds__(S::kThreadsWg, S::kWavesSimd) void poly_kernel(cons
     const int i0 = t.ti * S::kBM, j0 = t.tj * S::kBN;
     TileProduct<S> tile;
     run_tile<kRowsF16, kRowsF16>(tile, rows_of(n, i0, z.m, z.m), rows_of(n, j0, z.m, z.m), z.m / kStepF16, lds);
-    const float un_a = 1.0f / a.s.a, un_s = un_a * un_a;
+    const float un_a = a.s.un_a, un_s = un_a * un_a;
     const FP_GLOBAL float* d = gptr<float>((const void*)(a.ws + r.da));
     char* to = a.ws + r.b;
     // eight elements (row, col ..) of N, with their part of the diagonals; the
@@ -336,6 +339,13 @@ __global__ __launch_bounds__(S::kThreadsWg, S::kWavesSimd) void poly_kernel(cons
         });
 }
 
+// What the update is multiplied by beside the learning rate.
+__device__ __forceinline__ double adjust_of(int adjust, double rows, double cols) {
+    return adjust == FP_MUON_ADJUST_RMS     ? 0.2 * sqrt(rows > cols ? rows : cols)
+           : adjust == FP_MUON_ADJUST_SHAPE ? sqrt(rows > cols ? rows / cols : 1.0)
+                                            : 1.0;
+}
+
 // How the orthogonalised matrix leaves.
 enum { kGoesOn = 0, kToUpdate = 1, kToWeights = 2 };
 
@@ -359,16 +369,12 @@ __global__ __launch_bounds__(S::kThreadsWg, S::kWavesSimd) void next_kernel(cons
         if (z.turned) run_tile<kRowsF16, kRowsF16>(tile, rows_of(h, i0, z.n, z.m), rows_of(b, j0, z.m, z.m), steps, lds);
         else run_tile<kRowsF16, kColumnsF16>(tile, rows_of(b, i0, z.m, z.m), columns_of(h, j0, z.n), steps, lds);
     }
-    const float unscale = 1.0f / (a.s.b * a.s.x), un_x = 1.0f / a.s.x;
+    const float unscale = a.s.un_bx, un_x = a.s.un_x;
     const FP_GLOBAL float* d = gptr<float>((const void*)(a.ws + r.db));
     double rate = 0.0, decay = 1.0;
     if constexpr (kOut == kToWeights) {
-        const MuonGroup& hp = a.g[r.group];
-        const double rows = r.rows, cols = r.cols, most = rows > cols ? rows : cols;
-        rate = hp.lr * (hp.adjust == FP_MUON_ADJUST_RMS     ? 0.2 * sqrt(most)
-                        : hp.adjust == FP_MUON_ADJUST_SHAPE ? sqrt(rows > cols ? rows / cols : 1.0)
-                                                            : 1.0);
-        decay = hp.decay;
+        rate = a.g[r.group].lr * adjust_of(a.g[r.group].adjust, r.rows, r.cols);
+        decay = a.g[r.group].decay;
     }
     const int rows = kOut == kGoesOn ? r.rp : r.rows, cols = kOut == kGoesOn ? r.cp : r.cols;
     float dc[8];  // of a tall matrix: of the lane's columns
@@ -441,53 +447,375 @@ __global__ __launch_bounds__(S::kThreadsWg, S::kWavesSimd) void next_kernel(cons
         });
 }
 
-// Launches kernel(a) over the argument block's tiles.
-template <class K>
-hipError_t launch(K kernel, const MuonArgs& a, int threads, unsigned lds, hipStream_t s) {
-    if (lds > 65536u) {  // beyond 64 KiB dynamic LDS is asked for once per kernel and device
-        const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
-        if (e != hipSuccess) return e;
-    }
-    kernel<<<(unsigned)a.n_tiles, threads, lds, s>>>(a);
-    return hipGetLastError();
+// ---------------------------------------------------------------- small matrices
+
+__device__ __forceinline__ void put8_lds(char* p, float a, float b, float c, float d) {
+    *(u32x2_t*)p = u32x2_t{f16_pair(a, b), f16_pair(c, d)};
 }
 
+// A matrix that fits into one workgroup's LDS goes through all of it there: its
+// momentum, |U|, every step of the iteration and the weights, in one launch for
+// all such matrices (32 x 48 in five steps: 16 launches took 72 us).  It is worked
+// on as m x n with m <= n, a tall one turned while it is loaded.  The lane that
+// has an element of X in the product's output keeps it in fp32 from step to step;
+// LDS has h, A and B, with rows 16 bytes longer than their elements, so that the
+// 16 rows of a fragment sit in different banks.  A wave works on blocks of kSub x
+// kSub tiles of 16 x 16: 2 x 2, four products for four fragments, where LDS reads
+// bound a step (128 x 128 with 1 x 1: 11 us a step, with 2 x 2 KKK), 1 x 1 for the
+// smallest, whose steps are all latency and want every wave (32 x 48: LLL a step,
+// with 2 x 2 2.3).
+//
+// kTiles: tiles of X per wave.
+constexpr int kSmallWaves = kSmallThreads / 64;
+
+template <int kTiles, int kSub, int kGrad>
+__global__ __launch_bounds__(kSmallThreads, 2) void small_kernel(const MuonArgs a, const MuonSteps it) {
+    extern __shared__ __align__(16) char lds[];
+    __shared__ double sums[kSmallWaves];
+    const int mat = a.tiles[blockIdx.x].mat;
+    const MuonRec& r = a.recs[mat];
+    const bool step = a.momentum != nullptr, turned = r.rows > r.cols;
+    const bool skip = step && skipped(a);
+    const int m0 = turned ? r.cols : r.rows, n0 = turned ? r.rows : r.cols;
+    const int m = (m0 + 31) & ~31, n = (n0 + 31) & ~31;
+    const int hp = 2 * n + 16, ap = 2 * m + 16;
+    char* const h = lds;
+    char* const la = h + m * hp;
+    char* const lb = la + m * ap;
+    float* const da = reinterpret_cast<float*>(lb + m * ap);
+    float* const db = da + m;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int g = lane >> 4, j = lane & 15;
+    constexpr int kBlock = 16 * kSub;
+    const int across = n / kBlock, blocks = m / kBlock * across;
+    const MuonGroup& hy = a.g[r.group];
+    const void* grad = a.grads[mat];
+
+    // The lane's four elements of its tile i: row `row` of X, columns col ..
+    // col + 3; `have` of them exist.  In memory they are neighbours, or a row
+    // apart.
+    struct At {
+        int row, col, have;
+        uint32_t e, apart;
+    };
+    auto at = [&](int i) {
+        At p;
+        const int t = wave + i / (kSub * kSub) * kSmallWaves;
+        p.row = t / across * kBlock + i / kSub % kSub * 16 + j;
+        p.col = t % across * kBlock + i % kSub * 16 + 4 * g;
+        const int left = n0 - p.col;
+        p.have = t >= blocks || p.row >= m0 || left <= 0 ? 0 : left < 4 ? left : 4;
+        p.e = (uint32_t)(turned ? p.col * m0 + p.row : p.row * n0 + p.col);
+        p.apart = turned ? (uint32_t)m0 : 1u;
+        return p;
+    };
+    // The loads of kGroup tiles are under way before the first is waited for;
+    // lanes without an element load the first one.
+    constexpr int kGroup = kTiles < 8 ? kTiles : 8;
+    auto ld = [&](const auto* from, auto convert, int first, float (&f)[kGroup][4]) {
+#pragma unroll
+        for (int i = 0; i < kGroup; ++i) {
+            const At p = at(first + i);
+            if (!turned && p.have == 4) {
+                typedef std::remove_cv_t<std::remove_reference_t<decltype(from[0])>> T;
+                typedef T four_t __attribute__((ext_vector_type(4), aligned(sizeof(T))));
+                const four_t v = *(const FP_GLOBAL four_t*)(from + p.e);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) f[i][k] = convert(v[k]);
+                continue;
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) f[i][k] = convert(from[k < p.have ? p.e + (uint32_t)k * p.apart : 0u]);
+        }
+    };
+    auto st = [&](auto* to, const At& p, const auto (&f)[4]) {
+        if (!turned && p.have == 4) {
+            typedef std::remove_reference_t<decltype(to[0])> T;
+            typedef T four_t __attribute__((ext_vector_type(4), aligned(sizeof(T))));
+            *(FP_GLOBAL four_t*)(to + p.e) = four_t{f[0], f[1], f[2], f[3]};
+            return;
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (k < p.have) to[p.e + (uint32_t)k * p.apart] = f[k];
+    };
+    auto same = [](float f) { return f; };
+
+    float x[kTiles][4];
+    double sum = 0.0;
+    if (!skip) {
+        const double k = step && a.g_coef != nullptr ? *a.g_coef : 1.0;
+        const double beta = step ? hy.beta : 0.0, mine = step ? (1.0 - beta) * k : 1.0;
+#pragma unroll
+        for (int i0 = 0; i0 < kTiles; i0 += kGroup) {
+            float u[kGroup][4], w[kGroup][4];
+            if constexpr (kGrad == FP_DTYPE_F32) ld(gptr<float>(grad), same, i0, u);
+            else ld(gptr<uint16_t>(grad), [](uint16_t v) { return kGrad == FP_DTYPE_BF16 ? bf16_lo(v) : f16_lo(v); }, i0, u);
+            if (step) ld(gptr<float>((const void*)(a.momentum + r.offset)), same, i0, w);
+#pragma unroll
+            for (int i = 0; i < kGroup; ++i) {
+                const At p = at(i0 + i);
+                if (step) {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) w[i][q] = (float)(beta * (double)w[i][q] + mine * (double)u[i][q]);
+                    st(gptr<float>((void*)(a.momentum + r.offset)), p, w[i]);
+                }
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    double v = (double)u[i][q];
+                    if (step) v = hy.nesterov ? beta * (double)w[i][q] + mine * v : (double)w[i][q];
+                    v = q < p.have ? v : 0.0;
+                    x[i0 + i][q] = (float)v;
+                    sum += v * v;
+                }
+            }
+            __builtin_amdgcn_sched_barrier(0);  // more at a time would not fit into the registers
+        }
+        sum = wave_sum(sum);
+        if (lane == 0) sums[wave] = sum;
+        __syncthreads();
+        sum = 0.0;
+#pragma unroll
+        for (int w = 0; w < kSmallWaves; ++w) sum += sums[w];
+        const double scale = 1.0 / (sqrt(sum) + a.eps);
+#pragma unroll
+        for (int i = 0; i < kTiles; ++i)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) x[i][q] = (float)((double)x[i][q] * scale);
+
+        auto st_h = [&](float s) {
+#pragma unroll
+            for (int i = 0; i < kTiles; ++i) {
+                const int t = wave + i / (kSub * kSub) * kSmallWaves;
+                if (t >= blocks) continue;
+                const At p = at(i);
+                put8_lds(h + p.row * hp + 2 * p.col, x[i][0] * s, x[i][1] * s, x[i][2] * s, x[i][3] * s);
+            }
+        };
+        // fragments of kBlock rows from `row` on, the lane's 8 elements from k + 8 g on
+        struct Frags {
+            f16x8_t v[kSub];
+        };
+        auto rows_at = [&](const char* base, int pitch, int row, int k) {
+            const char* p = base + (row + j) * pitch + 2 * (k + 8 * g);
+            Frags f;
+#pragma unroll
+            for (int y = 0; y < kSub; ++y) f.v[y] = *(const f16x8_t*)(p + 16 * y * pitch);
+            return f;
+        };
+        struct Sums {
+            f32x4_t v[kSub][kSub];
+        };
+        auto product = [&](const Frags& right, const Frags& left, Sums& acc) {
+#pragma unroll
+            for (int y = 0; y < kSub; ++y)
+#pragma unroll
+                for (int z = 0; z < kSub; ++z)
+                    acc.v[y][z] = __builtin_amdgcn_mfma_f32_16x16x32_f16(right.v[z], left.v[y], acc.v[y][z], 0, 0, 0);
+        };
+        // base base^T, m x m, block by block: out(row, col, four values from col
+        // on, whether the diagonal may be among them)
+        const int side = m / kBlock, by_side = (256 + side - 1) / side;  // t / side = t by_side / 256 for t < 64
+        auto square = [&](const char* base, int pitch, int width, auto out) {
+            for (int t = wave; t < side * side; t += kSmallWaves) {
+                const int bi = t * by_side >> 8, ti = bi * kBlock, tj = (t - bi * side) * kBlock;
+                Sums acc = {};
+#pragma unroll 4
+                for (int k = 0; k < width; k += 32) product(rows_at(base, pitch, tj, k), rows_at(base, pitch, ti, k), acc);
+#pragma unroll
+                for (int y = 0; y < kSub; ++y)
+#pragma unroll
+                    for (int z = 0; z < kSub; ++z)
+                        out(ti + 16 * y + j, tj + 16 * z + 4 * g, acc.v[y][z], ti + 16 * y == tj + 16 * z);
+            }
+        };
+        st_h(it.s[0].x);
+        for (int s = 0; s < it.n; ++s) {
+            const MuonScale sc = it.s[s];
+            const float ca = it.c[s][0], cb = it.c[s][1], cc = it.c[s][2];
+            __syncthreads();
+            square(h, hp, n, [&](int row, int col, const f32x4_t v, bool diagonal) {  // A
+                float f[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) f[q] = v[q] * sc.gram;
+                if (diagonal) {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        if (row == col + q) {
+                            da[row] = v[q] * sc.un_xx;
+                            f[q] = 0.0f;
+                        }
+                }
+                put8_lds(la + row * ap + 2 * col, f[0], f[1], f[2], f[3]);
+            });
+            __syncthreads();
+            square(la, ap, m, [&](int row, int col, const f32x4_t v, bool diagonal) {  // B
+                const u32x2_t w = *(const u32x2_t*)(la + row * ap + 2 * col);
+                const f32x4_t dc = *(const f32x4_t*)(da + col);
+                const float e[4] = {f16_lo(w.x), f16_hi(w.x), f16_lo(w.y), f16_hi(w.y)};
+                const float di = da[row];
+                float f[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const float a2 = v[q] * (sc.un_a * sc.un_a), a1 = e[q] * sc.un_a;
+                    f[q] = __builtin_fmaf(cb, a1, cc * __builtin_fmaf(di + dc[q], a1, a2)) * sc.b;
+                    if (diagonal && row == col + q) {
+                        db[row] = ca + (cb * di + cc * (a2 + di * di));
+                        f[q] = 0.0f;
+                    }
+                }
+                put8_lds(lb + row * ap + 2 * col, f[0], f[1], f[2], f[3]);
+            });
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < kTiles; i += kSub * kSub) {  // X
+                const int t = wave + i / (kSub * kSub) * kSmallWaves;
+                if (t >= blocks) continue;
+                const int ti = t / across * kBlock, tj = t % across * kBlock;
+                Sums acc = {};
+#pragma unroll 2
+                for (int k = 0; k < m; k += 32) {
+                    // rows k + 8 g .. + 7 of h, columns tj + j, tj + 16 + j
+                    const char* p = h + (k + 8 * g + (j >> 2)) * hp + 2 * (tj + (j & 3) * 4);
+                    Frags right;
+#pragma unroll
+                    for (int z = 0; z < kSub; ++z) {
+                        typedef short s16x8_t __attribute__((ext_vector_type(8)));
+                        const s16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((FP_LDS s16x4_t*)(p + 32 * z));
+                        const s16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((FP_LDS s16x4_t*)(p + 32 * z + 4 * hp));
+                        right.v[z] = __builtin_bit_cast(f16x8_t, (s16x8_t)__builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+                    }
+                    product(right, rows_at(lb, ap, ti, k), acc);
+                }
+#pragma unroll
+                for (int y = 0; y < kSub; ++y) {
+                    const float d = db[ti + 16 * y + j];
+#pragma unroll
+                    for (int z = 0; z < kSub; ++z)
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            float& e = x[i + kSub * y + z][q];
+                            e = __builtin_fmaf(d, e, acc.v[y][z][q] * sc.un_bx);
+                        }
+                }
+            }
+            if (s + 1 < it.n) {
+                __syncthreads();
+                st_h(sc.x_next);
+            }
+        }
+    } else if (r.copy == nullptr) {
+        return;
+    }
+
+    const double rate = step ? hy.lr * adjust_of(hy.adjust, r.rows, r.cols) : 0.0;
+    void* const to = step ? r.copy : r.update;
+    const int dtype = step ? a.copy_dtype : a.update_dtype;
+#pragma unroll
+    for (int i0 = 0; i0 < kTiles; i0 += kGroup) {
+        float w[kGroup][4];
+        if (step) ld(gptr<float>((const void*)r.master), same, i0, w);
+#pragma unroll
+        for (int i = 0; i < kGroup; ++i) {
+            const At p = at(i0 + i);
+            if (step && !skip) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q) w[i][q] = (float)(hy.decay * (double)w[i][q] - rate * (double)x[i0 + i][q]);
+                st(gptr<float>((void*)r.master), p, w[i]);
+            }
+            if (to == nullptr) continue;
+            float f[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                f[q] = x[i0 + i][q];
+                if (step) f[q] = w[i][q];
+            }
+            if (dtype == FP_DTYPE_F32) {
+                st(gptr<float>(to), p, f);
+                continue;
+            }
+            const uint32_t lo = dtype == FP_DTYPE_F16 ? f16_pair(f[0], f[1]) : bf16x2(f[0], f[1]);
+            const uint32_t hi = dtype == FP_DTYPE_F16 ? f16_pair(f[2], f[3]) : bf16x2(f[2], f[3]);
+            const uint16_t v[4] = {(uint16_t)lo, (uint16_t)(lo >> 16), (uint16_t)hi, (uint16_t)(hi >> 16)};
+            st(gptr<uint16_t>(to), p, v);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+    }
+}
+
+// Launches a kernel over the argument block's tiles.  Beyond 64 KiB, LDS is asked
+// for once per kernel and device.
+template <auto kKernel, class... More>
+hipError_t launch(const MuonArgs& a, int threads, unsigned lds, hipStream_t s, const More&... more) {
+    if (lds > 65536u) {
+        static std::atomic<uint64_t> asked{0};
+        int device = 0;
+        hipError_t e = hipGetDevice(&device);
+        if (e != hipSuccess) return e;
+        const uint64_t bit = 1ull << (device & 63);
+        if (!(asked.load() & bit)) {
+            e = hipFuncSetAttribute(reinterpret_cast<const void*>(kKernel), hipFuncAttributeMaxDynamicSharedMemorySize, (int)kMaxLds);
+            if (e != hipSuccess) return e;
+            asked.fetch_or(bit);
+        }
+    }
+    kKernel<<<(unsigned)a.n_tiles, threads, lds, s>>>(a, more...);
+    return hipGetLastError();
+}
 
 }  // namespace
 
 hipError_t launch_muon_moment(const MuonArgs& a, hipStream_t s) {
-#define FP_MOMENT(G) (a.momentum != nullptr ? launch(moment_kernel<G, true>, a, 256, 0, s) : launch(moment_kernel<G, false>, a, 256, 0, s))
+#define FP_MOMENT(G) (a.momentum != nullptr ? launch<moment_kernel<G, true>>(a, 256, 0, s) : launch<moment_kernel<G, false>>(a, 256, 0, s))
     return a.grad_dtype == FP_DTYPE_F32 ? FP_MOMENT(FP_DTYPE_F32) : a.grad_dtype == FP_DTYPE_BF16 ? FP_MOMENT(FP_DTYPE_BF16) : FP_MOMENT(FP_DTYPE_F16);
 #undef FP_MOMENT
 }
 
 hipError_t launch_muon_cast(const MuonArgs& a, hipStream_t s) {
-#define FP_CAST(G) (a.momentum != nullptr ? launch(cast_kernel<G, true>, a, 256, 0, s) : launch(cast_kernel<G, false>, a, 256, 0, s))
+#define FP_CAST(G) (a.momentum != nullptr ? launch<cast_kernel<G, true>>(a, 256, 0, s) : launch<cast_kernel<G, false>>(a, 256, 0, s))
     return a.grad_dtype == FP_DTYPE_F32 ? FP_CAST(FP_DTYPE_F32) : a.grad_dtype == FP_DTYPE_BF16 ? FP_CAST(FP_DTYPE_BF16) : FP_CAST(FP_DTYPE_F16);
 #undef FP_CAST
 }
 
+#define FP_BY_SHAPE(CALL)                                                                                            \
+    (shape == kTile256 ? CALL(Shape256) : shape == kTile128 ? CALL(Shape128) : shape == kTile64 ? CALL(Shape64) \
+                                                                                                : CALL(Shape64Deep))
+
 hipError_t launch_muon_gram(const MuonArgs& a, int shape, hipStream_t s) {
-    return shape == kTile256   ? launch(gram_kernel<Shape256>, a, Shape256::kThreadsWg, Shape256::kLds, s)
-           : shape == kTile128 ? launch(gram_kernel<Shape128>, a, Shape128::kThreadsWg, Shape128::kLds, s)
-                               : launch(gram_kernel<Shape64>, a, Shape64::kThreadsWg, Shape64::kLds, s);
+#define FP_CALL(S) launch<gram_kernel<S>>(a, S::kThreadsWg, S::kLds, s)
+    return FP_BY_SHAPE(FP_CALL);
+#undef FP_CALL
 }
 
 hipError_t launch_muon_poly(const MuonArgs& a, int shape, hipStream_t s) {
-    return shape == kTile256   ? launch(poly_kernel<Shape256>, a, Shape256::kThreadsWg, Shape256::kLds, s)
-           : shape == kTile128 ? launch(poly_kernel<Shape128>, a, Shape128::kThreadsWg, Shape128::kLds, s)
-                               : launch(poly_kernel<Shape64>, a, Shape64::kThreadsWg, Shape64::kLds, s);
+#define FP_CALL(S) launch<poly_kernel<S>>(a, S::kThreadsWg, S::kLds, s)
+    return FP_BY_SHAPE(FP_CALL);
+#undef FP_CALL
 }
 
 template <int kOut>
 static hipError_t launch_next(const MuonArgs& a, int shape, hipStream_t s) {
-    return shape == kTile256   ? launch(next_kernel<Shape256, kOut>, a, Shape256::kThreadsWg, Shape256::kLds, s)
-           : shape == kTile128 ? launch(next_kernel<Shape128, kOut>, a, Shape128::kThreadsWg, Shape128::kLds, s)
-                               : launch(next_kernel<Shape64, kOut>, a, Shape64::kThreadsWg, Shape64::kLds, s);
+#define FP_CALL(S) launch<next_kernel<S, kOut>>(a, S::kThreadsWg, S::kLds, s)
+    return FP_BY_SHAPE(FP_CALL);
+#undef FP_CALL
 }
 
 hipError_t launch_muon_next(const MuonArgs& a, int shape, bool last, bool to_weights, hipStream_t s) {
     return !last ? launch_next<kGoesOn>(a, shape, s) : to_weights ? launch_next<kToWeights>(a, shape, s) : launch_next<kToUpdate>(a, shape, s);
+}
+
+template <int kTiles, int kSub>
+static hipError_t launch_small(const MuonArgs& a, const MuonSteps& steps, unsigned lds, hipStream_t s) {
+    return a.grad_dtype == FP_DTYPE_F32    ? launch<small_kernel<kTiles, kSub, FP_DTYPE_F32>>(a, kSmallThreads, lds, s, steps)
+           : a.grad_dtype == FP_DTYPE_BF16 ? launch<small_kernel<kTiles, kSub, FP_DTYPE_BF16>>(a, kSmallThreads, lds, s, steps)
+                                           : launch<small_kernel<kTiles, kSub, FP_DTYPE_F16>>(a, kSmallThreads, lds, s, steps);
+}
+
+hipError_t launch_muon_small(const MuonArgs& a, const MuonSteps& steps, int tiles, unsigned lds, hipStream_t s) {
+    return tiles <= 2   ? launch_small<2, 1>(a, steps, lds, s)
+           : tiles <= 4 ? launch_small<4, 1>(a, steps, lds, s)
+           : tiles <= 8 ? launch_small<8, 2>(a, steps, lds, s)
+                        : launch_small<kSmallTiles, 2>(a, steps, lds, s);
 }
 
 }  // namespace fpk

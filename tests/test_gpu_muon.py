@@ -62,7 +62,7 @@ def test_orthogonalize(fp, gd, ud, kind):
         assert rel(x.cpu(), want) <= OFF + torch.finfo(DT[ud]).eps / 2
 
 
-@pytest.mark.parametrize("shape", [(512, 512), (700, 1900), (1900, 700), (2100, 2050)])
+@pytest.mark.parametrize("shape", [(512, 512), (700, 1900), (1900, 700), (2100, 2050), (128, 288), (288, 128), (130, 140), (64, 830)])
 def test_orthogonalize_large(fp, shape):
     g = gradient(*shape, 4, "spiked")
     x = torch.empty(shape, device=dev())
@@ -293,14 +293,14 @@ def test_captured_step(fp):
 
 
 def test_binding_refuses(fp):
-    g = [gradient(8, 12, 1).to(dev())]
-    w = [torch.zeros(8, 12, device=dev())]
+    g = [gradient(200, 300, 1).to(dev())]
+    w = [torch.zeros(200, 300, device=dev())]
     with pytest.raises(ValueError, match="neither"):
         fp.Muon(g)
     with pytest.raises(ValueError, match="shape"):
-        fp.Muon(g, [torch.zeros(12, 8, device=dev())])
+        fp.Muon(g, [torch.zeros(300, 200, device=dev())])
     with pytest.raises(ValueError, match="contiguous"):
-        fp.Muon([g[0].t()], [torch.zeros(12, 8, device=dev())])
+        fp.Muon([g[0].t()], [torch.zeros(300, 200, device=dev())])
     with pytest.raises(TypeError):
         fp.Muon(g, [w[0].double()])
     with pytest.raises(fp._lib.FlatParamError, match="overlap"):
@@ -329,7 +329,7 @@ def test_binding_refuses(fp):
     assert step._hp[0].lr == HP["lr"]
     with pytest.raises(ValueError, match="values for"):
         step(lr=[1.0, 2.0])
-    no = fp.Muon(g, updates=[torch.empty(8, 12, device=dev())])
+    no = fp.Muon(g, updates=[torch.empty(200, 300, device=dev())])
     with pytest.raises(ValueError, match="no master"):
         no.stepper(mom, ws, **HP)
     with pytest.raises(ValueError, match="shape"):
