@@ -44,27 +44,27 @@ typedef int i32x8_t __attribute__((ext_vector_type(8)));
 constexpr int kStepBytes = 128;  // of a row, per step along K
 constexpr int kStepF16 = 64;
 
-// A buffer's descriptor: raw bytes, offsets from `base` on.
-__device__ __forceinline__ i32x4_t buffer_of(const void* base) {
-    const uint64_t p = (uint64_t)base;
-    return i32x4_t{(int)(uint32_t)p, (int)(uint32_t)(p >> 32) & 0xFFFF, -1, 0x00020000};
-}
-
-// Loads 16 (4) bytes per lane into LDS, the wave's one behind the other from
-// `to` on; buffer, `to` and soffset are the same in all lanes.  Written out, as
-// the compiler waits for all such loads before every transposing read of LDS
-// that follows the builtin's (a 1400 x 64 matrix's A: 16 us, without 10).  It
-// counts neither these loads nor waits for them: the loop does (wait_loads).
-// M0 is LDS's base and needs a wait state behind its write.
-__device__ __forceinline__ void load_lds16(i32x4_t buffer, const char* to, int voffset, int soffset) {
-    const uint32_t at = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(FP_LDS const char*)to);
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
-                 :: "s"(at), "v"(voffset), "s"(buffer), "s"(soffset) : "memory", "m0");
-}
-__device__ __forceinline__ void load_lds4(i32x4_t buffer, const char* to, int voffset, int soffset) {
-    const uint32_t at = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(FP_LDS const char*)to);
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, %3 offen lds"
-                 :: "s"(at), "v"(voffset), "s"(buffer), "s"(soffset) : "memory", "m0");
+// Loads kBytes (16 or 4) per lane into LDS, the wave's one behind the other from
+// `to` on; base, `to` and soffset are the same in all lanes.  kWritten: as written
+// out here, for loops with transposing reads of LDS, before each of which the
+// compiler waits for all the loads that it knows of (a 1400 x 64 matrix's A: 16
+// us, without 10).  It counts neither such loads nor waits for them; the loop
+// does, for both (wait_loads).  M0 is LDS's base and needs a wait state behind its
+// write.
+template <bool kWritten, int kBytes>
+__device__ __forceinline__ void load_lds(const void* base, const char* to, int voffset, int soffset) {
+    if constexpr (kWritten) {
+        const uint64_t p = (uint64_t)base;
+        const i32x4_t buffer = {(int)(uint32_t)p, (int)(uint32_t)(p >> 32) & 0xFFFF, -1, 0x00020000};
+        const uint32_t at = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(FP_LDS const char*)to);
+        static_assert(kBytes == 16, "rows and columns of fp16");
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+                     :: "s"(at), "v"(voffset), "s"(buffer), "s"(soffset) : "memory", "m0");
+    } else {
+        const __amdgpu_buffer_rsrc_t buffer = __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, -1, 0x00020000);
+        if constexpr (kBytes == 16) __builtin_amdgcn_raw_ptr_buffer_load_lds(buffer, (FP_LDS void*)to, 16, voffset, soffset, 0, 0);
+        else __builtin_amdgcn_raw_ptr_buffer_load_lds(buffer, (FP_LDS void*)to, 4, voffset, soffset, 0, 0);
+    }
 }
 
 // kBM x kBN of the output per workgroup, kWM x kWN of it per wave; a power of
@@ -149,12 +149,12 @@ struct Side {
     }
     static __device__ __forceinline__ int swizzle(int k4, int k16) { return (k4 | k16 << 2) & (kB / 16 - 1); }
 
+    template <bool kWritten>
     __device__ __forceinline__ void load(char* stage, int wave, int step) const {
         const char* from = kColumns ? base + (int64_t)step * kStepF16 * pitch : base;
-        const i32x4_t buffer = buffer_of(from);
 #pragma unroll
         for (int i = 0; i < kLoads; ++i)
-            load_lds16(buffer, stage + (i * S::kWavesWg + wave) * 1024, voffset[i], kColumns ? 0 : step * kStepBytes);
+            load_lds<kWritten, 16>(from, stage + (i * S::kWavesWg + wave) * 1024, voffset[i], kColumns ? 0 : step * kStepBytes);
     }
     template <int kH>
     __device__ __forceinline__ void read(const char* stage, i32x4_t (&f)[kF]) const {
@@ -239,6 +239,7 @@ struct TileProduct {
     template <int kLeft, int kRight>
     __device__ __forceinline__ void run(const Operand& left, const Operand& right, int steps, char* lds) {
         constexpr bool kFp4 = kLeft == kRowsFp4;
+        constexpr bool kWritten = kLeft == kColumnsF16 || kRight == kColumnsF16;
         static_assert(kFp4 == (kRight == kRowsFp4), "both operands in MXFP4, or none");
         const int row0 = wave / S::kCols * S::kWM, col0 = wave % S::kCols * S::kWN;
         const Side<S, kLeft, S::kBM, S::kWM, S::kFM> l(left, wave, lane, row0);
@@ -266,14 +267,14 @@ struct TileProduct {
         auto load = [&](int k) {  // past the end the last step again: nothing reads it
             const int step = k < steps ? k : steps - 1;
             char* to = lds + k % S::kStages * S::kStage;
-            l.load(to, wave, step);
-            r.load(to + S::kBM * kStepBytes, wave, step);
+            l.template load<kWritten>(to, wave, step);
+            r.template load<kWritten>(to + S::kBM * kStepBytes, wave, step);
             if constexpr (kFp4) {
 #pragma unroll
                 for (int i = 0; i < kSLoads; ++i) {
                     const int dword = i * S::kThreadsWg + wave * 64;
                     const uint8_t* from = dword / 2 >= S::kBM ? right.scales : left.scales;
-                    load_lds4(buffer_of(from), scales + k % S::kStages * S::kScaleStage + dword * 4, soffset[i], step * 8);
+                    load_lds<false, 4>(from, scales + k % S::kStages * S::kScaleStage + dword * 4, soffset[i], step * 8);
                 }
             }
         };

@@ -230,7 +230,7 @@ __global__ __launch_bounds__(256) void dequantize_kernel(const Mx4DequantArgs a,
         for (int k = 0; k < 4; ++k)
             w[k] = kDtype == FP_DTYPE_F16 ? f16_pair(f[2 * k], f[2 * k + 1]) : bf16x2(f[2 * k], f[2 * k + 1]);
         if (left >= 8) {
-            put16h(p, make_uint4(w[0], w[1], w[2], w[3]));
+            st16h(p, make_uint4(w[0], w[1], w[2], w[3]));
         } else {
             for (int k = 0; k < (int)left; ++k) gptr<uint16_t>((void*)p)[k] = (uint16_t)(w[k >> 1] >> (16 * (k & 1)));
         }
@@ -287,7 +287,7 @@ __device__ __forceinline__ void st_out(const Mx4MatmulArgs& a, int64_t row, int6
 #pragma unroll
     for (int k = 0; k < 4; ++k) w[k] = half ? f16_pair(f[2 * k], f[2 * k + 1]) : bf16x2(f[2 * k], f[2 * k + 1]);
     if (have == 8) {
-        put16h(p, make_uint4(w[0], w[1], w[2], w[3]));
+        st16h(p, make_uint4(w[0], w[1], w[2], w[3]));
         return;
     }
 #pragma unroll

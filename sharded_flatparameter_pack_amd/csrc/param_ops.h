@@ -123,6 +123,9 @@ __device__ __forceinline__ uint2 get8(const void* p) {
     const u32x2_t v = *gptr<u32x2_t>(p);
     return make_uint2(v.x, v.y);
 }
+__device__ __forceinline__ void st16h(void* p, const uint4 v) {  // non-temporal, from a 2-byte boundary
+    __builtin_nontemporal_store((u32x4_a2{v.x, v.y, v.z, v.w}), (FP_GLOBAL u32x4_a2*)(p));
+}
 __device__ __forceinline__ void put16u(void* p, const uint4 v) {  // from a 4-byte boundary
     typedef unsigned int u32x4_a4u __attribute__((ext_vector_type(4), aligned(4)));
     *gptr<u32x4_a4u>(p) = u32x4_a4u{v.x, v.y, v.z, v.w};
