@@ -1302,46 +1302,52 @@ class MuonStep:
 
 # ------------------------------------------------------------------ MXFP4
 _MX4_DTYPES = None
+_MX4_PAD = 256
 
 
 def _mx4_dtypes():
-    """(dtypes of codes, dtypes of scales): bytes, or torch's own."""
+    """(dtypes of codes, dtypes of scales, {dtype of a matrix: its id})."""
     global _MX4_DTYPES
     if _MX4_DTYPES is None:
         torch = _torch()
         pair = getattr(torch, "float4_e2m1fn_x2", None)
-        _MX4_DTYPES = (torch.uint8, *([pair] if pair is not None else [])), (torch.float8_e8m0fnu, torch.uint8)
+        ids = {torch.float32: _lib.FP_DTYPE_F32, torch.float16: _lib.FP_DTYPE_F16,
+               **{d: _lib.FP_DTYPE_BF16 for d in _bf16_dtypes()}}
+        _MX4_DTYPES = (torch.uint8, *([pair] if pair is not None else [])), (torch.float8_e8m0fnu, torch.uint8), ids
     return _MX4_DTYPES
 
 
 def mx4_padded(n: int) -> int:
     """Elements that a row of n takes in MXFP4: n rounded up to a multiple of 256."""
-    p = lib().fp_mx4_padded(int(n))
-    if p < 0:
+    n = int(n)
+    if not 0 <= n <= 1 << 31:
         raise ValueError(f"rows of {n} elements")
-    return p
+    return -(-n // _MX4_PAD) * _MX4_PAD
 
 
-def _matrix(t, dtypes, name):
-    """(pointer, rows, columns, pitch) of a device matrix whose rows are contiguous."""
+def _matrix(t, name):
+    """(pointer, dtype id, rows, columns, pitch) of a device matrix whose rows are contiguous."""
     if not t.is_cuda:
         raise ValueError(f"{name} must be a device tensor")
-    if dtypes is not None and t.dtype not in dtypes:
-        raise TypeError(f"{name} has dtype {t.dtype}, expected one of {dtypes}")
+    dtype = _mx4_dtypes()[2].get(t.dtype)
+    if dtype is None:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected one of {tuple(_mx4_dtypes()[2])}")
     if t.dim() != 2:
         raise ValueError(f"{name} has {t.dim()} dimensions, a matrix has 2")
     r, c = t.shape
+    if t.is_contiguous():
+        return t.data_ptr(), dtype, r, c, c
     pitch = t.stride(0) if r > 1 else c
-    if (c > 1 and t.stride(1) != 1) or (r > 1 and pitch < c):
+    if (c > 1 and t.stride(1) != 1) or pitch < c:
         raise ValueError(f"{name}: a row's elements must be contiguous, and rows must not overlap (strides {t.stride()})")
-    return t.data_ptr(), r, c, pitch
+    return t.data_ptr(), dtype, r, c, pitch
 
 
 def _mx4_form(codes, scales, rows, width, name):
     """Pointers of one MXFP4 form, checked against its shape."""
-    cd, sd = _mx4_dtypes()
+    cd, sd, _ = _mx4_dtypes()
     p = mx4_padded(width)
-    if tuple(codes.shape) != (rows, p // 2) or tuple(scales.shape) != (rows, p // _lib.FP_MX_BLOCK):
+    if codes.shape != (rows, p // 2) or scales.shape != (rows, p // _lib.FP_MX_BLOCK):
         raise ValueError(f"{name}: codes {tuple(codes.shape)} and scales {tuple(scales.shape)}, expected "
                          f"{(rows, p // 2)} and {(rows, p // _lib.FP_MX_BLOCK)} for {rows} rows of {width}")
     return _dev_ptr(codes, cd, 0, f"{name} codes"), _dev_ptr(scales, sd, 0, f"{name} scales")
@@ -1350,8 +1356,8 @@ def _mx4_form(codes, scales, rows, width, name):
 def mx4_empty(rows: int, width: int, device):
     """(codes, scales) for `rows` rows of `width` elements, not filled."""
     torch, p = _torch(), mx4_padded(width)
-    return (torch.empty(rows, p // 2, dtype=torch.uint8, device=device),
-            torch.empty(rows, p // _lib.FP_MX_BLOCK, dtype=torch.uint8, device=device).view(_mx4_dtypes()[1][0]))
+    return (torch.empty((rows, p // 2), dtype=torch.uint8, device=device),
+            torch.empty((rows, p // _lib.FP_MX_BLOCK), dtype=_mx4_dtypes()[1][0], device=device))
 
 
 def mx4_quantize(src, codes=None, scales=None, codes_t=None, scales_t=None, *, rows: bool = True, transposed: bool = False,
@@ -1363,45 +1369,46 @@ def mx4_quantize(src, codes=None, scales=None, codes_t=None, scales_t=None, *, r
     rows=False that alone.  Rounded to nearest even, or with a seed
     stochastically (gradients; another seed for every call).  Buffers that are
     not given are allocated, those of a form that is not wanted may not be."""
-    _one_device(src, codes, scales, codes_t, scales_t)
-    x, r, c, pitch = _matrix(src, None, "src")
-    dtype = _dtype_id(src.dtype, "src")
+    x, dtype, r, c, pitch = _matrix(src, "src")
     if not rows and not transposed:
         raise ValueError("neither the rows' nor the columns' form is wanted")
-    got, ptrs = [], []
-    for want, held, shape, name in ((rows, (codes, scales), (r, c), "rows' form"),
-                                    (transposed, (codes_t, scales_t), (c, r), "columns' form")):
+    got, ptrs = (), ()
+    for want, held, high, wide, name in ((rows, (codes, scales), r, c, "rows' form"),
+                                         (transposed, (codes_t, scales_t), c, r, "columns' form")):
         if not want:
             if held != (None, None):
                 raise ValueError(f"buffers of the {name}, which is not wanted")
-            ptrs += [None, None]
-            continue
-        if (held[0] is None) != (held[1] is None):
-            raise ValueError("codes and scales go together")
-        if held[0] is None:
-            held = mx4_empty(*shape, src.device)
-        got += held
-        ptrs += _mx4_form(*held, *shape, name)
-    _on_device(src.device, lib().fp_mx4_quantize, r, c, pitch, dtype, x, *ptrs, int(seed is not None),
+            ptrs += (None, None)
+        elif held == (None, None):
+            held = mx4_empty(high, wide, src.device)
+            got += held
+            ptrs += (held[0].data_ptr(), held[1].data_ptr())
+        else:
+            if held[0] is None or held[1] is None:
+                raise ValueError("codes and scales go together")
+            _one_device(src, *held)
+            got += held
+            ptrs += _mx4_form(*held, high, wide, name)
+    _on_device(src.device, lib().fp_mx4_quantize, r, c, pitch, dtype, x, *ptrs, seed is not None,
                0 if seed is None else int(seed) & 0xFFFFFFFFFFFFFFFF)
-    return tuple(got)
+    return got
 
 
 def mx4_dequantize(codes, scales, cols: int, dst=None, *, dtype=None):
     """dst (rows x cols; allocated here in `dtype`, bf16 by default, when None):
     what MXFP4 codes and scales stand for."""
-    torch = _torch()
-    r = codes.shape[0]
-    ptrs = _mx4_form(codes, scales, r, int(cols), "operand")
+    r, c = codes.shape[0], int(cols)
+    ptrs = _mx4_form(codes, scales, r, c, "operand")
     if dst is None:
-        dst = torch.empty(r, int(cols), dtype=dtype or torch.bfloat16, device=codes.device)
+        torch = _torch()
+        dst = torch.empty((r, c), dtype=dtype or torch.bfloat16, device=codes.device)
     elif dtype is not None and dst.dtype != dtype:
         raise TypeError(f"dst has dtype {dst.dtype}, not {dtype}")
     _one_device(codes, scales, dst)
-    x, rows, width, pitch = _matrix(dst, None, "dst")
-    if (rows, width) != (r, int(cols)):
-        raise ValueError(f"dst has shape {(rows, width)}, expected {(r, int(cols))}")
-    _on_device(codes.device, lib().fp_mx4_dequantize, r, width, *ptrs, _dtype_id(dst.dtype, "dst"), x, pitch)
+    x, did, rows, width, pitch = _matrix(dst, "dst")
+    if (rows, width) != (r, c):
+        raise ValueError(f"dst has shape {(rows, width)}, expected {(r, c)}")
+    _on_device(codes.device, lib().fp_mx4_dequantize, r, c, *ptrs, did, x, pitch)
     return dst
 
 
@@ -1411,24 +1418,25 @@ def mx4_matmul(a, b, out=None, *, accumulate: bool = False, dtype=None):
     padded length; accumulate adds to out.  A layer y = x w^T with x and w by
     rows; its input's gradient: dy by rows, w by columns; its weights' gradient:
     dy by columns, x by columns."""
-    torch = _torch()
     (ac, asc), (bc, bsc) = a, b
-    k = 2 * ac.shape[1]
-    if bc.shape[1] != ac.shape[1]:
-        raise ValueError(f"rows of {k} and {2 * bc.shape[1]} elements (padded)")
-    m, n = ac.shape[0], bc.shape[0]
-    ptrs = (*_mx4_form(ac, asc, m, k, "a"), *_mx4_form(bc, bsc, n, k, "b"))
+    m, k = ac.shape
+    n, k2 = bc.shape
+    k, k2 = 2 * k, 2 * k2
+    if k2 != k:
+        raise ValueError(f"rows of {k} and {k2} elements (padded)")
+    ap, bp = _mx4_form(ac, asc, m, k, "a"), _mx4_form(bc, bsc, n, k, "b")
     if out is None:
         if accumulate:
             raise ValueError("accumulate needs out")
-        out = torch.empty(m, n, dtype=dtype or torch.bfloat16, device=ac.device)
+        torch = _torch()
+        out = torch.empty((m, n), dtype=dtype or torch.bfloat16, device=ac.device)
     elif dtype is not None and out.dtype != dtype:
         raise TypeError(f"out has dtype {out.dtype}, not {dtype}")
     _one_device(ac, asc, bc, bsc, out)
-    x, rows, cols, pitch = _matrix(out, None, "out")
+    x, did, rows, cols, pitch = _matrix(out, "out")
     if (rows, cols) != (m, n):
         raise ValueError(f"out has shape {(rows, cols)}, expected {(m, n)}")
-    _on_device(ac.device, lib().fp_mx4_matmul, m, n, k, *ptrs, _dtype_id(out.dtype, "out"), x, pitch, int(bool(accumulate)))
+    _on_device(ac.device, lib().fp_mx4_matmul, m, n, k, *ap, *bp, did, x, pitch, accumulate)
     return out
 
 

@@ -14,6 +14,8 @@
 //
 // Compiled with -ffp-contract=off.
 
+#include <type_traits>
+
 #include "fp_matrix.h"
 #include "mma_tile.h"
 #include "param_ops.h"
@@ -51,143 +53,189 @@ __device__ __forceinline__ uint32_t mx4_encode(const float f[8], uint32_t byte) 
     return byte == 255u ? 0u : w;
 }
 
-// Code of one value, rounded stochastically: with y = |x| / scale in [0, 6] and
-// q the distance of the codes' values around y (0.5, 1 or 2), that of
-// q floor(y / q + d / 2^16), d in [0, 2^16), in whole numbers.
-__device__ __forceinline__ uint32_t mx4_encode_one(float x, float unscale, uint32_t d) {
-    const float y = fabsf(x) * unscale;
-    const bool two = y >= 2.0f, four = y >= 4.0f;
-    const float t = y * (four ? 32768.0f : two ? 65536.0f : 131072.0f);
-    const uint32_t u = ((uint32_t)t + d) >> 16;  // exact: y has 24 bits, its last one at 2^-24 of t or cut by the floor
-    return (u + (four ? 4u : two ? 2u : 0u)) | (__float_as_uint(x) >> 31 << 3);
+// Eight values rounded stochastically: with y = |x| / scale in [0, 6] and q the
+// distance of the codes' values around y (0.5, 1 or 2), the code is that of
+// q floor(y / q + d / 2^16).  y 2^-126 in fp32 has e2m1's exponent steps, and
+// below y = 1, where fp32's subnormals begin, e2m1's even ones: its bits, with d
+// added below e2m1's last one (bit 22), are the code after a cut.  The product
+// that gives y 2^-126 has to be cut too, not rounded (what is cut lies below d's
+// last bit): the kernel's rounding is towards zero (round_to_zero).
+__device__ __forceinline__ uint32_t mx4_encode(const float f[8], uint32_t byte, const uint32_t d[8]) {
+    uint32_t w = 0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        const float y = __builtin_amdgcn_ldexpf(f[k], 1 - (int)byte);    // times 2^(127 - byte) 2^-126
+        const uint32_t c = (__float_as_uint(y) + (d[k] << 6)) >> 22;     // sign, 6 unused bits, code
+        w |= ((c & 7u) | (c >> 6 & 8u)) << (4 * k);
+    }
+    return byte == 255u ? 0u : w;
 }
 
-// 1 / scale, in two factors' range: 2^(127 - byte) for byte <= 254.
-__device__ __forceinline__ float unscale_f32(uint32_t byte) {
-    return byte == 255u ? 0.0f : __builtin_amdgcn_ldexpf(1.0f, 127 - (int)byte);
+// fp32 operations of the wave round towards zero from here on.
+__device__ __forceinline__ void round_to_zero() {
+    __builtin_amdgcn_s_setreg(1 /* MODE */ | 0 << 6 | (2 - 1) << 11, 3);
 }
 
+// Elements [at, at + 8) of x as they are in memory, those past `have` 0.
 template <int kDtype>
-struct Held {  // what LDS keeps of an element
-    typedef uint16_t type;
+struct Eight {
+    uint32_t w[kDtype == FP_DTYPE_F32 ? 8 : 4];
 };
-template <>
-struct Held<FP_DTYPE_F32> {
-    typedef uint32_t type;
-};
-
-constexpr int kQTile = 128;
-
-// Elements [col, col + 8) of a row as bits, those past `cols` 0.
 template <int kDtype>
-__device__ __forceinline__ void ld_bits(const void* x, int64_t at, int have, uint32_t w[8]) {
+__device__ __forceinline__ Eight<kDtype> ld_eight(const void* x, int64_t at, int have) {
+    Eight<kDtype> r;
     if constexpr (kDtype == FP_DTYPE_F32) {
         const float* p = static_cast<const float*>(x) + at;
         if (have >= 8) {
             const uint4 a = ld16u(p), b = ld16u(p + 4);
-            w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
-            w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
-            return;
+            r.w[0] = a.x; r.w[1] = a.y; r.w[2] = a.z; r.w[3] = a.w;
+            r.w[4] = b.x; r.w[5] = b.y; r.w[6] = b.z; r.w[7] = b.w;
+            return r;
         }
 #pragma unroll
-        for (int k = 0; k < 8; ++k) w[k] = k < have ? gptr<uint32_t>((const void*)p)[k] : 0u;
+        for (int k = 0; k < 8; ++k) r.w[k] = k < have ? gptr<uint32_t>((const void*)p)[k] : 0u;
     } else {
         const uint16_t* p = static_cast<const uint16_t*>(x) + at;
         if (have >= 8) {
             const uint4 a = ld16u(p);
-            w[0] = a.x & 0xFFFFu; w[1] = a.x >> 16; w[2] = a.y & 0xFFFFu; w[3] = a.y >> 16;
-            w[4] = a.z & 0xFFFFu; w[5] = a.z >> 16; w[6] = a.w & 0xFFFFu; w[7] = a.w >> 16;
-            return;
+            r.w[0] = a.x; r.w[1] = a.y; r.w[2] = a.z; r.w[3] = a.w;
+            return r;
         }
+        uint32_t e[8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) w[k] = k < have ? (uint32_t)gptr<uint16_t>((const void*)p)[k] : 0u;
+        for (int k = 0; k < 8; ++k) e[k] = k < have ? (uint32_t)gptr<uint16_t>((const void*)p)[k] : 0u;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) r.w[k] = e[2 * k] | e[2 * k + 1] << 16;
     }
+    return r;
+}
+// Element k's bits.
+template <int kDtype>
+__device__ __forceinline__ uint32_t bits_at(const Eight<kDtype>& r, int k) {
+    if constexpr (kDtype == FP_DTYPE_F32) return r.w[k];
+    else return k & 1 ? r.w[k >> 1] >> 16 : r.w[k >> 1] & 0xFFFFu;
 }
 
-// A 128 x 128 tile.  Rows' form: four lanes hold a block, eight elements each.
-// Columns' form: a lane holds a block, read down a column of the tile in LDS.
-template <int kDtype, bool kRows, bool kColumns, bool kRandom>
+// The dither of elements e .. e + 7.
+__device__ __forceinline__ void dither8(uint32_t e, uint32_t key, uint32_t h[8]) {
+    const uint32_t p = e * kDitherStep;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) h[k] = dither_at(p + (uint32_t)k * kDitherStep, key);
+}
+
+// A block's eight elements of four lanes, along a row: its codes and scale.
+template <int kDtype, bool kRandom>
+__device__ __forceinline__ void row_block(const Mx4QuantArgs& a, const Eight<kDtype>& r, const uint32_t (&h)[8], int64_t row, int64_t col) {
+    float f[8];
+    uint32_t top = 0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        f[k] = to_f32<kDtype>(bits_at<kDtype>(r, k));
+        const uint32_t m = __float_as_uint(f[k]) & 0x7FFFFFFFu;
+        top = top > m ? top : m;
+    }
+    uint32_t y = (uint32_t)__builtin_amdgcn_mov_dpp((int)top, 0xB1 /* quad_perm 1,0,3,2 */, 0xF, 0xF, true);
+    top = top > y ? top : y;
+    y = (uint32_t)__builtin_amdgcn_mov_dpp((int)top, 0x4E /* quad_perm 2,3,0,1 */, 0xF, 0xF, true);
+    top = top > y ? top : y;
+    const uint32_t byte = mx4_byte<kRandom>(top);
+    uint32_t codes;
+    if constexpr (kRandom) {
+        uint32_t d[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) d[k] = h[k] >> 16;
+        codes = mx4_encode(f, byte, d);
+    } else {
+        codes = mx4_encode(f, byte);
+    }
+    if (row >= a.rows || col >= a.cp) return;
+    gptr<uint32_t>((void*)a.codes)[(row * a.cp + col) >> 3] = codes;
+    if ((threadIdx.x & 3) == 0) gptr<uint8_t>((void*)a.scales)[(row * a.cp + col) >> 5] = (uint8_t)byte;
+}
+
+// The rows' form alone: eight elements per lane, rows behind each other.
+template <int kDtype, bool kRandom>
+__global__ __launch_bounds__(256) void quantize_rows_kernel(const Mx4QuantArgs a) {
+    if (kRandom) round_to_zero();
+    const uint32_t lane = blockIdx.x * 256u + threadIdx.x, across = (uint32_t)(a.cp >> 3);
+    const int64_t row = lane / across, col = (int64_t)(lane - (uint32_t)row * across) * 8, left = a.cols - col;
+    const int have = row >= a.rows || left <= 0 ? 0 : left < 8 ? (int)left : 8;
+    const Eight<kDtype> r = ld_eight<kDtype>(a.x, row * a.pitch + col, have);
+    uint32_t h[8] = {};
+    if constexpr (kRandom) dither8((uint32_t)(row * a.cols + col), a.key, h);
+    row_block<kDtype, kRandom>(a, r, h, row, col);
+}
+
+// A 128 x 128 tile.  Rows' form: four lanes hold a block, eight elements each,
+// and all of a lane's rows are loaded before the first is worked on.  Columns'
+// form: a lane holds a block, read down a column of the tile in LDS, where an
+// element of 16 bits has its half of the dither beside it (the hash is most of
+// the stochastic form's work: 8192 x 8192 bf16 values twice over, 118 us).
+constexpr int kQTile = 128;
+template <int kDtype, bool kRows, bool kRandom>
 __global__ __launch_bounds__(256) void quantize_kernel(const Mx4QuantArgs a) {
-    typedef typename Held<kDtype>::type held_t;
-    __shared__ held_t tile[kColumns ? kQTile : 1][kQTile + 2];
+    constexpr bool kWide = kDtype == FP_DTYPE_F32, kBeside = kRandom && !kWide;
+    typedef typename std::conditional<kWide || kBeside, uint32_t, uint16_t>::type held_t;
+    __shared__ held_t tile[kQTile][kQTile + 2];
+    if (kRandom) round_to_zero();
     const unsigned across = kRows ? (unsigned)(a.cp / kQTile) : (unsigned)((a.cols + kQTile - 1) / kQTile);
     const int64_t row0 = (int64_t)(blockIdx.x / across) * kQTile, col0 = (int64_t)(blockIdx.x % across) * kQTile;
-    const int c8 = (threadIdx.x & 15) * 8;
+    const int c8 = (threadIdx.x & 15) * 8, r0 = threadIdx.x >> 4;
     const int64_t left = a.cols - (col0 + c8);
-    for (int i = 0; i < 8; ++i) {
-        const int lr = (threadIdx.x >> 4) + 16 * i;
-        const int64_t row = row0 + lr;
-        const int have = row >= a.rows || left <= 0 ? 0 : left < 8 ? (int)left : 8;
-        uint32_t w[8];
-        ld_bits<kDtype>(a.x, row * a.pitch + col0 + c8, have, w);
-        if constexpr (kColumns) {
+    Eight<kDtype> r[8];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) tile[lr][c8 + k] = (held_t)w[k];
+    for (int i = 0; i < 8; ++i) {
+        const int64_t row = row0 + r0 + 16 * i;
+        r[i] = ld_eight<kDtype>(a.x, row * a.pitch + col0 + c8, row >= a.rows || left <= 0 ? 0 : left < 8 ? (int)left : 8);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int lr = r0 + 16 * i;
+        uint32_t h[8] = {};
+        if constexpr (kRandom && (kRows || kBeside)) dither8((uint32_t)((row0 + lr) * a.cols + col0 + c8), a.key, h);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const uint32_t w = bits_at<kDtype>(r[i], k);
+            tile[lr][c8 + k] = (held_t)(kBeside ? w | h[k] << 16 : w);
         }
-        if constexpr (kRows) {
+        if constexpr (kRows) row_block<kDtype, kRandom>(a, r[i], h, row0 + lr, col0 + c8);
+    }
+    __syncthreads();
+    const int lc = threadIdx.x & 127;
+    const int64_t col = col0 + lc;
+    if (col >= a.cols) return;
+#pragma unroll 1
+    for (int i = 0; i < 2; ++i) {
+        const int lr = ((threadIdx.x >> 7) * 2 + i) * 32;
+        held_t e[32];
+        uint32_t top = 0;
+#pragma unroll
+        for (int k = 0; k < 32; ++k) {
+            e[k] = tile[lr + k][lc];
+            const uint32_t m = __float_as_uint(to_f32<kDtype>(kBeside ? e[k] & 0xFFFFu : (uint32_t)e[k])) & 0x7FFFFFFFu;
+            top = top > m ? top : m;
+        }
+        const uint32_t byte = mx4_byte<kRandom>(top);
+        const uint32_t step = (uint32_t)a.cols * kDitherStep;
+        uint32_t product = (uint32_t)((row0 + lr) * a.cols + col) * kDitherStep;
+        uint32_t codes[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
             float f[8];
-            uint32_t top = 0;
+            uint32_t d[8];
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
-                f[k] = to_f32<kDtype>(w[k]);
-                const uint32_t m = __float_as_uint(f[k]) & 0x7FFFFFFFu;
-                top = top > m ? top : m;
+                const uint32_t w = (uint32_t)e[8 * q + k];
+                f[k] = to_f32<kDtype>(kBeside ? w & 0xFFFFu : w);
+                if constexpr (kBeside) d[k] = w >> 16;
+                else if constexpr (kRandom) d[k] = dither_at(product, a.key) & 0xFFFFu, product += step;
             }
-            uint32_t y = (uint32_t)__builtin_amdgcn_mov_dpp((int)top, 0xB1 /* quad_perm 1,0,3,2 */, 0xF, 0xF, true);
-            top = top > y ? top : y;
-            y = (uint32_t)__builtin_amdgcn_mov_dpp((int)top, 0x4E /* quad_perm 2,3,0,1 */, 0xF, 0xF, true);
-            top = top > y ? top : y;
-            const uint32_t byte = mx4_byte<kRandom>(top);
-            uint32_t codes = 0;
-            if constexpr (kRandom) {
-                const float u = unscale_f32(byte);
-                const uint32_t e = (uint32_t)(row * a.cols + col0 + c8);
-#pragma unroll
-                for (int k = 0; k < 8; ++k) codes |= mx4_encode_one(f[k], u, dither(e + k, a.key) >> 16) << (4 * k);
-                codes = byte == 255u ? 0u : codes;
-            } else {
-                codes = mx4_encode(f, byte);
-            }
-            if (row < a.rows && col0 + c8 < a.cp) {
-                gptr<uint32_t>((void*)a.codes)[(row * a.cp + col0 + c8) >> 3] = codes;
-                if ((threadIdx.x & 3) == 0) gptr<uint8_t>((void*)a.scales)[(row * a.cp + col0 + c8) >> 5] = (uint8_t)byte;
-            }
+            if constexpr (kRandom) codes[q] = mx4_encode(f, byte, d);
+            else codes[q] = mx4_encode(f, byte);
         }
-    }
-    if constexpr (kColumns) {
-        __syncthreads();
-        const int lc = threadIdx.x & 127;
-        const int64_t col = col0 + lc;
-        if (col >= a.cols) return;
-        for (int i = 0; i < 2; ++i) {
-            const int lr = ((threadIdx.x >> 7) * 2 + i) * 32;
-            float f[32];
-            uint32_t top = 0;
-#pragma unroll
-            for (int k = 0; k < 32; ++k) {
-                f[k] = to_f32<kDtype>(tile[lr + k][lc]);
-                const uint32_t m = __float_as_uint(f[k]) & 0x7FFFFFFFu;
-                top = top > m ? top : m;
-            }
-            const uint32_t byte = mx4_byte<kRandom>(top);
-            uint32_t codes[4] = {0u, 0u, 0u, 0u};
-            if constexpr (kRandom) {
-                const float u = unscale_f32(byte);
-                uint32_t e = (uint32_t)((row0 + lr) * a.cols + col);
-#pragma unroll
-                for (int k = 0; k < 32; ++k) {
-                    codes[k >> 3] |= mx4_encode_one(f[k], u, dither(e, a.key) & 0xFFFFu) << (4 * (k & 7));
-                    e += (uint32_t)a.cols;
-                }
-                if (byte == 255u) codes[0] = codes[1] = codes[2] = codes[3] = 0u;
-            } else {
-#pragma unroll
-                for (int k = 0; k < 4; ++k) codes[k] = mx4_encode(f + 8 * k, byte);
-            }
-            const int64_t at = col * a.rp + row0 + lr;
-            put16(a.codes_t + (at >> 1), make_uint4(codes[0], codes[1], codes[2], codes[3]));
-            gptr<uint8_t>((void*)a.scales_t)[at >> 5] = (uint8_t)byte;
-        }
+        const int64_t at = col * a.rp + row0 + lr;
+        put16(a.codes_t + (at >> 1), make_uint4(codes[0], codes[1], codes[2], codes[3]));
+        gptr<uint8_t>((void*)a.scales_t)[at >> 5] = (uint8_t)byte;
     }
 }
 
@@ -206,10 +254,9 @@ __device__ __forceinline__ void mx4_decode(uint32_t codes, uint32_t byte, float 
 
 // Eight values per lane, a row's columns side by side.
 template <int kDtype>
-__global__ __launch_bounds__(256) void dequantize_kernel(const Mx4DequantArgs a, int lanes) {
-    const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    const int64_t row = at / lanes;
-    const int64_t col = (at - row * lanes) * 8;
+__global__ __launch_bounds__(256) void dequantize_kernel(const Mx4DequantArgs a, uint32_t across) {
+    const uint32_t lane = blockIdx.x * 256u + threadIdx.x;
+    const int64_t row = lane / across, col = (int64_t)(lane - (uint32_t)row * across) * 8;
     if (row >= a.rows || col >= a.cols) return;
     const int64_t e = row * a.cp + col;
     float f[8];
@@ -252,8 +299,15 @@ __device__ __forceinline__ Old ld_old(const Mx4MatmulArgs& a, int64_t row, int64
     if (a.accumulate && row < a.m && col < a.n) {
         const int64_t left = a.n - col, at = row * a.pitch + col;
         const int have = left < 8 ? (int)left : 8;
-        if (a.dtype == FP_DTYPE_F32) ld_bits<FP_DTYPE_F32>(a.out, at, have, o.w);
-        else ld_bits<FP_DTYPE_BF16>(a.out, at, have, o.w);
+        if (a.dtype == FP_DTYPE_F32) {
+            const Eight<FP_DTYPE_F32> e = ld_eight<FP_DTYPE_F32>(a.out, at, have);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) o.w[k] = e.w[k];
+        } else {
+            const Eight<FP_DTYPE_BF16> e = ld_eight<FP_DTYPE_BF16>(a.out, at, have);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) o.w[k] = bits_at<FP_DTYPE_BF16>(e, k);
+        }
     }
     return o;
 }
@@ -315,6 +369,88 @@ __global__ __launch_bounds__(S::kThreadsWg, S::kWavesSimd) void matmul_kernel(co
         [&](int r, int c, const float* v, const Old& o) { st_out(a, i0 + r, j0 + c, v, o); });
 }
 
+// Products with few rows on one side (a: up to 16 kF; tokens of a generation):
+// the other side is read once, and that bounds them, so a workgroup has 16 of its
+// rows and its waves share K.  Fragments come straight from memory, a wave's
+// steps kAhead at a time; the waves' sums meet in LDS, in their order.
+constexpr int kThinWaves = 8;
+constexpr int64_t kThinRows = 64;
+template <int kF>
+__global__ __launch_bounds__(64 * kThinWaves, 2) void thin_kernel(const Mx4MatmulArgs a) {
+    __shared__ f32x4_t sums[kThinWaves][kF][64];
+    constexpr int kAhead = kF == 1 ? 4 : 2;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int g = lane >> 4, j = lane & 15;
+    const int64_t pitch = a.kp >> 1, j0 = (int64_t)blockIdx.x * 16;
+    const int64_t rb = j0 + j < a.n ? j0 + j : a.n - 1;
+    const uint8_t* pb = a.b + rb * pitch + 32 * g;
+    const uint8_t* sb = a.bs + rb * (pitch >> 4) + 2 * g;
+    const uint8_t *pa[kF], *sa[kF];
+#pragma unroll
+    for (int m = 0; m < kF; ++m) {
+        const int64_t ra = 16 * m + j < a.m ? 16 * m + j : a.m - 1;
+        pa[m] = a.a + ra * pitch + 32 * g;
+        sa[m] = a.as + ra * (pitch >> 4) + 2 * g;
+    }
+    f32x4_t acc[kF];
+#pragma unroll
+    for (int m = 0; m < kF; ++m) acc[m] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    struct Step {  // a lane's 64 codes of a row, with their two scales
+        uint4 lo, hi;
+        uint32_t s;
+    };
+    auto ld = [&](const uint8_t* p, const uint8_t* s, int k) {
+        return Step{get16(p + (int64_t)k * kStepBytes), get16(p + (int64_t)k * kStepBytes + 16), *gptr<uint16_t>(s + (int64_t)k * 8)};
+    };
+    auto wide = [](const uint4 v) { return i32x8_t{(int)v.x, (int)v.y, (int)v.z, (int)v.w, 0, 0, 0, 0}; };
+    const int steps = (int)(a.kp >> 8), each = (steps + kThinWaves - 1) / kThinWaves;
+    const int from = wave * each, to = from + each < steps ? from + each : steps;
+    for (int k = from; k < to; k += kAhead) {
+        Step b[kAhead], x[kAhead][kF];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            const int at = k + i < to ? k + i : to - 1;
+            b[i] = ld(pb, sb, at);
+#pragma unroll
+            for (int m = 0; m < kF; ++m) x[i][m] = ld(pa[m], sa[m], at);
+        }
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            if (k + i >= to) break;
+#pragma unroll
+            for (int m = 0; m < kF; ++m) {
+                acc[m] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wide(b[i].lo), wide(x[i][m].lo), acc[m], 4, 4, 0, (int)b[i].s, 0, (int)x[i][m].s);
+                acc[m] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wide(b[i].hi), wide(x[i][m].hi), acc[m], 4, 4, 1, (int)b[i].s, 1, (int)x[i][m].s);
+            }
+        }
+    }
+#pragma unroll
+    for (int m = 0; m < kF; ++m) sums[wave][m][lane] = acc[m];
+    __syncthreads();
+    if (wave >= kF) return;
+    f32x4_t v = sums[0][wave][lane];
+#pragma unroll
+    for (int w = 1; w < kThinWaves; ++w) v += sums[w][wave][lane];
+    // row 16 wave + j, columns j0 + 4 g .. + 3
+    const int64_t row = 16 * wave + j, col = j0 + 4 * g;
+    if (row >= a.m) return;
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+        if (col + q < a.n) {
+            const int64_t at = row * a.pitch + col + q;
+            float f = v[q];
+            if (a.dtype == FP_DTYPE_F32) {
+                FP_GLOBAL float* o = gptr<float>(a.out) + at;
+                *o = a.accumulate ? f + *o : f;
+            } else {
+                FP_GLOBAL uint16_t* o = gptr<uint16_t>(a.out) + at;
+                const bool half = a.dtype == FP_DTYPE_F16;
+                if (a.accumulate) f += half ? f16_lo(*o) : bf16_lo(*o);
+                *o = (uint16_t)(half ? f16_pair(f, f) : bf16x2(f, f));
+            }
+        }
+}
+
 using Shape256 = TileShape<256, 256, 128, 64>;
 using Shape128 = TileShape<128, 128, 64, 64>;
 using Shape64 = TileShape<64, 64, 32, 32>;
@@ -332,24 +468,27 @@ hipError_t run_matmul(Mx4MatmulArgs a, hipStream_t s) {
 }
 
 // Tiles across and down: the padding of a form that is wanted is written too.
-int64_t quant_tiles_x(const Mx4QuantArgs& a) { return ceil_div64(a.codes != nullptr ? a.cp : a.cols, kQTile); }
-int64_t quant_tiles_y(const Mx4QuantArgs& a) { return ceil_div64(a.codes_t != nullptr ? a.rp : a.rows, kQTile); }
+int64_t quant_tiles(const Mx4QuantArgs& a) { return ceil_div64(a.codes != nullptr ? a.cp : a.cols, kQTile) * (a.rp / kQTile); }
+int64_t quant_groups(const Mx4QuantArgs& a) { return a.codes_t != nullptr ? quant_tiles(a) : ceil_div64(a.rows * a.cp, 8 * 256); }
 
 template <int kDtype, bool kRandom>
 hipError_t run_quantize(const Mx4QuantArgs& a, hipStream_t s) {
-    const bool rows = a.codes != nullptr, columns = a.codes_t != nullptr;
-    const unsigned grid = (unsigned)(quant_tiles_x(a) * quant_tiles_y(a));
-    if (rows && columns) quantize_kernel<kDtype, true, true, kRandom><<<grid, 256, 0, s>>>(a);
-    else if (rows) quantize_kernel<kDtype, true, false, kRandom><<<grid, 256, 0, s>>>(a);
-    else quantize_kernel<kDtype, false, true, kRandom><<<grid, 256, 0, s>>>(a);
+    const unsigned grid = (unsigned)quant_groups(a);
+    if (a.codes_t == nullptr) quantize_rows_kernel<kDtype, kRandom><<<grid, 256, 0, s>>>(a);
+    else if (a.codes != nullptr) quantize_kernel<kDtype, true, kRandom><<<grid, 256, 0, s>>>(a);
+    else quantize_kernel<kDtype, false, kRandom><<<grid, 256, 0, s>>>(a);
     return hipGetLastError();
 }
 
 }  // namespace
 
-int64_t mx4_quantize_lanes(const Mx4QuantArgs& a) { return quant_tiles_x(a) * quant_tiles_y(a) * 256; }
-// Of the 256-wide tiles, which a product with so many lanes is run on.
-int64_t mx4_matmul_lanes(const Mx4MatmulArgs& a) { return ceil_div64(a.m, 256) * ceil_div64(a.n, 256) * Shape256::kThreadsWg; }
+int64_t mx4_quantize_lanes(const Mx4QuantArgs& a) { return quant_groups(a) * 256; }
+// Of the thin kernel, or of the 256-wide tiles, which a product with so many lanes is run on.
+static int64_t thin_lanes(const Mx4MatmulArgs& a) { return ceil_div64(a.n, 16) * 64 * kThinWaves; }
+static bool is_thin(const Mx4MatmulArgs& a) { return a.m <= kThinRows && thin_lanes(a) <= 0xFFFFFFFFLL; }
+int64_t mx4_matmul_lanes(const Mx4MatmulArgs& a) {
+    return is_thin(a) ? thin_lanes(a) : ceil_div64(a.m, 256) * ceil_div64(a.n, 256) * Shape256::kThreadsWg;
+}
 
 hipError_t launch_mx4_quantize(const Mx4QuantArgs& a, hipStream_t s) {
 #define FP_QUANT(D) (a.stochastic ? run_quantize<D, true>(a, s) : run_quantize<D, false>(a, s))
@@ -358,8 +497,8 @@ hipError_t launch_mx4_quantize(const Mx4QuantArgs& a, hipStream_t s) {
 }
 
 hipError_t launch_mx4_dequantize(const Mx4DequantArgs& a, hipStream_t s) {
-    const int lanes = (int)ceil_div64(a.cols, 8);
-    const unsigned grid = (unsigned)ceil_div64(a.rows * lanes, 256);
+    const uint32_t lanes = (uint32_t)ceil_div64(a.cols, 8);
+    const unsigned grid = (unsigned)ceil_div64(a.rows * (int64_t)lanes, 256);
     if (a.dtype == FP_DTYPE_F32) dequantize_kernel<FP_DTYPE_F32><<<grid, 256, 0, s>>>(a, lanes);
     else if (a.dtype == FP_DTYPE_BF16) dequantize_kernel<FP_DTYPE_BF16><<<grid, 256, 0, s>>>(a, lanes);
     else dequantize_kernel<FP_DTYPE_F16><<<grid, 256, 0, s>>>(a, lanes);
@@ -367,6 +506,13 @@ hipError_t launch_mx4_dequantize(const Mx4DequantArgs& a, hipStream_t s) {
 }
 
 hipError_t launch_mx4_matmul(const Mx4MatmulArgs& a, hipStream_t s) {
+    if (is_thin(a)) {
+        const unsigned grid = (unsigned)ceil_div64(a.n, 16);
+        if (a.m <= 16) thin_kernel<1><<<grid, 64 * kThinWaves, 0, s>>>(a);
+        else if (a.m <= 32) thin_kernel<2><<<grid, 64 * kThinWaves, 0, s>>>(a);
+        else thin_kernel<4><<<grid, 64 * kThinWaves, 0, s>>>(a);
+        return hipGetLastError();
+    }
     auto tiles = [&](int64_t side) { return ceil_div64(a.m, side) * ceil_div64(a.n, side); };
     if (tiles(256) >= 160) return run_matmul<Shape256>(a, s);
     if (tiles(128) >= 160) return run_matmul<Shape128>(a, s);

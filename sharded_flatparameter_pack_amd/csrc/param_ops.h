@@ -140,14 +140,16 @@ __device__ __forceinline__ void put8(void* p, const uint2 v) { *gptr<u32x2_t>(p)
 // 32 bits of dither for partition element e: the element's index and the
 // call's key through two multiplications.  The multipliers are the golden
 // ratio's and the fractions of sqrt(2) and sqrt(3).
-__device__ __forceinline__ uint32_t dither(uint32_t e, uint32_t key) {
-    uint32_t x = (e * 0x9E3779B1u) ^ key;
+constexpr uint32_t kDitherStep = 0x9E3779B1u;
+__device__ __forceinline__ uint32_t dither_at(uint32_t product, uint32_t key) {  // of e kDitherStep
+    uint32_t x = product ^ key;
     x ^= x >> 16;
     x *= 0x6A09E667u;
     x ^= x >> 15;
     x *= 0xBB67AE85u;
     return x;
 }
+__device__ __forceinline__ uint32_t dither(uint32_t e, uint32_t key) { return dither_at(e * kDitherStep, key); }
 
 }  // namespace
 }  // namespace fpk
