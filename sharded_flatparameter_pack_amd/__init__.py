@@ -1376,10 +1376,10 @@ def mx4_quantize(src, codes=None, scales=None, codes_t=None, scales_t=None, *, r
     for want, held, high, wide, name in ((rows, (codes, scales), r, c, "rows' form"),
                                          (transposed, (codes_t, scales_t), c, r, "columns' form")):
         if not want:
-            if held != (None, None):
+            if held[0] is not None or held[1] is not None:
                 raise ValueError(f"buffers of the {name}, which is not wanted")
             ptrs += (None, None)
-        elif held == (None, None):
+        elif held[0] is None and held[1] is None:
             held = mx4_empty(high, wide, src.device)
             got += held
             ptrs += (held[0].data_ptr(), held[1].data_ptr())

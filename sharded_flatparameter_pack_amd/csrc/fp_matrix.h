@@ -26,7 +26,7 @@ struct MuonRec {
     int64_t h[2], l;          // h has two places: a step of the iteration reads one and writes the other
     int64_t a, b;             // fp16 [m][m], their diagonals zero
     int64_t da, db;           // fp32 [m]: the diagonals
-    int64_t part;             // fp64 [chunks]
+    int64_t part;             // fp64 [chunks + 1]: the norm's partial sums, and 1 / (norm + eps)
 };
 
 constexpr int kPad = 64;
@@ -75,6 +75,11 @@ struct MuonArgs {
     MuonGroup g[FP_MAX_GROUPS];
 };
 
+// A chunk of the norm's sum: kChunk elements, or so many that a matrix has
+// kMaxChunks.
+constexpr int64_t kChunk = 8192, kMaxChunks = 1024;
+constexpr int kOwnChunks = 64;  // up to so many, the kernel that writes X adds them up itself
+
 // Of the kernel that writes X: the padded matrix in pieces of so many rows and columns.
 constexpr int kCastRows = 16, kCastCols = 128;
 
@@ -82,8 +87,6 @@ constexpr int kCastRows = 16, kCastCols = 128;
 // workgroup that has its CU to itself.
 enum { kTile256 = 0, kTile128 = 1, kTile64 = 2, kTile64Deep = 3, kTileShapes = 4 };
 constexpr int kTileSide[kTileShapes] = {256, 128, 64, 64};
-
-constexpr unsigned kMaxLds = (160u << 10) - 512;  // a workgroup's, without what a kernel declares itself
 
 // Small matrices: what one workgroup needs for one of rows x cols, in bytes of
 // LDS and in 16 x 16 tiles per wave: up to 4 as they come, else four by four.
@@ -98,11 +101,12 @@ inline int64_t small_tiles(int64_t rows, int64_t cols) {
     return 4 * blocks <= 4 * waves ? ceil_div64(4 * blocks, waves) : 4 * ceil_div64(blocks, waves);
 }
 inline bool is_small(int64_t rows, int64_t cols) {
-    return small_tiles(rows, cols) <= kSmallTiles && small_lds(rows, cols) <= (int64_t)kMaxLds;
+    return small_tiles(rows, cols) <= kSmallTiles && small_lds(rows, cols) <= (160 << 10) - 512;
 }
 
 hipError_t launch_muon_small(const MuonArgs& a, const MuonSteps& steps, int tiles, unsigned lds, hipStream_t s);
 hipError_t launch_muon_moment(const MuonArgs& a, hipStream_t s);
+hipError_t launch_muon_norm(const MuonArgs& a, hipStream_t s);
 hipError_t launch_muon_cast(const MuonArgs& a, hipStream_t s);
 hipError_t launch_muon_gram(const MuonArgs& a, int shape, hipStream_t s);
 hipError_t launch_muon_poly(const MuonArgs& a, int shape, hipStream_t s);

@@ -26,6 +26,7 @@
 // instead, the same tiles take 121 and 250 us.
 #pragma once
 
+#include <atomic>
 #include <type_traits>
 
 #include "fp_device.h"
@@ -55,11 +56,12 @@ template <bool kWritten, int kBytes>
 __device__ __forceinline__ void load_lds(const void* base, const char* to, int voffset, int soffset) {
     if constexpr (kWritten) {
         const uint64_t p = (uint64_t)base;
-        const i32x4_t buffer = {(int)(uint32_t)p, (int)(uint32_t)(p >> 32) & 0xFFFF, -1, 0x00020000};
+        const i32x4_t buffer = {__builtin_amdgcn_readfirstlane((int)(uint32_t)p),
+                                __builtin_amdgcn_readfirstlane((int)(uint32_t)(p >> 32) & 0xFFFF), -1, 0x00020000};
         const uint32_t at = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(FP_LDS const char*)to);
         static_assert(kBytes == 16, "rows and columns of fp16");
         asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
-                     :: "s"(at), "v"(voffset), "s"(buffer), "s"(soffset) : "memory", "m0");
+                     :: "s"(at), "v"(voffset), "s"(buffer), "s"(__builtin_amdgcn_readfirstlane(soffset)) : "memory", "m0");
     } else {
         const __amdgpu_buffer_rsrc_t buffer = __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, -1, 0x00020000);
         if constexpr (kBytes == 16) __builtin_amdgcn_raw_ptr_buffer_load_lds(buffer, (FP_LDS void*)to, 16, voffset, soffset, 0, 0);
@@ -324,37 +326,64 @@ struct TileProduct {
         barrier_lds();
     }
 
-    // The column that a lane has in each(): the first of its eight.
-    static __device__ __forceinline__ int each_col() { return (int)threadIdx.x % (S::kBN / 8) * 8; }
+    // The column that a lane has in each(): the first of its kVec.
+    template <int kVec>
+    static __device__ __forceinline__ int each_col() { return (int)threadIdx.x % (S::kBN / kVec) * kVec; }
 
     // Walks the tile along its rows, through LDS (the lanes' own fragments are
-    // 16 rows of 16 bytes): body(row, col, v, f) with 8 neighbouring columns from
-    // each_col() on, a row's neighbours in neighbouring lanes.  f is what
-    // fetch(row, col) gave: it is called one pass of kPer fragments ahead, so that
-    // what the lane reads from memory is there when it is needed (without, the
-    // tile of a 1024-wide product waited 25 us for its 16 reads, one by one).
-    // kTurned: also turned(row, col, v, f) with 8 neighbouring rows from `row` on
-    // and f = fetch_turned(row, col).
-    template <int kPer, bool kTurned, class L, class F, class M, class G>
-    __device__ __forceinline__ void each(char* lds, L fetch, F body, M fetch_turned, G turned) {
+    // 16 rows of 16 bytes): body(row, col, v, f) with kVec (8 or 4) neighbouring
+    // columns from each_col() on, a row's neighbours in neighbouring lanes: 8 for
+    // values that are 16 bits in memory, 4 for 32, so that a wave's access is one
+    // run.  f is what fetch(row, col) gave: it is called one pass of kPer fragments
+    // ahead, so that what the lane reads from memory is there when it is needed
+    // (without, the tile of a 1024-wide product waited 25 us for its 16 reads, one
+    // by one).  kTurned: also turned(row, col, v, f) with 8 neighbouring rows from
+    // `row` on and f = fetch_turned(row, col).
+    // fetch_early: the same for the whole tile, for what is fetched before the
+    // product; body gets it as one more argument.
+    template <int kPer, int kVec, class L>
+    static __device__ __forceinline__ auto fetch_early(L fetch) {
+        constexpr int kPassRows = S::kRows * kPer * 16, kAcross = S::kBN / kVec;
+        constexpr int kTimes = kPassRows * kAcross / S::kThreadsWg;
+        struct All {
+            decltype(fetch(0, 0)) f[S::kFM / kPer][kTimes];
+        } all;
+#pragma unroll
+        for (int p = 0; p < S::kFM; p += kPer)
+#pragma unroll
+            for (int t = 0; t < kTimes; ++t) {
+                const int i = (int)threadIdx.x / kAcross + t * (S::kThreadsWg / kAcross);
+                all.f[p / kPer][t] = fetch(i / (kPer * 16) * S::kWM + p * 16 + i % (kPer * 16), each_col<kVec>());
+            }
+        return all;
+    }
+    struct Nothing {};
+    static __device__ __forceinline__ Nothing nothing(int, int) { return {}; }
+
+    template <int kPer, int kVec, bool kTurned, class L, class F, class M, class G, class E = Nothing>
+    __device__ __forceinline__ void each(char* lds, L fetch, F body, M fetch_turned, G turned, E&& early = E{}) {
+        constexpr bool kEarly = !std::is_same<std::decay_t<E>, Nothing>::value;
         constexpr int kPitch = S::kBN + 4;              // floats
         constexpr int kPassRows = S::kRows * kPer * 16;
-        constexpr int kAcross = S::kBN / 8, kDown = kPassRows / 8;
+        constexpr int kAcross = S::kBN / kVec, kDown = kPassRows / 8;
         constexpr int kTimes = kPassRows * kAcross / S::kThreadsWg;
+        constexpr int kTimesTurned = kTurned ? kPassRows * S::kBN / 8 / S::kThreadsWg : 1;
         static_assert(S::kFM % kPer == 0 && kTimes >= 1 && kTimes * S::kThreadsWg == kPassRows * kAcross, "whole passes");
         static_assert(S::kThreadsWg % kAcross == 0 && S::kThreadsWg % kDown == 0, "whole rows");
         static_assert(kPassRows * kPitch * 4 <= S::kLds, "a pass fits into the stages");
         float* to = reinterpret_cast<float*>(lds);
-        const int c = each_col(), r = (int)threadIdx.x / kAcross;
+        const int c = each_col<kVec>(), r = (int)threadIdx.x / kAcross;
         const int tr = (int)threadIdx.x % kDown * 8, tc = (int)threadIdx.x / kDown;
         auto tile_row = [&](int p, int i) { return i / (kPer * 16) * S::kWM + p * 16 + i % (kPer * 16); };
         decltype(fetch(0, 0)) f[kTimes], ahead[kTimes];
-        decltype(fetch_turned(0, 0)) ft[kTimes], ahead_t[kTimes];
+        decltype(fetch_turned(0, 0)) ft[kTimesTurned], ahead_t[kTimesTurned];
         auto fetch_pass = [&](int p) {
 #pragma unroll
-            for (int t = 0; t < kTimes; ++t) {
-                ahead[t] = fetch(tile_row(p, r + t * (S::kThreadsWg / kAcross)), c);
-                if constexpr (kTurned) ahead_t[t] = fetch_turned(tile_row(p, tr), tc + t * (S::kThreadsWg / kDown));
+            for (int t = 0; t < kTimes; ++t) ahead[t] = fetch(tile_row(p, r + t * (S::kThreadsWg / kAcross)), c);
+            if constexpr (kTurned) {
+#pragma unroll
+                for (int t = 0; t < kTimesTurned; ++t)
+                    ahead_t[t] = fetch_turned(tile_row(p, tr), tc + t * (S::kThreadsWg / kDown));
             }
         };
         fetch_pass(0);
@@ -367,19 +396,28 @@ struct TileProduct {
                 for (int n = 0; n < S::kFN; ++n)
                     *(f32x4_t*)(to + (wave / S::kCols * kPer * 16 + m * 16 + (lane & 15)) * kPitch + col0() + 16 * n) = acc[p + m][n];
 #pragma unroll
-            for (int t = 0; t < kTimes; ++t) f[t] = ahead[t], ft[t] = ahead_t[t];
+            for (int t = 0; t < kTimes; ++t) f[t] = ahead[t];
+            if constexpr (kTurned) {
+#pragma unroll
+                for (int t = 0; t < kTimesTurned; ++t) ft[t] = ahead_t[t];
+            }
             if (p + kPer < S::kFM) fetch_pass(p + kPer);
             barrier_lds();
 #pragma unroll
             for (int t = 0; t < kTimes; ++t) {
                 const int i = r + t * (S::kThreadsWg / kAcross);
-                const f32x4_t a = *(const f32x4_t*)(to + i * kPitch + c), b = *(const f32x4_t*)(to + i * kPitch + c + 4);
-                const float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-                body(tile_row(p, i), c, v, f[t]);
+                float v[kVec];
+#pragma unroll
+                for (int q = 0; q < kVec; q += 4) {
+                    const f32x4_t x = *(const f32x4_t*)(to + i * kPitch + c + q);
+                    v[q] = x.x; v[q + 1] = x.y; v[q + 2] = x.z; v[q + 3] = x.w;
+                }
+                if constexpr (kEarly) body(tile_row(p, i), c, v, f[t], early.f[p / kPer][t]);
+                else body(tile_row(p, i), c, v, f[t]);
             }
             if constexpr (kTurned) {
 #pragma unroll
-                for (int t = 0; t < kTimes; ++t) {
+                for (int t = 0; t < kTimesTurned; ++t) {
                     const int i = tc + t * (S::kThreadsWg / kDown);
                     float v[8];
 #pragma unroll
@@ -389,11 +427,9 @@ struct TileProduct {
             }
         }
     }
-    struct Nothing {};
-    static __device__ __forceinline__ Nothing nothing(int, int) { return {}; }
-    template <int kPer, class L, class F>
-    __device__ __forceinline__ void each(char* lds, L fetch, F body) {
-        each<kPer, false>(lds, fetch, body, nothing, 0);
+    template <int kPer, int kVec, class L, class F, class E = Nothing>
+    __device__ __forceinline__ void each(char* lds, L fetch, F body, E&& early = E{}) {
+        each<kPer, kVec, false>(lds, fetch, body, nothing, 0, early);
     }
 
     // Waits until at most kN of the wave's memory accesses are on their way.
@@ -414,6 +450,27 @@ struct TileProduct {
 template <int kLeft, int kRight, class S>
 __device__ __forceinline__ void run_tile(TileProduct<S>& tile, const Operand& left, const Operand& right, int steps, char* lds) {
     tile.template run<kLeft, kRight>(left, right, steps, lds);
+}
+
+constexpr unsigned kMaxLds = (160u << 10) - 512;  // a workgroup's, without what a kernel declares itself
+
+// Launches a kernel.  Beyond 64 KiB, LDS is asked for once per kernel and device.
+template <auto kKernel, class... Args>
+hipError_t launch(unsigned groups, int threads, unsigned lds, hipStream_t s, const Args&... args) {
+    if (lds > 65536u) {
+        static std::atomic<uint64_t> asked{0};
+        int device = 0;
+        hipError_t e = hipGetDevice(&device);
+        if (e != hipSuccess) return e;
+        const uint64_t bit = 1ull << (device & 63);
+        if (!(asked.load() & bit)) {
+            e = hipFuncSetAttribute(reinterpret_cast<const void*>(kKernel), hipFuncAttributeMaxDynamicSharedMemorySize, (int)kMaxLds);
+            if (e != hipSuccess) return e;
+            asked.fetch_or(bit);
+        }
+    }
+    kKernel<<<groups, threads, lds, s>>>(args...);
+    return hipGetLastError();
 }
 
 // Tile number of a workgroup: the hardware deals workgroups out to the 8 dies

@@ -30,6 +30,8 @@ struct Run {
     int64_t first = 0, n = 0;
 };
 
+constexpr int64_t kFewSmall = 128;
+
 // Small matrices that need about as much: one launch.
 struct Small {
     Run run;
@@ -39,7 +41,7 @@ struct Small {
 
 struct Batch {
     std::vector<int32_t> mats;
-    Run moment, cast, half, full;
+    Run moment, norm, cast, half, full;
     int half_shape = kTile64, full_shape = kTile64;
 };
 
@@ -121,7 +123,7 @@ int64_t lay_out(MuonRec* r, int64_t at) {
     r->b = take(2 * m * m);
     r->da = take(4 * m);
     r->db = take(4 * m);
-    r->part = take(8 * r->chunks);
+    r->part = take(8 * (r->chunks + 1));
     return at;
 }
 
@@ -151,7 +153,7 @@ std::vector<MatTile> ordered(const MuonRec& r, int32_t mat, int side, bool half)
 // alone there, and from what a tile takes beside its steps (MI355X, the tiles'
 // kernels at 1024 to 4096).
 double finish(const std::vector<MuonRec>& recs, const Batch& b, int shape, bool half) {
-    constexpr double kStep[] = {1.6, 0.56, 0.26, 0.4}, kAlone[] = {1.3, 0.65, 0.36, 0.2}, kBeside[] = {14.0, 6.0, 2.0, 3.0};
+    constexpr double kStep[] = {1.6, 0.56, 0.26, 0.4}, kAlone[] = {1.3, 0.65, 0.36, 0.2}, kBeside[] = {20.0, 6.0, 2.5, 3.0};
     std::vector<std::pair<int64_t, int64_t>> runs;  // steps, tiles
     for (int32_t i : b.mats) {
         const MuonRec& r = recs[(size_t)i];
@@ -232,8 +234,9 @@ void close_batch(const std::vector<MuonRec>& recs, Batch* b, std::vector<MatTile
                 for (int64_t tj = 0; tj < cols(recs[(size_t)i]); ++tj) table->push_back({i, (int32_t)ti, (int32_t)tj, 0});
     };
     run(&b->moment, [&] { grid([](const MuonRec& r) { return (int64_t)r.chunks; }, [](const MuonRec&) { return (int64_t)1; }); });
+    run(&b->norm, [&] { grid([](const MuonRec& r) { return (int64_t)(r.chunks > kOwnChunks); }, [](const MuonRec&) { return (int64_t)1; }); });
     run(&b->cast, [&] {
-        grid([](const MuonRec& r) { return (int64_t)r.rp / kCastRows; }, [](const MuonRec& r) { return ceil_div64(r.cp, kCastCols); });
+        grid([](const MuonRec& r) { return ceil_div64(r.rp, kCastRows); }, [](const MuonRec& r) { return ceil_div64(r.cp, kCastCols); });
     });
     b->half_shape = choose_shape(recs, *b, true);
     b->full_shape = choose_shape(recs, *b, false);
@@ -289,6 +292,8 @@ fp_status create(int32_t n, const int64_t* rows, const int64_t* cols, const int3
     int32_t max_group = 0;
     Batch open;
     std::vector<int32_t> small;
+    int64_t few = 0;
+    bool any_large = false;
     for (int32_t i = 0; i < n; ++i) {
         if (rows[i] < 0 || rows[i] > kMaxSide || cols[i] < 0 || cols[i] > kMaxSide)
             return bad(FP_ERR_RANGE, "matrix %d: %lld x %lld, sides go up to %lld", i, (long long)rows[i], (long long)cols[i],
@@ -329,12 +334,22 @@ fp_status create(int32_t n, const int64_t* rows, const int64_t* cols, const int3
             }
             r.rp = (int32_t)pad64(rows[i]);
             r.cp = (int32_t)pad64(cols[i]);
-            r.chunk = std::max<int64_t>(8192, ceil_div64(ceil_div64(numel, 256), 1024) * 1024);
+            r.chunk = std::max<int64_t>(kChunk, ceil_div64(ceil_div64(numel, kMaxChunks), 1024) * 1024);
             r.chunks = (int32_t)ceil_div64(numel, r.chunk);
             partition += ceil_div64(numel, 32) * 32;
-            if (r.rp / kCastRows * ceil_div64(r.cp, kCastCols) > 0xFFFFFFFFLL / 256)
+            if (ceil_div64(r.rp, kCastRows) * ceil_div64(r.cp, kCastCols) > 0xFFFFFFFFLL / 256)
                 return bad(FP_ERR_RANGE, "matrix %d needs more workgroups than one launch holds", i);
-            if (is_small(rows[i], cols[i])) {
+            if (is_small(rows[i], cols[i])) ++few;
+            else any_large = true;
+        }
+    }
+    // A few small matrices beside a large one: its launches have room for them, and
+    // one of their own would come on top (24 matrices of 1 to 1400: 190 us, KKK with).
+    const bool apart = !any_large || few > kFewSmall;
+    for (int32_t i = 0; i < n; ++i) {
+        MuonRec& r = recs[(size_t)i];
+        if (r.rows > 0 && r.cols > 0) {
+            if (apart && is_small(r.rows, r.cols)) {
                 small.push_back(i);
             } else {
                 open.mats.push_back(i);
@@ -535,6 +550,8 @@ fp_status run(fp_muon* p, MuonArgs a, const std::vector<Step>& steps, bool to_we
     for (const Batch& b : p->batches) {
         over(b.moment);
         if ((e = launch_muon_moment(a, s)) != hipSuccess) return device_error(e, "momentum launch");
+        over(b.norm);
+        if (b.norm.n > 0 && (e = launch_muon_norm(a, s)) != hipSuccess) return device_error(e, "norm launch");
         over(b.cast);
         a.s = steps[0].s;
         if ((e = launch_muon_cast(a, s)) != hipSuccess) return device_error(e, "cast launch");

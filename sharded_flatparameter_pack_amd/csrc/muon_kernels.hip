@@ -25,7 +25,6 @@
 //
 // Compiled with -ffp-contract=off.
 
-#include <atomic>
 #include <type_traits>
 
 #include "fp_matrix.h"
@@ -110,28 +109,37 @@ __global__ __launch_bounds__(256) void moment_kernel(const MuonArgs a) {
     const double k = kStep && a.g_coef != nullptr ? *a.g_coef : 1.0;
     const double mine = kStep ? (1.0 - hp.beta) * k : 1.0;
     double sum = 0.0;
-    for (int64_t e = from + 4 * threadIdx.x; e < to; e += 1024) {
-        const int have = to - e < 4 ? (int)(to - e) : 4;
-        float g[4];
-        grad4<kGrad>(grad, e, have, g);
-        double u[4];
-        if constexpr (kStep) {
-            float m[4];
-            float* at = a.momentum + r.offset + e;  // room up to the next multiple of 32
-            f32x4_of(ld16(at), m);
+    constexpr int kAtOnce = 4;  // loads under way per lane
+    for (int64_t e0 = from + 4 * threadIdx.x; e0 < to; e0 += 1024 * kAtOnce) {
+        float g[kAtOnce][4], m[kAtOnce][4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                m[i] = (float)(hp.beta * (double)m[i] + mine * (double)g[i]);
-                u[i] = hp.nesterov ? hp.beta * (double)m[i] + mine * (double)g[i] : (double)m[i];
-            }
-            st_f32(at, have, m);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) u[i] = (double)g[i];
+        for (int i = 0; i < kAtOnce; ++i) {
+            const int64_t e = e0 + 1024 * i;
+            if (e >= to) continue;
+            grad4<kGrad>(grad, e, to - e < 4 ? (int)(to - e) : 4, g[i]);
+            if constexpr (kStep) f32x4_of(get16(a.momentum + r.offset + e), m[i]);  // room up to the next multiple of 32
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (i < have) sum += u[i] * u[i];
+        for (int i = 0; i < kAtOnce; ++i) {
+            const int64_t e = e0 + 1024 * i;
+            if (e >= to) continue;
+            const int have = to - e < 4 ? (int)(to - e) : 4;
+            double u[4];
+            if constexpr (kStep) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    m[i][q] = (float)(hp.beta * (double)m[i][q] + mine * (double)g[i][q]);
+                    u[q] = hp.nesterov ? hp.beta * (double)m[i][q] + mine * (double)g[i][q] : (double)m[i][q];
+                }
+                st_f32(a.momentum + r.offset + e, have, m[i]);
+            } else {
+#pragma unroll
+                for (int q = 0; q < 4; ++q) u[q] = (double)g[i][q];
+            }
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                if (q < have) sum += u[q] * u[q];
+        }
     }
     sum = sum256(sum, lds);
     if (threadIdx.x == 0) gptr<double>((void*)(a.ws + r.part))[t.ti] = sum;
@@ -139,21 +147,22 @@ __global__ __launch_bounds__(256) void moment_kernel(const MuonArgs a) {
 
 // ---------------------------------------------------------------- the forms of X
 
-// Eight values, scaled, into both parts.
-__device__ __forceinline__ void st_x(char* ws, int64_t h, int64_t l, int64_t at, const float x[8]) {
+// Eight values, scaled, into both parts, `at` elements from a tile's start (less
+// than 2^28: an offset in one register, beside a base that all lanes share).
+__device__ __forceinline__ void st_x(char* h, char* l, uint32_t at, const float x[8]) {
     uint32_t hw[4], lw[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
         hw[k] = f16_pair(x[2 * k], x[2 * k + 1]);
         lw[k] = bf16x2(x[2 * k] - f16_lo(hw[k]), x[2 * k + 1] - f16_hi(hw[k]));
     }
-    put16(ws + h + 2 * at, make_uint4(hw[0], hw[1], hw[2], hw[3]));
-    put16(ws + l + 2 * at, make_uint4(lw[0], lw[1], lw[2], lw[3]));
+    put16(h + 2 * at, make_uint4(hw[0], hw[1], hw[2], hw[3]));
+    put16(l + 2 * at, make_uint4(lw[0], lw[1], lw[2], lw[3]));
 }
-__device__ __forceinline__ void x_of(const uint4 a, const uint4 b, float x[8]) {
-    const uint32_t hw[4] = {a.x, a.y, a.z, a.w}, lw[4] = {b.x, b.y, b.z, b.w};
+template <int kVec>
+__device__ __forceinline__ void x_of(const uint32_t* hw, const uint32_t* lw, float* x) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
+    for (int k = 0; k < kVec / 2; ++k) {
         x[2 * k] = f16_lo(hw[k]) + bf16_lo(lw[k]);
         x[2 * k + 1] = f16_hi(hw[k]) + bf16_hi(lw[k]);
     }
@@ -167,23 +176,43 @@ __device__ __forceinline__ void st_f16(void* p, const float x[8]) {
     put16(p, make_uint4(f16_pair(x[0], x[1]), f16_pair(x[2], x[3]), f16_pair(x[4], x[5]), f16_pair(x[6], x[7])));
 }
 
+// ---------------------------------------------------------------- norm
+
+// Each matrix's 1 / (|U| + eps), behind its partial sums, where those are more
+// than the cast kernel's waves add up themselves.
+__global__ __launch_bounds__(256) void norm_kernel(const MuonArgs a) {
+    __shared__ double lds[4];
+    if (skipped(a)) return;
+    const MuonRec& r = a.recs[a.tiles[blockIdx.x].mat];
+    FP_GLOBAL double* part = gptr<double>((void*)(a.ws + r.part));
+    double sum = 0.0;
+    for (int i = threadIdx.x; i < r.chunks; i += 256) sum += part[i];
+    sum = sum256(sum, lds);
+    if (threadIdx.x == 0) part[r.chunks] = 1.0 / (sqrt(sum) + a.eps);
+}
+
 // ---------------------------------------------------------------- cast
 
 // kCastRows x kCastCols of the padded matrix: X = U / (|U| + eps).
 template <int kGrad, bool kStep>
 __global__ __launch_bounds__(256) void cast_kernel(const MuonArgs a) {
-    __shared__ double lds[4];
     if (kStep && skipped(a)) return;
     const MatTile t = a.tiles[blockIdx.x];
     const MuonRec& r = a.recs[t.mat];
-    double sum = 0.0;
-    for (int i = threadIdx.x; i < r.chunks; i += 256) sum += gptr<double>((const void*)(a.ws + r.part))[i];
-    const double scale = 1.0 / (sqrt(sum256(sum, lds)) + a.eps);
+    const FP_GLOBAL double* part = gptr<double>((const void*)(a.ws + r.part));
+    double scale;
+    if (r.chunks > kOwnChunks) {
+        scale = part[r.chunks];
+    } else {
+        const int lane = threadIdx.x & 63;
+        scale = 1.0 / (sqrt(wave_sum(lane < r.chunks ? part[lane] : 0.0)) + a.eps);
+    }
     const void* grad = a.grads[t.mat];
     const MuonGroup& hp = a.g[kStep ? r.group : 0];
     const double k = kStep && a.g_coef != nullptr ? *a.g_coef : 1.0;
     const double mine = kStep ? (1.0 - hp.beta) * k : 1.0;
-    const int row = t.ti * kCastRows + (threadIdx.x >> 4), col = t.tj * kCastCols + (threadIdx.x & 15) * 8;
+    const int row0 = t.ti * kCastRows, col0 = t.tj * kCastCols;
+    const int row = row0 + (threadIdx.x >> 4), col = col0 + (threadIdx.x & 15) * 8;
     if (row >= r.rp || col >= r.cp) return;
     float x[8];
 #pragma unroll
@@ -204,7 +233,8 @@ __global__ __launch_bounds__(256) void cast_kernel(const MuonArgs a) {
                 }
         }
     }
-    st_x(a.ws, r.h[0], r.l, (int64_t)row * r.cp + col, x);
+    const int64_t base = 2 * ((int64_t)row0 * r.cp + col0);
+    st_x(a.ws + r.h[0] + base, a.ws + r.l + base, (uint32_t)((row - row0) * r.cp + col - col0), x);
 }
 
 // ---------------------------------------------------------------- products
@@ -242,7 +272,8 @@ __global__ __launch_bounds__(S::kThreadsWg, S::kWavesSimd) void gram_kernel(cons
     if (z.turned) run_tile<kColumnsF16, kColumnsF16>(tile, columns_of(h, i0, z.m), columns_of(h, j0, z.m), steps, lds);
     else run_tile<kRowsF16, kRowsF16>(tile, rows_of(h, i0, z.m, z.n), rows_of(h, j0, z.m, z.n), steps, lds);
     const float unscale = a.s.un_xx, out = a.s.gram;
-    char* to = a.ws + r.a;
+    char* const to = a.ws + r.a + 2 * ((int64_t)i0 * z.m + j0);
+    char* const mirror = a.ws + r.a + 2 * ((int64_t)j0 * z.m + i0);
     typedef typename TileProduct<S>::Nothing Nothing;
     auto body = [&](int tr, int tc, const float* v, Nothing) {
         const int row = i0 + tr, col = j0 + tc;
@@ -256,19 +287,19 @@ __global__ __launch_bounds__(S::kThreadsWg, S::kWavesSimd) void gram_kernel(cons
                 f[k] = 0.0f;
             }
         }
-        st_f16(to + 2 * ((int64_t)row * z.m + col), f);
+        st_f16(to + 2 * (uint32_t)(tr * z.m + tc), f);
     };
     if (t.ti == t.tj) {
-        tile.template each<2>(lds, tile.nothing, body);
+        tile.template each<2, 8>(lds, tile.nothing, body);
         return;
     }
-    tile.template each<2, true>(lds, tile.nothing, body, tile.nothing, [&](int tr, int tc, const float* v, Nothing) {
+    tile.template each<2, 8, true>(lds, tile.nothing, body, tile.nothing, [&](int tr, int tc, const float* v, Nothing) {
         const int row = i0 + tr, col = j0 + tc;
         if (row >= z.m || col >= z.m) return;
         float f[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k) f[k] = v[k] * out;
-        st_f16(to + 2 * ((int64_t)col * z.m + row), f);
+        st_f16(mirror + 2 * (uint32_t)(tc * z.m + tr), f);
     });
 }
 
@@ -288,19 +319,19 @@ __global__ __launch_bounds__(S::kThreadsWg, S::kWavesSimd) void poly_kernel(cons
     run_tile<kRowsF16, kRowsF16>(tile, rows_of(n, i0, z.m, z.m), rows_of(n, j0, z.m, z.m), z.m / kStepF16, lds);
     const float un_a = a.s.un_a, un_s = un_a * un_a;
     const FP_GLOBAL float* d = gptr<float>((const void*)(a.ws + r.da));
-    char* to = a.ws + r.b;
     // eight elements (row, col ..) of N, with their part of the diagonals; the
     // mirror images of a tile are those of the other row, N being symmetric
     struct Fetched {
         uint4 n;
         float row;
     };
-    auto fetch = [&](int row, int col) {
+    const int64_t straight_at = 2 * ((int64_t)i0 * z.m + j0), mirror_at = 2 * ((int64_t)j0 * z.m + i0);
+    auto fetch = [&](int row, int col, int64_t base, uint32_t at) {
         Fetched f = {make_uint4(0u, 0u, 0u, 0u), 0.0f};
-        if (row < z.m && col < z.m) f = {get16(n + 2 * ((int64_t)row * z.m + col)), d[row]};
+        if (row < z.m && col < z.m) f = {get16(n + base + 2 * at), d[row]};
         return f;
     };
-    auto poly = [&](int row, int col, const float* v, const Fetched& e, const float dc[8]) {
+    auto poly = [&](int row, int col, int64_t base, uint32_t at, const float* v, const Fetched& e, const float dc[8]) {
         if (row >= z.m || col >= z.m) return;
         float x[8], f[8];
         f16x8_to_f32(e.n, x);
@@ -314,28 +345,31 @@ __global__ __launch_bounds__(S::kThreadsWg, S::kWavesSimd) void poly_kernel(cons
                 f[k] = 0.0f;
             }
         }
-        st_f16(to + 2 * ((int64_t)row * z.m + col), f);
+        st_f16(a.ws + r.b + base + 2 * at, f);
     };
     float dc[8], dr[8];  // of the lane's columns; of the eight rows of a mirror image, per pass
 #pragma unroll
-    for (int k = 0; k < 8; ++k) dc[k] = j0 + tile.each_col() < z.m ? d[j0 + tile.each_col() + k] : 0.0f;
-    auto body = [&](int tr, int tc, const float* v, const Fetched& e) { poly(i0 + tr, j0 + tc, v, e, dc); };
-    auto straight = [&](int tr, int tc) { return fetch(i0 + tr, j0 + tc); };
+    for (int k = 0; k < 8; ++k) dc[k] = j0 + tile.template each_col<8>() < z.m ? d[j0 + tile.template each_col<8>() + k] : 0.0f;
+    auto body = [&](int tr, int tc, const float* v, const Fetched& e) {
+        poly(i0 + tr, j0 + tc, straight_at, (uint32_t)(tr * z.m + tc), v, e, dc);
+    };
+    auto straight = [&](int tr, int tc) { return fetch(i0 + tr, j0 + tc, straight_at, (uint32_t)(tr * z.m + tc)); };
     constexpr int kPer = S::kFM > 4 ? 1 : 2;  // as many registers as there are
     if (t.ti == t.tj) {
-        tile.template each<kPer>(lds, straight, body);
+        tile.template each<kPer, 8>(lds, straight, body);
         return;
     }
     int had = -1;
-    tile.template each<kPer, true>(
-        lds, straight, body, [&](int tr, int tc) { return fetch(j0 + tc, i0 + tr); },
+    tile.template each<kPer, 8, true>(
+        lds, straight, body,
+        [&](int tr, int tc) { return fetch(j0 + tc, i0 + tr, mirror_at, (uint32_t)(tc * z.m + tr)); },
         [&](int tr, int tc, const float* v, const Fetched& e) {
             if (tr != had) {
                 had = tr;
 #pragma unroll
                 for (int k = 0; k < 8; ++k) dr[k] = i0 + tr < z.m ? d[i0 + tr + k] : 0.0f;
             }
-            poly(j0 + tc, i0 + tr, v, e, dr);
+            poly(j0 + tc, i0 + tr, mirror_at, (uint32_t)(tc * z.m + tr), v, e, dr);
         });
 }
 
@@ -363,88 +397,121 @@ __global__ __launch_bounds__(S::kThreadsWg, S::kWavesSimd) void next_kernel(cons
     if (skip && (kOut != kToWeights || r.copy == nullptr)) return;
     const char* h = a.ws + r.h[a.step & 1];
     const char* b = a.ws + r.b;
-    TileProduct<S> tile;
-    if (!skip) {
-        const int steps = z.m / kStepF16;
-        if (z.turned) run_tile<kRowsF16, kRowsF16>(tile, rows_of(h, i0, z.n, z.m), rows_of(b, j0, z.m, z.m), steps, lds);
-        else run_tile<kRowsF16, kColumnsF16>(tile, rows_of(b, i0, z.m, z.m), columns_of(h, j0, z.n), steps, lds);
-    }
-    const float unscale = a.s.un_bx, un_x = a.s.un_x;
+    // x = (D x_old + sums) as the next step wants it, or as it is
+    const float next = kOut == kGoesOn ? a.s.x_next : 1.0f;
+    const float un_x = a.s.un_x * next, unscale = a.s.un_bx * next;
     const FP_GLOBAL float* d = gptr<float>((const void*)(a.ws + r.db));
-    double rate = 0.0, decay = 1.0;
-    if constexpr (kOut == kToWeights) {
-        rate = a.g[r.group].lr * adjust_of(a.g[r.group].adjust, r.rows, r.cols);
-        decay = a.g[r.group].decay;
-    }
-    const int rows = kOut == kGoesOn ? r.rp : r.rows, cols = kOut == kGoesOn ? r.cp : r.cols;
-    float dc[8];  // of a tall matrix: of the lane's columns
-    const int c0 = j0 + tile.each_col();
-#pragma unroll
-    for (int k = 0; k < 8; ++k) dc[k] = !skip && z.turned && c0 < z.m ? d[c0 + k] : 0.0f;
-    struct Fetched {
-        uint4 h, l;
-        float d;
-        float w[kOut == kToWeights ? 8 : 1];
+    const double rate = kOut == kToWeights ? a.g[r.group].lr * adjust_of(a.g[r.group].adjust, r.rows, r.cols) : 0.0;
+    const double decay = a.g[r.group].decay;
+    const int rows = (kOut == kGoesOn ? r.rp : r.rows) - i0, cols = (kOut == kGoesOn ? r.cp : r.cols) - j0;
+    const int64_t base = 2 * ((int64_t)i0 * r.cp + j0);         // of the tile, in X's parts
+    const int64_t out = (int64_t)i0 * r.cols + j0;              // in the matrix
+    const char* const h_old = h + base;
+    char* const h_new = a.ws + r.h[(a.step + 1) & 1] + base;
+    char* const l = a.ws + r.l + base;
+    // eight columns a lane, or four with the weights, and passes of one fragment
+    constexpr int kVec = kOut == kToWeights ? 4 : 8, kPer = kOut == kToWeights ? 1 : 2;
+    // What comes from memory: X's old value and the weights.  Tiles of 128 and less
+    // have registers for the weights beside the product's, and fetch them before it
+    // (32 matrices of 1408 x 512: 113 us, else 148; X, which is in the caches, gains
+    // nothing by it).
+    constexpr bool kEarly = kOut == kToWeights && S::kBM <= 128;
+    struct OldX {
+        uint32_t h[kVec / 2], l[kVec / 2];
     };
-    auto have_of = [&](int col, int q) { const int left = cols - col - q; return left < 4 ? left : 4; };
-    // a pass ahead: two fragments' rows, or one's with the weights, which take as many registers again
-    tile.template each<kOut == kToWeights ? 1 : 2>(
-        lds,
-        [&](int tr, int tc) {
-            const int row = i0 + tr, col = j0 + tc;
-            const uint4 none = make_uint4(0u, 0u, 0u, 0u);
-            Fetched f;
-            f.h = f.l = none;
-            f.d = 0.0f;
-            if (row >= rows || col >= cols) return f;
-            const int64_t at = 2 * ((int64_t)row * r.cp + col);
+    struct OldW {
+        float w[kOut == kToWeights ? kVec : 1];
+    };
+    struct Row {
+        float d;
+    };
+    auto inside = [&](int tr, int tc) { return tr < rows && tc < cols; };
+    auto have_of = [&](int tc, int q) { const int left = cols - tc - q; return left < 4 ? left : 4; };
+    auto fetch_x = [&](int tr, int tc) {
+        OldX f = {};
+        if (skip || !inside(tr, tc)) return f;
+        const uint32_t at = 2 * (uint32_t)(tr * r.cp + tc);
+        if constexpr (kVec == 8) {
+            const uint4 hi = get16(h_old + at), lo = get16(l + at);
+            f.h[0] = hi.x; f.h[1] = hi.y; f.h[2] = hi.z; f.h[3] = hi.w;
+            f.l[0] = lo.x; f.l[1] = lo.y; f.l[2] = lo.z; f.l[3] = lo.w;
+        } else {
+            const uint2 hi = get8(h_old + at), lo = get8(l + at);
+            f.h[0] = hi.x; f.h[1] = hi.y;
+            f.l[0] = lo.x; f.l[1] = lo.y;
+        }
+        return f;
+    };
+    auto fetch_w = [&](int tr, int tc) {
+        OldW f = {};
+        if constexpr (kOut == kToWeights)
+            if (inside(tr, tc)) ld_f32(r.master + out + (uint32_t)(tr * r.cols + tc), have_of(tc, 0), f.w);
+        return f;
+    };
+    auto fetch_d = [&](int tr, int) { return Row{!skip && !z.turned && tr < rows ? d[i0 + tr] * un_x : 0.0f}; };
+    typedef TileProduct<S> Tile;
+    Tile tile;
+    float dc[kVec];  // of a tall matrix: of the lane's columns
+    auto leave = [&](int tr, int tc, const float* v, const Row& row, const OldX& old, float* w) {
+        if (!inside(tr, tc)) return;
+        float x[kVec];
+        x_of<kVec>(old.h, old.l, x);
+#pragma unroll
+        for (int k = 0; k < kVec; ++k) x[k] = __builtin_fmaf(z.turned ? dc[k] : row.d, x[k], v[k] * unscale);
+        const uint32_t e = (uint32_t)(tr * r.cols + tc);
+        if constexpr (kOut == kGoesOn) {
+            st_x(h_new, l, (uint32_t)(tr * r.cp + tc), x);
+        } else if constexpr (kOut == kToUpdate) {
+#pragma unroll
+            for (int q = 0; q < kVec; q += 4) {
+                const int have = have_of(tc, q);
+                if (have <= 0) break;
+                if (a.update_dtype == FP_DTYPE_F32) st_f32(static_cast<float*>(r.update) + out + e + q, have, x + q);
+                else st_16bit(static_cast<uint16_t*>(r.update) + out + e + q, have,
+                              a.update_dtype == FP_DTYPE_F16 ? f16x4(x + q) : f32x4_to_bf16(x + q));
+            }
+        } else {
+            const int have = have_of(tc, 0);
             if (!skip) {
-                f.h = get16(h + at);
-                f.l = get16(a.ws + r.l + at);
-                f.d = z.turned ? 0.0f : d[row];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) w[k] = (float)(decay * (double)w[k] - rate * (double)x[k]);
+                st_f32(r.master + out + e, have, w);
             }
-            if constexpr (kOut == kToWeights) {
+            if (r.copy != nullptr)
+                st_16bit(static_cast<uint16_t*>(r.copy) + out + e, have, a.copy_dtype == FP_DTYPE_F16 ? f16x4(w) : f32x4_to_bf16(w));
+        }
+    };
+    auto multiply = [&] {
+        if (!skip) {
+            const int steps = z.m / kStepF16;
+            if (z.turned) run_tile<kRowsF16, kRowsF16>(tile, rows_of(h, i0, z.n, z.m), rows_of(b, j0, z.m, z.m), steps, lds);
+            else run_tile<kRowsF16, kColumnsF16>(tile, rows_of(b, i0, z.m, z.m), columns_of(h, j0, z.n), steps, lds);
+        }
+        const int tc = Tile::template each_col<kVec>();
 #pragma unroll
-                for (int q = 0; q < 8; q += 4)
-                    if (have_of(col, q) > 0) ld_f32(r.master + (int64_t)row * r.cols + col + q, have_of(col, q), f.w + q);
-            }
-            return f;
-        },
-        [&](int tr, int tc, const float* v, Fetched& f) {
-            const int row = i0 + tr, col = j0 + tc;
-            if (row >= rows || col >= cols) return;
-            float x[8];
-            x_of(f.h, f.l, x);
-#pragma unroll
-            for (int k = 0; k < 8; ++k) x[k] = __builtin_fmaf((z.turned ? dc[k] : f.d) * un_x, x[k], v[k] * unscale);
-            if constexpr (kOut == kGoesOn) {
-#pragma unroll
-                for (int k = 0; k < 8; ++k) x[k] *= a.s.x_next;
-                st_x(a.ws, r.h[(a.step + 1) & 1], r.l, (int64_t)row * r.cp + col, x);
-            } else {
-#pragma unroll
-                for (int q = 0; q < 8; q += 4) {
-                    const int have = have_of(col, q);
-                    if (have <= 0) break;
-                    const int64_t e = (int64_t)row * r.cols + col + q;
-                    if constexpr (kOut == kToUpdate) {
-                        if (a.update_dtype == FP_DTYPE_F32) st_f32(static_cast<float*>(r.update) + e, have, x + q);
-                        else st_16bit(static_cast<uint16_t*>(r.update) + e, have,
-                                      a.update_dtype == FP_DTYPE_F16 ? f16x4(x + q) : f32x4_to_bf16(x + q));
-                    } else {
-                        float* w = f.w + q;
-                        if (!skip) {
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) w[k] = (float)(decay * (double)w[k] - rate * (double)x[q + k]);
-                            st_f32(r.master + e, have, w);
-                        }
-                        if (r.copy != nullptr)
-                            st_16bit(static_cast<uint16_t*>(r.copy) + e, have,
-                                     a.copy_dtype == FP_DTYPE_F16 ? f16x4(w) : f32x4_to_bf16(w));
-                    }
-                }
-            }
-        });
+        for (int k = 0; k < kVec; ++k) dc[k] = !skip && z.turned && tc < cols && j0 + tc + k < z.m ? d[j0 + tc + k] * un_x : 0.0f;
+    };
+    if constexpr (kEarly) {
+        struct XD {
+            OldX x;
+            Row d;
+        };
+        auto early = Tile::template fetch_early<kPer, kVec>(fetch_w);
+        multiply();
+        tile.template each<kPer, kVec>(
+            lds, [&](int tr, int tc) { return XD{fetch_x(tr, tc), fetch_d(tr, tc)}; },
+            [&](int tr, int tc, const float* v, const XD& f, OldW& w) { leave(tr, tc, v, f.d, f.x, w.w); }, early);
+    } else {
+        struct All {
+            OldX x;
+            OldW w;
+            Row d;
+        };
+        multiply();
+        tile.template each<kPer, kVec>(
+            lds, [&](int tr, int tc) { return All{fetch_x(tr, tc), fetch_w(tr, tc), fetch_d(tr, tc)}; },
+            [&](int tr, int tc, const float* v, All& f) { leave(tr, tc, v, f.d, f.x, f.w.w); });
+    }
 }
 
 // ---------------------------------------------------------------- small matrices
@@ -743,36 +810,18 @@ __global__ __launch_bounds__(kSmallThreads, 2) void small_kernel(const MuonArgs 
     }
 }
 
-// Launches a kernel over the argument block's tiles.  Beyond 64 KiB, LDS is asked
-// for once per kernel and device.
-template <auto kKernel, class... More>
-hipError_t launch(const MuonArgs& a, int threads, unsigned lds, hipStream_t s, const More&... more) {
-    if (lds > 65536u) {
-        static std::atomic<uint64_t> asked{0};
-        int device = 0;
-        hipError_t e = hipGetDevice(&device);
-        if (e != hipSuccess) return e;
-        const uint64_t bit = 1ull << (device & 63);
-        if (!(asked.load() & bit)) {
-            e = hipFuncSetAttribute(reinterpret_cast<const void*>(kKernel), hipFuncAttributeMaxDynamicSharedMemorySize, (int)kMaxLds);
-            if (e != hipSuccess) return e;
-            asked.fetch_or(bit);
-        }
-    }
-    kKernel<<<(unsigned)a.n_tiles, threads, lds, s>>>(a, more...);
-    return hipGetLastError();
-}
-
 }  // namespace
 
 hipError_t launch_muon_moment(const MuonArgs& a, hipStream_t s) {
-#define FP_MOMENT(G) (a.momentum != nullptr ? launch<moment_kernel<G, true>>(a, 256, 0, s) : launch<moment_kernel<G, false>>(a, 256, 0, s))
+#define FP_MOMENT(G) (a.momentum != nullptr ? launch<moment_kernel<G, true>>((unsigned)a.n_tiles, 256, 0, s, a) : launch<moment_kernel<G, false>>((unsigned)a.n_tiles, 256, 0, s, a))
     return a.grad_dtype == FP_DTYPE_F32 ? FP_MOMENT(FP_DTYPE_F32) : a.grad_dtype == FP_DTYPE_BF16 ? FP_MOMENT(FP_DTYPE_BF16) : FP_MOMENT(FP_DTYPE_F16);
 #undef FP_MOMENT
 }
 
+hipError_t launch_muon_norm(const MuonArgs& a, hipStream_t s) { return launch<norm_kernel>((unsigned)a.n_tiles, 256, 0, s, a); }
+
 hipError_t launch_muon_cast(const MuonArgs& a, hipStream_t s) {
-#define FP_CAST(G) (a.momentum != nullptr ? launch<cast_kernel<G, true>>(a, 256, 0, s) : launch<cast_kernel<G, false>>(a, 256, 0, s))
+#define FP_CAST(G) (a.momentum != nullptr ? launch<cast_kernel<G, true>>((unsigned)a.n_tiles, 256, 0, s, a) : launch<cast_kernel<G, false>>((unsigned)a.n_tiles, 256, 0, s, a))
     return a.grad_dtype == FP_DTYPE_F32 ? FP_CAST(FP_DTYPE_F32) : a.grad_dtype == FP_DTYPE_BF16 ? FP_CAST(FP_DTYPE_BF16) : FP_CAST(FP_DTYPE_F16);
 #undef FP_CAST
 }
@@ -782,20 +831,20 @@ hipError_t launch_muon_cast(const MuonArgs& a, hipStream_t s) {
                                                                                                 : CALL(Shape64Deep))
 
 hipError_t launch_muon_gram(const MuonArgs& a, int shape, hipStream_t s) {
-#define FP_CALL(S) launch<gram_kernel<S>>(a, S::kThreadsWg, S::kLds, s)
+#define FP_CALL(S) launch<gram_kernel<S>>((unsigned)a.n_tiles, S::kThreadsWg, S::kLds, s, a)
     return FP_BY_SHAPE(FP_CALL);
 #undef FP_CALL
 }
 
 hipError_t launch_muon_poly(const MuonArgs& a, int shape, hipStream_t s) {
-#define FP_CALL(S) launch<poly_kernel<S>>(a, S::kThreadsWg, S::kLds, s)
+#define FP_CALL(S) launch<poly_kernel<S>>((unsigned)a.n_tiles, S::kThreadsWg, S::kLds, s, a)
     return FP_BY_SHAPE(FP_CALL);
 #undef FP_CALL
 }
 
 template <int kOut>
 static hipError_t launch_next(const MuonArgs& a, int shape, hipStream_t s) {
-#define FP_CALL(S) launch<next_kernel<S, kOut>>(a, S::kThreadsWg, S::kLds, s)
+#define FP_CALL(S) launch<next_kernel<S, kOut>>((unsigned)a.n_tiles, S::kThreadsWg, S::kLds, s, a)
     return FP_BY_SHAPE(FP_CALL);
 #undef FP_CALL
 }
@@ -806,9 +855,9 @@ hipError_t launch_muon_next(const MuonArgs& a, int shape, bool last, bool to_wei
 
 template <int kTiles, int kSub>
 static hipError_t launch_small(const MuonArgs& a, const MuonSteps& steps, unsigned lds, hipStream_t s) {
-    return a.grad_dtype == FP_DTYPE_F32    ? launch<small_kernel<kTiles, kSub, FP_DTYPE_F32>>(a, kSmallThreads, lds, s, steps)
-           : a.grad_dtype == FP_DTYPE_BF16 ? launch<small_kernel<kTiles, kSub, FP_DTYPE_BF16>>(a, kSmallThreads, lds, s, steps)
-                                           : launch<small_kernel<kTiles, kSub, FP_DTYPE_F16>>(a, kSmallThreads, lds, s, steps);
+    return a.grad_dtype == FP_DTYPE_F32    ? launch<small_kernel<kTiles, kSub, FP_DTYPE_F32>>((unsigned)a.n_tiles, kSmallThreads, lds, s, a, steps)
+           : a.grad_dtype == FP_DTYPE_BF16 ? launch<small_kernel<kTiles, kSub, FP_DTYPE_BF16>>((unsigned)a.n_tiles, kSmallThreads, lds, s, a, steps)
+                                           : launch<small_kernel<kTiles, kSub, FP_DTYPE_F16>>((unsigned)a.n_tiles, kSmallThreads, lds, s, a, steps);
 }
 
 hipError_t launch_muon_small(const MuonArgs& a, const MuonSteps& steps, int tiles, unsigned lds, hipStream_t s) {

@@ -286,70 +286,75 @@ __global__ __launch_bounds__(256) void dequantize_kernel(const Mx4DequantArgs a,
 
 // ---------------------------------------------------------------- product
 
-// Up to eight neighbouring elements of the output, as bits.
+// kVec neighbouring elements of the output, 4 of fp32 or 8 of 16 bits, as they are
+// in memory: 16 bytes.
 struct Old {
-    uint32_t w[8];
+    uint4 w;
 };
 
-// The output's old values, where they are added to.
+// The output's old values, where they are added to; those past its end are 0.
+template <int kVec>
 __device__ __forceinline__ Old ld_old(const Mx4MatmulArgs& a, int64_t row, int64_t col) {
-    Old o;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) o.w[k] = 0u;
-    if (a.accumulate && row < a.m && col < a.n) {
-        const int64_t left = a.n - col, at = row * a.pitch + col;
-        const int have = left < 8 ? (int)left : 8;
-        if (a.dtype == FP_DTYPE_F32) {
-            const Eight<FP_DTYPE_F32> e = ld_eight<FP_DTYPE_F32>(a.out, at, have);
-#pragma unroll
-            for (int k = 0; k < 8; ++k) o.w[k] = e.w[k];
+    Old o = {make_uint4(0u, 0u, 0u, 0u)};
+    if (!a.accumulate || row >= a.m || col >= a.n) return o;
+    const int64_t left = a.n - col, at = row * a.pitch + col;
+    if constexpr (kVec == 4) {
+        const float* p = static_cast<const float*>(a.out) + at;
+        if (left >= 4) {
+            o.w = ld16u(p);
         } else {
-            const Eight<FP_DTYPE_BF16> e = ld_eight<FP_DTYPE_BF16>(a.out, at, have);
-#pragma unroll
-            for (int k = 0; k < 8; ++k) o.w[k] = bits_at<FP_DTYPE_BF16>(e, k);
+            const FP_GLOBAL uint32_t* q = gptr<uint32_t>((const void*)p);
+            o.w = make_uint4(q[0], left > 1 ? q[1] : 0u, left > 2 ? q[2] : 0u, 0u);
         }
+    } else {
+        const Eight<FP_DTYPE_BF16> e = ld_eight<FP_DTYPE_BF16>(a.out, at, left < 8 ? (int)left : 8);
+        o.w = make_uint4(e.w[0], e.w[1], e.w[2], e.w[3]);
     }
     return o;
 }
 
-// Stores eight neighbouring elements (row, col ..), those that the output has.
-__device__ __forceinline__ void st_out(const Mx4MatmulArgs& a, int64_t row, int64_t col, const float v[8], const Old& o) {
+// Stores kVec neighbouring elements (row, col ..), those that the output has.
+template <int kVec>
+__device__ __forceinline__ void st_out(const Mx4MatmulArgs& a, int64_t row, int64_t col, const float* v, const Old& o) {
     if (row >= a.m || col >= a.n) return;
     const int64_t left = a.n - col, at = row * a.pitch + col;
-    const int have = left < 8 ? (int)left : 8;
-    const bool half = a.dtype == FP_DTYPE_F16;
-    float f[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-        f[k] = v[k];
-        if (a.accumulate) f[k] += a.dtype == FP_DTYPE_F32 ? __uint_as_float(o.w[k]) : half ? f16_lo(o.w[k]) : bf16_lo(o.w[k]);
-    }
-    if (a.dtype == FP_DTYPE_F32) {
+    const uint32_t old[4] = {o.w.x, o.w.y, o.w.z, o.w.w};
+    if constexpr (kVec == 4) {
         float* p = static_cast<float*>(a.out) + at;
-        if (have == 8) {
-            put16u(p, bits_of(f));
-            put16u(p + 4, bits_of(f + 4));
+        float f[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) f[k] = a.accumulate ? v[k] + __uint_as_float(old[k]) : v[k];
+        if (left >= 4) {
+            st16u(p, bits_of(f));
+            return;
+        }
+#pragma unroll
+        for (int k = 0; k < 3; ++k)
+            if (k < left) gptr<float>((void*)p)[k] = f[k];
+    } else {
+        const bool half = a.dtype == FP_DTYPE_F16;
+        uint16_t* p = static_cast<uint16_t*>(a.out) + at;
+        uint32_t w[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            float lo = v[2 * k], hi = v[2 * k + 1];
+            if (a.accumulate) {
+                lo += half ? f16_lo(old[k]) : bf16_lo(old[k]);
+                hi += half ? f16_hi(old[k]) : bf16_hi(old[k]);
+            }
+            w[k] = half ? f16_pair(lo, hi) : bf16x2(lo, hi);
+        }
+        if (left >= 8) {
+            st16h(p, make_uint4(w[0], w[1], w[2], w[3]));
             return;
         }
 #pragma unroll
         for (int k = 0; k < 7; ++k)
-            if (k < have) gptr<float>((void*)p)[k] = f[k];
-        return;
+            if (k < left) gptr<uint16_t>((void*)p)[k] = (uint16_t)(w[k >> 1] >> (16 * (k & 1)));
     }
-    uint16_t* p = static_cast<uint16_t*>(a.out) + at;
-    uint32_t w[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) w[k] = half ? f16_pair(f[2 * k], f[2 * k + 1]) : bf16x2(f[2 * k], f[2 * k + 1]);
-    if (have == 8) {
-        st16h(p, make_uint4(w[0], w[1], w[2], w[3]));
-        return;
-    }
-#pragma unroll
-    for (int k = 0; k < 7; ++k)
-        if (k < have) gptr<uint16_t>((void*)p)[k] = (uint16_t)(w[k >> 1] >> (16 * (k & 1)));
 }
 
-template <class S>
+template <class S, int kVec>
 __global__ __launch_bounds__(S::kThreadsWg, S::kWavesSimd) void matmul_kernel(const Mx4MatmulArgs a) {
     extern __shared__ __align__(16) char lds[];
     const int t = die_tile(blockIdx.x, a.tiles_m * a.tiles_n);
@@ -364,9 +369,9 @@ __global__ __launch_bounds__(S::kThreadsWg, S::kWavesSimd) void matmul_kernel(co
     run_tile<kRowsFp4, kRowsFp4>(tile, {a.a + i0 * pitch, pitch, lm < S::kBM ? (int)lm : S::kBM, a.as + i0 * spitch},
                                  {a.b + j0 * pitch, pitch, ln < S::kBN ? (int)ln : S::kBN, a.bs + j0 * spitch},
                                  (int)(a.kp >> 8), lds);
-    tile.template each<S::kFM < 2 ? 1 : 2>(
-        lds, [&](int r, int c) { return ld_old(a, i0 + r, j0 + c); },
-        [&](int r, int c, const float* v, const Old& o) { st_out(a, i0 + r, j0 + c, v, o); });
+    tile.template each<2, kVec>(
+        lds, [&](int r, int c) { return ld_old<kVec>(a, i0 + r, j0 + c); },
+        [&](int r, int c, const float* v, const Old& o) { st_out<kVec>(a, i0 + r, j0 + c, v, o); });
 }
 
 // Products with few rows on one side (a: up to 16 kF; tokens of a generation):
@@ -455,16 +460,15 @@ using Shape256 = TileShape<256, 256, 128, 64>;
 using Shape128 = TileShape<128, 128, 64, 64>;
 using Shape64 = TileShape<64, 64, 32, 32>;
 
-template <class S>
+template <class S, int kVec>
 hipError_t run_matmul(Mx4MatmulArgs a, hipStream_t s) {
     a.tiles_m = (int32_t)ceil_div64(a.m, S::kBM);
     a.tiles_n = (int32_t)ceil_div64(a.n, S::kBN);
-    if (S::kLdsFp4 > 65536) {
-        const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(matmul_kernel<S>), hipFuncAttributeMaxDynamicSharedMemorySize, S::kLdsFp4);
-        if (e != hipSuccess) return e;
-    }
-    matmul_kernel<S><<<(unsigned)(a.tiles_m * a.tiles_n), S::kThreadsWg, S::kLdsFp4, s>>>(a);
-    return hipGetLastError();
+    return launch<matmul_kernel<S, kVec>>((unsigned)(a.tiles_m * a.tiles_n), S::kThreadsWg, S::kLdsFp4, s, a);
+}
+template <class S>
+hipError_t run_matmul(const Mx4MatmulArgs& a, hipStream_t s) {
+    return a.dtype == FP_DTYPE_F32 ? run_matmul<S, 4>(a, s) : run_matmul<S, 8>(a, s);
 }
 
 // Tiles across and down: the padding of a form that is wanted is written too.
