@@ -58,20 +58,27 @@ struct MuonSteps {
     float c[FP_MUON_MAX_STEPS][3];
 };
 
+// What every kernel takes.  Arguments lie in host memory: the fewer lines, the
+// sooner a small product starts.
 struct MuonArgs {
+    const MatTile* tiles;
     const MuonRec* recs;
-    const void* const* grads;
     char* ws;
-    float* momentum;          // null: the gradients themselves are orthogonalised
     const int32_t* found_inf;
+    MuonScale s;
+    float ca, cb, cc;         // the iteration's coefficients
+    int32_t step;             // of the iteration: which h is read
+    int32_t n_tiles;
+    int32_t update_dtype, copy_dtype;
+};
+
+// What those that read the gradients or write the weights take besides.
+struct MuonMore {
+    const void* const* grads;
+    float* momentum;          // null: the gradients themselves are orthogonalised
     const double* g_coef;
     double eps;
-    int32_t grad_dtype, copy_dtype, update_dtype;
-    float ca, cb, cc;         // the iteration's coefficients
-    MuonScale s;
-    int32_t step;             // of the iteration: which h is read
-    const MatTile* tiles;
-    int32_t n_tiles;
+    int32_t grad_dtype;
     MuonGroup g[FP_MAX_GROUPS];
 };
 
@@ -104,14 +111,16 @@ inline bool is_small(int64_t rows, int64_t cols) {
     return small_tiles(rows, cols) <= kSmallTiles && small_lds(rows, cols) <= (160 << 10) - 512;
 }
 
-hipError_t launch_muon_small(const MuonArgs& a, const MuonSteps& steps, int tiles, unsigned lds, hipStream_t s);
-hipError_t launch_muon_moment(const MuonArgs& a, hipStream_t s);
-hipError_t launch_muon_norm(const MuonArgs& a, hipStream_t s);
-hipError_t launch_muon_cast(const MuonArgs& a, hipStream_t s);
+hipError_t launch_muon_small(const MuonArgs& a, const MuonMore& more, const MuonSteps& steps, int tiles, unsigned lds, hipStream_t s);
+hipError_t launch_muon_moment(const MuonArgs& a, const MuonMore& more, hipStream_t s);
+hipError_t launch_muon_norm(const MuonArgs& a, double eps, hipStream_t s);
+hipError_t launch_muon_cast(const MuonArgs& a, const MuonMore& more, hipStream_t s);
 hipError_t launch_muon_gram(const MuonArgs& a, int shape, hipStream_t s);
 hipError_t launch_muon_poly(const MuonArgs& a, int shape, hipStream_t s);
-// last: the matrix leaves, as update (to_weights 0) or into the weights.
-hipError_t launch_muon_next(const MuonArgs& a, int shape, bool last, bool to_weights, hipStream_t s);
+// The matrix goes on, or (the iteration's last) leaves as update or, where there
+// are weights to change, into them.
+hipError_t launch_muon_next(const MuonArgs& a, int shape, hipStream_t s);
+hipError_t launch_muon_last(const MuonArgs& a, const MuonMore* weights, int shape, hipStream_t s);
 
 // ---------------------------------------------------------------- MXFP4
 

@@ -344,7 +344,7 @@ fp_status create(int32_t n, const int64_t* rows, const int64_t* cols, const int3
         }
     }
     // A few small matrices beside a large one: its launches have room for them, and
-    // one of their own would come on top (24 matrices of 1 to 1400: 190 us, KKK with).
+    // one of their own would come on top (24 matrices of 1 to 1400: 190 us, 159 with).
     const bool apart = !any_large || few > kFewSmall;
     for (int32_t i = 0; i < n; ++i) {
         MuonRec& r = recs[(size_t)i];
@@ -520,11 +520,11 @@ fp_status plan_steps(int32_t steps, const double* coefs, std::vector<Step>* out)
     return FP_OK;
 }
 
-fp_status run(fp_muon* p, MuonArgs a, const std::vector<Step>& steps, bool to_weights, void* stream) {
+fp_status run(fp_muon* p, MuonArgs a, MuonMore more, const std::vector<Step>& steps, void* stream) {
     hipStream_t s = static_cast<hipStream_t>(stream);
     a.recs = p->recs();
-    a.grads = p->grads();
-    a.grad_dtype = p->grad_dtype;
+    more.grads = p->grads();
+    more.grad_dtype = p->grad_dtype;
     a.copy_dtype = p->copy_dtype;
     a.update_dtype = p->update_dtype;
     auto over = [&](const Run& r) {
@@ -544,17 +544,17 @@ fp_status run(fp_muon* p, MuonArgs a, const std::vector<Step>& steps, bool to_we
         }
         for (const Small& m : p->smalls) {
             over(m.run);
-            if ((e = launch_muon_small(a, it, m.tiles, m.lds, s)) != hipSuccess) return device_error(e, "small matrices' launch");
+            if ((e = launch_muon_small(a, more, it, m.tiles, m.lds, s)) != hipSuccess) return device_error(e, "small matrices' launch");
         }
     }
     for (const Batch& b : p->batches) {
         over(b.moment);
-        if ((e = launch_muon_moment(a, s)) != hipSuccess) return device_error(e, "momentum launch");
+        if ((e = launch_muon_moment(a, more, s)) != hipSuccess) return device_error(e, "momentum launch");
         over(b.norm);
-        if (b.norm.n > 0 && (e = launch_muon_norm(a, s)) != hipSuccess) return device_error(e, "norm launch");
+        if (b.norm.n > 0 && (e = launch_muon_norm(a, more.eps, s)) != hipSuccess) return device_error(e, "norm launch");
         over(b.cast);
         a.s = steps[0].s;
-        if ((e = launch_muon_cast(a, s)) != hipSuccess) return device_error(e, "cast launch");
+        if ((e = launch_muon_cast(a, more, s)) != hipSuccess) return device_error(e, "cast launch");
         for (size_t i = 0; i < steps.size(); ++i) {
             a.s = steps[i].s;
             a.ca = steps[i].a;
@@ -565,8 +565,9 @@ fp_status run(fp_muon* p, MuonArgs a, const std::vector<Step>& steps, bool to_we
             if ((e = launch_muon_gram(a, b.half_shape, s)) != hipSuccess) return device_error(e, "product launch");
             if ((e = launch_muon_poly(a, b.half_shape, s)) != hipSuccess) return device_error(e, "product launch");
             over(b.full);
-            if ((e = launch_muon_next(a, b.full_shape, i + 1 == steps.size(), to_weights, s)) != hipSuccess)
-                return device_error(e, "product launch");
+            if (i + 1 < steps.size()) e = launch_muon_next(a, b.full_shape, s);
+            else e = launch_muon_last(a, more.momentum != nullptr ? &more : nullptr, b.full_shape, s);
+            if (e != hipSuccess) return device_error(e, "product launch");
         }
     }
     return FP_OK;
@@ -619,10 +620,12 @@ extern "C" fp_status fp_muon_orthogonalize(fp_muon* muon, int32_t steps, const d
         if ((st = check_buffers(muon, nullptr, false, workspace)) != FP_OK) return st;
         if ((st = check_device(muon)) != FP_OK) return st;
         MuonArgs a;
+        MuonMore more;
         std::memset(&a, 0, sizeof a);
+        std::memset(&more, 0, sizeof more);
         a.ws = static_cast<char*>(workspace);
-        a.eps = eps;
-        return run(muon, a, it, false, stream);
+        more.eps = eps;
+        return run(muon, a, more, it, stream);
     });
 }
 
@@ -637,14 +640,16 @@ extern "C" fp_status fp_muon_step(fp_muon* muon, int32_t n_groups, const fp_muon
                        FP_MAX_GROUPS);
         if (hp == nullptr) return bad(FP_ERR_INVALID, "hparams is NULL");
         MuonArgs a;
+        MuonMore more;
         std::memset(&a, 0, sizeof a);
+        std::memset(&more, 0, sizeof more);
         for (int32_t g = 0; g < n_groups; ++g) {
             const fp_muon_hparams& h = hp[g];
             if (!std::isfinite(h.lr) || !std::isfinite(h.weight_decay) || !(h.beta >= 0.0 && h.beta < 1.0))
                 return bad(FP_ERR_RANGE, "group %d: lr and weight_decay must be finite, beta in [0, 1)", g);
             if (h.adjust < FP_MUON_ADJUST_NONE || h.adjust > FP_MUON_ADJUST_SHAPE)
                 return bad(FP_ERR_INVALID, "group %d: unknown adjust %d", g, h.adjust);
-            a.g[g] = {h.lr, h.beta, 1.0 - h.lr * h.weight_decay, h.nesterov != 0, h.adjust};
+            more.g[g] = {h.lr, h.beta, 1.0 - h.lr * h.weight_decay, h.nesterov != 0, h.adjust};
         }
         std::vector<Step> it;
         fp_status st = plan_steps(steps, coefs, &it);
@@ -654,10 +659,10 @@ extern "C" fp_status fp_muon_step(fp_muon* muon, int32_t n_groups, const fp_muon
         if ((st = check_buffers(muon, momentum, true, workspace)) != FP_OK) return st;
         if ((st = check_device(muon)) != FP_OK) return st;
         a.ws = static_cast<char*>(workspace);
-        a.eps = eps;
-        a.momentum = momentum;
         a.found_inf = found_inf;
-        a.g_coef = grad_coef;
-        return run(muon, a, it, true, stream);
+        more.eps = eps;
+        more.momentum = momentum;
+        more.g_coef = grad_coef;
+        return run(muon, a, more, it, stream);
     });
 }

@@ -97,16 +97,16 @@ __device__ __forceinline__ uint2 f16x4(const float f[4]) { return make_uint2(f16
 // One chunk of one matrix: the momentum m' = beta m + (1 - beta) k g, in fp64
 // rounded once, and the sum of u^2 in fp64, in an order of its own.
 template <int kGrad, bool kStep>
-__global__ __launch_bounds__(256) void moment_kernel(const MuonArgs a) {
+__global__ __launch_bounds__(256) void moment_kernel(const MuonArgs a, const MuonMore b) {
     __shared__ double lds[4];
     if (kStep && skipped(a)) return;
     const MatTile t = a.tiles[blockIdx.x];
     const MuonRec& r = a.recs[t.mat];
-    const void* grad = a.grads[t.mat];
+    const void* grad = b.grads[t.mat];
     const int64_t n = (int64_t)r.rows * r.cols;
     const int64_t from = r.chunk * t.ti, to = from + r.chunk < n ? from + r.chunk : n;
-    const MuonGroup& hp = a.g[kStep ? r.group : 0];
-    const double k = kStep && a.g_coef != nullptr ? *a.g_coef : 1.0;
+    const MuonGroup& hp = b.g[kStep ? r.group : 0];
+    const double k = kStep && b.g_coef != nullptr ? *b.g_coef : 1.0;
     const double mine = kStep ? (1.0 - hp.beta) * k : 1.0;
     double sum = 0.0;
     constexpr int kAtOnce = 4;  // loads under way per lane
@@ -117,7 +117,7 @@ __global__ __launch_bounds__(256) void moment_kernel(const MuonArgs a) {
             const int64_t e = e0 + 1024 * i;
             if (e >= to) continue;
             grad4<kGrad>(grad, e, to - e < 4 ? (int)(to - e) : 4, g[i]);
-            if constexpr (kStep) f32x4_of(get16(a.momentum + r.offset + e), m[i]);  // room up to the next multiple of 32
+            if constexpr (kStep) f32x4_of(get16(b.momentum + r.offset + e), m[i]);  // room up to the next multiple of 32
         }
 #pragma unroll
         for (int i = 0; i < kAtOnce; ++i) {
@@ -131,7 +131,7 @@ __global__ __launch_bounds__(256) void moment_kernel(const MuonArgs a) {
                     m[i][q] = (float)(hp.beta * (double)m[i][q] + mine * (double)g[i][q]);
                     u[q] = hp.nesterov ? hp.beta * (double)m[i][q] + mine * (double)g[i][q] : (double)m[i][q];
                 }
-                st_f32(a.momentum + r.offset + e, have, m[i]);
+                st_f32(b.momentum + r.offset + e, have, m[i]);
             } else {
 #pragma unroll
                 for (int q = 0; q < 4; ++q) u[q] = (double)g[i][q];
@@ -180,7 +180,7 @@ __device__ __forceinline__ void st_f16(void* p, const float x[8]) {
 
 // Each matrix's 1 / (|U| + eps), behind its partial sums, where those are more
 // than the cast kernel's waves add up themselves.
-__global__ __launch_bounds__(256) void norm_kernel(const MuonArgs a) {
+__global__ __launch_bounds__(256) void norm_kernel(const MuonArgs a, const double eps) {
     __shared__ double lds[4];
     if (skipped(a)) return;
     const MuonRec& r = a.recs[a.tiles[blockIdx.x].mat];
@@ -188,14 +188,14 @@ __global__ __launch_bounds__(256) void norm_kernel(const MuonArgs a) {
     double sum = 0.0;
     for (int i = threadIdx.x; i < r.chunks; i += 256) sum += part[i];
     sum = sum256(sum, lds);
-    if (threadIdx.x == 0) part[r.chunks] = 1.0 / (sqrt(sum) + a.eps);
+    if (threadIdx.x == 0) part[r.chunks] = 1.0 / (sqrt(sum) + eps);
 }
 
 // ---------------------------------------------------------------- cast
 
 // kCastRows x kCastCols of the padded matrix: X = U / (|U| + eps).
 template <int kGrad, bool kStep>
-__global__ __launch_bounds__(256) void cast_kernel(const MuonArgs a) {
+__global__ __launch_bounds__(256) void cast_kernel(const MuonArgs a, const MuonMore b) {
     if (kStep && skipped(a)) return;
     const MatTile t = a.tiles[blockIdx.x];
     const MuonRec& r = a.recs[t.mat];
@@ -205,11 +205,11 @@ __global__ __launch_bounds__(256) void cast_kernel(const MuonArgs a) {
         scale = part[r.chunks];
     } else {
         const int lane = threadIdx.x & 63;
-        scale = 1.0 / (sqrt(wave_sum(lane < r.chunks ? part[lane] : 0.0)) + a.eps);
+        scale = 1.0 / (sqrt(wave_sum(lane < r.chunks ? part[lane] : 0.0)) + b.eps);
     }
-    const void* grad = a.grads[t.mat];
-    const MuonGroup& hp = a.g[kStep ? r.group : 0];
-    const double k = kStep && a.g_coef != nullptr ? *a.g_coef : 1.0;
+    const void* grad = b.grads[t.mat];
+    const MuonGroup& hp = b.g[kStep ? r.group : 0];
+    const double k = kStep && b.g_coef != nullptr ? *b.g_coef : 1.0;
     const double mine = kStep ? (1.0 - hp.beta) * k : 1.0;
     const int row0 = t.ti * kCastRows, col0 = t.tj * kCastCols;
     const int row = row0 + (threadIdx.x >> 4), col = col0 + (threadIdx.x & 15) * 8;
@@ -223,7 +223,7 @@ __global__ __launch_bounds__(256) void cast_kernel(const MuonArgs a) {
             const int64_t e = (int64_t)row * r.cols + col + q;
             float g[4], m[4];
             if (!kStep || hp.nesterov) grad4<kGrad>(grad, e, have, g);
-            if constexpr (kStep) ld_f32(a.momentum + r.offset + e, have, m);
+            if constexpr (kStep) ld_f32(b.momentum + r.offset + e, have, m);
 #pragma unroll
             for (int j = 0; j < 4; ++j)
                 if (j < have) {
@@ -385,8 +385,8 @@ enum { kGoesOn = 0, kToUpdate = 1, kToWeights = 2 };
 
 // X <- (a + D) X + R X_h, in the matrix's own orientation: B X of a wide
 // matrix, X B of a tall one.
-template <class S, int kOut>
-__global__ __launch_bounds__(S::kThreadsWg, S::kWavesSimd) void next_kernel(const MuonArgs a) {
+template <class S, int kOut, class More>
+__device__ __forceinline__ void next_tile(const MuonArgs& a, const More& more) {
     extern __shared__ __align__(16) char lds[];
     const MatTile t = a.tiles[blockIdx.x];
     if (t.mat < 0) return;
@@ -401,8 +401,12 @@ __global__ __launch_bounds__(S::kThreadsWg, S::kWavesSimd) void next_kernel(cons
     const float next = kOut == kGoesOn ? a.s.x_next : 1.0f;
     const float un_x = a.s.un_x * next, unscale = a.s.un_bx * next;
     const FP_GLOBAL float* d = gptr<float>((const void*)(a.ws + r.db));
-    const double rate = kOut == kToWeights ? a.g[r.group].lr * adjust_of(a.g[r.group].adjust, r.rows, r.cols) : 0.0;
-    const double decay = a.g[r.group].decay;
+    double rate = 0.0, decay = 1.0;
+    if constexpr (kOut == kToWeights) {
+        const MuonGroup& hp = more.g[r.group];
+        rate = hp.lr * adjust_of(hp.adjust, r.rows, r.cols);
+        decay = hp.decay;
+    }
     const int rows = (kOut == kGoesOn ? r.rp : r.rows) - i0, cols = (kOut == kGoesOn ? r.cp : r.cols) - j0;
     const int64_t base = 2 * ((int64_t)i0 * r.cp + j0);         // of the tile, in X's parts
     const int64_t out = (int64_t)i0 * r.cols + j0;              // in the matrix
@@ -514,6 +518,15 @@ __global__ __launch_bounds__(S::kThreadsWg, S::kWavesSimd) void next_kernel(cons
     }
 }
 
+template <class S, int kOut>
+__global__ __launch_bounds__(S::kThreadsWg, S::kWavesSimd) void next_kernel(const MuonArgs a) {
+    next_tile<S, kOut>(a, 0);
+}
+template <class S>
+__global__ __launch_bounds__(S::kThreadsWg, S::kWavesSimd) void weights_kernel(const MuonArgs a, const MuonMore b) {
+    next_tile<S, kToWeights>(a, b);
+}
+
 // ---------------------------------------------------------------- small matrices
 
 __device__ __forceinline__ void put8_lds(char* p, float a, float b, float c, float d) {
@@ -528,20 +541,20 @@ __device__ __forceinline__ void put8_lds(char* p, float a, float b, float c, flo
 // LDS has h, A and B, with rows 16 bytes longer than their elements, so that the
 // 16 rows of a fragment sit in different banks.  A wave works on blocks of kSub x
 // kSub tiles of 16 x 16: 2 x 2, four products for four fragments, where LDS reads
-// bound a step (128 x 128 with 1 x 1: 11 us a step, with 2 x 2 KKK), 1 x 1 for the
-// smallest, whose steps are all latency and want every wave (32 x 48: LLL a step,
+// bound a step (128 x 128 with 1 x 1: 11 us a step, with 2 x 2 6.2), 1 x 1 for the
+// smallest, whose steps are all latency and want every wave (32 x 48: 1.25 us a step,
 // with 2 x 2 2.3).
 //
 // kTiles: tiles of X per wave.
 constexpr int kSmallWaves = kSmallThreads / 64;
 
 template <int kTiles, int kSub, int kGrad>
-__global__ __launch_bounds__(kSmallThreads, 2) void small_kernel(const MuonArgs a, const MuonSteps it) {
+__global__ __launch_bounds__(kSmallThreads, 2) void small_kernel(const MuonArgs a, const MuonMore b, const MuonSteps it) {
     extern __shared__ __align__(16) char lds[];
     __shared__ double sums[kSmallWaves];
     const int mat = a.tiles[blockIdx.x].mat;
     const MuonRec& r = a.recs[mat];
-    const bool step = a.momentum != nullptr, turned = r.rows > r.cols;
+    const bool step = b.momentum != nullptr, turned = r.rows > r.cols;
     const bool skip = step && skipped(a);
     const int m0 = turned ? r.cols : r.rows, n0 = turned ? r.rows : r.cols;
     const int m = (m0 + 31) & ~31, n = (n0 + 31) & ~31;
@@ -555,8 +568,8 @@ __global__ __launch_bounds__(kSmallThreads, 2) void small_kernel(const MuonArgs 
     const int g = lane >> 4, j = lane & 15;
     constexpr int kBlock = 16 * kSub;
     const int across = n / kBlock, blocks = m / kBlock * across;
-    const MuonGroup& hy = a.g[r.group];
-    const void* grad = a.grads[mat];
+    const MuonGroup& hy = b.g[r.group];
+    const void* grad = b.grads[mat];
 
     // The lane's four elements of its tile i: row `row` of X, columns col ..
     // col + 3; `have` of them exist.  In memory they are neighbours, or a row
@@ -611,21 +624,21 @@ __global__ __launch_bounds__(kSmallThreads, 2) void small_kernel(const MuonArgs 
     float x[kTiles][4];
     double sum = 0.0;
     if (!skip) {
-        const double k = step && a.g_coef != nullptr ? *a.g_coef : 1.0;
+        const double k = step && b.g_coef != nullptr ? *b.g_coef : 1.0;
         const double beta = step ? hy.beta : 0.0, mine = step ? (1.0 - beta) * k : 1.0;
 #pragma unroll
         for (int i0 = 0; i0 < kTiles; i0 += kGroup) {
             float u[kGroup][4], w[kGroup][4];
             if constexpr (kGrad == FP_DTYPE_F32) ld(gptr<float>(grad), same, i0, u);
             else ld(gptr<uint16_t>(grad), [](uint16_t v) { return kGrad == FP_DTYPE_BF16 ? bf16_lo(v) : f16_lo(v); }, i0, u);
-            if (step) ld(gptr<float>((const void*)(a.momentum + r.offset)), same, i0, w);
+            if (step) ld(gptr<float>((const void*)(b.momentum + r.offset)), same, i0, w);
 #pragma unroll
             for (int i = 0; i < kGroup; ++i) {
                 const At p = at(i0 + i);
                 if (step) {
 #pragma unroll
                     for (int q = 0; q < 4; ++q) w[i][q] = (float)(beta * (double)w[i][q] + mine * (double)u[i][q]);
-                    st(gptr<float>((void*)(a.momentum + r.offset)), p, w[i]);
+                    st(gptr<float>((void*)(b.momentum + r.offset)), p, w[i]);
                 }
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
@@ -644,7 +657,7 @@ __global__ __launch_bounds__(kSmallThreads, 2) void small_kernel(const MuonArgs 
         sum = 0.0;
 #pragma unroll
         for (int w = 0; w < kSmallWaves; ++w) sum += sums[w];
-        const double scale = 1.0 / (sqrt(sum) + a.eps);
+        const double scale = 1.0 / (sqrt(sum) + b.eps);
 #pragma unroll
         for (int i = 0; i < kTiles; ++i)
 #pragma unroll
@@ -812,18 +825,24 @@ __global__ __launch_bounds__(kSmallThreads, 2) void small_kernel(const MuonArgs 
 
 }  // namespace
 
-hipError_t launch_muon_moment(const MuonArgs& a, hipStream_t s) {
-#define FP_MOMENT(G) (a.momentum != nullptr ? launch<moment_kernel<G, true>>((unsigned)a.n_tiles, 256, 0, s, a) : launch<moment_kernel<G, false>>((unsigned)a.n_tiles, 256, 0, s, a))
-    return a.grad_dtype == FP_DTYPE_F32 ? FP_MOMENT(FP_DTYPE_F32) : a.grad_dtype == FP_DTYPE_BF16 ? FP_MOMENT(FP_DTYPE_BF16) : FP_MOMENT(FP_DTYPE_F16);
-#undef FP_MOMENT
+hipError_t launch_muon_moment(const MuonArgs& a, const MuonMore& b, hipStream_t s) {
+#define FP_CALL(G)                                                                                  \
+    (b.momentum != nullptr ? launch<moment_kernel<G, true>>((unsigned)a.n_tiles, 256, 0, s, a, b) \
+                           : launch<moment_kernel<G, false>>((unsigned)a.n_tiles, 256, 0, s, a, b))
+    return b.grad_dtype == FP_DTYPE_F32 ? FP_CALL(FP_DTYPE_F32) : b.grad_dtype == FP_DTYPE_BF16 ? FP_CALL(FP_DTYPE_BF16) : FP_CALL(FP_DTYPE_F16);
+#undef FP_CALL
 }
 
-hipError_t launch_muon_norm(const MuonArgs& a, hipStream_t s) { return launch<norm_kernel>((unsigned)a.n_tiles, 256, 0, s, a); }
+hipError_t launch_muon_norm(const MuonArgs& a, double eps, hipStream_t s) {
+    return launch<norm_kernel>((unsigned)a.n_tiles, 256, 0, s, a, eps);
+}
 
-hipError_t launch_muon_cast(const MuonArgs& a, hipStream_t s) {
-#define FP_CAST(G) (a.momentum != nullptr ? launch<cast_kernel<G, true>>((unsigned)a.n_tiles, 256, 0, s, a) : launch<cast_kernel<G, false>>((unsigned)a.n_tiles, 256, 0, s, a))
-    return a.grad_dtype == FP_DTYPE_F32 ? FP_CAST(FP_DTYPE_F32) : a.grad_dtype == FP_DTYPE_BF16 ? FP_CAST(FP_DTYPE_BF16) : FP_CAST(FP_DTYPE_F16);
-#undef FP_CAST
+hipError_t launch_muon_cast(const MuonArgs& a, const MuonMore& b, hipStream_t s) {
+#define FP_CALL(G)                                                                                \
+    (b.momentum != nullptr ? launch<cast_kernel<G, true>>((unsigned)a.n_tiles, 256, 0, s, a, b) \
+                           : launch<cast_kernel<G, false>>((unsigned)a.n_tiles, 256, 0, s, a, b))
+    return b.grad_dtype == FP_DTYPE_F32 ? FP_CALL(FP_DTYPE_F32) : b.grad_dtype == FP_DTYPE_BF16 ? FP_CALL(FP_DTYPE_BF16) : FP_CALL(FP_DTYPE_F16);
+#undef FP_CALL
 }
 
 #define FP_BY_SHAPE(CALL)                                                                                            \
@@ -842,29 +861,34 @@ hipError_t launch_muon_poly(const MuonArgs& a, int shape, hipStream_t s) {
 #undef FP_CALL
 }
 
-template <int kOut>
-static hipError_t launch_next(const MuonArgs& a, int shape, hipStream_t s) {
-#define FP_CALL(S) launch<next_kernel<S, kOut>>((unsigned)a.n_tiles, S::kThreadsWg, S::kLds, s, a)
+hipError_t launch_muon_next(const MuonArgs& a, int shape, hipStream_t s) {
+#define FP_CALL(S) launch<next_kernel<S, kGoesOn>>((unsigned)a.n_tiles, S::kThreadsWg, S::kLds, s, a)
     return FP_BY_SHAPE(FP_CALL);
 #undef FP_CALL
 }
 
-hipError_t launch_muon_next(const MuonArgs& a, int shape, bool last, bool to_weights, hipStream_t s) {
-    return !last ? launch_next<kGoesOn>(a, shape, s) : to_weights ? launch_next<kToWeights>(a, shape, s) : launch_next<kToUpdate>(a, shape, s);
+hipError_t launch_muon_last(const MuonArgs& a, const MuonMore* weights, int shape, hipStream_t s) {
+#define FP_WEIGHTS(S) launch<weights_kernel<S>>((unsigned)a.n_tiles, S::kThreadsWg, S::kLds, s, a, *weights)
+#define FP_UPDATE(S) launch<next_kernel<S, kToUpdate>>((unsigned)a.n_tiles, S::kThreadsWg, S::kLds, s, a)
+    return weights != nullptr ? FP_BY_SHAPE(FP_WEIGHTS) : FP_BY_SHAPE(FP_UPDATE);
+#undef FP_WEIGHTS
+#undef FP_UPDATE
 }
+#undef FP_BY_SHAPE
 
 template <int kTiles, int kSub>
-static hipError_t launch_small(const MuonArgs& a, const MuonSteps& steps, unsigned lds, hipStream_t s) {
-    return a.grad_dtype == FP_DTYPE_F32    ? launch<small_kernel<kTiles, kSub, FP_DTYPE_F32>>((unsigned)a.n_tiles, kSmallThreads, lds, s, a, steps)
-           : a.grad_dtype == FP_DTYPE_BF16 ? launch<small_kernel<kTiles, kSub, FP_DTYPE_BF16>>((unsigned)a.n_tiles, kSmallThreads, lds, s, a, steps)
-                                           : launch<small_kernel<kTiles, kSub, FP_DTYPE_F16>>((unsigned)a.n_tiles, kSmallThreads, lds, s, a, steps);
+static hipError_t launch_small(const MuonArgs& a, const MuonMore& b, const MuonSteps& steps, unsigned lds, hipStream_t s) {
+#define FP_CALL(G) launch<small_kernel<kTiles, kSub, G>>((unsigned)a.n_tiles, kSmallThreads, lds, s, a, b, steps)
+    return b.grad_dtype == FP_DTYPE_F32 ? FP_CALL(FP_DTYPE_F32) : b.grad_dtype == FP_DTYPE_BF16 ? FP_CALL(FP_DTYPE_BF16) : FP_CALL(FP_DTYPE_F16);
+#undef FP_CALL
 }
 
-hipError_t launch_muon_small(const MuonArgs& a, const MuonSteps& steps, int tiles, unsigned lds, hipStream_t s) {
-    return tiles <= 2   ? launch_small<2, 1>(a, steps, lds, s)
-           : tiles <= 4 ? launch_small<4, 1>(a, steps, lds, s)
-           : tiles <= 8 ? launch_small<8, 2>(a, steps, lds, s)
-                        : launch_small<kSmallTiles, 2>(a, steps, lds, s);
+hipError_t launch_muon_small(const MuonArgs& a, const MuonMore& b, const MuonSteps& steps, int tiles, unsigned lds,
+                             hipStream_t s) {
+    return tiles <= 2   ? launch_small<2, 1>(a, b, steps, lds, s)
+           : tiles <= 4 ? launch_small<4, 1>(a, b, steps, lds, s)
+           : tiles <= 8 ? launch_small<8, 2>(a, b, steps, lds, s)
+                        : launch_small<kSmallTiles, 2>(a, b, steps, lds, s);
 }
 
 }  // namespace fpk
