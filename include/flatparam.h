@@ -820,9 +820,10 @@ fp_status fp_mx8_dequantize(int64_t n, int32_t root, const uint8_t* codes, const
  *   fp_muon_orthogonalize writes, or NULL.  At least one of master and
  *   updates.  Weights, copies and updates overlap nothing else.
  * fp_muon_info: partition as in fp_params_info, of the momentum;
- *   workspace_bytes: of every call, 6 bytes per element and 4 per element of A of the matrices
- *   that are worked on together (up to 2 GiB, or the largest matrix's), with
- *   both sides counted in multiples of 64.
+ *   workspace_bytes: of every call, 6 bytes per element and 4 per element of A,
+ *   with both sides counted in multiples of 64, of the matrices that are worked
+ *   on together (2 GiB of them, the last one over that edge included).  Small
+ *   matrices alone (32768 elements, as 160 x 160 or 32 x 1024) need none.
  * Creation, destruction, fp_muon_set_grads and devices as for fp_params.
  * Errors: FP_ERR_RANGE, FP_ERR_INVALID, FP_ERR_ALIGN, FP_ERR_DEVICE. */
 #define FP_MUON_ADJUST_NONE 0

@@ -1372,7 +1372,7 @@ def mx4_quantize(src, codes=None, scales=None, codes_t=None, scales_t=None, *, r
     x, dtype, r, c, pitch = _matrix(src, "src")
     if not rows and not transposed:
         raise ValueError("neither the rows' nor the columns' form is wanted")
-    got, ptrs = (), ()
+    got, ptrs, given = (), (), []
     for want, held, high, wide, name in ((rows, (codes, scales), r, c, "rows' form"),
                                          (transposed, (codes_t, scales_t), c, r, "columns' form")):
         if not want:
@@ -1388,9 +1388,12 @@ def mx4_quantize(src, codes=None, scales=None, codes_t=None, scales_t=None, *, r
                 raise ValueError("codes and scales go together")
             _one_device(src, *held)
             got += held
+            given += held
             ptrs += _mx4_form(*held, high, wide, name)
     _on_device(src.device, lib().fp_mx4_quantize, r, c, pitch, dtype, x, *ptrs, seed is not None,
                0 if seed is None else int(seed) & 0xFFFFFFFFFFFFFFFF)
+    if given:
+        _bump_versions(_version_holders(given))
     return got
 
 
@@ -1409,6 +1412,7 @@ def mx4_dequantize(codes, scales, cols: int, dst=None, *, dtype=None):
     if (rows, width) != (r, c):
         raise ValueError(f"dst has shape {(rows, width)}, expected {(r, c)}")
     _on_device(codes.device, lib().fp_mx4_dequantize, r, c, *ptrs, did, x, pitch)
+    _bump_versions(_version_holders([dst]))
     return dst
 
 
@@ -1425,7 +1429,8 @@ def mx4_matmul(a, b, out=None, *, accumulate: bool = False, dtype=None):
     if k2 != k:
         raise ValueError(f"rows of {k} and {k2} elements (padded)")
     ap, bp = _mx4_form(ac, asc, m, k, "a"), _mx4_form(bc, bsc, n, k, "b")
-    if out is None:
+    given = out is not None
+    if not given:
         if accumulate:
             raise ValueError("accumulate needs out")
         torch = _torch()
@@ -1437,6 +1442,8 @@ def mx4_matmul(a, b, out=None, *, accumulate: bool = False, dtype=None):
     if (rows, cols) != (m, n):
         raise ValueError(f"out has shape {(rows, cols)}, expected {(m, n)}")
     _on_device(ac.device, lib().fp_mx4_matmul, m, n, k, *ap, *bp, did, x, pitch, accumulate)
+    if given:
+        _bump_versions(_version_holders([out]))
     return out
 
 

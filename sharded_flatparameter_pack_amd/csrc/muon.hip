@@ -61,10 +61,8 @@ struct fp_muon {
     void* dev = nullptr;               // records, gradient table, tile table
     void* staging = nullptr;           // pinned, of the gradient table's uploads
     hipEvent_t uploaded = nullptr;
-    std::mutex mu;                     // guards the fields below
-    std::vector<Span> read;            // gradients
-    const void* checked[2] = {};       // momentum and workspace that last passed the overlap checks
-    bool have_checked = false;
+    std::mutex mu;                     // guards the gradients: their table's upload and
+    std::vector<Span> read;            // where they lie
 
     const MuonRec* recs() const { return static_cast<const MuonRec*>(dev); }
     const void** grads() const { return reinterpret_cast<const void**>(static_cast<char*>(dev) + sizeof(MuonRec) * (size_t)n); }
@@ -161,6 +159,12 @@ double finish(const std::vector<MuonRec>& recs, const Batch& b, int shape, bool 
         runs.push_back({(half ? n : m) / 64, half ? t * (t + 1) / 2 : t * ceil_div64(n, kTileSide[shape])});
     }
     std::sort(runs.rbegin(), runs.rend());
+    size_t kept = 0;  // runs of as many steps are one
+    for (size_t i = 1; i < runs.size(); ++i) {
+        if (runs[i].first == runs[kept].first) runs[kept].second += runs[i].second;
+        else runs[++kept] = runs[i];
+    }
+    runs.resize(kept + 1);
     constexpr int kCus = 256;
     double load[kCus] = {};
     int64_t held[kCus] = {};
@@ -439,7 +443,6 @@ fp_status set_grads(fp_muon* p, const void* const* grads, void* stream) {
         return device_error(e, "uploading the gradient table");
     if ((e = hipEventRecord(p->uploaded, s)) != hipSuccess) return device_error(e, "hipEventRecord");
     p->read = std::move(read);
-    p->have_checked = false;
     return FP_OK;
 }
 
@@ -451,14 +454,10 @@ fp_status check_buffers(fp_muon* p, const float* momentum, bool step, const void
     if (workspace == nullptr && p->workspace > 0) return bad(FP_ERR_INVALID, "workspace is NULL");
     if (!on(workspace, 256)) return bad(FP_ERR_ALIGN, "workspace is not 256-byte aligned");
     std::lock_guard<std::mutex> lock(p->mu);
-    if (p->have_checked && p->checked[0] == momentum && p->checked[1] == workspace) return FP_OK;
     const Span ws = span_of(workspace, p->workspace), mo = span_of(momentum, step ? 4 * p->partition : 0);
     if (meets_any(ws, p->written) || meets_any(ws, p->read)) return bad(FP_ERR_INVALID, "workspace overlaps one of the plan's tensors");
     if (meet(ws, mo)) return bad(FP_ERR_INVALID, "workspace overlaps momentum");
     if (meets_any(mo, p->written) || meets_any(mo, p->read)) return bad(FP_ERR_INVALID, "momentum overlaps one of the plan's tensors");
-    p->checked[0] = momentum;
-    p->checked[1] = workspace;
-    p->have_checked = true;
     return FP_OK;
 }
 

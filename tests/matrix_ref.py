@@ -22,14 +22,17 @@ def key_of(seed):
     return (z ^ (z >> 32)) & M32
 
 
-def dither(rows, cols, seed):
-    """The hash of every element's index: 32 bits."""
-    x = (np.arange(rows * cols, dtype=np.uint64) * np.uint64(0x9E3779B1) & np.uint64(M32)) ^ np.uint64(key_of(seed))
+def hashes(index, seed):
+    """The hash of elements' indices: 32 bits."""
+    x = (np.asarray(index).astype(np.uint64) * np.uint64(0x9E3779B1) & np.uint64(M32)) ^ np.uint64(key_of(seed))
     x ^= x >> np.uint64(16)
     x = x * np.uint64(0x6A09E667) & np.uint64(M32)
     x ^= x >> np.uint64(15)
-    x = x * np.uint64(0xBB67AE85) & np.uint64(M32)
-    return x.reshape(rows, cols)
+    return x * np.uint64(0xBB67AE85) & np.uint64(M32)
+
+
+def dither(rows, cols, seed):
+    return hashes(np.arange(rows * cols, dtype=np.uint64), seed).reshape(rows, cols)
 
 
 def quantize(x, d=None):

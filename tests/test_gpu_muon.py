@@ -188,6 +188,154 @@ def test_step(fp, gd, cd, nesterov, adjust, odd):
     assert bool((mom.cpu()[~used] == 3).all())
 
 
+# Matrices that one workgroup takes through everything, by what a wave of it holds; each list a plan of its own.
+SMALL = [[(1, 1), (1, 7), (5, 3), (16, 16), (32, 48), (48, 32), (64, 32)], [(64, 64), (64, 60), (33, 127), (128, 64), (1, 256)],
+         [(100, 90), (128, 128), (90, 130), (32, 500)], [(160, 160), (159, 131), (128, 256), (250, 100), (32, 1024), (1024, 1)]]
+
+
+@pytest.mark.parametrize("shapes", SMALL)
+@pytest.mark.parametrize("gd,cd,ud,odd", [("f32", None, "f32", 0), ("bf16", "bf16", "bf16", 1), ("f16", "f16", "f16", 3)])
+def test_small(fp, shapes, gd, cd, ud, odd):
+    flats, grads, master, copies = state(shapes, gd, cd, odd)
+    fu = torch.full((odd + sum(r * c + 3 for r, c in shapes) + 3,), 7.0, dtype=DT[ud], device=dev())
+    out, at = [], odd
+    for r, c in shapes:
+        out.append(fu[at:at + r * c].view(r, c))
+        at += r * c + 3
+    plan = fp.Muon(grads, master, copies, out)
+    assert plan.workspace_bytes == 0
+    ws, mom = plan.new_workspace(), plan.new_momentum()
+    plan.orthogonalize(ws)
+    for g, x, sh in zip(grads, out, shapes):
+        say("orthogonalize", sh, gd, ud)
+        assert rel(x.cpu(), ref.orthogonalize(g.cpu())) <= OFF + torch.finfo(DT[ud]).eps / 2
+    for nesterov in (True, False):
+        ms = [plan.tensor_slice(mom, i).cpu().view(sh) for i, sh in enumerate(shapes)]
+        before = [w.cpu().clone() for w in master]
+        plan.step(mom, ws, **{**HP, "nesterov": nesterov})
+        for i, sh in enumerate(shapes):
+            say("step", sh, gd, cd, nesterov)
+            m, w, x = ref.muon(grads[i].cpu(), ms[i], before[i], **{**HP, "nesterov": nesterov})
+            got_m = plan.tensor_slice(mom, i).cpu().view(sh).double()
+            assert bool(((got_m - m.double()).abs() <= 2.0 ** -23 * m.double().abs() + 2.0 ** -149).all())
+            rate = HP["lr"] * ref.adjust_of(sh, "rms")
+            assert float((master[i].cpu().double() - w).norm()) <= OFF * rate * float(x.norm()) + 2.0 ** -24 * float(w.norm())
+            if copies:
+                assert torch.equal(copies[i].cpu(), master[i].cpu().to(DT[cd]))
+    for f in (*flats, fu):
+        assert f is None or bool((gaps(f, shapes, odd) == 7).all())
+
+
+def test_many_small(fp):
+    """More small matrices than one launch takes, of sizes far apart."""
+    shapes = [(8 + i % 30, 8 + i % 23) for i in range(700)] + [(128, 100 + i) for i in range(20)]
+    grads = [gradient(r, c, i) for i, (r, c) in enumerate(shapes)]
+    out = [torch.empty(s, device=dev()) for s in shapes]
+    plan = fp.Muon([g.to(dev()) for g in grads], updates=out)
+    plan.orthogonalize(plan.new_workspace())
+    for g, x in zip(grads, out):
+        assert rel(x.cpu(), ref.orthogonalize(g)) <= OFF
+
+
+BIG = [(1300, 2050), (2300, 700), (512, 1408), (31, 40)]
+
+
+@pytest.mark.parametrize("gd,cd,odd", [("f32", "f16", 0), ("bf16", "bf16", 1), ("bf16", None, 0)])
+def test_step_of_large_matrices(fp, gd, cd, odd):
+    """Steps through the launches that a batch shares, one of them skipped; nothing is written outside the matrices, nor
+    behind the workspace."""
+    flats, grads, master, copies = state(BIG, gd, cd, odd)
+    plan = fp.Muon(grads, master, copies)
+    mom = plan.new_momentum()
+    whole = torch.full((plan.workspace_bytes + 256,), 0xA5, dtype=torch.uint8, device=dev())
+    step = plan.stepper(mom, whole[:plan.workspace_bytes], **HP, found_inf=(flag := torch.zeros(1, dtype=torch.int32, device=dev())))
+    for t in range(2):
+        ms = [plan.tensor_slice(mom, i).cpu().view(s) for i, s in enumerate(BIG)]
+        before = [w.cpu().clone() for w in master]
+        step()
+        for i, s in enumerate(BIG):
+            say("step", t, s, gd, cd)
+            m, w, x = ref.muon(grads[i].cpu(), ms[i], before[i], **HP)
+            got_m = plan.tensor_slice(mom, i).cpu().view(s).double()
+            assert bool(((got_m - m.double()).abs() <= 2.0 ** -23 * m.double().abs() + 2.0 ** -149).all())
+            rate = HP["lr"] * ref.adjust_of(s, "rms")
+            assert float((master[i].cpu().double() - w).norm()) <= OFF * rate * float(x.norm()) + 2.0 ** -24 * float(w.norm())
+            if copies:
+                assert torch.equal(copies[i].cpu(), master[i].cpu().to(DT[cd]))
+        if t == 0:
+            flag.fill_(1)
+            keep = [w.clone() for w in master], mom.clone()
+            for c in copies or ():
+                c.zero_()
+            grads[0][5, 6] = float("nan")
+            step()
+            assert all(torch.equal(a, b) for a, b in zip(master, keep[0])) and torch.equal(mom, keep[1])
+            assert all(torch.equal(c, w.to(c.dtype)) for c, w in zip(copies or (), master))
+            grads[0][5, 6] = 0
+            flag.zero_()
+    for f in flats:
+        assert f is None or bool((gaps(f, BIG, odd) == 7).all())
+    assert bool((whole[plan.workspace_bytes:] == 0xA5).all())
+
+
+def test_large_matrices_with_zeros_and_not_finite(fp):
+    g = [torch.zeros(500, 600), gradient(700, 500, 1), gradient(500, 700, 2), gradient(400, 420, 3)]
+    g[1][3, 4] = float("inf")
+    g[2][7, 0] = float("nan")
+    out = [torch.empty(t.shape, device=dev()) for t in g]
+    plan = fp.Muon([t.to(dev()) for t in g], updates=out)
+    plan.orthogonalize(plan.new_workspace())
+    assert bool((out[0] == 0).all())
+    assert bool(torch.isnan(out[1]).all()) and bool(torch.isnan(out[2]).all())
+    assert rel(out[3].cpu(), ref.orthogonalize(g[3])) <= OFF
+
+
+def test_more_than_one_batch(fp):
+    """Matrices whose workspace passes what one batch holds: bit for bit what each gives in a plan of its own."""
+    shapes = [(6000, 16000), (16000, 6000), (5990, 16001), (6000, 16000), (300, 500)]
+    grads = [(torch.randn(s, generator=torch.Generator(device=dev()).manual_seed(i), device=dev()) * 1e-3).bfloat16()
+             for i, s in enumerate(shapes)]
+    out = [torch.zeros(s, dtype=torch.bfloat16, device=dev()) for s in shapes]
+    plan = fp.Muon(grads, updates=out)
+    plan.orthogonalize(plan.new_workspace())
+    alone = 0
+    for g, x in zip(grads, out):
+        say("batch", tuple(g.shape))
+        y = torch.empty_like(x)
+        one = fp.Muon([g], updates=[y])
+        one.orthogonalize(one.new_workspace())
+        assert torch.equal(x, y)
+        alone += one.workspace_bytes
+    assert plan.workspace_bytes < alone
+    assert rel(out[4].cpu(), ref.orthogonalize(grads[4].cpu())) <= OFF + 2.0 ** -8
+
+
+@pytest.mark.parametrize("shape", [(2176, 1000001), (1000001, 2176)])
+def test_more_than_31_bits_of_elements(fp, shape):
+    """The iteration is a polynomial Q of A times X; Q comes from A in 64 bits, for parts of X far apart."""
+    say("orthogonalize", shape)
+    assert shape[0] * shape[1] > 1 << 31
+    g = torch.randn(shape, generator=torch.Generator(device=dev()).manual_seed(3), dtype=torch.bfloat16, device=dev())
+    x = torch.empty(shape, dtype=torch.float16, device=dev())
+    plan = fp.Muon([g], updates=[x])
+    plan.orthogonalize(plan.new_workspace())
+    tall = shape[0] > shape[1]
+    part = lambda t, lo, hi: (t[lo:hi].double().t() if tall else t[:, lo:hi].double())  # noqa: E731
+    m, n = min(shape), max(shape)
+    a = torch.zeros(m, m, dtype=torch.float64, device=dev())
+    for lo in range(0, n, 1 << 17):
+        p = part(g, lo, min(n, lo + (1 << 17))).contiguous()
+        a += p @ p.t().contiguous()
+    norm = float(a.diagonal().sum()) ** 0.5
+    a /= norm * norm
+    q = torch.eye(m, dtype=torch.float64, device=dev())
+    for ca, cb, cc in [ref.COEFS] * 5:
+        s = q @ a @ q.t().contiguous()
+        q = (ca * torch.eye(m, dtype=torch.float64, device=dev()) + cb * s + cc * (s @ s)) @ q
+    for lo in (0, 493447, 986895, n - 300):  # at 2^30 and 2^31 elements among them
+        assert rel(part(x, lo, lo + 300), q @ (part(g, lo, lo + 300).contiguous() / norm)) <= OFF + 2.0 ** -11, lo
+
+
 def test_steps_follow_the_formula(fp):
     """Several steps with changing gradients and rates, groups of their own hyperparameters."""
     shapes = [(40, 60), (60, 40), (30, 30)]
@@ -260,10 +408,36 @@ def test_repeatable_and_in_any_workspace(fp):
     assert all(torch.equal(a, b) for a, b in zip(out, first))
 
 
-def test_captured_step(fp):
+def test_two_streams_at_once(fp):
+    """Two plans with workspaces of their own on two streams beside each other."""
+    shapes = [(600, 900), (900, 300), (40, 50)]
+    grads = [[gradient(r, c, 5 + r + k).to(dev()) for r, c in shapes] for k in range(2)]
+    out = [[torch.empty(s, device=dev()) for s in shapes] for _ in range(2)]
+    plans = [fp.Muon(g, updates=o) for g, o in zip(grads, out)]
+    ws = [p.new_workspace() for p in plans]
+    want = []
+    for p, w, o in zip(plans, ws, out):
+        p.orthogonalize(w)
+        want.append([t.clone() for t in o])
+    streams = [torch.cuda.Stream() for _ in plans]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for o in out:
+            for t in o:
+                t.zero_()
+        torch.cuda.synchronize()
+        for p, w, s in zip(plans, ws, streams):
+            with torch.cuda.stream(s):
+                p.orthogonalize(w)
+                p.orthogonalize(w)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for o, v in zip(out, want) for a, b in zip(o, v))
+
+
+@pytest.mark.parametrize("shapes", [[(64, 96), (130, 50)], [(1200, 900), (300, 700), (20, 30)]])
+def test_captured_step(fp, shapes):
     """A step captured into a graph: every replay against an eager step from the same state, with new gradients and with
     eager work between the replays."""
-    shapes = [(64, 96), (130, 50)]
     _, grads, master, copies = state(shapes, "bf16", "bf16")
     plan = fp.Muon(grads, master, copies)
     mom, ws = plan.new_momentum(), plan.new_workspace()

@@ -289,6 +289,96 @@ def test_other_stream_and_graph(fp):
         assert torch.equal(out, want)
 
 
+@pytest.mark.parametrize("seed", [None, 7])
+def test_given_buffers_of_one_form(fp, seed):
+    """Either form alone into the caller's buffers, which count as changed in place."""
+    x = matrix(50, 300, "bf16", 3).to(dev())
+    want = fp.mx4_quantize(x, transposed=True, seed=seed)
+    rows, cols = fp.mx4_empty(50, 300, dev()), fp.mx4_empty(300, 50, dev())
+    before = [t._version for t in (*rows, *cols)]
+    assert fp.mx4_quantize(x, *rows, seed=seed) == rows
+    assert fp.mx4_quantize(x, None, None, *cols, rows=False, transposed=True, seed=seed) == cols
+    for got, w in zip((*rows, *cols), want):
+        assert torch.equal(got.view(torch.uint8), w.view(torch.uint8))
+    assert all(t._version > v for t, v in zip((*rows, *cols), before))
+    out = torch.zeros(50, 50, device=dev())
+    v = out._version
+    fp.mx4_matmul(rows, rows, out)
+    assert out._version > v
+    # one form given, the other allocated
+    both = fp.mx4_quantize(x, None, None, *cols, transposed=True, seed=seed)
+    for got, w in zip(both, want):
+        assert torch.equal(got.view(torch.uint8), w.view(torch.uint8))
+
+
+@pytest.mark.parametrize("m,n,k", [(16, 300, 5000), (17, 300, 300), (32, 90, 4000), (33, 90, 700), (64, 20, 3000), (65, 20, 3000),
+                                   (5, 4099, 256), (2000, 7, 500)])
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+def test_product_of_few_rows(fp, m, n, k, dtype):
+    check_product(fp, m, n, k, dtype, True, 31)
+
+
+def test_one_operand_for_both_sides(fp):
+    q = fp.mx4_quantize(matrix(300, 400, "f32", 3).to(dev()))
+    y = fp.mx4_matmul(q, q, dtype=torch.float32)
+    assert torch.equal(y, y.t())
+
+
+def test_two_streams_at_once(fp):
+    """Calls on two streams beside each other: bit for bit what they give one after the other."""
+    x = [matrix(700, 900, "bf16", 40 + i).to(dev()) for i in range(2)]
+    want = [fp.mx4_matmul(fp.mx4_quantize(t), fp.mx4_quantize(t, seed=5)) for t in x]
+    streams = [torch.cuda.Stream() for _ in x]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(5):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(fp.mx4_matmul(fp.mx4_quantize(x[i]), fp.mx4_quantize(x[i], seed=5)))
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, want[i]) for i in range(2) for y in got[i])
+
+
+def test_more_than_32_bits_of_elements(fp):
+    """Both forms, their values and a product whose output has over 2^32 elements: their last rows and columns."""
+    r, c, seed = 66001, 65120, 77
+    assert r * c > 1 << 32
+    say("quantize", r, c)
+    x = torch.zeros(r, c, dtype=torch.bfloat16, device=dev())
+    tail_r, tail_c = matrix(3, c, "bf16", 1, 1.0), matrix(r, 2, "bf16", 2, 1.0)
+    x[-3:] = tail_r.to(dev())
+    x[:, -2:] = tail_c.to(dev())
+    tail_r[:, -2:] = tail_c[-3:]
+    for s in (None, seed):
+        codes, scales, codes_t, scales_t = fp.mx4_quantize(x, transposed=True, seed=s)
+        at_r = np.arange(r - 3, r, dtype=np.uint64)[:, None] * np.uint64(c) + np.arange(c, dtype=np.uint64)
+        at_c = np.arange(r, dtype=np.uint64) * np.uint64(c) + np.arange(c - 2, c, dtype=np.uint64)[:, None]
+        at_r, at_c = at_r & np.uint64(ref.M32), at_c & np.uint64(ref.M32)
+        want = ref.quantize(tail_r.float().numpy(), None if s is None else ref.hashes(at_r, s) >> np.uint64(16))
+        want_t = ref.quantize(np.ascontiguousarray(tail_c.float().numpy().T),
+                              None if s is None else ref.hashes(at_c, s) & np.uint64(0xFFFF))
+        assert np.array_equal(codes[-3:].cpu().numpy(), want[0])
+        assert np.array_equal(scales[-3:].view(torch.uint8).cpu().numpy(), want[1])
+        assert np.array_equal(codes_t[-2:].cpu().numpy(), want_t[0])
+        assert np.array_equal(scales_t[-2:].view(torch.uint8).cpu().numpy(), want_t[1])
+    del codes_t, scales_t
+    say("dequantize", r, c)
+    fp.mx4_dequantize(codes, scales, c, x)
+    assert np.array_equal(x[-3:].float().cpu().numpy(), ref.values(*want, c).astype(np.float32))
+    del codes, scales
+    say("product", r, c)
+    k = 40
+    a, b = matrix(r, k, "f32", 3, 0.5), matrix(c, k, "f32", 4, 0.5)
+    qa, qb = fp.mx4_quantize(a.to(dev())), fp.mx4_quantize(b.to(dev()))
+    x.fill_(5)
+    fp.mx4_matmul(qa, qb, x)
+    va, vb = (torch.from_numpy(ref.values(*ref.quantize(t.numpy()), k)) for t in (a, b))
+    for rows in (slice(0, 3), slice(r - 300, r)):
+        y = va[rows] @ vb.t()
+        bound = (k + 1) * 2.0 ** -24 * (va[rows].abs() @ vb.t().abs()) + 2.0 ** -8 * y.abs() * 1.01
+        assert bool(((x[rows].cpu().double() - y).abs() <= bound).all())
+
+
 def test_binding_refuses(fp):
     x = torch.zeros(8, 64, device=dev())
     with pytest.raises(ValueError, match="contiguous"):
