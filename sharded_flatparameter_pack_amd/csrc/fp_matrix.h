@@ -91,9 +91,11 @@ constexpr int kOwnChunks = 64;  // up to so many, the kernel that writes X adds 
 constexpr int kCastRows = 16, kCastCols = 128;
 
 // Tiles of the products.  kTile64Deep: with eight stages in LDS, for a
-// workgroup that has its CU to itself.
-enum { kTile256 = 0, kTile128 = 1, kTile64 = 2, kTile64Deep = 3, kTileShapes = 4 };
-constexpr int kTileSide[kTileShapes] = {256, 128, 64, 64};
+// workgroup that has its CU to itself.  kTile192: of the symmetric products, where
+// a triangle's 256-wide tiles leave CUs idle (4096 x 4096: 136 tiles, A 107 us and B
+// 119; 253 of these 92 and 98).
+enum { kTile256 = 0, kTile128 = 1, kTile64 = 2, kTile64Deep = 3, kFullShapes = 4, kTile192 = 4, kHalfShapes = 5 };
+constexpr int kTileSide[kHalfShapes] = {256, 128, 64, 64, 192};
 
 // Small matrices: what one workgroup needs for one of rows x cols, in bytes of
 // LDS and in 16 x 16 tiles per wave: up to 4 as they come, else four by four.

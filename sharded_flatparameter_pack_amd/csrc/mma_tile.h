@@ -80,7 +80,7 @@ struct TileShape {
     // with the tile's LDS.  Said to the compiler, it holds everything in plain
     // registers; unsaid, it moved 88 in and out of the accumulation ones per step
     // of a 128-wide tile.
-    static constexpr int kWavesSimd = kBM >= 128 ? 2 : 4;
+    static constexpr int kWavesSimd = kBM < 128 ? 4 : kWavesWg > 8 ? kWavesWg / 4 : 2;
     static constexpr int kFM = kWM / 16, kFN = kWN / 16;        // 16x16 fragments of a wave
     static constexpr int kStage = (kBM + kBN) * kStepBytes;
     static constexpr int kScaleStage = (kBM + kBN) * 8;
@@ -149,7 +149,10 @@ struct Side {
             for (int h = 0; h < 2; ++h) at[h] = (wave0 + j) * kStepBytes + (((2 * g + h) ^ (j & 7)) << 4);
         }
     }
-    static __device__ __forceinline__ int swizzle(int k4, int k16) { return (k4 | k16 << 2) & (kB / 16 - 1); }
+    static __device__ __forceinline__ int swizzle(int k4, int k16) {
+        if constexpr ((kB & (kB - 1)) == 0) return (k4 | k16 << 2) & (kB / 16 - 1);
+        else return (k4 >> 1) ^ k16;  // rows of an odd number of 128 bytes: k4's lowest bit is in the address already
+    }
 
     template <bool kWritten>
     __device__ __forceinline__ void load(char* stage, int wave, int step) const {

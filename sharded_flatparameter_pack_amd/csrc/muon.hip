@@ -151,7 +151,8 @@ std::vector<MatTile> ordered(const MuonRec& r, int32_t mat, int side, bool half)
 // alone there, and from what a tile takes beside its steps (MI355X, the tiles'
 // kernels at 1024 to 4096).
 double finish(const std::vector<MuonRec>& recs, const Batch& b, int shape, bool half) {
-    constexpr double kStep[] = {1.6, 0.56, 0.26, 0.4}, kAlone[] = {1.3, 0.65, 0.36, 0.2}, kBeside[] = {20.0, 6.0, 2.5, 3.0};
+    constexpr double kStep[] = {1.6, 0.56, 0.26, 0.4, 1.2}, kAlone[] = {1.3, 0.65, 0.36, 0.2, 1.2},
+                     kBeside[] = {20.0, 6.0, 2.5, 3.0, 14.0};
     std::vector<std::pair<int64_t, int64_t>> runs;  // steps, tiles
     for (int32_t i : b.mats) {
         const MuonRec& r = recs[(size_t)i];
@@ -189,7 +190,7 @@ double finish(const std::vector<MuonRec>& recs, const Batch& b, int shape, bool 
 
 int choose_shape(const std::vector<MuonRec>& recs, const Batch& b, bool half) {
     int best = kTile256;
-    for (int shape = kTile128; shape < kTileShapes; ++shape)
+    for (int shape = kTile128; shape < (half ? kHalfShapes : kFullShapes); ++shape)
         if (finish(recs, b, shape, half) < finish(recs, b, best, half)) best = shape;
     return best;
 }
@@ -208,16 +209,16 @@ void deal(const std::vector<MuonRec>& recs, const Batch& b, int side, bool half,
         chunks.push_back(std::move(c));
     }
     std::stable_sort(chunks.begin(), chunks.end(), [](const Chunk& x, const Chunk& y) { return x.steps > y.steps; });
-    // at most a quarter of a die's share, so that the shares come out alike
-    const size_t most = (size_t)std::max<int64_t>(1, std::min<int64_t>(32, total / (4 * kDies)));
     std::vector<MatTile> die[kDies];
     int64_t load[kDies] = {};
     for (const Chunk& c : chunks)
-        for (size_t at = 0; at < c.tiles.size(); at += most) {
-            const size_t n = std::min(most, c.tiles.size() - at);
+        for (int64_t at = 0, n; at < (int64_t)c.tiles.size(); at += n) {
+            // ever shorter towards the end, so that the shares come out alike
+            n = std::min({(int64_t)c.tiles.size() - at, (int64_t)32, std::max<int64_t>(1, total / (4 * kDies))});
+            total -= n;
             const int d = (int)(std::min_element(load, load + kDies) - load);
-            load[d] += c.steps * (int64_t)n;
-            die[d].insert(die[d].end(), c.tiles.begin() + (int64_t)at, c.tiles.begin() + (int64_t)(at + n));
+            load[d] += c.steps * n;
+            die[d].insert(die[d].end(), c.tiles.begin() + at, c.tiles.begin() + (at + n));
         }
     size_t rows = 0;
     for (const auto& d : die) rows = std::max(rows, d.size());

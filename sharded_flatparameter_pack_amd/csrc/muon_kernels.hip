@@ -39,6 +39,7 @@ using Shape256 = TileShape<256, 256, 128, 64>;
 using Shape128 = TileShape<128, 128, 64, 64>;
 using Shape64 = TileShape<64, 64, 32, 32>;
 using Shape64Deep = TileShape<64, 64, 32, 32, 8>;
+using Shape192 = TileShape<192, 192, 64, 48>;
 
 __device__ __forceinline__ bool skipped(const MuonArgs& a) { return a.found_inf != nullptr && *a.found_inf != 0; }
 
@@ -851,13 +852,13 @@ hipError_t launch_muon_cast(const MuonArgs& a, const MuonMore& b, hipStream_t s)
 
 hipError_t launch_muon_gram(const MuonArgs& a, int shape, hipStream_t s) {
 #define FP_CALL(S) launch<gram_kernel<S>>((unsigned)a.n_tiles, S::kThreadsWg, S::kLds, s, a)
-    return FP_BY_SHAPE(FP_CALL);
+    return shape == kTile192 ? FP_CALL(Shape192) : FP_BY_SHAPE(FP_CALL);
 #undef FP_CALL
 }
 
 hipError_t launch_muon_poly(const MuonArgs& a, int shape, hipStream_t s) {
 #define FP_CALL(S) launch<poly_kernel<S>>((unsigned)a.n_tiles, S::kThreadsWg, S::kLds, s, a)
-    return FP_BY_SHAPE(FP_CALL);
+    return shape == kTile192 ? FP_CALL(Shape192) : FP_BY_SHAPE(FP_CALL);
 #undef FP_CALL
 }
 

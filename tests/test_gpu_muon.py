@@ -71,6 +71,15 @@ def test_orthogonalize_large(fp, shape):
     assert rel(x.cpu(), ref.orthogonalize(g)) <= OFF
 
 
+@pytest.mark.parametrize("shape", [(4090, 4001), (3800, 5000), (5000, 3800), (1, 300000), (300000, 3), (40, 70000)])
+def test_orthogonalize_larger(fp, shape):
+    g = gradient(*shape, 6, "spiked").to(dev())
+    x = torch.empty(shape, device=dev())
+    plan = fp.Muon([g], updates=[x])
+    plan.orthogonalize(plan.new_workspace())
+    assert rel(x, ref.orthogonalize(g)) <= OFF
+
+
 def test_many_small_and_one_large(fp):
     """A batch of sizes that lie far apart shares its launches."""
     shapes = [(1400, 1300)] + [(16 + i % 40, 8 + i % 23) for i in range(300)]
