@@ -543,8 +543,10 @@ __device__ __forceinline__ void put8_lds(char* p, float a, float b, float c, flo
 // 16 rows of a fragment sit in different banks.  A wave works on blocks of kSub x
 // kSub tiles of 16 x 16: 2 x 2, four products for four fragments, where LDS reads
 // bound a step (128 x 128 with 1 x 1: 11 us a step, with 2 x 2 6.2), 1 x 1 for the
-// smallest, whose steps are all latency and want every wave (32 x 48: 1.25 us a step,
-// with 2 x 2 2.3).
+// smallest, whose steps are all latency and want every wave (32 x 48: 1.2 us a step,
+// with 2 x 2 2.3); A and B of at most 64 rows in blocks of 2 x 1, of which there is
+// one for each wave (64 x 256: 3.5 us a step, so 3.2; 32 x 1024: 5.8, so 4.4).  The
+// rest of a step with weights, 16 us for 64 x 256, is one CU's loads, fp64 and stores.
 //
 // kTiles: tiles of X per wave.
 constexpr int kSmallWaves = kSmallThreads / 64;
@@ -658,11 +660,15 @@ __global__ __launch_bounds__(kSmallThreads, 2) void small_kernel(const MuonArgs 
         sum = 0.0;
 #pragma unroll
         for (int w = 0; w < kSmallWaves; ++w) sum += sums[w];
-        const double scale = 1.0 / (sqrt(sum) + b.eps);
+        // x / norm in fp32, whose operations take a quarter of fp64's: times a power
+        // of two, then by a number in (1, 2]
+        const double norm = sqrt(sum) + b.eps;
+        const int e = __builtin_amdgcn_frexp_exp(norm);
+        const float scale = (float)(1.0 / __builtin_amdgcn_ldexp(norm, -e));
 #pragma unroll
         for (int i = 0; i < kTiles; ++i)
 #pragma unroll
-            for (int q = 0; q < 4; ++q) x[i][q] = (float)((double)x[i][q] * scale);
+            for (int q = 0; q < 4; ++q) x[i][q] = __builtin_amdgcn_ldexpf(x[i][q], -e) * scale;
 
         auto st_h = [&](float s) {
 #pragma unroll
@@ -673,42 +679,46 @@ __global__ __launch_bounds__(kSmallThreads, 2) void small_kernel(const MuonArgs 
                 put8_lds(h + p.row * hp + 2 * p.col, x[i][0] * s, x[i][1] * s, x[i][2] * s, x[i][3] * s);
             }
         };
-        // fragments of kBlock rows from `row` on, the lane's 8 elements from k + 8 g on
-        struct Frags {
-            f16x8_t v[kSub];
-        };
-        auto rows_at = [&](const char* base, int pitch, int row, int k) {
+        // kN fragments of 16 rows from `row` on, the lane's 8 elements from k + 8 g on
+        auto rows_at = [&](const char* base, int pitch, int row, int k, auto& f) {
             const char* p = base + (row + j) * pitch + 2 * (k + 8 * g);
-            Frags f;
 #pragma unroll
-            for (int y = 0; y < kSub; ++y) f.v[y] = *(const f16x8_t*)(p + 16 * y * pitch);
-            return f;
+            for (int y = 0; y < (int)(sizeof f / sizeof f[0]); ++y) f[y] = *(const f16x8_t*)(p + 16 * y * pitch);
         };
-        struct Sums {
-            f32x4_t v[kSub][kSub];
-        };
-        auto product = [&](const Frags& right, const Frags& left, Sums& acc) {
+        auto product = [&](const auto& right, const auto& left, auto& acc) {
 #pragma unroll
             for (int y = 0; y < kSub; ++y)
 #pragma unroll
-                for (int z = 0; z < kSub; ++z)
-                    acc.v[y][z] = __builtin_amdgcn_mfma_f32_16x16x32_f16(right.v[z], left.v[y], acc.v[y][z], 0, 0, 0);
+                for (int z = 0; z < (int)(sizeof right / sizeof right[0]); ++z)
+                    acc[y][z] = __builtin_amdgcn_mfma_f32_16x16x32_f16(right[z], left[y], acc[y][z], 0, 0, 0);
         };
         // base base^T, m x m, block by block: out(row, col, four values from col
-        // on, whether the diagonal may be among them)
+        // on, whether the diagonal may be among them).  Blocks are kBlock down, and
+        // across kBlock or, where that leaves waves without one, half of it.
         const int side = m / kBlock, by_side = (256 + side - 1) / side;  // t / side = t by_side / 256 for t < 64
-        auto square = [&](const char* base, int pitch, int width, auto out) {
-            for (int t = wave; t < side * side; t += kSmallWaves) {
-                const int bi = t * by_side >> 8, ti = bi * kBlock, tj = (t - bi * side) * kBlock;
-                Sums acc = {};
+        auto square_by = [&](auto wide, const char* base, int pitch, int width, auto out) {
+            constexpr int kWide = decltype(wide)::value, kParts = kSub / kWide;
+            for (int t = wave; t < side * side * kParts; t += kSmallWaves) {
+                const int block = t / kParts, bi = block * by_side >> 8, ti = bi * kBlock;
+                const int tj = (block - bi * side) * kBlock + t % kParts * 16;
+                f32x4_t acc[kSub][kWide] = {};
 #pragma unroll 4
-                for (int k = 0; k < width; k += 32) product(rows_at(base, pitch, tj, k), rows_at(base, pitch, ti, k), acc);
+                for (int k = 0; k < width; k += 32) {
+                    f16x8_t left[kSub], right[kWide];
+                    rows_at(base, pitch, tj, k, right);
+                    rows_at(base, pitch, ti, k, left);
+                    product(right, left, acc);
+                }
 #pragma unroll
                 for (int y = 0; y < kSub; ++y)
 #pragma unroll
-                    for (int z = 0; z < kSub; ++z)
-                        out(ti + 16 * y + j, tj + 16 * z + 4 * g, acc.v[y][z], ti + 16 * y == tj + 16 * z);
+                    for (int z = 0; z < kWide; ++z)
+                        out(ti + 16 * y + j, tj + 16 * z + 4 * g, acc[y][z], ti + 16 * y == tj + 16 * z);
             }
+        };
+        auto square = [&](const char* base, int pitch, int width, auto out) {
+            if (kSub == 1 || side * side >= kSmallWaves) square_by(std::integral_constant<int, kSub>{}, base, pitch, width, out);
+            else square_by(std::integral_constant<int, 1>{}, base, pitch, width, out);
         };
         st_h(it.s[0].x);
         for (int s = 0; s < it.n; ++s) {
@@ -753,20 +763,21 @@ __global__ __launch_bounds__(kSmallThreads, 2) void small_kernel(const MuonArgs 
                 const int t = wave + i / (kSub * kSub) * kSmallWaves;
                 if (t >= blocks) continue;
                 const int ti = t / across * kBlock, tj = t % across * kBlock;
-                Sums acc = {};
+                f32x4_t acc[kSub][kSub] = {};
 #pragma unroll 2
                 for (int k = 0; k < m; k += 32) {
                     // rows k + 8 g .. + 7 of h, columns tj + j, tj + 16 + j
                     const char* p = h + (k + 8 * g + (j >> 2)) * hp + 2 * (tj + (j & 3) * 4);
-                    Frags right;
+                    f16x8_t left[kSub], right[kSub];
 #pragma unroll
                     for (int z = 0; z < kSub; ++z) {
                         typedef short s16x8_t __attribute__((ext_vector_type(8)));
                         const s16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((FP_LDS s16x4_t*)(p + 32 * z));
                         const s16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((FP_LDS s16x4_t*)(p + 32 * z + 4 * hp));
-                        right.v[z] = __builtin_bit_cast(f16x8_t, (s16x8_t)__builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+                        right[z] = __builtin_bit_cast(f16x8_t, (s16x8_t)__builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
                     }
-                    product(right, rows_at(lb, ap, ti, k), acc);
+                    rows_at(lb, ap, ti, k, left);
+                    product(right, left, acc);
                 }
 #pragma unroll
                 for (int y = 0; y < kSub; ++y) {
@@ -776,7 +787,7 @@ __global__ __launch_bounds__(kSmallThreads, 2) void small_kernel(const MuonArgs 
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
                             float& e = x[i + kSub * y + z][q];
-                            e = __builtin_fmaf(d, e, acc.v[y][z][q] * sc.un_bx);
+                            e = __builtin_fmaf(d, e, acc[y][z][q] * sc.un_bx);
                         }
                 }
             }
