@@ -51,12 +51,17 @@ __device__ __forceinline__ double sum256(double x, double* lds) {
     return (lds[0] + lds[1]) + (lds[2] + lds[3]);
 }
 
-// Elements [e, e + have) of a gradient, have in [1, 4].
-template <int kGrad>
+// Elements [e, e + have) of a gradient, have in [1, 4]; kKept: to be found in the
+// caches afterwards.
+template <int kGrad, bool kKept>
 __device__ __forceinline__ void grad4(const void* g, int64_t e, int have, float f[4]) {
     constexpr int kSize = kGrad == FP_DTYPE_F32 ? 4 : 2;
-    const GradQuad<kGrad> q = have == 4 ? ld_grad<kGrad>(g, e)
-                                        : ld_grad_few<kGrad>(static_cast<const char*>(g) + e * kSize, have);
+    const char* p = static_cast<const char*>(g) + e * kSize;
+    GradQuad<kGrad> q;
+    if (have < 4) q = ld_grad_few<kGrad>(p, have);
+    else if constexpr (!kKept) q = ld_grad<kGrad>(g, e);
+    else if constexpr (kGrad == FP_DTYPE_F32) q.w = get16u(p);
+    else q.w = get8h(p);
     grad_f32(q, f);
 }
 
@@ -117,7 +122,7 @@ __global__ __launch_bounds__(256) void moment_kernel(const MuonArgs a, const Muo
         for (int i = 0; i < kAtOnce; ++i) {
             const int64_t e = e0 + 1024 * i;
             if (e >= to) continue;
-            grad4<kGrad>(grad, e, to - e < 4 ? (int)(to - e) : 4, g[i]);
+            grad4<kGrad, false>(grad, e, to - e < 4 ? (int)(to - e) : 4, g[i]);
             if constexpr (kStep) f32x4_of(get16(b.momentum + r.offset + e), m[i]);  // room up to the next multiple of 32
         }
 #pragma unroll
@@ -215,24 +220,28 @@ __global__ __launch_bounds__(256) void cast_kernel(const MuonArgs a, const MuonM
     const int row0 = t.ti * kCastRows, col0 = t.tj * kCastCols;
     const int row = row0 + (threadIdx.x >> 4), col = col0 + (threadIdx.x & 15) * 8;
     if (row >= r.rp || col >= r.cp) return;
+    const int left = row < r.rows ? r.cols - col : 0;
+    const int64_t e = (int64_t)row * r.cols + col;
+    const bool both = !kStep || hp.nesterov;  // else the gradient is in the momentum
+    float g[8] = {}, m[8] = {};
+    if (left >= 8) {  // both halves of a lane's run at once, through the cache: apart they were read twice over
+        if (both) grad4<kGrad, true>(grad, e, 4, g), grad4<kGrad, true>(grad, e + 4, 4, g + 4);
+        if constexpr (kStep) f32x4_of(get16u(b.momentum + r.offset + e), m), f32x4_of(get16u(b.momentum + r.offset + e + 4), m + 4);
+    } else {
+#pragma unroll
+        for (int q = 0; q < 8; q += 4) {
+            const int have = left - q < 4 ? left - q : 4;
+            if (have <= 0) break;
+            if (both) grad4<kGrad, true>(grad, e + q, have, g + q);
+            if constexpr (kStep) ld_f32(b.momentum + r.offset + e + q, have, m + q);
+        }
+    }
     float x[8];
 #pragma unroll
-    for (int q = 0; q < 8; q += 4) {
-        const int left = r.cols - col - q, have = row >= r.rows || left <= 0 ? 0 : left < 4 ? left : 4;
-        x[q] = x[q + 1] = x[q + 2] = x[q + 3] = 0.0f;
-        if (have > 0) {
-            const int64_t e = (int64_t)row * r.cols + col + q;
-            float g[4], m[4];
-            if (!kStep || hp.nesterov) grad4<kGrad>(grad, e, have, g);
-            if constexpr (kStep) ld_f32(b.momentum + r.offset + e, have, m);
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (j < have) {
-                    const double u = !kStep ? (double)g[j]
-                                     : hp.nesterov ? hp.beta * (double)m[j] + mine * (double)g[j] : (double)m[j];
-                    x[q + j] = (float)(u * scale) * a.s.x;
-                }
-        }
+    for (int k8 = 0; k8 < 8; ++k8) {
+        double u = kStep ? (double)m[k8] : (double)g[k8];
+        if (kStep && hp.nesterov) u = hp.beta * u + mine * (double)g[k8];
+        x[k8] = k8 < left ? (float)(u * scale) * a.s.x : 0.0f;
     }
     const int64_t base = 2 * ((int64_t)row0 * r.cp + col0);
     st_x(a.ws + r.h[0] + base, a.ws + r.l + base, (uint32_t)((row - row0) * r.cp + col - col0), x);

@@ -127,15 +127,18 @@ __device__ __forceinline__ void st16h(void* p, const uint4 v) {  // non-temporal
     __builtin_nontemporal_store((u32x4_a2{v.x, v.y, v.z, v.w}), (FP_GLOBAL u32x4_a2*)(p));
 }
 __device__ __forceinline__ void put16u(void* p, const uint4 v) {  // from a 4-byte boundary
-    typedef unsigned int u32x4_a4u __attribute__((ext_vector_type(4), aligned(4)));
-    *gptr<u32x4_a4u>(p) = u32x4_a4u{v.x, v.y, v.z, v.w};
+    *gptr<u32x4_a4>(p) = u32x4_a4{v.x, v.y, v.z, v.w};
 }
-__device__ __forceinline__ void put16h(void* p, const uint4 v) {  // from a 2-byte boundary
-    *gptr<u32x4_a2>(p) = u32x4_a2{v.x, v.y, v.z, v.w};
+__device__ __forceinline__ uint4 get16u(const void* p) {
+    const u32x4_a4 v = *gptr<u32x4_a4>(p);
+    return make_uint4(v.x, v.y, v.z, v.w);
+}
+__device__ __forceinline__ uint2 get8h(const void* p) {
+    const u32x2_a2 v = *gptr<u32x2_a2>(p);
+    return make_uint2(v.x, v.y);
 }
 __device__ __forceinline__ void put8h(void* p, const uint2 v) { *gptr<u32x2_a2>(p) = u32x2_a2{v.x, v.y}; }
 __device__ __forceinline__ void put16(void* p, const uint4 v) { *gptr<u32x4_t>(p) = u32x4_t{v.x, v.y, v.z, v.w}; }
-__device__ __forceinline__ void put8(void* p, const uint2 v) { *gptr<u32x2_t>(p) = u32x2_t{v.x, v.y}; }
 
 // 32 bits of dither for partition element e: the element's index and the
 // call's key through two multiplications.  The multipliers are the golden
