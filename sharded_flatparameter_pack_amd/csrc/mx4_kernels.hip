@@ -61,12 +61,13 @@ __device__ __forceinline__ uint32_t mx4_encode(const float f[8], uint32_t byte) 
 // that gives y 2^-126 has to be cut too, not rounded (what is cut lies below d's
 // last bit): the kernel's rounding is towards zero (round_to_zero).
 __device__ __forceinline__ uint32_t mx4_encode(const float f[8], uint32_t byte, const uint32_t d[8]) {
-    uint32_t w = 0;
+    uint32_t w = 0, c[8];  // c: sign, 6 zeros, code, 22 bits to cut
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-        const float y = __builtin_amdgcn_ldexpf(f[k], 1 - (int)byte);    // times 2^(127 - byte) 2^-126
-        const uint32_t c = (__float_as_uint(y) + (d[k] << 6)) >> 22;     // sign, 6 unused bits, code
-        w |= ((c & 7u) | (c >> 6 & 8u)) << (4 * k);
+    for (int k = 0; k < 8; ++k) c[k] = __float_as_uint(__builtin_amdgcn_ldexpf(f[k], 1 - (int)byte)) + (d[k] << 6);  // times 2^(127 - byte) 2^-126
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {  // two at a time, in the word's halves
+        const uint32_t p = __builtin_amdgcn_perm(c[k + 4], c[k], 0x07060302u);
+        w |= ((p >> 6 & 0x00070007u) | (p >> 12 & 0x00080008u)) << (4 * k);
     }
     return byte == 255u ? 0u : w;
 }
