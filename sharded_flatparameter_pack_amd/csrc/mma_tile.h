@@ -10,20 +10,22 @@
 // lane holds is free as long as both agree: lane group g = lane / 16 has word
 // 2 g + h (16 bytes) of the step's 128 in half h.
 //
-// What bounds it: LDS.  A 256 x 256 tile on 8 waves of 128 x 64 reads 192 KiB
-// of fragments per step and takes 64 KiB in, at 128 bytes per clock as long as
-// its 512 fp16 instructions; smaller wave tiles read more for the same work.
-// Measured on MI355X, fp16 at 4096^3: 128 x 64 waves 109 us (1.26 PFLOP/s),
-// 128 x 128 on 4 waves 169 (one wave per SIMD hides nothing), a 128-wide
-// tile on 4 waves of 64 x 64 145, a 64-wide one 275.  MXFP4 at 4096^2 x 16384
-// (scales from LDS): 125 us (4.4 PFLOP/s).
+// What bounds it: the matrix cores' clock under load, with LDS close behind.  A
+// 256 x 256 tile on 8 waves of 128 x 64 reads 192 KiB of fragments per step and
+// takes 64 KiB in, at 128 bytes per clock as long as its 512 fp16 instructions;
+// smaller wave tiles read more for the same work.  Measured on MI355X, fp16 at
+// 4096^3 without an epilogue: 101 us (1.36 PFLOP/s; the same tiles with waves of
+// 128 x 128 took 169, one wave per SIMD hiding nothing, 128-wide tiles of 64 x 64
+// waves 145, 64-wide ones 275).  MXFP4 at 4096^2 x 16384: 107 to 120 us (4.6 to
+// 5.1 PFLOP/s).  Swizzles that spread a fragment's rows over all banks or half of
+// them, and 32 x 32 instructions, make no difference.
 //
 // The loop: stages in LDS, filled by loads that go to LDS directly, and two sets
 // of fragments in registers.  While the first half's products run, the second
 // half's fragments are read; then, behind the step's one barrier, the stage just
 // read is refilled for a later step and the next step's first fragments are read
 // under the second half's products.  Read as they are needed
-// instead, the same tiles take 121 and 250 us.
+// instead, the same tiles take 121 us.
 #pragma once
 
 #include <atomic>

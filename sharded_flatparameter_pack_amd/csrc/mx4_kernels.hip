@@ -154,7 +154,9 @@ __device__ __forceinline__ void row_block(const Mx4QuantArgs& a, const Eight<kDt
     if ((threadIdx.x & 3) == 0) gptr<uint8_t>((void*)a.scales)[(row * a.cp + col) >> 5] = (uint8_t)byte;
 }
 
-// The rows' form alone: eight elements per lane, rows behind each other.
+// The rows' form alone: eight elements per lane, rows behind each other, so that a
+// single row's blocks spread over many CUs (1 x 4096: 2 us, a launch's latency; in
+// 128 x 128 tiles 4.9).
 template <int kDtype, bool kRandom>
 __global__ __launch_bounds__(256) void quantize_rows_kernel(const Mx4QuantArgs a) {
     if (kRandom) round_to_zero();
@@ -170,8 +172,10 @@ __global__ __launch_bounds__(256) void quantize_rows_kernel(const Mx4QuantArgs a
 // A 128 x 128 tile.  Rows' form: four lanes hold a block, eight elements each,
 // and all of a lane's rows are loaded before the first is worked on.  Columns'
 // form: a lane holds a block, read down a column of the tile in LDS, where an
-// element of 16 bits has its half of the dither beside it (the hash is most of
-// the stochastic form's work: 8192 x 8192 bf16 values twice over, 118 us).
+// element of 16 bits has its half of the dither beside it (a hash of its own for
+// each form: 118 us for 8192 x 8192 bf16, so 77).  To nearest, memory bounds it (8192 x
+// 8192 fp32: 80 us, 4.3 TB/s); stochastically its instructions do, 31 per element,
+// the hash's two products as long as four others each.
 constexpr int kQTile = 128;
 template <int kDtype, bool kRows, bool kRandom>
 __global__ __launch_bounds__(256) void quantize_kernel(const Mx4QuantArgs a) {
@@ -253,7 +257,8 @@ __device__ __forceinline__ void mx4_decode(uint32_t codes, uint32_t byte, float 
     f[4] = c.x; f[5] = c.y; f[6] = d.x; f[7] = d.y;
 }
 
-// Eight values per lane, a row's columns side by side.
+// Eight values per lane, a row's columns side by side.  Its writes bound it (8192 x
+// 8192 to bf16: 25 us, 6.8 TB/s with the codes in the last-level cache).
 template <int kDtype>
 __global__ __launch_bounds__(256) void dequantize_kernel(const Mx4DequantArgs a, uint32_t across) {
     const uint32_t lane = blockIdx.x * 256u + threadIdx.x;
@@ -355,6 +360,9 @@ __device__ __forceinline__ void st_out(const Mx4MatmulArgs& a, int64_t row, int6
     }
 }
 
+// A tile per workgroup.  8192 x 8192 x 4096 (16 steps a tile) to bf16: 167 us (3.3
+// PFLOP/s), of which a tile's start and its outputs take a third; 8192 x 4096 x 8192 to
+// bf16 140, with fp32 outputs 150.
 template <class S, int kVec>
 __global__ __launch_bounds__(S::kThreadsWg, S::kWavesSimd) void matmul_kernel(const Mx4MatmulArgs a) {
     extern __shared__ __align__(16) char lds[];
@@ -375,12 +383,13 @@ __global__ __launch_bounds__(S::kThreadsWg, S::kWavesSimd) void matmul_kernel(co
         [&](int r, int c, const float* v, const Old& o) { st_out<kVec>(a, i0 + r, j0 + c, v, o); });
 }
 
-// Products with few rows on one side (a: up to 16 kF; tokens of a generation):
-// the other side is read once, and that bounds them, so a workgroup has 16 of its
-// rows and its waves share K.  Fragments come straight from memory, a wave's
-// steps kAhead at a time; the waves' sums meet in LDS, in their order.
+// Products of few rows (a: up to 16 kF; tokens of a generation) with a matrix that
+// is no larger than its workgroups fill the card (shape_of): b is read once, and
+// that bounds them, so a workgroup has 16 of its rows and its waves share K.  Fragments come straight from memory, a wave's
+// steps kAhead at a time; the waves' sums meet in LDS, in their order.  1 x 8192 x
+// 4096: 6.3 us (2.8 TB/s; the weights' bytes alone 3.8), a launch's latency and two
+// trips to memory; on 64-wide tiles 11.8.
 constexpr int kThinWaves = 8;
-constexpr int64_t kThinRows = 64;
 template <int kF>
 __global__ __launch_bounds__(64 * kThinWaves, 2) void thin_kernel(const Mx4MatmulArgs a) {
     __shared__ f32x4_t sums[kThinWaves][kF][64];
@@ -488,11 +497,32 @@ hipError_t run_quantize(const Mx4QuantArgs& a, hipStream_t s) {
 }  // namespace
 
 int64_t mx4_quantize_lanes(const Mx4QuantArgs& a) { return quant_groups(a) * 256; }
-// Of the thin kernel, or of the 256-wide tiles, which a product with so many lanes is run on.
-static int64_t thin_lanes(const Mx4MatmulArgs& a) { return ceil_div64(a.n, 16) * 64 * kThinWaves; }
-static bool is_thin(const Mx4MatmulArgs& a) { return a.m <= kThinRows && thin_lanes(a) <= 0xFFFFFFFFLL; }
+
+// What a product is run on.  Tiles are the smaller the fewer there are: a shape
+// serves while two workgroups per CU hold all of its tiles at once, for then a
+// product takes as long as one tile does (4096 wide in K and across, to bf16: 512
+// rows on 64-wide tiles 11.7 us, on 128-wide ones 15.9; 1024 rows 24.2 and 17.6; 2048
+// rows on 128-wide tiles 27.6, on 256-wide ones 33.7; 2304 rows 40.7 and 33.8), and
+// where larger tiles would be mostly empty.  The thin kernel, whose workgroups
+// read all of a, for as many workgroups per 16 rows of a (1 x 8192 x 4096: 5.6 us, on
+// 64-wide tiles 7.4; 16 x 8192 x 16384: 24 and 34; 32 x 2048 x 4096: 6.4 and 7.7; 32 x
+// 8192 x 4096: 10.6 and 7.7; 64 x 2048 x 4096 with kF 4: 9.2 and 8.2).
+enum { kThin1, kThin2, kTiles64, kTiles128, kTiles256 };
+static int64_t tiles_of(const Mx4MatmulArgs& a, int64_t side) { return ceil_div64(a.m, side) * ceil_div64(a.n, side); }
+static int shape_of(const Mx4MatmulArgs& a) {
+    constexpr int64_t kAtOnce = 512, kMaxLanes = 0xFFFFFFFFLL;
+    const int64_t least = a.m < a.n ? a.m : a.n, thin = ceil_div64(a.n, 16);
+    if (a.m <= 16 && thin <= kAtOnce) return kThin1;
+    if (a.m <= 32 && 2 * thin <= kAtOnce) return kThin2;
+    auto serves = [&](int64_t side, int64_t threads) {
+        const int64_t tiles = tiles_of(a, side);
+        return tiles <= kAtOnce || (least <= side && tiles * threads <= kMaxLanes);
+    };
+    return serves(64, Shape64::kThreadsWg) ? kTiles64 : serves(128, Shape128::kThreadsWg) ? kTiles128 : kTiles256;
+}
+// More than a launch holds only where the largest tiles do not suffice.
 int64_t mx4_matmul_lanes(const Mx4MatmulArgs& a) {
-    return is_thin(a) ? thin_lanes(a) : ceil_div64(a.m, 256) * ceil_div64(a.n, 256) * Shape256::kThreadsWg;
+    return shape_of(a) == kTiles256 ? tiles_of(a, 256) * Shape256::kThreadsWg : 0;
 }
 
 hipError_t launch_mx4_quantize(const Mx4QuantArgs& a, hipStream_t s) {
@@ -511,17 +541,14 @@ hipError_t launch_mx4_dequantize(const Mx4DequantArgs& a, hipStream_t s) {
 }
 
 hipError_t launch_mx4_matmul(const Mx4MatmulArgs& a, hipStream_t s) {
-    if (is_thin(a)) {
-        const unsigned grid = (unsigned)ceil_div64(a.n, 16);
-        if (a.m <= 16) thin_kernel<1><<<grid, 64 * kThinWaves, 0, s>>>(a);
-        else if (a.m <= 32) thin_kernel<2><<<grid, 64 * kThinWaves, 0, s>>>(a);
-        else thin_kernel<4><<<grid, 64 * kThinWaves, 0, s>>>(a);
-        return hipGetLastError();
+    const unsigned thin = (unsigned)ceil_div64(a.n, 16);
+    switch (shape_of(a)) {
+        case kThin1: return launch<thin_kernel<1>>(thin, 64 * kThinWaves, 0, s, a);
+        case kThin2: return launch<thin_kernel<2>>(thin, 64 * kThinWaves, 0, s, a);
+        case kTiles64: return run_matmul<Shape64>(a, s);
+        case kTiles128: return run_matmul<Shape128>(a, s);
+        default: return run_matmul<Shape256>(a, s);
     }
-    auto tiles = [&](int64_t side) { return ceil_div64(a.m, side) * ceil_div64(a.n, side); };
-    if (tiles(256) >= 160) return run_matmul<Shape256>(a, s);
-    if (tiles(128) >= 160) return run_matmul<Shape128>(a, s);
-    return run_matmul<Shape64>(a, s);
 }
 
 }  // namespace fpk

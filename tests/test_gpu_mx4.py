@@ -312,7 +312,8 @@ def test_given_buffers_of_one_form(fp, seed):
 
 
 @pytest.mark.parametrize("m,n,k", [(16, 300, 5000), (17, 300, 300), (32, 90, 4000), (33, 90, 700), (64, 20, 3000), (65, 20, 3000),
-                                   (5, 4099, 256), (2000, 7, 500)])
+                                   (5, 4099, 256), (2000, 7, 500), (16, 8192, 300), (16, 8193, 300), (32, 4096, 40), (20, 5000, 40),
+                                   (3, 40000, 256), (100, 40000, 40)])
 @pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
 def test_product_of_few_rows(fp, m, n, k, dtype):
     check_product(fp, m, n, k, dtype, True, 31)
