@@ -9,6 +9,9 @@ still small and so is R): over the three last steps sqrt(3) * (2.8^2 + 3.4^2)^(1
 """
 
 import math
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -415,6 +418,68 @@ def test_repeatable_and_in_any_workspace(fp):
         plan.orthogonalize(other)
     torch.cuda.current_stream().wait_stream(s)
     assert all(torch.equal(a, b) for a, b in zip(out, first))
+
+
+def test_no_elements(fp):
+    """A plan whose matrices are all empty: its calls do nothing."""
+    shapes = [(0, 5), (3, 0)]
+    _, grads, master, copies = state(shapes, "bf16", "bf16")
+    plan = fp.Muon(grads, master, copies, [torch.empty(s, device=dev()) for s in shapes])
+    assert plan.partition == 0 and plan.workspace_bytes == 0
+    mom, ws = plan.new_momentum(), plan.new_workspace()
+    plan.step(mom, ws, **HP)
+    plan.orthogonalize(ws)
+    plan.set_grads(grads)
+    torch.cuda.synchronize()
+
+
+def test_one_gradient_for_two_matrices(fp):
+    """One gradient for two matrices: each as by itself."""
+    g = gradient(70, 50, 3).to(dev())
+    w = [gradient(70, 50, 10 + i).to(dev()) for i in range(2)]
+    plan = fp.Muon([g, g], w)
+    mom, ws = plan.new_momentum(), plan.new_workspace()
+    want = [ref.muon(g.cpu(), torch.zeros(70, 50), x.cpu(), **HP) for x in w]
+    plan.step(mom, ws, **HP)
+    for i in range(2):
+        m, x, o = want[i]
+        assert float((w[i].cpu().double() - x).norm()) <= OFF * HP["lr"] * ref.adjust_of((70, 50), "rms") * float(o.norm()) + 2.0 ** -24 * float(x.norm())
+    assert torch.equal(plan.tensor_slice(mom, 0), plan.tensor_slice(mom, 1))
+
+
+def test_first_calls_in_a_capture(fp):
+    """Calls that have not run before are captured as they are; replays against eager calls, with new gradients."""
+    code = """
+import sys, torch
+sys.path[:0] = [%r, %r]
+import sharded_flatparameter_pack_amd as fp
+d = torch.device("cuda:0")
+g = [torch.randn(s, device=d) for s in ((1500, 1300), (300, 4000), (90, 70), (4000, 3900))]
+out = [torch.zeros_like(t) for t in g]
+plan = fp.Muon(g, updates=out)
+ws = plan.new_workspace()
+x, w = torch.randn(700, 900, device=d), torch.randn(500, 900, device=d)
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    plan.orthogonalize(ws)
+    y = fp.mx4_matmul(fp.mx4_quantize(x), fp.mx4_quantize(w, seed=3))
+for t in range(3):
+    for k in (*g, x):
+        k.normal_()
+    torch.cuda.synchronize()
+    graph.replay()
+    torch.cuda.synchronize()
+    got = [o.clone() for o in out], y.clone()
+    plan.orthogonalize(ws)
+    assert all(torch.equal(a, b) for a, b in zip(out, got[0]))
+    assert torch.equal(fp.mx4_matmul(fp.mx4_quantize(x), fp.mx4_quantize(w, seed=3)), got[1])
+    assert abs(float(out[0].norm()) / 1300 ** 0.5 - 1) < 0.3
+print("captured")
+"""
+    here = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code % (here, os.path.join(here, "tests"))], capture_output=True, text=True, timeout=100)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stderr[-2000:]
 
 
 def test_two_streams_at_once(fp):
