@@ -172,10 +172,13 @@ __global__ __launch_bounds__(256) void quantize_rows_kernel(const Mx4QuantArgs a
 // A 128 x 128 tile.  Rows' form: four lanes hold a block, eight elements each,
 // and all of a lane's rows are loaded before the first is worked on.  Columns'
 // form: a lane holds a block, read down a column of the tile in LDS, where an
-// element of 16 bits has its half of the dither beside it (a hash of its own for
-// each form: 118 us for 8192 x 8192 bf16, so 77).  To nearest, memory bounds it (8192 x
-// 8192 fp32: 80 us, 4.3 TB/s); stochastically its instructions do, 31 per element,
-// the hash's two products as long as four others each.
+// element of 16 bits has its half of the dither beside it (a hash of its own for each
+// form: 118 us for 8192 x 8192 bf16, so 77 to 87).  A tile's part of a row's or a
+// column's codes is half a line: its neighbours follow on the same die, so that one
+// L2 gets both halves (else 45 % more is written: 5003 x 2730 stochastically 31 us, so
+// 28).  To nearest, memory bounds it (8192 x 8192 fp32: 77 us, 4.4 TB/s);
+// stochastically its instructions do, 31 per element, the hash's two products as
+// long as four others each.
 constexpr int kQTile = 128;
 template <int kDtype, bool kRows, bool kRandom>
 __global__ __launch_bounds__(256) void quantize_kernel(const Mx4QuantArgs a) {
@@ -183,8 +186,11 @@ __global__ __launch_bounds__(256) void quantize_kernel(const Mx4QuantArgs a) {
     typedef typename std::conditional<kWide || kBeside, uint32_t, uint16_t>::type held_t;
     __shared__ held_t tile[kQTile][kQTile + 2];
     if (kRandom) round_to_zero();
-    const unsigned across = kRows ? (unsigned)(a.cp / kQTile) : (unsigned)((a.cols + kQTile - 1) / kQTile);
-    const int64_t row0 = (int64_t)(blockIdx.x / across) * kQTile, col0 = (int64_t)(blockIdx.x % across) * kQTile;
+    const unsigned across = kRows ? (unsigned)(a.cp / kQTile) : (unsigned)((a.cols + kQTile - 1) / kQTile), fours = (across + 1) / 2;
+    // blockIdx % 8 is the die, on which 2 x 2 tiles follow each other
+    const unsigned in = blockIdx.x >> 3, four = (in >> 2) * 8 + (blockIdx.x & 7);
+    const int64_t row0 = ((int64_t)(four / fours) * 2 + (in >> 1 & 1)) * kQTile, col0 = ((int64_t)(four % fours) * 2 + (in & 1)) * kQTile;
+    if (row0 >= a.rp || col0 >= (int64_t)across * kQTile) return;
     const int c8 = (threadIdx.x & 15) * 8, r0 = threadIdx.x >> 4;
     const int64_t left = a.cols - (col0 + c8);
     Eight<kDtype> r[8];
@@ -481,8 +487,12 @@ hipError_t run_matmul(const Mx4MatmulArgs& a, hipStream_t s) {
     return a.dtype == FP_DTYPE_F32 ? run_matmul<S, 4>(a, s) : run_matmul<S, 8>(a, s);
 }
 
-// Tiles across and down: the padding of a form that is wanted is written too.
-int64_t quant_tiles(const Mx4QuantArgs& a) { return ceil_div64(a.codes != nullptr ? a.cp : a.cols, kQTile) * (a.rp / kQTile); }
+// Workgroups: whole 2 x 2 tiles (columns in padding that no form wants have none),
+// as many on each die.
+int64_t quant_tiles(const Mx4QuantArgs& a) {
+    const int64_t across = ceil_div64(a.codes != nullptr ? a.cp : a.cols, kQTile), down = a.rp / kQTile;
+    return ceil_div64(ceil_div64(across, 2) * (down / 2), 8) * 8 * 4;
+}
 int64_t quant_groups(const Mx4QuantArgs& a) { return a.codes_t != nullptr ? quant_tiles(a) : ceil_div64(a.rows * a.cp, 8 * 256); }
 
 template <int kDtype, bool kRandom>
