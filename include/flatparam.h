@@ -822,7 +822,8 @@ fp_status fp_mx8_dequantize(int64_t n, int32_t root, const uint8_t* codes, const
  * fp_muon_info: partition as in fp_params_info, of the momentum;
  *   workspace_bytes: of every call, 6 bytes per element and 4 per element of A,
  *   with both sides counted in multiples of 64, of the matrices that are worked
- *   on together (2 GiB of them, the last one over that edge included).  Small
+ *   on together (2 GiB of them, the last one over that edge included), and up to
+ *   4 MiB where few of them have long rows.  Small
  *   matrices alone (32768 elements, as 160 x 160 or 32 x 1024) need none.
  * Creation, destruction, fp_muon_set_grads and devices as for fp_params.
  * Errors: FP_ERR_RANGE, FP_ERR_INVALID, FP_ERR_ALIGN, FP_ERR_DEVICE. */

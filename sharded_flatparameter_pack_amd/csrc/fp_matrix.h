@@ -27,15 +27,18 @@ struct MuonRec {
     int64_t a, b;             // fp16 [m][m], their diagonals zero
     int64_t da, db;           // fp32 [m]: the diagonals
     int64_t part;             // fp64 [chunks + 1]: the norm's partial sums, and 1 / (norm + eps)
+    int64_t split;            // fp32 [slices][tiles][kTile64Deep's]: A's sums over slices of n
+    int32_t slices, slice_steps;  // 1: none
 };
 
 constexpr int kPad = 64;
 inline int64_t pad64(int64_t n) { return (n + kPad - 1) / kPad * kPad; }
 
 // Tile (ti, tj) of matrix `mat`; what a tile is depends on the kernel.  mat < 0:
-// none, in the tables of the products, which deal each die its own.
+// none, in the tables of the products, which deal each die its own.  slice: of A's
+// sums.
 struct MatTile {
-    int32_t mat, ti, tj, pad;
+    int32_t mat, ti, tj, slice;
 };
 
 struct MuonGroup {
@@ -97,6 +100,9 @@ constexpr int kCastRows = 16, kCastCols = 128;
 enum { kTile256 = 0, kTile128 = 1, kTile64 = 2, kTile64Deep = 3, kFullShapes = 4, kTile192 = 4, kHalfShapes = 5 };
 constexpr int kTileSide[kHalfShapes] = {256, 128, 64, 64, 192};
 
+// Of the kernel that adds A's slices up.
+constexpr int kJoins = 4, kMaxSlices = 32;
+
 // Small matrices: what one workgroup needs for one of rows x cols, in bytes of
 // LDS and in 16 x 16 tiles per wave: up to 4 as they come, else four by four.
 constexpr int kSmallThreads = 512;
@@ -118,6 +124,7 @@ hipError_t launch_muon_moment(const MuonArgs& a, const MuonMore& more, hipStream
 hipError_t launch_muon_norm(const MuonArgs& a, double eps, hipStream_t s);
 hipError_t launch_muon_cast(const MuonArgs& a, const MuonMore& more, hipStream_t s);
 hipError_t launch_muon_gram(const MuonArgs& a, int shape, hipStream_t s);
+hipError_t launch_muon_join(const MuonArgs& a, hipStream_t s);  // kJoins workgroups a tile
 hipError_t launch_muon_poly(const MuonArgs& a, int shape, hipStream_t s);
 // The matrix goes on, or (the iteration's last) leaves as update or, where there
 // are weights to change, into them.

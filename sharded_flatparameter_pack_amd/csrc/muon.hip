@@ -41,8 +41,8 @@ struct Small {
 
 struct Batch {
     std::vector<int32_t> mats;
-    Run moment, norm, cast, half, full;
-    int half_shape = kTile64, full_shape = kTile64;
+    Run moment, norm, cast, gram, join, half, full;
+    int gram_shape = kTile64, half_shape = kTile64, full_shape = kTile64;
 };
 
 }  // namespace
@@ -198,15 +198,20 @@ int choose_shape(const std::vector<MuonRec>& recs, const Batch& b, bool half) {
 // The table of a product.  The hardware deals workgroups out to the 8 dies in
 // turn, each with an L2 of its own: entry 8 i + d is die d's i-th tile.  Runs of
 // neighbours go to the die with the least work so far, the longest tiles first.
-void deal(const std::vector<MuonRec>& recs, const Batch& b, int side, bool half, std::vector<MatTile>* table) {
+// sliced: A's, of which a matrix's slices are apart.
+void deal(const std::vector<MuonRec>& recs, const Batch& b, int side, bool half, bool sliced, std::vector<MatTile>* table) {
     constexpr int kDies = 8;
     std::vector<Chunk> chunks;
     int64_t total = 0;
     for (int32_t i : b.mats) {
         const MuonRec& r = recs[(size_t)i];
-        Chunk c = {i, (half ? std::max(r.rp, r.cp) : std::min(r.rp, r.cp)) / 64, ordered(r, i, side, half)};
-        total += (int64_t)c.tiles.size();
-        chunks.push_back(std::move(c));
+        const bool slices = sliced && r.slices > 1;
+        for (int32_t k = 0; k < (slices ? r.slices : 1); ++k) {
+            Chunk c = {i, slices ? r.slice_steps : (half ? std::max(r.rp, r.cp) : std::min(r.rp, r.cp)) / 64, ordered(r, i, side, half)};
+            for (MatTile& t : c.tiles) t.slice = k;
+            total += (int64_t)c.tiles.size();
+            chunks.push_back(std::move(c));
+        }
     }
     std::stable_sort(chunks.begin(), chunks.end(), [](const Chunk& x, const Chunk& y) { return x.steps > y.steps; });
     std::vector<MatTile> die[kDies];
@@ -226,8 +231,50 @@ void deal(const std::vector<MuonRec>& recs, const Batch& b, int side, bool half,
         for (const auto& d : die) table->push_back(i < d.size() ? d[i] : MatTile{-1, 0, 0, 0});
 }
 
-// Closes a batch: its tiles, appended to the table.
-void close_batch(const std::vector<MuonRec>& recs, Batch* b, std::vector<MatTile>* table) {
+int64_t half_tiles(const MuonRec& r, int side) {
+    const int64_t t = ceil_div64(std::min(r.rp, r.cp), side);
+    return t * (t + 1) / 2;
+}
+
+// Where few tiles of A contract long rows, most CUs would be idle: the rows are cut
+// into slices, one launch more adds their sums up (one matrix of 40 x 70000: FFF us a
+// pass, else GGG).  Slices are as long as lets every one have a CU to itself, and
+// worth it where that ends earlier by more than the launch takes.  Returns whether
+// there are any, and lays their sums out from byte *at on.
+bool slice_gram(std::vector<MuonRec>* recs, const Batch& b, int64_t* at) {
+    constexpr double kJoin = 6.0, kStep = 0.2, kBeside = 3.0;  // us; of the deep tiles
+    constexpr int64_t kCus = 256;
+    const int side = kTileSide[kTile64Deep];
+    int64_t longest = 0, tiles = 0;
+    for (int32_t i : b.mats) {
+        const MuonRec& r = (*recs)[(size_t)i];
+        longest = std::max<int64_t>(longest, std::max(r.rp, r.cp) / 64);
+        tiles += half_tiles(r, side);
+    }
+    if (tiles > kCus) return false;
+    int64_t steps = std::max<int64_t>(4, ceil_div64(longest, kMaxSlices));
+    for (;; ++steps) {
+        int64_t slots = 0;
+        for (int32_t i : b.mats) {
+            const MuonRec& r = (*recs)[(size_t)i];
+            slots += half_tiles(r, side) * ceil_div64(std::max(r.rp, r.cp) / 64, steps);
+        }
+        if (slots <= kCus) break;  // ends: one slice each are no more than the tiles
+    }
+    if (kStep * (double)steps + kBeside + kJoin >= finish(*recs, b, b.half_shape, true)) return false;
+    for (int32_t i : b.mats) {
+        MuonRec& r = (*recs)[(size_t)i];
+        r.slices = (int32_t)ceil_div64(std::max(r.rp, r.cp) / 64, steps);
+        r.slice_steps = (int32_t)steps;
+        r.split = *at;
+        if (r.slices > 1) *at += (int64_t)r.slices * half_tiles(r, side) * side * side * 4;
+    }
+    return true;
+}
+
+// Closes a batch: its tiles, appended to the table; *at: the end of its workspace.
+void close_batch(std::vector<MuonRec>* all, Batch* b, int64_t* at, std::vector<MatTile>* table) {
+    const std::vector<MuonRec>& recs = *all;
     auto run = [&](Run* r, auto&& fill) {
         r->first = (int64_t)table->size();
         fill();
@@ -245,8 +292,18 @@ void close_batch(const std::vector<MuonRec>& recs, Batch* b, std::vector<MatTile
     });
     b->half_shape = choose_shape(recs, *b, true);
     b->full_shape = choose_shape(recs, *b, false);
-    run(&b->half, [&] { deal(recs, *b, kTileSide[b->half_shape], true, table); });
-    run(&b->full, [&] { deal(recs, *b, kTileSide[b->full_shape], false, table); });
+    run(&b->half, [&] { deal(recs, *b, kTileSide[b->half_shape], true, false, table); });
+    run(&b->full, [&] { deal(recs, *b, kTileSide[b->full_shape], false, false, table); });
+    b->gram = b->half;
+    b->gram_shape = b->half_shape;
+    if (!slice_gram(all, *b, at)) return;
+    b->gram_shape = kTile64Deep;
+    run(&b->gram, [&] { deal(recs, *b, kTileSide[kTile64Deep], true, true, table); });
+    run(&b->join, [&] {
+        for (int32_t i : b->mats)
+            if (recs[(size_t)i].slices > 1)
+                for (const MatTile& t : ordered(recs[(size_t)i], i, kTileSide[kTile64Deep], true)) table->push_back(t);
+    });
 }
 
 // The small matrices by what they need, largest first, in launches: a new one
@@ -363,7 +420,8 @@ fp_status create(int32_t n, const int64_t* rows, const int64_t* cols, const int3
             }
         }
         if (at >= kBatchBytes || (i + 1 == n && at > 0)) {
-            close_batch(recs, &open, &table);
+            close_batch(&recs, &open, &at, &table);
+            workspace = std::max(workspace, at);
             batches.push_back(std::move(open));
             open = Batch();
             at = 0;
@@ -561,8 +619,11 @@ fp_status run(fp_muon* p, MuonArgs a, MuonMore more, const std::vector<Step>& st
             a.cb = steps[i].b;
             a.cc = steps[i].c;
             a.step = (int32_t)i;
+            over(b.gram);
+            if ((e = launch_muon_gram(a, b.gram_shape, s)) != hipSuccess) return device_error(e, "product launch");
+            over(b.join);
+            if (b.join.n > 0 && (e = launch_muon_join(a, s)) != hipSuccess) return device_error(e, "slices' launch");
             over(b.half);
-            if ((e = launch_muon_gram(a, b.half_shape, s)) != hipSuccess) return device_error(e, "product launch");
             if ((e = launch_muon_poly(a, b.half_shape, s)) != hipSuccess) return device_error(e, "product launch");
             over(b.full);
             if (i + 1 < steps.size()) e = launch_muon_next(a, b.full_shape, s);

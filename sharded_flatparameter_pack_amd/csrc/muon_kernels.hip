@@ -270,6 +270,13 @@ __device__ __forceinline__ Operand columns_of(const char* base, int64_t first, i
     return {base + 2 * first, 2 * width, (int)(width - first), nullptr};
 }
 
+// A slice's sums of tile (ti, tj) of A.
+__device__ __forceinline__ float* slice_sums(const MuonArgs& a, const MuonRec& r, const Sides& z, int slice, int ti, int tj) {
+    constexpr int kSide = Shape64Deep::kBM;
+    const int t = (z.m + kSide - 1) / kSide, tile = ti * (ti + 1) / 2 + tj;
+    return reinterpret_cast<float*>(a.ws + r.split) + (int64_t)(slice * (t * (t + 1) / 2) + tile) * (kSide * kSide);
+}
+
 // A = X X^T (X^T X of a tall matrix): the tiles on and below the diagonal, and
 // their mirror images, half the work of all tiles.  4096 x 4096: 92 us, 253 tiles at
 // once on 256 CUs (0.75 PFLOP/s of the half; it ends with its last tile, and the
@@ -282,11 +289,23 @@ __global__ __launch_bounds__(S::kThreadsWg, S::kWavesSimd) void gram_kernel(cons
     if (t.mat < 0) return;
     const MuonRec& r = a.recs[t.mat];
     const Sides z = sides(r);
-    const char* h = a.ws + r.h[a.step & 1];
-    const int i0 = t.ti * S::kBM, j0 = t.tj * S::kBN, steps = z.n / kStepF16;
+    constexpr bool kSlices = std::is_same<S, Shape64Deep>::value;
+    const bool sliced = kSlices && r.slices > 1;
+    const int i0 = t.ti * S::kBM, j0 = t.tj * S::kBN, from = sliced ? t.slice * r.slice_steps : 0;
+    const int left = z.n / kStepF16 - from, steps = sliced && r.slice_steps < left ? r.slice_steps : left;
+    const char* h = a.ws + r.h[a.step & 1] + (int64_t)from * kStepBytes * (z.turned ? z.m : 1);
     TileProduct<S> tile;
     if (z.turned) run_tile<kColumnsF16, kColumnsF16>(tile, columns_of(h, i0, z.m), columns_of(h, j0, z.m), steps, lds);
     else run_tile<kRowsF16, kRowsF16>(tile, rows_of(h, i0, z.m, z.n), rows_of(h, j0, z.m, z.n), steps, lds);
+    if constexpr (kSlices) {
+        if (sliced) {
+            float* const sums = slice_sums(a, r, z, t.slice, t.ti, t.tj);
+            tile.template each<2, 4>(lds, tile.nothing, [&](int tr, int tc, const float* v, typename TileProduct<S>::Nothing) {
+                put16(sums + tr * S::kBN + tc, bits_of(v));
+            });
+            return;
+        }
+    }
     const float unscale = a.s.un_xx, out = a.s.gram;
     char* const to = a.ws + r.a + 2 * ((int64_t)i0 * z.m + j0);
     char* const mirror = a.ws + r.a + 2 * ((int64_t)j0 * z.m + i0);
@@ -317,6 +336,44 @@ __global__ __launch_bounds__(S::kThreadsWg, S::kWavesSimd) void gram_kernel(cons
         for (int k = 0; k < 8; ++k) f[k] = v[k] * out;
         st_f16(mirror + 2 * (uint32_t)(tc * z.m + tr), f);
     });
+}
+
+// A from its slices' sums, in their order: a quarter of a tile per workgroup, four
+// neighbours of a row per lane.
+__global__ __launch_bounds__(256) void join_kernel(const MuonArgs a) {
+    if (skipped(a)) return;
+    const MatTile t = a.tiles[blockIdx.x / kJoins];
+    const MuonRec& r = a.recs[t.mat];
+    const Sides z = sides(r);
+    constexpr int kSide = Shape64Deep::kBM;
+    const int tr = (int)(blockIdx.x % kJoins) * 16 + (int)(threadIdx.x >> 4), tc = (int)(threadIdx.x & 15) * 4;
+    const float* const sums = slice_sums(a, r, z, 0, t.ti, t.tj) + tr * kSide + tc;
+    const int64_t apart = slice_sums(a, r, z, 1, 0, 0) - slice_sums(a, r, z, 0, 0, 0);
+    float v[4] = {};
+#pragma unroll 8
+    for (int k = 0; k < r.slices; ++k) {
+        float f[4];
+        f32x4_of(get16(sums + k * apart), f);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) v[q] += f[q];
+    }
+    const int row = t.ti * kSide + tr, col = t.tj * kSide + tc;
+    uint32_t w[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        float f = v[q] * a.s.gram;
+        if (row == col + q) {
+            gptr<float>((void*)(a.ws + r.da))[row] = v[q] * a.s.un_xx;
+            f = 0.0f;
+        }
+        w[q] = f16_pair(f, f);
+    }
+    FP_GLOBAL uint16_t* const out = gptr<uint16_t>((void*)(a.ws + r.a));
+    *reinterpret_cast<FP_GLOBAL u32x2_t*>(out + (int64_t)row * z.m + col) =
+        u32x2_t{(w[0] & 0xFFFFu) | w[1] << 16, (w[2] & 0xFFFFu) | w[3] << 16};
+    if (t.ti == t.tj) return;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) out[(int64_t)(col + q) * z.m + row] = (uint16_t)w[q];
 }
 
 // B = b A + c A^2 in the same way; db holds a + B's diagonal.  With d the
@@ -885,6 +942,10 @@ hipError_t launch_muon_gram(const MuonArgs& a, int shape, hipStream_t s) {
 #define FP_CALL(S) launch<gram_kernel<S>>((unsigned)a.n_tiles, S::kThreadsWg, S::kLds, s, a)
     return shape == kTile192 ? FP_CALL(Shape192) : FP_BY_SHAPE(FP_CALL);
 #undef FP_CALL
+}
+
+hipError_t launch_muon_join(const MuonArgs& a, hipStream_t s) {
+    return launch<join_kernel>((unsigned)(a.n_tiles * kJoins), 256, 0, s, a);
 }
 
 hipError_t launch_muon_poly(const MuonArgs& a, int shape, hipStream_t s) {

@@ -74,7 +74,8 @@ def test_orthogonalize_large(fp, shape):
     assert rel(x.cpu(), ref.orthogonalize(g)) <= OFF
 
 
-@pytest.mark.parametrize("shape", [(4090, 4001), (3800, 5000), (5000, 3800), (1, 300000), (300000, 3), (40, 70000)])
+@pytest.mark.parametrize("shape", [(4090, 4001), (3800, 5000), (5000, 3800), (1, 300000), (300000, 3), (40, 70000),
+                                   (70000, 90), (130, 9001), (9001, 130), (600, 9000), (9000, 700), (200, 2000)])
 def test_orthogonalize_larger(fp, shape):
     g = gradient(*shape, 6, "spiked").to(dev())
     x = torch.empty(shape, device=dev())
@@ -252,20 +253,24 @@ def test_many_small(fp):
 BIG = [(1300, 2050), (2300, 700), (512, 1408), (31, 40)]
 
 
+LONG = [(20, 5000), (5000, 30), (128, 4096), (64, 64), (300, 310), (7000, 65)]
+
+
+@pytest.mark.parametrize("shapes", [BIG, LONG])
 @pytest.mark.parametrize("gd,cd,odd", [("f32", "f16", 0), ("bf16", "bf16", 1), ("bf16", None, 0)])
-def test_step_of_large_matrices(fp, gd, cd, odd):
+def test_step_of_large_matrices(fp, shapes, gd, cd, odd):
     """Steps through the launches that a batch shares, one of them skipped; nothing is written outside the matrices, nor
     behind the workspace."""
-    flats, grads, master, copies = state(BIG, gd, cd, odd)
+    flats, grads, master, copies = state(shapes, gd, cd, odd)
     plan = fp.Muon(grads, master, copies)
     mom = plan.new_momentum()
     whole = torch.full((plan.workspace_bytes + 256,), 0xA5, dtype=torch.uint8, device=dev())
     step = plan.stepper(mom, whole[:plan.workspace_bytes], **HP, found_inf=(flag := torch.zeros(1, dtype=torch.int32, device=dev())))
     for t in range(2):
-        ms = [plan.tensor_slice(mom, i).cpu().view(s) for i, s in enumerate(BIG)]
+        ms = [plan.tensor_slice(mom, i).cpu().view(s) for i, s in enumerate(shapes)]
         before = [w.cpu().clone() for w in master]
         step()
-        for i, s in enumerate(BIG):
+        for i, s in enumerate(shapes):
             say("step", t, s, gd, cd)
             m, w, x = ref.muon(grads[i].cpu(), ms[i], before[i], **HP)
             got_m = plan.tensor_slice(mom, i).cpu().view(s).double()
@@ -286,7 +291,7 @@ def test_step_of_large_matrices(fp, gd, cd, odd):
             grads[0][5, 6] = 0
             flag.zero_()
     for f in flats:
-        assert f is None or bool((gaps(f, BIG, odd) == 7).all())
+        assert f is None or bool((gaps(f, shapes, odd) == 7).all())
     assert bool((whole[plan.workspace_bytes:] == 0xA5).all())
 
 
@@ -508,7 +513,7 @@ def test_two_streams_at_once(fp):
         assert all(torch.equal(a, b) for o, v in zip(out, want) for a, b in zip(o, v))
 
 
-@pytest.mark.parametrize("shapes", [[(64, 96), (130, 50)], [(1200, 900), (300, 700), (20, 30)]])
+@pytest.mark.parametrize("shapes", [[(64, 96), (130, 50)], [(1200, 900), (300, 700), (20, 30)], [(100, 6000), (6000, 40)]])
 def test_captured_step(fp, shapes):
     """A step captured into a graph: every replay against an eager step from the same state, with new gradients and with
     eager work between the replays."""
