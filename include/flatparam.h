@@ -808,10 +808,12 @@ fp_status fp_mx8_dequantize(int64_t n, int32_t root, const uint8_t* codes, const
  * adjust: FP_MUON_ADJUST_RMS 0.2 sqrt(max(r, c)) (updates of AdamW's size),
  * FP_MUON_ADJUST_SHAPE sqrt(max(1, r / c)), FP_MUON_ADJUST_NONE 1.
  * Momentum and weights are fp32, each rounded once from fp64.  The products
- * take fp16 operands, with X and the diagonals of A and of b A + c A^2 held in
- * fp32 and fp32 sums: five steps end within 4e-3 (2-norm, relative; mostly
- * within 1e-3) of the formula.  A matrix of zeros gives zeros; one with an
- * element that is not finite gives NaN (pass found_inf).
+ * take fp16 operands and sum in fp32; the diagonals of A and of b A + c A^2 are
+ * held in fp32, X in fp32 or, between the launches of larger matrices, in 20
+ * bits: five steps end within 4e-3 (2-norm, relative; mostly within 1.5e-3) of
+ * the formula, whatever the matrix's rank, and within 3e-2 where its elements
+ * have a few values, which are all rounded alike.  A matrix of zeros gives
+ * zeros; one with an element that is not finite gives NaN (pass found_inf).
  *
  * fp_muon_create: n >= 1 matrices of rows[i] x cols[i], each side in
  *   [0, 2^20], row-major and contiguous; group, grad_dtype, grads, master,

@@ -52,6 +52,7 @@ struct MuonScale {
     float x, b, x_next;       // X's, B's and the next X's
     float gram;               // what the products of X's fp16 forms become A's by: a / x^2
     float un_x, un_xx, un_a, un_bx;  // 1 / x, 1 / x^2, 1 / a, 1 / (b x)
+    int32_t whole;            // B's diagonal multiplies X as it is, not its fp16 form
 };
 
 // A whole iteration, for the kernel that runs all of it.

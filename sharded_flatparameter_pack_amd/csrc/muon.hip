@@ -530,6 +530,10 @@ struct Step {
 // The largest power of two that keeps values up to `most` below 60000.
 float scale_for(double most) { return (float)std::ldexp(1.0, (int)std::floor(std::log2(60000.0 / most))); }
 
+// B's diagonal multiplies the unrounded X only where the later steps let what this
+// puts into directions that X does not hold grow by no more than this (muon_kernels.hip).
+constexpr double kWholeGrowth = 4.0;
+
 // Bounds of what fp16 has to hold.  With s the largest singular value of X, no
 // element of X passes s, none of A s^2, none of B the largest |b t + c t^2| for
 // t in [0, s^2]; the next s is the largest |a x + b x^3 + c x^5| for x in [0, s].
@@ -575,6 +579,11 @@ fp_status plan_steps(int32_t steps, const double* coefs, std::vector<Step>* out)
         s = std::max(next, 1e-3);
         t.s.x_next = scale_for(s * (1.0 + 1.0 / 64));
         out->push_back(t);
+    }
+    double growth = 1.0;  // of a direction near 0, over the later steps
+    for (int32_t i = steps - 1; i >= 0; --i) {
+        (*out)[(size_t)i].s.whole = growth <= kWholeGrowth;
+        growth *= std::max(1.0, std::fabs(coefs[3 * i]));
     }
     return FP_OK;
 }

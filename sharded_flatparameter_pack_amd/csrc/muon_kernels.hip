@@ -16,11 +16,20 @@
 // first of two parts goes into products (h in fp16 + l in bf16: 20 bits, and
 // fp32's range for a matrix far below eps), and in fp32 the diagonals of A and
 // B, which stand far above the other elements.  With D the
-// diagonal of B and R the rest, X <- (a + D) X + R X_h: only R's product sees the
-// rounded X.  Relative 2-norm errors of five steps
-// against 64 bits (512 x 512: normal / singular values i^-1 / 8 of them 8 times
-// the rest's norm): 7e-4 / 3e-4 / 1e-4; fp16 for everything 1.7e-3 / 3e-3 /
-// 6e-3, bf16 for everything 1e-2 / 2e-2 / 5e-2 (2^-8 is 4e-3).
+// diagonal of B and R the rest, a step is X <- a X + D X_h + R X_h, and in the last
+// ones X <- (a + D) X + R X_h.  In a matrix of full rank the second is the better:
+// only R's product sees the rounded X.  But B = D + R is 0 in directions that X does
+// not hold and R alone is not: X - X_h has parts there, R leaves |D| 2^-12 of them,
+// and every later step multiplies those by a = 3.44 (a gradient of rank 1: off by 4e-2
+// for 2 x 512, and at any size if few of its rows are not zero).  With D
+// and R on the same X_h nothing leaves X's rank but products of two roundings; the
+// roundings of A and R act on X from its left and cannot.  So the second form is for the
+// steps after which such a part grows by 4 at most (the last two of five).  Relative
+// 2-norm errors of five steps against 64 bits (512 x 512, this arithmetic in torch: normal /
+// singular values i^-1 / 8 of them 8 times the rest's norm / rank 1 / rank 1 in three rows):
+// 8e-4 / 3e-4 / 3e-4 / 3e-4 / 1.5e-3, the second form throughout 7e-4 / 3e-4 / 3e-4 / 9e-4 /
+// 3.4e-2, the first 1.2e-3 / 4e-4 / 5e-4 / 3e-4 / 1.6e-3; fp16 for everything 1.7e-3 / 3e-3 /
+// 6e-3 for the first three, bf16 1e-2 / 2e-2 / 5e-2 (2^-8 is 4e-3).
 // Powers of two (MuonScale) keep every fp16 form in its normal range.
 //
 // Compiled with -ffp-contract=off.
@@ -454,18 +463,21 @@ __device__ __forceinline__ double adjust_of(int adjust, double rows, double cols
                                             : 1.0;
 }
 
-// How the orthogonalised matrix leaves.
-enum { kGoesOn = 0, kToUpdate = 1, kToWeights = 2 };
+// How the matrix leaves: into the next step, orthogonalised as an update or into the
+// weights; kGoesOnHalf: into the next step, with B's diagonal on X_h (MuonScale::whole).
+enum { kGoesOn = 0, kToUpdate = 1, kToWeights = 2, kGoesOnHalf = 3 };
 
-// X <- (a + D) X + R X_h, in the matrix's own orientation: B X of a wide
-// matrix, X B of a tall one.  What stands between it and the product alone is the
+// X <- a X + D X_h + R X_h or (a + D) X + R X_h, in the matrix's own orientation: B X of a
+// wide matrix, X B of a tall one.  What stands between it and the product alone is the
 // epilogue, which reads and writes 8 bytes per element (14 with weights and copies)
 // while the matrix cores wait, a 256-wide tile having its CU to itself.  4096 x 4096:
 // 150 us, the product alone 101; a d = 4096 layer 1550, with weights 2110 (memory
 // alone 260 and 455).
-template <class S, int kOut, class More>
+template <class S, int kAs, class More>
 __device__ __forceinline__ void next_tile(const MuonArgs& a, const More& more) {
     extern __shared__ __align__(16) char lds[];
+    constexpr bool kWhole = kAs != kGoesOnHalf;
+    constexpr int kOut = kWhole ? kAs : kGoesOn;
     const MatTile t = a.tiles[blockIdx.x];
     if (t.mat < 0) return;
     const MuonRec& r = a.recs[t.mat];
@@ -475,9 +487,9 @@ __device__ __forceinline__ void next_tile(const MuonArgs& a, const More& more) {
     if (skip && (kOut != kToWeights || r.copy == nullptr)) return;
     const char* h = a.ws + r.h[a.step & 1];
     const char* b = a.ws + r.b;
-    // x = (D x_old + sums) as the next step wants it, or as it is
+    // x = ((a + D) x_old + sums) as the next step wants it, or as it is
     const float next = kOut == kGoesOn ? a.s.x_next : 1.0f;
-    const float un_x = a.s.un_x * next, unscale = a.s.un_bx * next;
+    const float un_x = a.s.un_x * next, unscale = a.s.un_bx * next, a_x = a.ca * un_x;
     const FP_GLOBAL float* d = gptr<float>((const void*)(a.ws + r.db));
     double rate = 0.0, decay = 1.0;
     if constexpr (kOut == kToWeights) {
@@ -537,9 +549,17 @@ __device__ __forceinline__ void next_tile(const MuonArgs& a, const More& more) {
     auto leave = [&](int tr, int tc, const float* v, const Row& row, const OldX& old, float* w) {
         if (!inside(tr, tc)) return;
         float x[kVec];
-        x_of<kVec>(old.h, old.l, x);
+        if constexpr (kWhole) {
+            x_of<kVec>(old.h, old.l, x);
 #pragma unroll
-        for (int k = 0; k < kVec; ++k) x[k] = __builtin_fmaf(z.turned ? dc[k] : row.d, x[k], v[k] * unscale);
+            for (int k = 0; k < kVec; ++k) x[k] = __builtin_fmaf(z.turned ? dc[k] : row.d, x[k], v[k] * unscale);
+        } else {
+#pragma unroll
+            for (int k = 0; k < kVec; ++k)
+                x[k] = __builtin_fmaf(z.turned ? dc[k] : row.d, k & 1 ? f16_hi(old.h[k / 2]) : f16_lo(old.h[k / 2]), v[k] * unscale);
+#pragma unroll
+            for (int k = 0; k < kVec; ++k) x[k] = __builtin_fmaf(a_x, k & 1 ? bf16_hi(old.l[k / 2]) : bf16_lo(old.l[k / 2]), x[k]);
+        }
         const uint32_t e = (uint32_t)(tr * r.cols + tc);
         if constexpr (kOut == kGoesOn) {
             st_x(h_new, l, (uint32_t)(tr * r.cp + tc), x);
@@ -859,13 +879,26 @@ __global__ __launch_bounds__(kSmallThreads, 2) void small_kernel(const MuonArgs 
 #pragma unroll
                 for (int y = 0; y < kSub; ++y) {
                     const float d = db[ti + 16 * y + j];
+                    if (sc.whole) {
 #pragma unroll
-                    for (int z = 0; z < kSub; ++z)
+                        for (int z = 0; z < kSub; ++z)
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            float& e = x[i + kSub * y + z][q];
-                            e = __builtin_fmaf(d, e, acc[y][z][q] * sc.un_bx);
-                        }
+                            for (int q = 0; q < 4; ++q) {
+                                float& e = x[i + kSub * y + z][q];
+                                e = __builtin_fmaf(d, e, acc[y][z][q] * sc.un_bx);
+                            }
+                    } else {
+                        const float dh = (d - ca) * sc.un_x;  // of X_h as it is in LDS
+#pragma unroll
+                        for (int z = 0; z < kSub; ++z)
+#pragma unroll
+                            for (int q = 0; q < 4; q += 2) {
+                                float* const e = x[i + kSub * y + z] + q;
+                                const uint32_t h2 = f16_pair(e[0] * sc.x, e[1] * sc.x);
+                                e[0] = __builtin_fmaf(dh, f16_lo(h2), __builtin_fmaf(ca, e[0], acc[y][z][q] * sc.un_bx));
+                                e[1] = __builtin_fmaf(dh, f16_hi(h2), __builtin_fmaf(ca, e[1], acc[y][z][q + 1] * sc.un_bx));
+                            }
+                    }
                 }
             }
             if (s + 1 < it.n) {
@@ -955,7 +988,9 @@ hipError_t launch_muon_poly(const MuonArgs& a, int shape, hipStream_t s) {
 }
 
 hipError_t launch_muon_next(const MuonArgs& a, int shape, hipStream_t s) {
-#define FP_CALL(S) launch<next_kernel<S, kGoesOn>>((unsigned)a.n_tiles, S::kThreadsWg, S::kLds, s, a)
+#define FP_CALL(S)                                                                                    \
+    (a.s.whole ? launch<next_kernel<S, kGoesOn>>((unsigned)a.n_tiles, S::kThreadsWg, S::kLds, s, a) \
+               : launch<next_kernel<S, kGoesOnHalf>>((unsigned)a.n_tiles, S::kThreadsWg, S::kLds, s, a))
     return FP_BY_SHAPE(FP_CALL);
 #undef FP_CALL
 }
