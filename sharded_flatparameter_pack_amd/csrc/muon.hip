@@ -559,11 +559,13 @@ fp_status plan_steps(int32_t steps, const double* coefs, std::vector<Step>* out)
         auto at = [&](double t2) {  // x^2 where the polynomial may be largest
             if (t2 > 0.0 && t2 < s2) next = std::max(next, std::fabs(std::sqrt(t2) * (a + t2 * (b + c * t2))));
         };
-        if (c != 0.0) {
-            const double disc = 9 * b * b - 20 * a * c;
-            if (disc >= 0.0) at((-3 * b + std::sqrt(disc)) / (10 * c)), at((-3 * b - std::sqrt(disc)) / (10 * c));
-        } else if (b != 0.0) {
-            at(-a / (3 * b));
+        // a + 3 b t + 5 c t^2 = 0: one root from the sum of what has b's sign, the other, which a difference would
+        // lose where c is small, from their product; what is not a number, or is infinite, is not taken
+        const double disc = 9 * b * b - 20 * a * c;
+        if (disc >= 0.0) {
+            const double q = -0.5 * (3 * b + std::copysign(std::sqrt(disc), b));
+            at(q / (5 * c));
+            at(a / q);
         }
         // beyond these the fp32 sums and the fp16 scales leave their ranges
         if (!(s <= 256.0) || !(top <= 60000.0) || !(next <= 256.0))
