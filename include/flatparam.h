@@ -852,7 +852,7 @@ fp_status fp_muon_set_grads(fp_muon* muon, const void* const* grads, void* strea
 /* updates[i] = the orthogonalised grads[i] (U = g above).  steps in
  * [1, FP_MUON_MAX_STEPS]; coefs: host array of steps x (a, b, c), which may
  * differ from step to step; FP_ERR_RANGE for coefficients that let a singular
- * value of X, which starts at 1 at most, pass 256.  eps > 0.  workspace:
+ * value of X, which starts at 1 at most, pass 256.  eps >= 2^-1022.  workspace:
  * device, fp_muon_info's size, 256-byte aligned, in any state; calls that may
  * run concurrently, graphs' replays among them, need separate ones. */
 fp_status fp_muon_orthogonalize(fp_muon* muon, int32_t steps, const double* coefs, double eps, void* workspace,

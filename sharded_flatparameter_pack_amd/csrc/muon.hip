@@ -646,8 +646,9 @@ fp_status run(fp_muon* p, MuonArgs a, MuonMore more, const std::vector<Step>& st
     return FP_OK;
 }
 
+// Of zeros the norm is eps, and fp64 has to hold its reciprocal.
 fp_status check_eps(double eps) {
-    return std::isfinite(eps) && eps > 0.0 ? FP_OK : bad(FP_ERR_RANGE, "eps must be positive and finite");
+    return std::isnormal(eps) && eps > 0.0 ? FP_OK : bad(FP_ERR_RANGE, "eps must be positive, finite and not subnormal");
 }
 
 }  // namespace

@@ -32,3 +32,23 @@ def test_a_polynomial_whose_highest_coefficient_is_next_to_nothing(fp, c, beside
         # 3 rows have singular values of about 0.58, where x loses 49 x^2 = 16 of its 50 to the products, whose operands are
         # rounded by 2^-12 four times: 2 * 16 / 34 * 2^-12 = 2.3e-4, less elsewhere
         assert float((x.cpu().double() - want).norm() / want.norm()) <= OFF
+
+
+@pytest.mark.parametrize("beside", [False, True])
+def test_the_smallest_eps(fp, beside):
+    """Zeros stay zeros under the smallest normal eps; smaller ones, whose reciprocal fp64 does not hold, are refused."""
+    grads = [torch.zeros(s) for s in SHAPES] + [torch.randn(20, 30, generator=torch.Generator().manual_seed(1))]
+    if beside:
+        grads += [torch.zeros(LARGE), torch.randn(LARGE, generator=torch.Generator().manual_seed(2))]
+    plan, out = plan_of(fp, grads)
+    ws = plan.new_workspace()
+    plan.orthogonalize(ws, eps=2.3e-308)
+    for g, x in zip(grads, out):
+        if not bool(g.any()):
+            assert bool((x == 0).all())
+        else:
+            want = ref.orthogonalize(g, eps=2.3e-308)
+            assert float((x.cpu().double() - want).norm() / want.norm()) <= OFF
+    for eps in (1e-310, 5e-324, 0.0, -1.0, float("inf"), float("nan")):
+        with pytest.raises(fp._lib.FlatParamError, match="eps"):
+            plan.orthogonalize(ws, eps=eps)
