@@ -901,7 +901,8 @@ fp_status fp_muon_step(fp_muon* muon, int32_t n_groups, const fp_muon_hparams* h
  * b of n rows of k elements, summed in fp32 and rounded once to `dtype`;
  * accumulate = 1 adds out's old value to the fp32 sum first.  A layer y = x w^T
  * is (x by rows, w by rows), its input's gradient (dy by rows, w by columns), its
- * weights' gradient (dy by columns, x by columns).  k in [1, 2^22].
+ * weights' gradient (dy by columns, x by columns).  k in [1, 2^22] (the caller
+ * fills the empty sums of k = 0), or 0 where out has no elements.
  * Rows and columns in [0, 2^31]; calls without elements do nothing.  codes are
  * 16-byte aligned, scales 8-byte, x and out to their element size.  No buffer
  * overlaps another that a call writes. */

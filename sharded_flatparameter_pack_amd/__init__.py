@@ -1421,7 +1421,8 @@ def mx4_matmul(a, b, out=None, *, accumulate: bool = False, dtype=None):
     when None) = a b^T of two MXFP4 operands (codes, scales) with rows of one
     padded length; accumulate adds to out.  A layer y = x w^T with x and w by
     rows; its input's gradient: dy by rows, w by columns; its weights' gradient:
-    dy by columns, x by columns."""
+    dy by columns, x by columns.  Rows of no elements (a layer's weights' gradient
+    without tokens) give zeros, or leave out as it is."""
     (ac, asc), (bc, bsc) = a, b
     m, k = ac.shape
     n, k2 = bc.shape
@@ -1441,6 +1442,11 @@ def mx4_matmul(a, b, out=None, *, accumulate: bool = False, dtype=None):
     x, did, rows, cols, pitch = _matrix(out, "out")
     if (rows, cols) != (m, n):
         raise ValueError(f"out has shape {(rows, cols)}, expected {(m, n)}")
+    if k == 0:  # empty sums
+        if not accumulate:
+            with _torch().no_grad():
+                out.zero_()
+        return out
     _on_device(ac.device, lib().fp_mx4_matmul, m, n, k, *ap, *bp, did, x, pitch, accumulate)
     if given:
         _bump_versions(_version_holders([out]))

@@ -107,9 +107,10 @@ extern "C" fp_status fp_mx4_matmul(int64_t m, int64_t n, int64_t k, const uint8_
     return guarded([&]() -> fp_status {
         fp_status st = check_shape(m, n, pitch);
         if (st != FP_OK) return st;
-        if (k < 1 || k > kMaxK) return bad(FP_ERR_RANGE, "k %lld outside [1, %lld]", (long long)k, (long long)kMaxK);
+        const bool empty = m == 0 || n == 0;
+        if (k < (empty ? 0 : 1) || k > kMaxK) return bad(FP_ERR_RANGE, "k %lld outside [1, %lld]", (long long)k, (long long)kMaxK);
         if (!known(dtype)) return bad(FP_ERR_INVALID, "unknown dtype %d", dtype);
-        if (m == 0 || n == 0) return FP_OK;
+        if (empty) return FP_OK;
         if ((st = check_form(a_codes, a_scales, "a")) != FP_OK) return st;
         if ((st = check_form(b_codes, b_scales, "b")) != FP_OK) return st;
         if (out == nullptr) return bad(FP_ERR_INVALID, "out is NULL");
