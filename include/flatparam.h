@@ -890,8 +890,11 @@ fp_status fp_muon_step(fp_muon* muon, int32_t n_groups, const fp_muon_hparams* h
  *   nearest whole number, ties to even);
  * stochastic = 1: h = 2^22 - 1, the code is that of q * floor(y / q + d / 2^16),
  *   d the high (columns' form: the low) half of the hash of fp_params_adamw8
- *   with i = r * cols + c modulo 2^32 and the call's seed: unbiased but for
- *   2^-17 of q, for gradients.  Give every call another seed.
+ *   with i = r * cols + c modulo 2^32 and the call's seed, for gradients: over
+ *   all d a value comes out low by less than 2^-16 of q, by 2^-17 of it on
+ *   average.  Give every call another seed: with one seed an element is rounded
+ *   the same way every time, and what that leaves adds up.  A call captured into
+ *   a graph repeats its seed at every replay.
  * The code takes x's sign; codes of an s = 255 block are 0 (a block with an
  * element that is not finite, or whose scale would pass fp32's range).
  * fp_mx4_dequantize: out (rows x cols, pitch as above, of `dtype`) receives what

@@ -1367,7 +1367,8 @@ def mx4_quantize(src, codes=None, scales=None, codes_t=None, scales_t=None, *, r
     with transposed also (codes_t, scales_t) along its columns, as a matrix of
     src.shape[1] rows, what a product that contracts the rows reads; with
     rows=False that alone.  Rounded to nearest even, or with a seed
-    stochastically (gradients; another seed for every call).  Buffers that are
+    stochastically (gradients; another seed for every call: a captured call
+    repeats its seed, so that its replays round alike).  Buffers that are
     not given are allocated, those of a form that is not wanted may not be."""
     x, dtype, r, c, pitch = _matrix(src, "src")
     if not rows and not transposed:
