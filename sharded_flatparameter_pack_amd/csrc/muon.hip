@@ -30,7 +30,9 @@ struct Run {
     int64_t first = 0, n = 0;
 };
 
-constexpr int64_t kFewSmall = 128;
+// Of matrices, how many small ones are few beside large ones (create()), and how many
+// are few for a launch of their own (group_small()).
+constexpr int64_t kFewSmall = 128, kFewForLaunch = 512;
 
 // Small matrices that need about as much: one launch.
 struct Small {
@@ -53,7 +55,7 @@ struct fp_muon {
     int32_t grad_dtype = FP_DTYPE_F32, copy_dtype = FP_DTYPE_BF16, update_dtype = FP_DTYPE_BF16;
     bool has_master = false, has_update = false;
     int32_t max_group = 0;
-    int64_t partition = 0, workspace = 0, tiles = 0;
+    int64_t partition = 0, workspace = 0;
     std::vector<int64_t> numel, offset;
     std::vector<Batch> batches;
     std::vector<Small> smalls;
@@ -310,7 +312,9 @@ void close_batch(std::vector<MuonRec>* all, Batch* b, int64_t* at, std::vector<M
 // The small matrices by what they need, largest first, in launches: a new one
 // where a matrix needs half as much as the launch's first or less (its LDS
 // decides how many workgroups a CU holds, its tiles how many registers), but not
-// for the few that a launch of their own would cost more than it saves.
+// for the few that a launch of their own would cost more than it saves (one of 160 x
+// 160 and 512 of 32 x 48: 81 us in one launch, 93 in two; 1024 of them 118 and 98, 4096
+// 385 and 141; with 64 x 64 82 and 102, 131 and 116, 428 and 204).
 std::vector<Small> group_small(const std::vector<MuonRec>& recs, std::vector<int32_t> mats, std::vector<MatTile>* table) {
     auto lds = [&](int32_t i) { return small_lds(recs[(size_t)i].rows, recs[(size_t)i].cols); };
     auto tiles = [&](int32_t i) { return small_tiles(recs[(size_t)i].rows, recs[(size_t)i].cols); };
@@ -318,7 +322,7 @@ std::vector<Small> group_small(const std::vector<MuonRec>& recs, std::vector<int
     std::vector<Small> v;
     for (size_t at = 0; at < mats.size(); ++at) {
         const int32_t i = mats[at];
-        if (v.empty() || (2 * lds(i) <= (int64_t)v.back().lds && mats.size() - at > 512)) {
+        if (v.empty() || (2 * lds(i) <= (int64_t)v.back().lds && (int64_t)(mats.size() - at) > kFewForLaunch)) {
             Small s;
             s.run.first = (int64_t)table->size();
             s.lds = (unsigned)lds(i);
@@ -407,7 +411,13 @@ fp_status create(int32_t n, const int64_t* rows, const int64_t* cols, const int3
         }
     }
     // A few small matrices beside a large one: its launches have room for them, and
-    // one of their own would come on top (24 matrices of 1 to 1400: 190 us, 159 with).
+    // one of their own would come on top.  Five steps of ragged matrices, together and
+    // apart: 24 of 1 to 1448, 15 of them small, 205 and 248 us; 64 of 1 to 512, 61 small,
+    // 128 and 182; 128 of 1 to 1448, 101 small, 319 and 344; 128 of 1 to 2048, 93 small,
+    // 540 and 494.  Beside one large matrix they pay up to about 32 (3000 x 3000 with 32 of
+    // 128 x 128: 886 and 931; 1000 x 1000 with 64: 244 and 219), and not where its tiles
+    // just fill the CUs (4096 x 4096 with 8 of 32 x 48: 1550 and 1467, with 128: 2101 and
+    // 1469).
     const bool apart = !any_large || few > kFewSmall;
     for (int32_t i = 0; i < n; ++i) {
         MuonRec& r = recs[(size_t)i];
@@ -447,7 +457,6 @@ fp_status create(int32_t n, const int64_t* rows, const int64_t* cols, const int3
     p->max_group = max_group;
     p->partition = partition;
     p->workspace = workspace;
-    p->tiles = (int64_t)table.size();
     p->numel = std::move(sizes);
     p->offset = std::move(offsets);
     p->batches = std::move(batches);
