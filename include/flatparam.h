@@ -814,6 +814,9 @@ fp_status fp_mx8_dequantize(int64_t n, int32_t root, const uint8_t* codes, const
  * the formula, whatever the matrix's rank, and within 3e-2 where its elements
  * have a few values, which are all rounded alike.  A matrix of zeros gives
  * zeros; one with an element that is not finite gives NaN (pass found_inf).
+ * A plan repeats its results bit for bit.  Another plan's differ within those
+ * errors: the sizes of all its matrices decide which kernels each goes through,
+ * so that ranks that step copies of one matrix need plans over the same sizes.
  *
  * fp_muon_create: n >= 1 matrices of rows[i] x cols[i], each side in
  *   [0, 2^20], row-major and contiguous; group, grad_dtype, grads, master,
@@ -904,7 +907,9 @@ fp_status fp_muon_step(fp_muon* muon, int32_t n_groups, const fp_muon_hparams* h
  * b of n rows of k elements, summed in fp32 and rounded once to `dtype`;
  * accumulate = 1 adds out's old value to the fp32 sum first.  A layer y = x w^T
  * is (x by rows, w by rows), its input's gradient (dy by rows, w by columns), its
- * weights' gradient (dy by columns, x by columns).  k in [1, 2^22] (the caller
+ * weights' gradient (dy by columns, x by columns).  Operands whose own lengths
+ * differ but pad to the same are not told apart: what one lacks counts as zeros.
+ * k in [1, 2^22] (the caller
  * fills the empty sums of k = 0), or 0 where out has no elements.
  * Rows and columns in [0, 2^31]; calls without elements do nothing.  codes are
  * 16-byte aligned, scales 8-byte, x and out to their element size.  No buffer

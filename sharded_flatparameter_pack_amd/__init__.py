@@ -1122,6 +1122,10 @@ class Muon:
     multiple of 32) on.  The tensors must stay alive and in place for the plan's
     life (set_grads changes the gradients); the plan is bound to their device.
     A workspace belongs to calls that run one after the other.
+    Matrices are whole: a flat shard whose border cuts one cannot be given here.
+    A plan repeats its results bit for bit; ranks that step copies of one matrix
+    need plans over the same sizes, which decide the kernels that each goes
+    through (another plan's result differs within the iteration's error).
     Written tensors count as changed in place, as with Params.
     """
 
@@ -1420,7 +1424,8 @@ def mx4_dequantize(codes, scales, cols: int, dst=None, *, dtype=None):
 def mx4_matmul(a, b, out=None, *, accumulate: bool = False, dtype=None):
     """out (rows of a x rows of b; allocated here in `dtype`, bf16 by default,
     when None) = a b^T of two MXFP4 operands (codes, scales) with rows of one
-    padded length; accumulate adds to out.  A layer y = x w^T with x and w by
+    padded length (300 and 400 elements, which both pad to 512, are not told apart:
+    what is missing counts as zeros); accumulate adds to out.  A layer y = x w^T with x and w by
     rows; its input's gradient: dy by rows, w by columns; its weights' gradient:
     dy by columns, x by columns.  Rows of no elements (a layer's weights' gradient
     without tokens) give zeros, or leave out as it is."""

@@ -127,3 +127,27 @@ def test_matrices_of_few_values(fp, beside):
         off = rel(x.cpu(), ref.orthogonalize(g))
         say("few values", i, tuple(g.shape), off)
         assert off <= 2.8e-2
+
+
+def test_a_matrix_alone_and_beside_others(fp):
+    """Another plan's kernels give another result within the iteration's error; a plan over the same sizes gives the same bits."""
+    shapes = [(40, 70), (128, 128), (30, 5000), (16, 4096), (300, 310)]
+
+    def run(more):
+        grads = [torch.randn(s, generator=torch.Generator().manual_seed(i)).to(dev()) for i, s in enumerate(shapes + more)]
+        out = [torch.empty(s, device=dev()) for s in shapes + more]
+        plan = fp.Muon(grads, updates=out)
+        plan.orthogonalize(plan.new_workspace())
+        return out[:len(shapes)]
+
+    first, again, other = run([(20, 30)]), run([(20, 30)]), run([(1200, 1100)] * 20)
+    for i, s in enumerate(shapes):
+        g = torch.randn(s, generator=torch.Generator().manual_seed(i))
+        alone = torch.empty(s, device=dev())
+        one = fp.Muon([g.to(dev())], updates=[alone])
+        one.orthogonalize(one.new_workspace())
+        want = ref.orthogonalize(g)
+        assert torch.equal(first[i], again[i])
+        for x in (first[i], other[i], alone):
+            assert rel(x.cpu(), want) <= OFF
+        say("alone and beside others", s, rel(first[i], alone.double()), rel(other[i], alone.double()))

@@ -85,6 +85,15 @@ def test_scales_of_the_whole_range(fp, m, n, k):
     assert bool(((got - want).abs() <= k * 2.0 ** -24 * size).all())
 
 
+def test_lengths_that_pad_alike(fp):
+    """300 and 400 elements are both padded to 512: what the shorter rows lack counts as zeros."""
+    gen = torch.Generator().manual_seed(4)
+    a, b = torch.randn(20, 300, generator=gen), torch.randn(30, 400, generator=gen)
+    got = fp.mx4_matmul(fp.mx4_quantize(a.to(dev())), fp.mx4_quantize(b.to(dev())), dtype=torch.float32)
+    longer = torch.cat([a, torch.zeros(20, 100)], 1)
+    assert torch.equal(got, fp.mx4_matmul(fp.mx4_quantize(longer.to(dev())), fp.mx4_quantize(b.to(dev())), dtype=torch.float32))
+
+
 LARGE = {}
 
 
