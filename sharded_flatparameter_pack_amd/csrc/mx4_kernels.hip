@@ -393,8 +393,8 @@ __global__ __launch_bounds__(S::kThreadsWg, S::kWavesSimd) void matmul_kernel(co
 // is no larger than its workgroups fill the card (shape_of): b is read once, and
 // that bounds them, so a workgroup has 16 of its rows and its waves share K.  Fragments come straight from memory, a wave's
 // steps kAhead at a time; the waves' sums meet in LDS, in their order.  1 x 8192 x
-// 4096: 6.3 us (2.8 TB/s; the weights' bytes alone 3.8), a launch's latency and two
-// trips to memory; on 64-wide tiles 11.8.
+// 4096: 5.6 us with b in the last-level cache, 7.2 from memory (2.5 TB/s; b's bytes alone
+// 2.9), a launch's latency and two trips to memory; on 64-wide tiles 7.4 and 14.8.
 constexpr int kThinWaves = 8;
 template <int kF>
 __global__ __launch_bounds__(64 * kThinWaves, 2) void thin_kernel(const Mx4MatmulArgs a) {
@@ -514,9 +514,11 @@ int64_t mx4_quantize_lanes(const Mx4QuantArgs& a) { return quant_groups(a) * 256
 // rows on 64-wide tiles 11.7 us, on 128-wide ones 15.9; 1024 rows 24.2 and 17.6; 2048
 // rows on 128-wide tiles 27.6, on 256-wide ones 33.7; 2304 rows 40.7 and 33.8), and
 // where larger tiles would be mostly empty.  The thin kernel, whose workgroups
-// read all of a, for as many workgroups per 16 rows of a (1 x 8192 x 4096: 5.6 us, on
-// 64-wide tiles 7.4; 16 x 8192 x 16384: 24 and 34; 32 x 2048 x 4096: 6.4 and 7.7; 32 x
-// 8192 x 4096: 10.6 and 7.7; 64 x 2048 x 4096 with kF 4: 9.2 and 8.2).
+// read all of a, for as many workgroups per 16 rows of a (with b in the last-level
+// cache, 1 x 8192 x 4096: 5.6 us, on 64-wide tiles 7.4; 16 x 8192 x 16384: 24 and 34; 32 x
+// 2048 x 4096: 6.4 and 7.7; 32 x 8192 x 4096: 10.6 and 7.7; 64 x 2048 x 4096 with kF 4: 9.2
+// and 8.2; with b from memory 7.2 and 14.8, 30 and 51, 7.3 and 15, 12 and 15 for the first
+// four).
 enum { kThin1, kThin2, kTiles64, kTiles128, kTiles256 };
 static int64_t tiles_of(const Mx4MatmulArgs& a, int64_t side) { return ceil_div64(a.m, side) * ceil_div64(a.n, side); }
 static int shape_of(const Mx4MatmulArgs& a) {
