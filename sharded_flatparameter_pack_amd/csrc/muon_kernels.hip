@@ -642,7 +642,9 @@ __device__ __forceinline__ void put8_lds(char* p, float a, float b, float c, flo
 // bound a step (128 x 128 with 1 x 1: 11 us a step, with 2 x 2 6.2), 1 x 1 for the
 // smallest, whose steps are all latency and want every wave (32 x 48: 1.2 us a step,
 // with 2 x 2 2.3); A and B of at most 64 rows in blocks of 2 x 1, of which there is
-// one for each wave (64 x 256: 3.5 us a step, so 3.2; 32 x 1024: 5.8, so 4.4).  The
+// one for each wave (64 x 256: 3.5 us a step, so 3.2; 32 x 1024: 5.8, so 4.4).  Where
+// B's diagonal multiplies X_h, a step takes 0.1 to 0.8 more (32 x 48 1.3, 64 x 256 3.5, 32 x
+// 1024 5.2, 128 x 128 6.6).  The
 // rest of a step with weights, 16 us for 64 x 256, is one CU's loads, fp64 and stores.
 //
 // kTiles: tiles of X per wave.
