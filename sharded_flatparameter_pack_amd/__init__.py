@@ -1424,11 +1424,11 @@ def mx4_dequantize(codes, scales, cols: int, dst=None, *, dtype=None):
 def mx4_matmul(a, b, out=None, *, accumulate: bool = False, dtype=None):
     """out (rows of a x rows of b; allocated here in `dtype`, bf16 by default,
     when None) = a b^T of two MXFP4 operands (codes, scales) with rows of one
-    padded length (300 and 400 elements, which both pad to 512, are not told apart:
-    what is missing counts as zeros); accumulate adds to out.  A layer y = x w^T with x and w by
-    rows; its input's gradient: dy by rows, w by columns; its weights' gradient:
-    dy by columns, x by columns.  Rows of no elements (a layer's weights' gradient
-    without tokens) give zeros, or leave out as it is."""
+    padded length (300 and 400 elements, which both pad to 512, are not told
+    apart: what is missing counts as zeros); accumulate adds to out.  A layer
+    y = x w^T with x and w by rows; its input's gradient: dy by rows, w by columns;
+    its weights' gradient: dy by columns, x by columns.  Rows of no elements (the
+    weights' gradient without tokens) give zeros, or leave out as it is."""
     (ac, asc), (bc, bsc) = a, b
     m, k = ac.shape
     n, k2 = bc.shape

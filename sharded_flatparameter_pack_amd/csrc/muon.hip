@@ -414,8 +414,9 @@ fp_status create(int32_t n, const int64_t* rows, const int64_t* cols, const int3
     // one of their own would come on top.  Five steps of ragged matrices, together and
     // apart: 24 of 1 to 1448, 15 of them small, 205 and 248 us; 64 of 1 to 512, 61 small,
     // 128 and 182; 128 of 1 to 1448, 101 small, 319 and 344; 128 of 1 to 2048, 93 small,
-    // 540 and 494.  Beside one large matrix they pay up to about 32 (3000 x 3000 with 32 of
-    // 128 x 128: 886 and 931; 1000 x 1000 with 64: 244 and 219), and not where its tiles
+    // 540 and 494.  Beside one large matrix they mostly pay up to about 32 (3000 x 3000 with
+    // 32 of 128 x 128: 886 and 931; 1400 x 1300 with 32 of 160 x 160 260 and 299, of 32 x 48
+    // 272 and 231; 1000 x 1000 with 64 of 128 x 128: 244 and 219), and not where its tiles
     // just fill the CUs (4096 x 4096 with 8 of 32 x 48: 1550 and 1467, with 128: 2101 and
     // 1469).
     const bool apart = !any_large || few > kFewSmall;

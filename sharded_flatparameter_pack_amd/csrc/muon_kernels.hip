@@ -15,10 +15,9 @@
 // loses is kept small by holding apart what carries most: X, of which only the
 // first of two parts goes into products (h in fp16 + l in bf16: 20 bits, and
 // fp32's range for a matrix far below eps), and in fp32 the diagonals of A and
-// B, which stand far above the other elements.  With D the
-// diagonal of B and R the rest, a step is X <- a X + D X_h + R X_h, and in the last
-// ones X <- (a + D) X + R X_h.  In a matrix of full rank the second is the better:
-// only R's product sees the rounded X.  But B = D + R is 0 in directions that X does
+// B, which stand far above the other elements.  With D the diagonal of B and R the
+// rest, a step is X <- a X + D X_h + R X_h, and in the last ones X <- (a + D) X + R X_h.
+// In a matrix of full rank the second is the better: only R's product sees the rounded X.  But B = D + R is 0 in directions that X does
 // not hold and R alone is not: X - X_h has parts there, R leaves |D| 2^-12 of them,
 // and every later step multiplies those by a = 3.44 (a gradient of rank 1: off by 4e-2
 // for 2 x 512, and at any size if few of its rows are not zero).  With D
@@ -644,8 +643,8 @@ __device__ __forceinline__ void put8_lds(char* p, float a, float b, float c, flo
 // with 2 x 2 2.3); A and B of at most 64 rows in blocks of 2 x 1, of which there is
 // one for each wave (64 x 256: 3.5 us a step, so 3.2; 32 x 1024: 5.8, so 4.4).  Where
 // B's diagonal multiplies X_h, a step takes 0.1 to 0.8 more (32 x 48 1.3, 64 x 256 3.5, 32 x
-// 1024 5.2, 128 x 128 6.6).  The
-// rest of a step with weights, 16 us for 64 x 256, is one CU's loads, fp64 and stores.
+// 1024 5.2, 128 x 128 6.6).  The rest of a step with weights, 16 us for 64 x 256, is one
+// CU's loads, fp64 and stores.
 //
 // kTiles: tiles of X per wave.
 constexpr int kSmallWaves = kSmallThreads / 64;
